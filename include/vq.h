@@ -352,6 +352,60 @@ vq_status vq_encode(const float *w, int32_t rows, int32_t cols, int32_t d, int32
                     uint32_t *codes, uint16_t *codebook, uint16_t *scales, double *relerr, void *workspace,
                     size_t workspace_bytes, void *stream);
 
+/*
+ * Routing to experts: the expert ids and route weights that vq_moe_gemv and
+ * vq_moe_gemm (VQ_EPILOGUE_COMBINE) take, from a router's logits.  Per token,
+ * with logits l_e:
+ *   score   VQ_SCORE_SOFTMAX p_e = exp(l_e) / sum over the experts in play, or
+ *           VQ_SCORE_SIGMOID p_e = 1 / (1 + exp(-l_e)).
+ *   in play an expert whose logit (and bias, if given) is neither NaN nor
+ *           -inf; an infinite logit counts as the largest finite fp32 value.
+ *           Logits of a type's lowest finite value are ordinary values.
+ *   key     l_e without a bias (the order of the scores), p_e + bias[e] with
+ *           one (a balance bias moves the choice, never the weights).
+ *   groups  of num_experts / groups consecutive experts; a group's score is
+ *           its largest key (VQ_GROUP_MAX) or the sum of its two largest
+ *           (VQ_GROUP_TOP2; of p_e without a bias; of one where only one is in
+ *           play).  The best top_groups groups stay, ties to the lowest
+ *           group; groups without an expert in play never stay.  groups = 1:
+ *           no group step (top_groups must be 1).
+ *   choice  the top_k largest keys left, in descending order, ties to the
+ *           lowest expert; slots nothing is left for get id -1 (skipped by
+ *           the routed products) and weight 0.  Scores are compared in 64
+ *           bits where they decide the choice.
+ *   weight  scale * p_e, with renormalize scale * p_e / (sum of the chosen
+ *           p_e; 0 where that sum is 0).
+ * logits: device [T][num_experts] of logits_dtype (vq_dtype), aligned to
+ * their element; expert_ids: device [T][top_k] int32 and route_weights:
+ * device [T][top_k] fp32, 4-byte aligned; bias: device [num_experts] fp32,
+ * 4-byte aligned, or NULL.  T >= 0 (0 enqueues nothing).  One launch, no
+ * workspace; the same inputs give the same bits.
+ * Errors (VQ_ERR_SHAPE): num_experts outside [1, 1024]; top_k outside [1, 64]
+ * or above top_groups * num_experts / groups; groups outside [1, 64] or not a
+ * divisor of num_experts; top_groups outside [1, groups]; an unknown score,
+ * group_score or logits_dtype; renormalize not 0 or 1; a scale that is not
+ * finite; reserved not 0; T * num_experts above 2^40 or T above 2^30.
+ */
+typedef enum { VQ_SCORE_SOFTMAX = 0, VQ_SCORE_SIGMOID = 1 } vq_score;
+typedef enum { VQ_GROUP_MAX = 0, VQ_GROUP_TOP2 = 1 } vq_group_score;
+
+typedef struct vq_router {
+  int32_t num_experts;  /* E                                                      */
+  int32_t top_k;        /* slots per token                                        */
+  int32_t score;        /* vq_score                                               */
+  int32_t logits_dtype; /* vq_dtype                                               */
+  int32_t groups;       /* 1: none                                                */
+  int32_t top_groups;   /* groups that stay                                       */
+  int32_t group_score;  /* vq_group_score                                         */
+  int32_t renormalize;  /* 0 or 1                                                 */
+  float scale;          /* factor of every weight                                 */
+  int32_t reserved;     /* must be 0                                              */
+  const float *bias;    /* device [E] fp32, or NULL                               */
+} vq_router;
+
+vq_status vq_moe_route(const vq_router *r, const void *logits, int32_t T, int32_t *expert_ids,
+                       float *route_weights, void *stream);
+
 /* Text for the last non-OK status returned on this thread ("" if none). */
 const char *vq_last_error(void);
 

@@ -1,0 +1,163 @@
+"""vq_moe_route against a plain loop in 64 bits: the ids exactly, the weights
+to fp32 rounding, over scores, biases, groups, types, odd sizes and masks."""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as O
+from tests.helpers import announce
+from vq_dequant_matmul_gemv_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+# Weights are exp, sums of at most 64 terms and one quotient in at least 32
+# bits: an exp of a rounded argument x (|x| e^x <= 0.37 of the largest, times
+# 2^-24) and its own 2 units, 6 tree additions, the quotient, the scale and the
+# final rounding stay below 32 half units of the row's largest weight.
+REL = 32 * 2.0 ** -24
+
+
+def _logits(T, E, dtype, key, masked=False):
+    import torch
+    g = synth.rng("route-logits", *key)
+    x = (1.5 * g.normal(size=(T, E)) + g.normal(size=E)).astype(np.float32)
+    t = torch.from_numpy(x).to(dtype)
+    if masked:
+        t[:, torch.from_numpy(g.random(E) < 0.2)] = torch.finfo(dtype).min
+        t[torch.from_numpy(g.random((T, E)) < 0.15)] = -np.inf
+        t[torch.from_numpy(g.random((T, E)) < 0.02)] = np.nan
+        t[torch.from_numpy(g.random((T, E)) < 0.01)] = np.inf
+        t[torch.from_numpy(g.random(T) < 0.2)] = -np.inf          # padded tokens
+        t[0] = -np.inf
+    return t
+
+
+def _check(logits, top_k, bias=None, **kw):
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    T, E = logits.shape
+    announce("moe_route", tuple(logits.shape), str(logits.dtype), top_k, "bias" if bias is not None else "", kw)
+    r = binding.Router(E, top_k, bias=None if bias is None else bias.cuda(), **kw)
+    # poisoned outputs with a guard behind the last row
+    ids = torch.full(((T + 1) * top_k,), 777, dtype=torch.int32, device="cuda")
+    w = torch.full(((T + 1) * top_k,), 777.0, device="cuda")
+    n = T * top_k
+    got = binding.moe_route(r, logits.cuda(), ids=ids[:n].view(T, top_k), weights=w[:n].view(T, top_k))
+    torch.cuda.synchronize()
+    rid, rw = O.route(logits.float().numpy(), top_k, bias=None if bias is None else bias.numpy(), **kw)
+    assert np.array_equal(got[0].cpu().numpy(), rid)
+    gw = got[1].cpu().numpy().astype(np.float64)
+    top = np.abs(rw).max(axis=1, keepdims=True)
+    assert np.all(np.abs(gw - rw) <= REL * top + 1e-37), np.max(np.abs(gw - rw))
+    assert torch.all(ids[n:] == 777).item() and torch.all(w[n:] == 777.0).item()
+
+
+def _dt(name):
+    import torch
+    return getattr(torch, name)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("E,k,T", [(1, 1, 5), (2, 1, 1), (7, 7, 13), (64, 6, 65), (65, 8, 3), (128, 64, 9),
+                                   (160, 6, 31), (256, 8, 130), (500, 10, 17), (1024, 16, 6)])
+def test_plain_choice(score, dtype, E, k, T):
+    _check(_logits(T, E, _dt(dtype), ("plain", score, E, T)), k, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k,groups,top_groups,group_score,bias", [
+    (256, 8, 8, 4, "top2", True), (256, 8, 8, 4, "top2", False), (256, 8, 8, 3, "max", True),
+    (160, 6, 8, 3, "max", False), (96, 4, 3, 2, "top2", True), (72, 12, 72 // 2, 20, "top2", True),
+    (64, 8, 64, 40, "max", True), (64, 3, 64, 3, "top2", False), (1000, 20, 10, 5, "top2", True),
+    (256, 32, 1, 1, "max", True), (6, 2, 2, 1, "top2", True),
+])
+def test_groups_and_bias(score, renorm, E, k, groups, top_groups, group_score, bias):
+    import torch
+    g = synth.rng("route-bias", E, groups)
+    b = torch.from_numpy((0.05 * g.normal(size=E)).astype(np.float32)) if bias else None
+    x = _logits(67, E, torch.float32, ("groups", E, groups))
+    _check(x, k, b, score=score, groups=groups, top_groups=top_groups, group_score=group_score,
+           renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("groups,top_groups,group_score,bias", [
+    (1, 1, "max", False), (1, 1, "max", True), (8, 3, "max", False), (8, 3, "top2", False), (8, 3, "top2", True)])
+def test_masks(score, dtype, groups, top_groups, group_score, bias):
+    """-inf, NaN, +inf and lowest-value logits, rows with nothing left, a bias
+    with -inf and NaN in it."""
+    import torch
+    b = None
+    if bias:
+        g = synth.rng("route-mask-bias")
+        b = torch.from_numpy((0.05 * g.normal(size=96)).astype(np.float32))
+        b[5], b[17], b[80] = -np.inf, np.nan, np.inf
+    _check(_logits(83, 96, _dt(dtype), ("mask", dtype), masked=True), 8, b, score=score, groups=groups,
+           top_groups=top_groups, group_score=group_score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_ties_go_to_the_lowest(score, bias):
+    """Rows of equal values, of few values, of +0 and -0, of one value a group."""
+    import torch
+    E = 96
+    g = synth.rng("route-ties")
+    rows = [np.zeros(E), np.where(g.random(E) < 0.5, 0.0, -0.0), g.integers(0, 3, E), np.repeat(np.arange(8), 12),
+            np.full(E, -100.0), np.full(E, 50.0), np.full(E, np.finfo(np.float32).min)]
+    x = torch.from_numpy(np.stack(rows).astype(np.float32))
+    b = torch.from_numpy(g.integers(0, 2, E).astype(np.float32)) if bias else None
+    for kw in (dict(), dict(groups=8, top_groups=3, group_score="top2"), dict(groups=8, top_groups=3)):
+        _check(x, 10, b, score=score, **kw)
+
+
+def test_nearly_equal_keys_are_ordered_in_64_bits():
+    """Sigmoid scores a few 32-bit units apart behind a bias: the order of the
+    64-bit keys decides, expert by expert and group by group."""
+    import torch
+    E, T = 256, 40
+    g = synth.rng("route-near")
+    base = g.normal(size=(T, 1))
+    x = (base + 2.0 ** -22 * g.integers(-8, 9, size=(T, E))).astype(np.float32)
+    b = torch.from_numpy((0.25 + 2.0 ** -24 * g.integers(-4, 5, size=E)).astype(np.float32))
+    for score in ("sigmoid", "softmax"):
+        _check(torch.from_numpy(x), 8, b, score=score)
+        _check(torch.from_numpy(x), 8, b, score=score, groups=8, top_groups=4, group_score="top2")
+        _check(torch.from_numpy(x), 8, None, score=score, groups=8, top_groups=4, group_score="top2")
+
+
+@pytest.mark.parametrize("low", [-80.0, -300.0, -700.0])
+def test_far_negative_scores_keep_their_weights(low):
+    """Sigmoids far below fp32's range still renormalise to their ratios."""
+    import torch
+    x = torch.tensor([[low, low + 1.0, low + 2.0, low - 1.0]])
+    _check(x, 3, score="sigmoid")
+    _check(x, 3, score="softmax")
+
+
+def test_empty_batch_and_other_stream_and_capture():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    r = binding.Router(64, 4)
+    ids, w = binding.moe_route(r, torch.zeros(0, 64, device="cuda"))
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+    x = _logits(33, 64, torch.float32, ("stream",)).cuda()
+    ref = binding.moe_route(r, x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = binding.moe_route(r, x, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    # a captured call replays on new logits
+    buf = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gi, gw = binding.moe_route(r, buf)
+    for seed in range(3):
+        buf.copy_(_logits(33, 64, torch.float32, ("replay", seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        ri, rw = binding.moe_route(r, buf)
+        assert torch.equal(gi, ri) and torch.equal(gw, rw)

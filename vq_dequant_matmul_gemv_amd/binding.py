@@ -43,6 +43,23 @@ class CIo(ctypes.Structure):
     ]
 
 
+class CRouter(ctypes.Structure):
+    """Mirror of `vq_router`."""
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
 class CTensor(ctypes.Structure):
     """Mirror of `vq_tensor`."""
     _fields_ = [
@@ -85,6 +102,7 @@ def _load():
         "vq_moe_gemm_no_alloc": (i32, [T, P, i32, P, i32, i32, P, P]),
         "vq_encode_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "vq_encode": (i32, [P, i32, i32, i32, i32, i32, P, i32, P, i32, P, P, P, P, P, ctypes.c_size_t, P]),
+        "vq_moe_route": (i32, [ctypes.POINTER(CRouter), P, i32, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
     }
@@ -100,7 +118,7 @@ LIB = _load()
 EXPORTED = ("vq_words_per_row", "vq_dequant", "vq_gemv", "vq_gemm", "vq_moe_gemv", "vq_gemv_ex",
             "vq_gemm_ex", "vq_moe_gemv_ex", "vq_moe_gemm_ex",
             "vq_moe_workspace_bytes", "vq_moe_gemm", "vq_moe_gemm_no_alloc", "vq_encode_workspace_bytes",
-            "vq_encode", "vq_last_error", "vq_status_name")
+            "vq_encode", "vq_moe_route", "vq_last_error", "vq_status_name")
 
 
 def check(status: int) -> None:
@@ -381,3 +399,86 @@ def encode(w, d: int, log2_k: int, group: int, sample_idx, uniforms, iters: int,
                         iters, _ptr(codes), _ptr(codebook), _ptr(scales), _ptr(relerr), _ptr(workspace),
                         workspace.numel(), _stream(stream)))
     return VQTensor(codes, codebook, scales, rows, cols, d, log2_k, group), relerr
+
+
+# --------------------------------------------------------------------------
+# routing to experts
+# --------------------------------------------------------------------------
+
+VQ_SCORE_SOFTMAX, VQ_SCORE_SIGMOID = 0, 1
+VQ_GROUP_MAX, VQ_GROUP_TOP2 = 0, 1
+SCORES = {"softmax": VQ_SCORE_SOFTMAX, "sigmoid": VQ_SCORE_SIGMOID}
+GROUP_SCORES = {"max": VQ_GROUP_MAX, "top2": VQ_GROUP_TOP2}
+
+
+def _on_device(device, stream, call, *shapes):
+    """Allocate an output for each (shape, dtype) that is not a tensor already,
+    on the stream the work goes to, then run call(outputs, raw stream) with
+    `device` current."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        with torch.cuda.stream(stream):   # makes the stream's device current too
+            return _run_alloc(torch, device, stream, call, shapes)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _run_alloc(torch, device, torch.cuda.current_stream(device), call, shapes)
+    return _run_alloc(torch, device, torch.cuda.current_stream(device), call, shapes)
+
+
+def _run_alloc(torch, device, stream, call, shapes):
+    outs = [s if isinstance(s, torch.Tensor) else None if s is None else
+            torch.empty(s[0], dtype=s[1], device=device) for s in shapes]
+    check(call(outs, stream.cuda_stream))
+    return outs
+
+
+@dataclass
+class Router:
+    """How a router's logits become expert ids and weights (see `vq_router` in
+    include/vq.h): score "softmax" or "sigmoid", bias fp32 [num_experts] or
+    None, group_score "max" or "top2"."""
+    num_experts: int
+    top_k: int
+    score: str = "softmax"
+    bias: object = None
+    groups: int = 1
+    top_groups: int = 1
+    group_score: str = "max"
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
+    """Expert ids int32 [T][top_k] and route weights fp32 [T][top_k] for
+    moe_gemv / moe_gemm, from logits [T][num_experts] (fp32, fp16 or bf16)."""
+    torch = _torch()
+    r = router
+    if r.score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    if r.group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}")
+    if logits.dim() != 2 or logits.shape[1] != r.num_experts:
+        raise ValueError(f"logits must be [T][{r.num_experts}]")
+    T, k = logits.shape[0], r.top_k
+    dev = logits.device
+    _dev_check(logits)
+    if r.bias is not None:
+        if r.bias.dtype != torch.float32 or tuple(r.bias.shape) != (r.num_experts,):
+            raise ValueError(f"bias must be fp32 [{r.num_experts}]")
+        _dev_check(r.bias, device=dev)
+    for t, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if t is not None:
+            _check_out(t, dt, (T, k), name)
+            _dev_check(t, device=dev)
+    cr = CRouter(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
+                 GROUP_SCORES[r.group_score], int(r.renormalize), r.scale, 0,
+                 None if r.bias is None else r.bias.data_ptr())
+
+    def call(outs, st):
+        return LIB.vq_moe_route(ctypes.byref(cr), logits.data_ptr(), T, outs[0].data_ptr(), outs[1].data_ptr(), st)
+
+    shape = (T, max(k, 0))
+    return tuple(_on_device(dev, stream, call, ids if ids is not None else (shape, torch.int32),
+                            weights if weights is not None else (shape, torch.float32)))

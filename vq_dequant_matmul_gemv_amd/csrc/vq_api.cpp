@@ -11,6 +11,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -120,6 +121,11 @@ vq_status check_xy(const void* x, const void* y, const char* yname) {
 vq_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return VQ_OK;
   return fail(VQ_ERR_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
+}
+
+// OutKind of a (checked) vq_dtype.
+int dtype_kind(int32_t dt) {
+  return dt == VQ_DTYPE_F32 ? vqmi::kOutF32 : dt == VQ_DTYPE_F16 ? vqmi::kOutF16 : vqmi::kOutBF16;
 }
 
 // Largest input width the streaming GEMV covers in one pass over x; wider
@@ -402,6 +408,54 @@ vq_status vq_encode(const float* w, int32_t rows, int32_t cols, int32_t d, int32
   return hip_status(vqmi::launch_encode(w, rows, cols, d, log2_k, group, sample_idx, n_sample, uniforms, iters, codes,
                                         codebook, scales, relerr, workspace, (hipStream_t)stream),
                     "vq_encode launch");
+}
+
+vq_status vq_moe_route(const vq_router* r, const void* logits, int32_t T, int32_t* expert_ids,
+                       float* route_weights, void* stream) {
+  if (!r) return fail(VQ_ERR_NULL, "vq_moe_route: router descriptor is NULL");
+  const int32_t E = r->num_experts;
+  if (E < 1 || E > 1024) return fail(VQ_ERR_SHAPE, "vq_moe_route: num_experts=%d outside [1, 1024]", E);
+  if (r->groups < 1 || r->groups > 64 || E % r->groups != 0)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: groups=%d must be in [1, 64] and divide num_experts=%d", r->groups, E);
+  if (r->top_groups < 1 || r->top_groups > r->groups)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: top_groups=%d outside [1, groups=%d]", r->top_groups, r->groups);
+  if (r->top_k < 1 || r->top_k > 64 || r->top_k > r->top_groups * (E / r->groups))
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: top_k=%d must be in [1, 64] and at most the %d experts of %d groups",
+                r->top_k, r->top_groups * (E / r->groups), r->top_groups);
+  if (r->score != VQ_SCORE_SOFTMAX && r->score != VQ_SCORE_SIGMOID)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: score=%d is not a vq_score", r->score);
+  if (r->group_score != VQ_GROUP_MAX && r->group_score != VQ_GROUP_TOP2)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: group_score=%d is not a vq_group_score", r->group_score);
+  if (r->logits_dtype != VQ_DTYPE_F32 && r->logits_dtype != VQ_DTYPE_F16 && r->logits_dtype != VQ_DTYPE_BF16)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: logits_dtype=%d is not a vq_dtype", r->logits_dtype);
+  if (r->renormalize != 0 && r->renormalize != 1)
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: renormalize=%d must be 0 or 1", r->renormalize);
+  if (!std::isfinite(r->scale)) return fail(VQ_ERR_SHAPE, "vq_moe_route: scale is not finite");
+  if (r->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_moe_route: reserved must be 0");
+  if (T < 0 || T > (1 << 30) || (int64_t)T * E > ((int64_t)1 << 40))
+    return fail(VQ_ERR_SHAPE, "vq_moe_route: T=%d out of range", T);
+  if (T == 0) return VQ_OK;
+  if (!logits || !expert_ids || !route_weights)
+    return fail(VQ_ERR_NULL, "vq_moe_route: a required pointer is NULL (logits=%p expert_ids=%p route_weights=%p)",
+                logits, (const void*)expert_ids, (const void*)route_weights);
+  const int kind = dtype_kind(r->logits_dtype);
+  if (!aligned(logits, kind == vqmi::kOutF32 ? 4 : 2))
+    return fail(VQ_ERR_ALIGN, "vq_moe_route: logits are not aligned to their element");
+  if (!aligned(expert_ids, 4) || !aligned(route_weights, 4) || !aligned(r->bias, 4))
+    return fail(VQ_ERR_ALIGN, "vq_moe_route: expert_ids, route_weights and bias need 4-byte alignment");
+  vqmi::RouterSpec sp{};
+  sp.num_experts = E;
+  sp.top_k = r->top_k;
+  sp.sigmoid = r->score == VQ_SCORE_SIGMOID;
+  sp.logits_kind = kind;
+  sp.groups = r->groups;
+  sp.top_groups = r->top_groups;
+  sp.top2 = r->group_score == VQ_GROUP_TOP2;
+  sp.renorm = r->renormalize;
+  sp.scale = r->scale;
+  sp.bias = r->bias;
+  return hip_status(vqmi::launch_router(sp, logits, T, expert_ids, route_weights, (hipStream_t)stream),
+                    "vq_moe_route launch");
 }
 
 }  // extern "C"

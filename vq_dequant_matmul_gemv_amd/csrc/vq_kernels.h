@@ -119,6 +119,16 @@ hipError_t launch_route(const int32_t* ids, int npairs, int num_experts, int32_t
 hipError_t launch_moe_gemm(const TensorView& w, const IoSpec& io, const void* x, int x_per_slot,
                            const int32_t* ids, int T, int top_k, void* y, void* ws, hipStream_t s);
 
+// Routing from logits to expert ids and weights (vq_router.hip).
+struct RouterSpec {
+  int num_experts, top_k, sigmoid, logits_kind;  // logits_kind: OutKind
+  int groups, top_groups, top2, renorm;
+  float scale;
+  const float* bias;
+};
+hipError_t launch_router(const RouterSpec& r, const void* logits, int T, int32_t* ids, float* weights,
+                         hipStream_t s);
+
 // The fit of one tensor (vq_encode.hip).
 size_t encode_workspace_bytes(int rows, int cols, int d, int log2_k, int n_sample);
 hipError_t launch_encode(const float* w, int rows, int cols, int d, int log2_k, int group, const int32_t* sample_idx,
