@@ -149,7 +149,8 @@ typedef struct vq_tensor {
  * vq_moe_gemv_ex with cols > 20480 accept only y_dtype F32 and no SWIGLU.
  * A NULL io means the defaults.
  */
-typedef enum { VQ_DTYPE_F32 = 0, VQ_DTYPE_F16 = 1, VQ_DTYPE_BF16 = 2 } vq_dtype;
+/* E4M3: 8-bit values with block scales, for the calls that name it. */
+typedef enum { VQ_DTYPE_F32 = 0, VQ_DTYPE_F16 = 1, VQ_DTYPE_BF16 = 2, VQ_DTYPE_E4M3 = 3 } vq_dtype;
 typedef enum { VQ_EPILOGUE_NONE = 0, VQ_EPILOGUE_SWIGLU = 1, VQ_EPILOGUE_COMBINE = 2 } vq_epilogue;
 
 typedef struct vq_io {
@@ -405,6 +406,66 @@ typedef struct vq_router {
 
 vq_status vq_moe_route(const vq_router *r, const void *logits, int32_t T, int32_t *expert_ids,
                        float *route_weights, void *stream);
+
+/*
+ * Tensors in 8-bit floating point with a scale for each block of 128, for the
+ * parts of a model that are not vector-quantized (shared experts, projections
+ * kept in 8 bits): values are OCP e4m3 (largest 448, no infinities, codes
+ * 0x7f and 0xff NaN), a value stands for code * scale.
+ *
+ * A weight: values [rows][cols], one fp32 scale for each 128 x 128 block (the
+ * last block of rows or columns may be partial).  rows >= 1; cols a positive
+ * multiple of 16, at most 2^20 (else VQ_ERR_SHAPE).  value_bytes == rows *
+ * cols and scale_elems == ceil(rows/128) * ceil(cols/128), so a short or
+ * sliced buffer is refused.  values 16-byte, scales 4-byte aligned.
+ * Activations: x [T][cols] with x_scales [T][ceil(cols/128)], one scale for a
+ * token's 128 columns, as vq_fp8_quant and vq_norm leave them.
+ */
+typedef struct vq_fp8_tensor {
+  const uint8_t *values; /* device [rows][cols] e4m3                             */
+  const float *scales;   /* device [ceil(rows/128)][ceil(cols/128)] fp32         */
+  int32_t rows;          /* output features                                     */
+  int32_t cols;          /* input features                                      */
+  int64_t value_bytes;   /* number of bytes behind `values`                      */
+  int64_t scale_elems;   /* number of fp32 values behind `scales`                */
+} vq_fp8_tensor;
+
+/*
+ * Quantize activations: for each token and 128 columns,
+ *   scale = max |x| / 448 rounded to fp32 (1 for a block of zeros),
+ *   q = the e4m3 value nearest to x / scale (ties to even; exact, no double
+ *       rounding), at most 448 in magnitude.
+ * NaN and infinite x become NaN codes and do not count for the scale, so they
+ * spoil only their own token's results.
+ *   x: device [T][cols] of x_dtype (F16 or BF16), 16-byte aligned;
+ *   q: device [T][cols] e4m3, 16-byte aligned; scales: device
+ *   [T][ceil(cols/128)] fp32, 4-byte aligned.  cols as for vq_fp8_tensor;
+ *   T >= 0 (0 enqueues nothing), T * ceil(cols/128) < 2^31.
+ */
+vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t *q, float *scales,
+                       void *stream);
+
+/*
+ * Product of e4m3 activations with an e4m3 weight:
+ *   y[t][r] = sum_b x_scales[t][b] * scales[r / 128][b] *
+ *             sum over the 128 columns of block b of x[t][c] * w[r][c],
+ * the products exact, all sums in fp32.  Any T (decode and prefill shapes
+ * run different kernels with the same result contract); the same call gives
+ * the same bits every time.
+ *   io: y_dtype and epilogue (NONE or SWIGLU on interleaved gate/up rows: y
+ *     has rows / 2 values per token) as for vq_gemm_ex; x_dtype must be
+ *     VQ_DTYPE_E4M3.  NULL: fp32 y, no epilogue.
+ *   x: device [T][cols] e4m3, 16-byte aligned; x_scales: device
+ *     [T][ceil(cols/128)] fp32, 4-byte aligned; y: device, 16-byte aligned.
+ *   workspace: device, >= vq_fp8_workspace_bytes(rows, cols, T) bytes, 16-byte
+ *     aligned, owned by the caller (may be NULL where that is 0); contents on
+ *     entry are ignored and on return are undefined.  Calls that overlap in
+ *     time need separate workspaces.
+ * T >= 0 (0 enqueues nothing), T <= 2^24, rows <= 2^24.
+ */
+size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T);
+vq_status vq_fp8_gemm(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x, const float *x_scales, int32_t T,
+                      void *y, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Text for the last non-OK status returned on this thread ("" if none). */
 const char *vq_last_error(void);

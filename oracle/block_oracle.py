@@ -57,3 +57,60 @@ def route(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups=1, 
         ids[t, :len(chosen)] = chosen
         weights[t, :len(chosen)] = w * scale
     return ids, weights
+
+
+# ---------------------------------------------------------------------------
+# e4m3 with a scale for each block of 128
+# ---------------------------------------------------------------------------
+
+BLOCK = 128
+
+# value of every e4m3 code: sign, 4 exponent bits (bias 7), 3 mantissa bits
+E4M3 = np.array([(-1.0) ** (c >> 7) * (np.nan if (c & 0x7f) == 0x7f else
+                                       (c & 7) * 2.0 ** -9 if ((c >> 3) & 15) == 0 else
+                                       (8 + (c & 7)) * 2.0 ** (((c >> 3) & 15) - 10)) for c in range(256)])
+
+
+def e4m3_nearest(v):
+    """Codes (uint8) of the e4m3 values nearest to float64 v, ties to the even
+    code, clamped to +-448; NaN and infinities give the NaN code 0x7f."""
+    v = np.asarray(v, dtype=np.float64)
+    bad = ~np.isfinite(v)
+    a = np.minimum(np.abs(np.where(bad, 0.0, v)), 448.0)
+    grid = E4M3[:127]
+    up = np.clip(np.searchsorted(grid, a), 1, 126)       # grid[up - 1] < a <= grid[up] (but for a = 0)
+    lo = up - 1
+    dl, du = a - grid[lo], grid[up] - a                  # exact: both within a factor of 2, or small multiples
+    code = np.where(dl < du, lo, np.where(du < dl, up, np.where(lo % 2 == 0, lo, up)))
+    code = code | np.where(np.signbit(v), 0x80, 0)
+    return np.where(bad, 0x7f, code).astype(np.uint8)
+
+
+def fp8_quant(x):
+    """(codes uint8 [T][C], scales fp32 [T][ceil(C/128)]) of x [T][C]."""
+    x = np.asarray(x, dtype=np.float64)
+    T, C = x.shape
+    codes = np.zeros((T, C), dtype=np.uint8)
+    scales = np.zeros((T, -(-C // BLOCK)), dtype=np.float32)
+    for b in range(scales.shape[1]):
+        part = x[:, b * BLOCK:(b + 1) * BLOCK]
+        amax = np.where(np.isfinite(part), np.abs(part), 0.0).max(axis=1)
+        s = np.where(amax > 0, amax / 448.0, 1.0).astype(np.float32)
+        scales[:, b] = s
+        # the float64 quotient of an fp16/bf16 value and an fp32 scale lies on
+        # a tie (5 bits) only if it is one: x = tie * s has at most 29 bits
+        codes[:, b * BLOCK:(b + 1) * BLOCK] = e4m3_nearest(part / s.astype(np.float64)[:, None])
+    return codes, scales
+
+
+def fp8_values(codes, scales, rows=1):
+    """float64 values of e4m3 codes [R][C] with a scale per rows x 128 block."""
+    R, C = codes.shape
+    s = np.repeat(np.repeat(np.asarray(scales, np.float64), rows, axis=0)[:R], BLOCK, axis=1)[:, :C]
+    return E4M3[codes] * s
+
+
+def fp8_product(xc, xs, wc, ws):
+    """(y [T][R], the sums of the magnitudes [T][R]) in float64."""
+    x, w = fp8_values(xc, xs), fp8_values(wc, ws, BLOCK)
+    return x @ w.T, np.abs(x) @ np.abs(w).T

@@ -106,3 +106,92 @@ def test_route_oracle_by_hand():
     assert ids.tolist() == [[1, 0]]
     ids, w = route(np.array([[0.0, -np.inf]]), 1, score="sigmoid", renormalize=False)
     assert ids.tolist() == [[0]] and w.tolist() == [[0.5]]
+
+
+# ---- e4m3 tensors ---------------------------------------------------------
+
+def _quant(b, x=0x10000, dtype=2, T=4, cols=256, q=0x20000, scales=0x30000):
+    return _status(b, b.LIB.vq_fp8_quant(x, dtype, T, cols, q, scales, None))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=0), "VQ_ERR_SHAPE"), (dict(dtype=3), "VQ_ERR_SHAPE"),
+    (dict(cols=0), "VQ_ERR_SHAPE"), (dict(cols=8), "VQ_ERR_SHAPE"), (dict(cols=136 + 1), "VQ_ERR_SHAPE"),
+    (dict(cols=(1 << 20) + 16), "VQ_ERR_SHAPE"), (dict(T=-1), "VQ_ERR_SHAPE"),
+    (dict(T=1 << 30, cols=256), "VQ_ERR_SHAPE"),             # 2^31 blocks
+    (dict(x=0), "VQ_ERR_NULL"), (dict(q=0), "VQ_ERR_NULL"), (dict(scales=0), "VQ_ERR_NULL"),
+    (dict(x=0x10008), "VQ_ERR_ALIGN"), (dict(q=0x20008), "VQ_ERR_ALIGN"), (dict(scales=0x30002), "VQ_ERR_ALIGN"),
+    (dict(T=0, x=0, q=0, scales=0), "VQ_OK"),
+])
+def test_quant_refuses(b, kw, status):
+    assert _quant(b, **kw) == status, b.LIB.vq_last_error()
+
+
+def _fp8(b, T=4, x=0x40000, xs=0x50000, y=0x60000, ws=0x70000, ws_bytes=1 << 40, io=None, **kw):
+    base = dict(values=0x10000, scales=0x20000, rows=300, cols=272)
+    base.update(kw)
+    base.setdefault("value_bytes", base["rows"] * base["cols"])
+    base.setdefault("scale_elems", -(-base["rows"] // 128) * -(-base["cols"] // 128))
+    w = b.CFP8Tensor(**base)
+    i = None if io is None else ctypes.byref(b.CIo(*io))
+    return _status(b, b.LIB.vq_fp8_gemm(ctypes.byref(w), i, x, xs, T, y, ws, ws_bytes, None))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(values=0), "VQ_ERR_NULL"), (dict(scales=0), "VQ_ERR_NULL"),
+    (dict(x=0), "VQ_ERR_NULL"), (dict(xs=0), "VQ_ERR_NULL"), (dict(y=0), "VQ_ERR_NULL"),
+    (dict(rows=0), "VQ_ERR_SHAPE"), (dict(rows=(1 << 24) + 1), "VQ_ERR_SHAPE"),
+    (dict(cols=8), "VQ_ERR_SHAPE"), (dict(cols=280), "VQ_ERR_SHAPE"), (dict(cols=-16), "VQ_ERR_SHAPE"),
+    (dict(T=-1), "VQ_ERR_SHAPE"), (dict(T=(1 << 24) + 1), "VQ_ERR_SHAPE"),
+    (dict(T=1 << 24, rows=1 << 24), "VQ_ERR_SHAPE"),
+    (dict(value_bytes=300 * 272 - 16), "VQ_ERR_SHAPE"),
+    (dict(scale_elems=8), "VQ_ERR_SHAPE"),                    # a slice of the scales
+    (dict(values=0x10008), "VQ_ERR_ALIGN"), (dict(scales=0x20002), "VQ_ERR_ALIGN"),
+    (dict(x=0x40008), "VQ_ERR_ALIGN"), (dict(xs=0x50001), "VQ_ERR_ALIGN"), (dict(y=0x60008), "VQ_ERR_ALIGN"),
+    (dict(io=(1, 0, 0, 0, None)), "VQ_ERR_SHAPE"),            # x_dtype is not e4m3
+    (dict(io=(3, 3, 0, 0, None)), "VQ_ERR_SHAPE"),            # y cannot be e4m3
+    (dict(io=(3, 0, 2, 0, None)), "VQ_ERR_SHAPE"),            # COMBINE
+    (dict(io=(3, 0, 0, 1, None)), "VQ_ERR_SHAPE"),            # reserved
+    (dict(io=(3, 0, 1, 0, None), rows=301), "VQ_ERR_SHAPE"),  # SWIGLU on odd rows
+    (dict(T=0, x=0, xs=0, y=0, ws=0, ws_bytes=0), "VQ_OK"),
+])
+def test_fp8_gemm_refuses(b, kw, status):
+    assert _fp8(b, **kw) == status, b.LIB.vq_last_error()
+
+
+def test_fp8_workspace(b):
+    """The size is a pure function of the sizes; a call that needs some and
+    gets less, none or a misaligned one is refused."""
+    assert b.LIB.vq_fp8_workspace_bytes(300, 272, 0) == 0
+    assert b.LIB.vq_fp8_workspace_bytes(300, 8, 4) == 0 and b"cols" in b.LIB.vq_last_error()
+    for T, rows, cols in [(1, 17408, 5120), (64, 512, 17408), (100, 5120, 17408), (200, 256, 4096), (2048, 5120, 17408)]:
+        need = b.LIB.vq_fp8_workspace_bytes(rows, cols, T)
+        if need:
+            kw = dict(T=T, rows=rows, cols=cols)
+            assert _fp8(b, ws=0, ws_bytes=need, **kw) == "VQ_ERR_WORKSPACE"
+            assert _fp8(b, ws_bytes=need - 1, **kw) == "VQ_ERR_WORKSPACE"
+            assert _fp8(b, ws=0x70008, ws_bytes=need, **kw) == "VQ_ERR_ALIGN"
+
+
+def test_fp8_wrapper_refuses_before_the_library(b):
+    import torch
+    x = torch.zeros(3, 32, dtype=torch.float16)
+    with pytest.raises(ValueError, match="GPU"):
+        b.fp8_quant(x)
+    with pytest.raises(ValueError, match="fp16 or bf16"):
+        b.fp8_quant(x.float())
+    with pytest.raises(ValueError, match="GPU"):
+        b.FP8Tensor(torch.zeros(8, 32, dtype=torch.uint8), torch.ones(1, 1)).cstruct()
+
+
+def test_e4m3_oracle_matches_the_type(b):
+    """The oracle's code table and rounding against torch's conversion."""
+    import numpy as np
+    import torch
+    from oracle import block_oracle as O
+    table = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(table, O.E4M3, equal_nan=True)
+    v = np.random.default_rng(3).normal(size=4000).astype(np.float32) * 60
+    v = np.concatenate([v, O.E4M3[:127], (O.E4M3[1:127] + O.E4M3[:126]) / 2, v * 2.0 ** -12]).astype(np.float32)
+    want = torch.from_numpy(np.clip(v, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(O.e4m3_nearest(v), want)

@@ -26,7 +26,7 @@ class VQError(RuntimeError):
         self.message = message
 
 
-VQ_DTYPE_F32, VQ_DTYPE_F16, VQ_DTYPE_BF16 = 0, 1, 2
+VQ_DTYPE_F32, VQ_DTYPE_F16, VQ_DTYPE_BF16, VQ_DTYPE_E4M3 = 0, 1, 2, 3
 VQ_EPILOGUE_NONE, VQ_EPILOGUE_SWIGLU, VQ_EPILOGUE_COMBINE = 0, 1, 2
 EPILOGUES = {None: VQ_EPILOGUE_NONE, "none": VQ_EPILOGUE_NONE, "swiglu": VQ_EPILOGUE_SWIGLU,
              "combine": VQ_EPILOGUE_COMBINE}
@@ -57,6 +57,18 @@ class CRouter(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("reserved", ctypes.c_int32),
         ("bias", ctypes.c_void_p),
+    ]
+
+
+class CFP8Tensor(ctypes.Structure):
+    """Mirror of `vq_fp8_tensor`."""
+    _fields_ = [
+        ("values", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("value_bytes", ctypes.c_int64),
+        ("scale_elems", ctypes.c_int64),
     ]
 
 
@@ -103,6 +115,9 @@ def _load():
         "vq_encode_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "vq_encode": (i32, [P, i32, i32, i32, i32, i32, P, i32, P, i32, P, P, P, P, P, ctypes.c_size_t, P]),
         "vq_moe_route": (i32, [ctypes.POINTER(CRouter), P, i32, P, P, P]),
+        "vq_fp8_quant": (i32, [P, i32, i32, i32, P, P, P]),
+        "vq_fp8_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "vq_fp8_gemm": (i32, [ctypes.POINTER(CFP8Tensor), IO, P, P, i32, P, P, ctypes.c_size_t, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
     }
@@ -118,7 +133,7 @@ LIB = _load()
 EXPORTED = ("vq_words_per_row", "vq_dequant", "vq_gemv", "vq_gemm", "vq_moe_gemv", "vq_gemv_ex",
             "vq_gemm_ex", "vq_moe_gemv_ex", "vq_moe_gemm_ex",
             "vq_moe_workspace_bytes", "vq_moe_gemm", "vq_moe_gemm_no_alloc", "vq_encode_workspace_bytes",
-            "vq_encode", "vq_moe_route", "vq_last_error", "vq_status_name")
+            "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm", "vq_last_error", "vq_status_name")
 
 
 def check(status: int) -> None:
@@ -482,3 +497,97 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
     shape = (T, max(k, 0))
     return tuple(_on_device(dev, stream, call, ids if ids is not None else (shape, torch.int32),
                             weights if weights is not None else (shape, torch.float32)))
+
+
+# --------------------------------------------------------------------------
+# e4m3 tensors with a scale for each block of 128
+# --------------------------------------------------------------------------
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+@dataclass
+class FP8Tensor:
+    """Device-resident e4m3 weight (see `vq_fp8_tensor` in include/vq.h).
+
+    values  float8_e4m3fn (or uint8 codes) [rows][cols]
+    scales  fp32 [ceil(rows/128)][ceil(cols/128)]
+    """
+    values: object
+    scales: object
+
+    @property
+    def device(self):
+        return self.values.device
+
+    def cstruct(self) -> CFP8Tensor:
+        torch = _torch()
+        v, s = self.values, self.scales
+        _dev_check(v, s, device=v.device)
+        if v.dtype not in (torch.float8_e4m3fn, torch.uint8) or v.dim() != 2:
+            raise ValueError("values must be float8_e4m3fn (or uint8 codes) [rows][cols]")
+        if s.dtype != torch.float32:
+            raise ValueError("scales must be fp32")
+        return CFP8Tensor(v.data_ptr(), s.data_ptr(), v.shape[0], v.shape[1], v.numel(), s.numel())
+
+
+def fp8_quant(x, q=None, scales=None, stream=None):
+    """e4m3 values [T][cols] and fp32 scales [T][ceil(cols/128)] of fp16 or
+    bf16 activations x [T][cols] (vq_fp8_quant)."""
+    torch = _torch()
+    if x.dtype not in (torch.float16, torch.bfloat16) or x.dim() != 2:
+        raise ValueError("x must be fp16 or bf16 [T][cols]")
+    T, cols = x.shape
+    dev = x.device
+    _dev_check(x)
+    sshape = (T, _blocks(cols))
+    if q is not None:
+        _check_out(q, torch.float8_e4m3fn, (T, cols), "q")
+        _dev_check(q, device=dev)
+    if scales is not None:
+        _check_out(scales, torch.float32, sshape, "scales")
+        _dev_check(scales, device=dev)
+    code = _dtype_code(x.dtype)
+
+    def call(outs, st):
+        return LIB.vq_fp8_quant(x.data_ptr(), code, T, cols, outs[0].data_ptr(), outs[1].data_ptr(), st)
+
+    return tuple(_on_device(dev, stream, call, q if q is not None else ((T, cols), torch.float8_e4m3fn),
+                            scales if scales is not None else (sshape, torch.float32)))
+
+
+def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_dtype=None, epilogue=None):
+    """y = x W^T of e4m3 activations (values [T][cols], scales
+    [T][ceil(cols/128)]) through vq_fp8_gemm, decode and prefill alike;
+    epilogue "swiglu" on interleaved gate/up rows gives silu(gate) * up."""
+    torch = _torch()
+    cs = w.cstruct()
+    rows, cols = cs.rows, cs.cols
+    if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.dim() != 2 or x.shape[1] != cols:
+        raise ValueError(f"x must be float8_e4m3fn (or uint8 codes) [T][{cols}]")
+    T = x.shape[0]
+    if x_scales.dtype != torch.float32 or tuple(x_scales.shape) != (T, _blocks(cols)):
+        raise ValueError(f"x_scales must be fp32 {(T, _blocks(cols))}")
+    if epilogue not in EPILOGUES or epilogue == "combine":
+        raise ValueError("epilogue must be None or 'swiglu'")
+    y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
+    yshape = (T, rows // 2 if epilogue == "swiglu" else rows)
+    dev = w.device
+    _dev_check(x, x_scales, device=dev)
+    if y is not None:
+        _check_out(y, y_dtype, yshape)
+        _dev_check(y, device=dev)
+    if workspace is not None:
+        _dev_check(workspace, device=dev)
+    need = LIB.vq_fp8_workspace_bytes(rows, cols, T)
+    io = CIo(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, None)
+
+    def call(outs, st):
+        ws = outs[1]
+        return LIB.vq_fp8_gemm(ctypes.byref(cs), ctypes.byref(io), x.data_ptr(), x_scales.data_ptr(), T,
+                               outs[0].data_ptr(), None if ws is None else ws.data_ptr(),
+                               0 if ws is None else ws.numel() * ws.element_size(), st)
+
+    return _on_device(dev, stream, call, y if y is not None else (yshape, y_dtype),
+                      workspace if workspace is not None or need == 0 else ((need,), torch.uint8))[0]

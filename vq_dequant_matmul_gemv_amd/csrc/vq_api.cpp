@@ -458,4 +458,89 @@ vq_status vq_moe_route(const vq_router* r, const void* logits, int32_t T, int32_
                     "vq_moe_route launch");
 }
 
+// Columns of an e4m3 tensor: whole 16-byte pieces.
+static bool fp8_cols_ok(int32_t cols) { return cols >= 16 && cols % 16 == 0 && cols <= (1 << 20); }
+
+vq_status vq_fp8_quant(const void* x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t* q, float* scales,
+                       void* stream) {
+  if (x_dtype != VQ_DTYPE_F16 && x_dtype != VQ_DTYPE_BF16)
+    return fail(VQ_ERR_SHAPE, "vq_fp8_quant: x_dtype=%d: x must be VQ_DTYPE_F16 or VQ_DTYPE_BF16", x_dtype);
+  if (!fp8_cols_ok(cols))
+    return fail(VQ_ERR_SHAPE, "vq_fp8_quant: cols=%d must be a multiple of 16 in [16, 2^20]", cols);
+  if (T < 0 || (int64_t)T * ((cols + 127) / 128) >= (int64_t)1 << 31)
+    return fail(VQ_ERR_SHAPE, "vq_fp8_quant: T=%d out of range for cols=%d", T, cols);
+  if (T == 0) return VQ_OK;
+  vq_status st = check_xy(x, q, "q");
+  if (st != VQ_OK) return st;
+  if (!scales) return fail(VQ_ERR_NULL, "vq_fp8_quant: scales is NULL");
+  if (!aligned(scales, 4)) return fail(VQ_ERR_ALIGN, "vq_fp8_quant: scales is not 4-byte aligned");
+  return hip_status(vqmi::launch_fp8_quant(x, x_dtype == VQ_DTYPE_BF16, T, cols, q, scales, (hipStream_t)stream),
+                    "vq_fp8_quant launch");
+}
+
+static vq_status check_fp8_sizes(int32_t rows, int32_t cols, int32_t T) {
+  if (rows < 1 || rows > (1 << 24)) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: rows=%d outside [1, 2^24]", rows);
+  if (!fp8_cols_ok(cols))
+    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: cols=%d must be a multiple of 16 in [16, 2^20]", cols);
+  if (T < 0 || T > (1 << 24)) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: T=%d outside [0, 2^24]", T);
+  if ((int64_t)((rows + 15) / 16) * ((T + 15) / 16) > (1 << 30))
+    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: T=%d x %d rows makes too many tiles", T, rows);
+  return VQ_OK;
+}
+
+size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T) {
+  if (check_fp8_sizes(rows, cols, T) != VQ_OK) return 0;
+  return T == 0 ? 0 : vqmi::fp8_workspace_bytes(rows, cols, T);
+}
+
+vq_status vq_fp8_gemm(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x, const float* x_scales, int32_t T,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!w) return fail(VQ_ERR_NULL, "vq_fp8_gemm: tensor descriptor is NULL");
+  if (!w->values || !w->scales)
+    return fail(VQ_ERR_NULL, "vq_fp8_gemm: tensor has a NULL pointer (values=%p scales=%p)", (const void*)w->values,
+                (const void*)w->scales);
+  vq_status st = check_fp8_sizes(w->rows, w->cols, T);
+  if (st != VQ_OK) return st;
+  if (w->value_bytes != (int64_t)w->rows * w->cols)
+    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: values hold %lld bytes but rows*cols = %lld", (long long)w->value_bytes,
+                (long long)w->rows * w->cols);
+  const int64_t want = (int64_t)((w->rows + 127) / 128) * ((w->cols + 127) / 128);
+  if (w->scale_elems != want)
+    return fail(VQ_ERR_SHAPE,
+                "vq_fp8_gemm: scales hold %lld values but a %d x %d weight has %lld blocks of 128 x 128: sliced, or "
+                "of another layout",
+                (long long)w->scale_elems, w->rows, w->cols, (long long)want);
+  if (!aligned(w->values, 16)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: values are not 16-byte aligned");
+  if (!aligned(w->scales, 4)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: scales are not 4-byte aligned");
+  vqmi::IoSpec ios{};
+  if (io) {
+    if (io->x_dtype != VQ_DTYPE_E4M3)
+      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->x_dtype=%d: x must be VQ_DTYPE_E4M3", io->x_dtype);
+    if (io->y_dtype != VQ_DTYPE_F32 && io->y_dtype != VQ_DTYPE_F16 && io->y_dtype != VQ_DTYPE_BF16)
+      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->y_dtype=%d must be F32, F16 or BF16", io->y_dtype);
+    if (io->epilogue != VQ_EPILOGUE_NONE && io->epilogue != VQ_EPILOGUE_SWIGLU)
+      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->epilogue=%d: NONE or SWIGLU", io->epilogue);
+    if (io->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->reserved must be 0");
+    if (io->epilogue == VQ_EPILOGUE_SWIGLU && w->rows % 2 != 0)
+      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: SWIGLU needs interleaved (gate, up) row pairs: rows=%d is odd", w->rows);
+    ios.y_kind = dtype_kind(io->y_dtype);
+    ios.epi = io->epilogue == VQ_EPILOGUE_SWIGLU ? vqmi::kEpiSwiglu : vqmi::kEpiNone;
+  }
+  if (T == 0) return VQ_OK;
+  st = check_xy(x, y, "y");
+  if (st != VQ_OK) return st;
+  if (!x_scales) return fail(VQ_ERR_NULL, "vq_fp8_gemm: x_scales is NULL");
+  if (!aligned(x_scales, 4)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: x_scales is not 4-byte aligned");
+  const size_t need = vqmi::fp8_workspace_bytes(w->rows, w->cols, T);
+  if (need > 0) {
+    if (!workspace) return fail(VQ_ERR_WORKSPACE, "vq_fp8_gemm: workspace is NULL (need %zu bytes)", need);
+    if (workspace_bytes < need)
+      return fail(VQ_ERR_WORKSPACE, "vq_fp8_gemm: workspace has %zu bytes, need %zu", workspace_bytes, need);
+    if (!aligned(workspace, 16)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: workspace is not 16-byte aligned");
+  }
+  const vqmi::Fp8View v{w->values, w->scales, w->rows, w->cols};
+  return hip_status(vqmi::launch_fp8_gemm(v, ios, x, x_scales, T, y, workspace, (hipStream_t)stream),
+                    "vq_fp8_gemm launch");
+}
+
 }  // extern "C"

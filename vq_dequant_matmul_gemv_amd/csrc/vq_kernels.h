@@ -129,6 +129,17 @@ struct RouterSpec {
 hipError_t launch_router(const RouterSpec& r, const void* logits, int T, int32_t* ids, float* weights,
                          hipStream_t s);
 
+// e4m3 tensors with a scale for each block of 128 (vq_fp8.hip).
+struct Fp8View {
+  const uint8_t* values;
+  const float* scales;
+  int rows, cols;
+};
+hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t* q, float* scales, hipStream_t s);
+size_t fp8_workspace_bytes(int rows, int cols, int T);
+hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x, const float* xs, int T, void* y,
+                           void* workspace, hipStream_t s);
+
 // The fit of one tensor (vq_encode.hip).
 size_t encode_workspace_bytes(int rows, int cols, int d, int log2_k, int n_sample);
 hipError_t launch_encode(const float* w, int rows, int cols, int d, int log2_k, int group, const int32_t* sample_idx,
