@@ -467,6 +467,60 @@ size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T);
 vq_status vq_fp8_gemm(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x, const float *x_scales, int32_t T,
                       void *y, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The norms before and after a block, fused with its gate and the scaled
+ * residual sum: what stands between one block's products and the next one's.
+ *   u = block * rsqrt(mean(block^2) + eps) * (post_weight + weight_offset),
+ *       or block itself where post_weight is NULL;
+ *   v = beta * residual + alpha * act(gate) * u;
+ *   h = v * rsqrt(mean(v^2) + eps) * (pre_weight + weight_offset), or with a
+ *       factor of 1 where pre_weight is NULL.
+ * Means over a token's cols values.  All arithmetic in fp32; v and h are
+ * rounded once, on their stores (h comes from the unrounded v).
+ *   block:    device [T][cols] of block_dtype (the products' y: F32, F16 or
+ *             BF16), or NULL: v = beta * residual (a plain norm).  Post norm
+ *             and gate need a block.
+ *   residual: device [T][cols] of residual_dtype (F32, F16 or BF16), or NULL:
+ *             no residual term.  Not both NULL.
+ *   gate:     VQ_GATE_NONE (1), VQ_GATE_CHANNEL gate_values [cols],
+ *             VQ_GATE_TOKEN [T], VQ_GATE_FULL [T][cols]; gate_act
+ *             VQ_ACT_NONE, VQ_ACT_SIGMOID or VQ_ACT_TANH is applied to them.
+ *   post_weight, pre_weight: device [cols]; like gate_values of weight_dtype.
+ *   residual_out: device [T][cols] of residual_dtype, v; may be `residual`
+ *             itself; NULL: not stored.
+ *   h:        device [T][cols] of h_dtype (F32, F16, BF16: the VQ products' x;
+ *             E4M3: vq_fp8_gemm's, quantized as vq_fp8_quant does, with
+ *             h_scales [T][ceil(cols/128)] fp32); NULL: not computed.  Not
+ *             both outputs NULL.  No other buffers may overlap.
+ * Pointers of [T][cols] and [cols] data 16-byte aligned, the others to their
+ * element.  T >= 0 (0 enqueues nothing), T <= 2^30.  One launch, no workspace;
+ * the same inputs give the same bits.
+ * Errors (VQ_ERR_SHAPE): cols outside [1, 32768], or not a multiple of 16 for
+ * an E4M3 h; an unknown dtype, gate or gate_act; a gate_act without a gate; a
+ * post norm or gate without a block; eps negative or not finite; alpha, beta
+ * or weight_offset not finite; reserved not 0.
+ */
+typedef enum { VQ_GATE_NONE = 0, VQ_GATE_CHANNEL = 1, VQ_GATE_TOKEN = 2, VQ_GATE_FULL = 3 } vq_gate;
+typedef enum { VQ_ACT_NONE = 0, VQ_ACT_SIGMOID = 1, VQ_ACT_TANH = 2 } vq_act;
+
+typedef struct vq_norm_spec {
+  int32_t cols;
+  int32_t block_dtype;     /* vq_dtype                                           */
+  int32_t residual_dtype;  /* vq_dtype                                           */
+  int32_t weight_dtype;    /* vq_dtype of the weights and the gate               */
+  int32_t h_dtype;         /* vq_dtype                                           */
+  int32_t gate;            /* vq_gate                                            */
+  int32_t gate_act;        /* vq_act                                             */
+  int32_t reserved;        /* must be 0                                          */
+  float alpha, beta, eps, weight_offset;
+  const void *post_weight; /* device [cols], or NULL                             */
+  const void *pre_weight;  /* device [cols], or NULL                             */
+  const void *gate_values; /* device, see gate                                   */
+} vq_norm_spec;
+
+vq_status vq_norm(const vq_norm_spec *n, const void *block, const void *residual, int32_t T, void *residual_out,
+                  void *h, float *h_scales, void *stream);
+
 /* Text for the last non-OK status returned on this thread ("" if none). */
 const char *vq_last_error(void);
 

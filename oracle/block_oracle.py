@@ -114,3 +114,29 @@ def fp8_product(xc, xs, wc, ws):
     """(y [T][R], the sums of the magnitudes [T][R]) in float64."""
     x, w = fp8_values(xc, xs), fp8_values(wc, ws, BLOCK)
     return x @ w.T, np.abs(x) @ np.abs(w).T
+
+
+# ---------------------------------------------------------------------------
+# norms around a block
+# ---------------------------------------------------------------------------
+
+def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=None, gate_act=None, alpha=1.0,
+         beta=1.0, weight_offset=0.0, eps=1e-6):
+    """vq_norm in float64: dict of u (the scaled, gated block term), r (the
+    residual term), v, rms (1 / rsqrt of v's mean square) and h."""
+    f = lambda t: np.asarray(t, dtype=np.float64)  # noqa: E731
+    u = r = 0.0
+    if block is not None:
+        u = f(block)
+        if post_weight is not None:
+            u = u / np.sqrt((u * u).mean(axis=1, keepdims=True) + eps) * (f(post_weight) + weight_offset)
+        if gate is not None:
+            g = f(gate)
+            u = u * (1 / (1 + np.exp(-g)) if gate_act == "sigmoid" else np.tanh(g) if gate_act == "tanh" else g)
+        u = alpha * u
+    if residual is not None:
+        r = beta * f(residual)
+    v = u + r
+    rms = np.sqrt((v * v).mean(axis=1, keepdims=True) + eps)
+    w = 1.0 if pre_weight is None else f(pre_weight) + weight_offset
+    return {"u": u * np.ones_like(v), "r": r * np.ones_like(v), "v": v, "rms": rms, "w": w, "h": v / rms * w}

@@ -195,3 +195,52 @@ def test_e4m3_oracle_matches_the_type(b):
     v = np.concatenate([v, O.E4M3[:127], (O.E4M3[1:127] + O.E4M3[:126]) / 2, v * 2.0 ** -12]).astype(np.float32)
     want = torch.from_numpy(np.clip(v, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     assert np.array_equal(O.e4m3_nearest(v), want)
+
+
+# ---- norms ----------------------------------------------------------------
+
+def _norm(b, T=4, block=0x10000, residual=0x20000, v=0x30000, h=0x40000, hs=0x50000, **kw):
+    base = dict(cols=256, block_dtype=0, residual_dtype=2, weight_dtype=2, h_dtype=2, gate=0, gate_act=0, reserved=0,
+                alpha=1.0, beta=1.0, eps=1e-6, weight_offset=0.0, post_weight=0x60000, pre_weight=0x70000,
+                gate_values=0x80000)
+    base.update(kw)
+    n = b.CNormSpec(**base)
+    return _status(b, b.LIB.vq_norm(ctypes.byref(n), block, residual, T, v, h, hs, None))
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(cols=0), "VQ_ERR_SHAPE"), (dict(cols=32769), "VQ_ERR_SHAPE"),
+    (dict(block_dtype=3), "VQ_ERR_SHAPE"), (dict(residual_dtype=3), "VQ_ERR_SHAPE"),
+    (dict(weight_dtype=-1), "VQ_ERR_SHAPE"), (dict(h_dtype=4), "VQ_ERR_SHAPE"),
+    (dict(h_dtype=3, cols=248), "VQ_ERR_SHAPE"),
+    (dict(gate=4), "VQ_ERR_SHAPE"), (dict(gate=1, gate_act=3), "VQ_ERR_SHAPE"), (dict(gate_act=1), "VQ_ERR_SHAPE"),
+    (dict(eps=-1.0), "VQ_ERR_SHAPE"), (dict(eps=float("nan")), "VQ_ERR_SHAPE"),
+    (dict(alpha=float("inf")), "VQ_ERR_SHAPE"), (dict(beta=float("nan")), "VQ_ERR_SHAPE"),
+    (dict(weight_offset=float("inf")), "VQ_ERR_SHAPE"), (dict(reserved=1), "VQ_ERR_SHAPE"),
+    (dict(T=-1), "VQ_ERR_SHAPE"), (dict(T=(1 << 30) + 1), "VQ_ERR_SHAPE"),
+    (dict(block=0), "VQ_ERR_SHAPE"),                            # a post norm without a block
+    (dict(block=0, post_weight=0, gate=1), "VQ_ERR_SHAPE"),
+    (dict(block=0, residual=0, post_weight=0), "VQ_ERR_NULL"),
+    (dict(v=0, h=0), "VQ_ERR_NULL"),
+    (dict(gate=2, gate_values=0), "VQ_ERR_NULL"),
+    (dict(h_dtype=3, hs=0), "VQ_ERR_NULL"),
+    (dict(block=0x10008), "VQ_ERR_ALIGN"), (dict(residual=0x20008), "VQ_ERR_ALIGN"),
+    (dict(v=0x30004), "VQ_ERR_ALIGN"), (dict(h=0x40002), "VQ_ERR_ALIGN"),
+    (dict(post_weight=0x60008), "VQ_ERR_ALIGN"), (dict(pre_weight=0x70002), "VQ_ERR_ALIGN"),
+    (dict(gate=1, gate_values=0x80008), "VQ_ERR_ALIGN"), (dict(gate=2, gate_values=0x80001), "VQ_ERR_ALIGN"),
+    (dict(hs=0x50002), "VQ_ERR_ALIGN"),
+    (dict(T=0, block=0, residual=0, v=0, h=0), "VQ_OK"),
+])
+def test_norm_refuses(b, kw, status):
+    assert _norm(b, **kw) == status, b.LIB.vq_last_error()
+
+
+def test_norm_wrapper_refuses_before_the_library(b):
+    import torch
+    x = torch.zeros(3, 32)
+    with pytest.raises(ValueError, match="needs a block or a residual"):
+        b.norm()
+    with pytest.raises(ValueError, match="GPU"):
+        b.norm(x)
+    with pytest.raises(ValueError, match="nothing to compute"):
+        b.norm(x, store_residual=False)

@@ -8,7 +8,7 @@ the first use of a binding name does, and fails loudly if it is not built.
 
 _BINDING_NAMES = {"VQTensor", "VQError", "dequant", "gemv", "gemm", "moe_gemv", "moe_gemm",
                   "words_per_row", "workspace_bytes", "Router", "moe_route",
-                  "FP8Tensor", "fp8_quant", "fp8_gemm"}
+                  "FP8Tensor", "fp8_quant", "fp8_gemm", "norm"}
 
 __all__ = sorted(_BINDING_NAMES | {"synth", "binding"})
 

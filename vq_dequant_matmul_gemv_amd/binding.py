@@ -72,6 +72,27 @@ class CFP8Tensor(ctypes.Structure):
     ]
 
 
+class CNormSpec(ctypes.Structure):
+    """Mirror of `vq_norm_spec`."""
+    _fields_ = [
+        ("cols", ctypes.c_int32),
+        ("block_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("h_dtype", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("gate_act", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("alpha", ctypes.c_float),
+        ("beta", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("post_weight", ctypes.c_void_p),
+        ("pre_weight", ctypes.c_void_p),
+        ("gate_values", ctypes.c_void_p),
+    ]
+
+
 class CTensor(ctypes.Structure):
     """Mirror of `vq_tensor`."""
     _fields_ = [
@@ -118,6 +139,7 @@ def _load():
         "vq_fp8_quant": (i32, [P, i32, i32, i32, P, P, P]),
         "vq_fp8_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
         "vq_fp8_gemm": (i32, [ctypes.POINTER(CFP8Tensor), IO, P, P, i32, P, P, ctypes.c_size_t, P]),
+        "vq_norm": (i32, [ctypes.POINTER(CNormSpec), P, P, i32, P, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
     }
@@ -133,7 +155,8 @@ LIB = _load()
 EXPORTED = ("vq_words_per_row", "vq_dequant", "vq_gemv", "vq_gemm", "vq_moe_gemv", "vq_gemv_ex",
             "vq_gemm_ex", "vq_moe_gemv_ex", "vq_moe_gemm_ex",
             "vq_moe_workspace_bytes", "vq_moe_gemm", "vq_moe_gemm_no_alloc", "vq_encode_workspace_bytes",
-            "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm", "vq_last_error", "vq_status_name")
+            "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm", "vq_norm",
+            "vq_last_error", "vq_status_name")
 
 
 def check(status: int) -> None:
@@ -591,3 +614,87 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
 
     return _on_device(dev, stream, call, y if y is not None else (yshape, y_dtype),
                       workspace if workspace is not None or need == 0 else ((need,), torch.uint8))[0]
+
+
+# --------------------------------------------------------------------------
+# norms before and after a block
+# --------------------------------------------------------------------------
+
+VQ_GATE_NONE, VQ_GATE_CHANNEL, VQ_GATE_TOKEN, VQ_GATE_FULL = range(4)
+VQ_ACT_NONE, VQ_ACT_SIGMOID, VQ_ACT_TANH = range(3)
+GATE_ACTS = {None: VQ_ACT_NONE, "none": VQ_ACT_NONE, "sigmoid": VQ_ACT_SIGMOID, "tanh": VQ_ACT_TANH}
+
+
+def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=None, gate_act=None, alpha=1.0,
+         beta=1.0, weight_offset=0.0, eps=1e-6, h_dtype=None, residual_out=None, h=None, h_scales=None,
+         store_residual=True, stream=None):
+    """The norms around a block with its gate and the residual sum (vq_norm):
+    u = norm(block) * post_weight (block itself without one), v = beta *
+    residual + alpha * act(gate) * u, h = norm(v) * pre_weight.  Returns (v,
+    h, h_scales).
+
+    block, residual  [T][cols], fp32, fp16 or bf16, either may be None
+    gate             [cols], [T][1] or [T][cols]; gate_act None, "sigmoid" or "tanh"
+    weights, gate    of one dtype
+    h_dtype          dtype of h (float8_e4m3fn: with h_scales [T][ceil(cols/128)]);
+                     None: no h unless pre_weight or h is given (then their dtype)
+    residual_out     may be `residual`; v has residual's dtype (block's without one)
+    """
+    torch = _torch()
+    first = block if block is not None else residual
+    if first is None:
+        raise ValueError("norm needs a block or a residual")
+    if first.dim() != 2:
+        raise ValueError("block and residual must be [T][cols]")
+    T, cols = first.shape
+    dev = first.device
+    v_dtype = (residual if residual is not None else block).dtype
+    if h_dtype is None:
+        h_dtype = h.dtype if h is not None else pre_weight.dtype if pre_weight is not None else None
+    e4m3 = h_dtype == torch.float8_e4m3fn
+    if h_dtype is None and not store_residual:
+        raise ValueError("norm has nothing to compute: neither v nor h is wanted")
+    given = [t for t in (block, residual, post_weight, pre_weight, gate) if t is not None]
+    _dev_check(*given, device=dev)
+    for t in (block, residual):
+        if t is not None and tuple(t.shape) != (T, cols):
+            raise ValueError("block and residual must have the same shape [T][cols]")
+    w_dtype = None
+    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (gate, "gate")):
+        if t is None:
+            continue
+        if name != "gate" and tuple(t.shape) != (cols,):
+            raise ValueError(f"{name} must be [{cols}]")
+        if w_dtype is not None and t.dtype != w_dtype:
+            raise ValueError("post_weight, pre_weight and gate must have one dtype")
+        w_dtype = t.dtype
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act must be None or one of {sorted(k for k in GATE_ACTS if k)}")
+    kind = VQ_GATE_NONE
+    if gate is not None:
+        kinds = {(cols,): VQ_GATE_CHANNEL, (T, 1): VQ_GATE_TOKEN, (T, cols): VQ_GATE_FULL}
+        if tuple(gate.shape) not in kinds:
+            raise ValueError(f"gate must be [{cols}], [{T}][1] or [{T}][{cols}]")
+        kind = kinds[tuple(gate.shape)]
+    sshape = (T, _blocks(cols))
+    for t, dt, shape, name in ((residual_out, v_dtype, (T, cols), "residual_out"), (h, h_dtype, (T, cols), "h"),
+                               (h_scales, torch.float32, sshape, "h_scales")):
+        if t is not None:
+            _check_out(t, dt, shape, name)
+            _dev_check(t, device=dev)
+    spec = CNormSpec(cols, _dtype_code((block if block is not None else first).dtype), _dtype_code(v_dtype),
+                     _dtype_code(w_dtype or torch.float32),
+                     VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind,
+                     GATE_ACTS[gate_act] if gate is not None else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset,
+                     *(None if t is None else t.data_ptr() for t in (post_weight, pre_weight, gate)))
+
+    def call(outs, st):
+        return LIB.vq_norm(ctypes.byref(spec), None if block is None else block.data_ptr(),
+                           None if residual is None else residual.data_ptr(), T,
+                           *(None if o is None else o.data_ptr() for o in outs), st)
+
+    return tuple(_on_device(
+        dev, stream, call,
+        residual_out if residual_out is not None else ((T, cols), v_dtype) if store_residual else None,
+        h if h is not None else ((T, cols), h_dtype) if h_dtype is not None else None,
+        h_scales if h_scales is not None else (sshape, torch.float32) if e4m3 else None))

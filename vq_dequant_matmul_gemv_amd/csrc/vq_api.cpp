@@ -543,4 +543,62 @@ vq_status vq_fp8_gemm(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x,
                     "vq_fp8_gemm launch");
 }
 
+vq_status vq_norm(const vq_norm_spec* n, const void* block, const void* residual, int32_t T, void* residual_out,
+                  void* h, float* h_scales, void* stream) {
+  if (!n) return fail(VQ_ERR_NULL, "vq_norm: descriptor is NULL");
+  auto plain = [](int32_t dt) { return dt == VQ_DTYPE_F32 || dt == VQ_DTYPE_F16 || dt == VQ_DTYPE_BF16; };
+  if (n->cols < 1 || n->cols > vqmi::kNormMaxCols)
+    return fail(VQ_ERR_SHAPE, "vq_norm: cols=%d outside [1, %d]", n->cols, vqmi::kNormMaxCols);
+  if (!plain(n->block_dtype) || !plain(n->residual_dtype) || !plain(n->weight_dtype))
+    return fail(VQ_ERR_SHAPE, "vq_norm: block_dtype=%d residual_dtype=%d weight_dtype=%d must be F32, F16 or BF16",
+                n->block_dtype, n->residual_dtype, n->weight_dtype);
+  const bool e4m3 = n->h_dtype == VQ_DTYPE_E4M3;
+  if (!e4m3 && !plain(n->h_dtype)) return fail(VQ_ERR_SHAPE, "vq_norm: h_dtype=%d is not a vq_dtype", n->h_dtype);
+  if (e4m3 && n->cols % 16 != 0)
+    return fail(VQ_ERR_SHAPE, "vq_norm: cols=%d must be a multiple of 16 for an E4M3 h", n->cols);
+  if (n->gate < VQ_GATE_NONE || n->gate > VQ_GATE_FULL)
+    return fail(VQ_ERR_SHAPE, "vq_norm: gate=%d is not a vq_gate", n->gate);
+  if (n->gate_act < VQ_ACT_NONE || n->gate_act > VQ_ACT_TANH)
+    return fail(VQ_ERR_SHAPE, "vq_norm: gate_act=%d is not a vq_act", n->gate_act);
+  if (n->gate == VQ_GATE_NONE && n->gate_act != VQ_ACT_NONE)
+    return fail(VQ_ERR_SHAPE, "vq_norm: gate_act without a gate");
+  if (!std::isfinite(n->eps) || n->eps < 0.0f) return fail(VQ_ERR_SHAPE, "vq_norm: eps must be finite and >= 0");
+  if (!std::isfinite(n->alpha) || !std::isfinite(n->beta) || !std::isfinite(n->weight_offset))
+    return fail(VQ_ERR_SHAPE, "vq_norm: alpha, beta and weight_offset must be finite");
+  if (n->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_norm: reserved must be 0");
+  if (T < 0 || T > (1 << 30)) return fail(VQ_ERR_SHAPE, "vq_norm: T=%d outside [0, 2^30]", T);
+  if (T == 0) return VQ_OK;
+  if (!block && !residual) return fail(VQ_ERR_NULL, "vq_norm: block and residual are both NULL");
+  if (!residual_out && !h) return fail(VQ_ERR_NULL, "vq_norm: residual_out and h are both NULL");
+  if (!block && (n->post_weight || n->gate != VQ_GATE_NONE))
+    return fail(VQ_ERR_SHAPE, "vq_norm: a post norm or a gate needs a block");
+  if (n->gate != VQ_GATE_NONE && !n->gate_values) return fail(VQ_ERR_NULL, "vq_norm: gate_values is NULL");
+  if (h && e4m3 && !h_scales) return fail(VQ_ERR_NULL, "vq_norm: an E4M3 h needs h_scales");
+  if (!aligned(block, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(h, 16))
+    return fail(VQ_ERR_ALIGN, "vq_norm: block, residual, residual_out and h need 16-byte alignment");
+  if (!aligned(n->post_weight, 16) || !aligned(n->pre_weight, 16))
+    return fail(VQ_ERR_ALIGN, "vq_norm: the weights need 16-byte alignment");
+  if (n->gate != VQ_GATE_NONE &&
+      !aligned(n->gate_values, n->gate != VQ_GATE_TOKEN ? 16 : n->weight_dtype == VQ_DTYPE_F32 ? 4 : 2))
+    return fail(VQ_ERR_ALIGN, "vq_norm: gate_values are not aligned (16 bytes; a gate per token: to its element)");
+  if (!aligned(h_scales, 4)) return fail(VQ_ERR_ALIGN, "vq_norm: h_scales is not 4-byte aligned");
+  vqmi::NormSpec s{};
+  s.cols = n->cols;
+  s.block_kind = dtype_kind(n->block_dtype);
+  s.res_kind = dtype_kind(n->residual_dtype);
+  s.w_kind = dtype_kind(n->weight_dtype);
+  s.h_kind = e4m3 ? vqmi::kNormE4m3 : dtype_kind(n->h_dtype);
+  s.gate_kind = n->gate;  // vq_gate and vq_act in the order of the launch enums
+  s.gate_act = n->gate_act;
+  s.alpha = n->alpha;
+  s.beta = n->beta;
+  s.eps = n->eps;
+  s.offset = n->weight_offset;
+  s.post_w = n->post_weight;
+  s.pre_w = n->pre_weight;
+  s.gate = n->gate_values;
+  return hip_status(vqmi::launch_norm(s, block, residual, T, residual_out, h, h_scales, (hipStream_t)stream),
+                    "vq_norm launch");
+}
+
 }  // extern "C"

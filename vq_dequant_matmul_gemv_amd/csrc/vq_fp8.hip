@@ -68,11 +68,7 @@ struct Fp8Args {
 __device__ __forceinline__ void store_as(void* y, int64_t i, float v, int kind) {
   if (kind == kOutF32) static_cast<float*>(y)[i] = v;
   else if (kind == kOutF16) static_cast<_Float16*>(y)[i] = (_Float16)v;
-  else {
-    const uint32_t u = __float_as_uint(v);
-    const bool nan = (u & 0x7fffffffu) > 0x7f800000u;
-    static_cast<uint16_t*>(y)[i] = nan ? (uint16_t)((u >> 16) | 0x40u) : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-  }
+  else static_cast<uint16_t*>(y)[i] = bf16_bits(v);
 }
 
 // Four consecutive rows of one token (row: the first, a multiple of 4).
