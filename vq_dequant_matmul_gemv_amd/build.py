@@ -38,6 +38,13 @@ COMMON = [
     "-fno-gpu-rdc", "-I", INCLUDE, "-I", CSRC,
 ]
 
+# Per-source flags.  vq_fp8.hip scales every matrix product's sum into its
+# accumulators with VALU instructions, which read VGPRs only: the products'
+# destinations must not be AGPRs.
+EXTRA = {
+    "vq_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+}
+
 
 def _hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
@@ -48,7 +55,7 @@ def _hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-    cmd = [_hipcc(), *COMMON, "-c", src, "-o", obj]
+    cmd = [_hipcc(), *COMMON, *EXTRA.get(os.path.basename(src), []), "-c", src, "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "hip"]
     res = subprocess.run(cmd, capture_output=True, text=True)

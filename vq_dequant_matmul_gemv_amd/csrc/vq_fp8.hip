@@ -65,10 +65,67 @@ struct Fp8Args {
   int y_kind, swiglu;
 };
 
-__device__ __forceinline__ void store_as(void* y, int64_t i, float v, int kind) {
-  if (kind == kOutF32) static_cast<float*>(y)[i] = v;
-  else if (kind == kOutF16) static_cast<_Float16*>(y)[i] = (_Float16)v;
-  else static_cast<uint16_t*>(y)[i] = bf16_bits(v);
+// One wave's LDS writes before its later reads of other lanes' values (LDS
+// runs a wave's accesses in order: only the compiler is held back).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// N consecutive outputs of one token, the first at y[i]; `whole`: i is a
+// multiple of N and all N exist.
+template <int N>
+__device__ __forceinline__ void store_run(void* y, int64_t i, const float* v, int kind, bool whole, int n) {
+  if (!whole) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (k < n) store_out(y, i + k, v[k], kind);
+    }
+    return;
+  }
+  if (kind == kOutF32) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+      *reinterpret_cast<float4_t*>(static_cast<float*>(y) + i + k) = float4_t{v[k], v[k + 1], v[k + 2], v[k + 3]};
+    return;
+  }
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int k = 0; k < N / 2; ++k) {
+    w[k] = kind == kOutF16 ? __builtin_bit_cast(uint32_t, half2_t{(_Float16)v[2 * k], (_Float16)v[2 * k + 1]})
+                           : (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16;
+  }
+  uint16_t* p = static_cast<uint16_t*>(y) + i;
+  if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+  else *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+}
+
+// Stores 16 tokens from t0 on of ROWS rows from r0 on (a multiple of 16) that
+// lie in LDS, `pitch` floats a token; 8 rows a lane, with whole pieces of y
+// where its rows allow them.
+template <int ROWS>
+__device__ __forceinline__ void store_tokens(const Fp8Args& a, const float* lds, int pitch, int t0, int r0, int lane) {
+  constexpr int kLanes = ROWS / 8, kPer = 64 / kLanes;  // lanes a token, tokens at once
+  const int row = r0 + lane % kLanes * 8, n = a.rows - row;
+  if (n <= 0) return;
+#pragma unroll 1
+  for (int k = lane / kLanes; k < 16; k += kPer) {
+    const int t = t0 + k;
+    if (t >= a.T) break;
+    const float4_t lo = *reinterpret_cast<const float4_t*>(lds + k * pitch + row - r0);
+    const float4_t hi = *reinterpret_cast<const float4_t*>(lds + k * pitch + row - r0 + 4);
+    if (a.swiglu) {
+      const float v[4] = {silu_mul(lo[0], lo[1]), silu_mul(lo[2], lo[3]), silu_mul(hi[0], hi[1]),
+                          silu_mul(hi[2], hi[3])};
+      store_run<4>(a.y, (int64_t)t * (a.rows / 2) + row / 2, v, a.y_kind, a.rows % 8 == 0, n / 2);
+    } else {
+      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      store_run<8>(a.y, (int64_t)t * a.rows + row, v, a.y_kind, a.rows % 8 == 0, n);
+    }
+  }
 }
 
 // Four consecutive rows of one token (row: the first, a multiple of 4).
@@ -77,13 +134,12 @@ __device__ __forceinline__ void store_rows4(const Fp8Args& a, int t, int row, co
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if (row + 2 * p < a.rows)
-        store_as(a.y, (int64_t)t * (a.rows / 2) + row / 2 + p, v[2 * p] / (1.0f + expf(-v[2 * p])) * v[2 * p + 1],
-                 a.y_kind);
+        store_out(a.y, (int64_t)t * (a.rows / 2) + row / 2 + p, silu_mul(v[2 * p], v[2 * p + 1]), a.y_kind);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (row + i < a.rows) store_as(a.y, (int64_t)t * a.rows + row + i, v[i], a.y_kind);
+      if (row + i < a.rows) store_out(a.y, (int64_t)t * a.rows + row + i, v[i], a.y_kind);
     }
   }
 }
@@ -155,6 +211,217 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args a) {
   if (t < a.T) store_rows4(a, t, r0 + (lane >> 4) * 4, v);
 }
 
+
+// ---------------------------------------------------------------------------
+// product, many tokens: four waves of 16*MT rows x 16*NT tokens a block
+// ---------------------------------------------------------------------------
+typedef int int8v __attribute__((ext_vector_type(8)));
+
+// One operand of the 16 x 16 x 128 products: e4m3 as it is, or as halves.
+template <bool EXACT>
+struct Op {
+  int8v v;
+  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    v = int8v{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  }
+};
+template <>
+struct Op<true> {
+  half8_t v[4];
+  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    v[0] = to_half8(lo.x, lo.y);
+    v[1] = to_half8(lo.z, lo.w);
+    v[2] = to_half8(hi.x, hi.y);
+    v[3] = to_half8(hi.z, hi.w);
+  }
+};
+template <bool EXACT>
+__device__ __forceinline__ float4_t dot128(const Op<EXACT>& a, const Op<EXACT>& b) {
+  float4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], p, 0, 0, 0);
+  } else {
+    p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, p, 0, 0, 0, 0, 0, 0);
+  }
+  return p;
+}
+
+template <bool EXACT, int MT, int NT>
+__global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
+  constexpr int kTileRows = 32 * MT, kTileTokens = 32 * NT;
+  static_assert(kTileTokens <= 256 && NT % 2 == 0, "scales of at most 256 tokens; the token operands alternate");
+  __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
+  __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
+  __shared__ __align__(1024) float lds_s[2][256][4];  // x scales of four steps, twice
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t cols = a.cols, kb = a.kb;
+
+  // XCD-aware order: blocks land on XCD (block % 8); each XCD takes a
+  // contiguous range of tiles, which run through up to 8 token tiles of one
+  // row tile before the next.
+  const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
+  int rt, tt;
+  {
+    const int n = row_tiles * tok_tiles, q = n / 8, r8 = n % 8, xcd = blockIdx.x % 8, j = blockIdx.x / 8;
+    const int tile = xcd * q + min(xcd, r8) + j;
+    const int g = tile / (8 * row_tiles), rem = tile - g * 8 * row_tiles, width = min(8, tok_tiles - 8 * g);
+    rt = rem / width;
+    tt = 8 * g + rem % width;
+  }
+  const int r0 = rt * kTileRows, t0 = tt * kTileTokens;
+  const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * cols, (uint64_t)min(kTileRows, a.rows - r0) * cols);
+  const rsrc_t xr = make_rsrc(a.x + (int64_t)t0 * cols, (uint64_t)min(kTileTokens, a.T - t0) * cols);
+  const rsrc_t sr = make_rsrc(a.xs + (int64_t)t0 * kb, (uint64_t)min(kTileTokens, a.T - t0) * kb * 4);
+  const int wm = (wave >> 1) * 16 * MT, wn = (wave & 1) * 16 * NT;  // the wave's rows and tokens
+  // rows past the end multiply zeros: any block of scales will do
+  const float* ws = a.ws + (int64_t)min((r0 + wm) / kFp8Block, (a.rows - 1) / kFp8Block) * kb;
+
+  // A wave loads 8 rows of 128 bytes at a time, 16 bytes a lane, through
+  // registers into LDS.  The 16-byte pieces of row r lie in the order piece ^
+  // (r % 8), so the fragment reads of 8 rows touch all banks.  Columns, rows
+  // and steps past the end arrive as zeros.
+  const uint32_t ld_piece = (lane & 7) * 16, ld_row = wave * 8 + (lane >> 3);
+  const uint32_t ld_dst = ld_row * 128 + (ld_piece ^ ((lane >> 3) * 16));
+  u32x4 stage[MT + NT];
+  float stage_s;
+  auto stage_off = [&](uint32_t s) {
+    const uint32_t c = s * kFp8Block + ld_piece;
+    return c < cols ? ld_row * cols + c : kOutOfRange;
+  };
+  auto load_piece = [&](uint32_t off, int i) {
+    stage[i] = i < MT ? buf_load_b128(wr, off + i * 32 * cols) : buf_load_b128(xr, off + (i - MT) * 32 * cols);
+  };
+  auto write_piece = [&](uint32_t s, int i) {
+    uint8_t* to = i < MT ? lds_w[s & 1] + i * 4096 : lds_x[s & 1] + (i - MT) * 4096;
+    *reinterpret_cast<u32x4*>(to + ld_dst) = stage[i];
+  };
+  // Scales of the four steps from v & ~3 on, for the quarter v % 4 of the
+  // tokens (four lanes a token).
+  auto load_scales = [&](uint32_t v) {
+    const uint32_t tok = (v & 3) * 64 + wave * 16 + (lane >> 2), k = (v & ~3u) + (lane & 3);
+    stage_s = __uint_as_float(buf_load_b32(sr, k < kb && tok < kTileTokens ? (tok * kb + k) * 4 : kOutOfRange));
+  };
+  auto write_scales = [&](uint32_t v) {
+    lds_s[(v >> 2) & 1][(v & 3) * 64 + wave * 16 + (lane >> 2)][lane & 3] = stage_s;
+  };
+  const int r = lane & 15, g = lane >> 4;
+  const uint32_t f_lo = r * 128 + ((g ^ (r & 7)) * 16), f_hi = r * 128 + (((g + 4) ^ (r & 7)) * 16);
+  auto read_op = [&](Op<EXACT>& o, const uint8_t* base) {
+    o.set(*reinterpret_cast<const u32x4*>(base + f_lo), *reinterpret_cast<const u32x4*>(base + f_hi));
+  };
+
+  float4_t acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // Steps 0 and 1 with the scales of their group (and a quarter of the next)
+  // in LDS, step 2 in registers.
+#pragma unroll
+  for (uint32_t v = 0; v < 5; ++v) {
+    load_scales(v);
+    write_scales(v);
+  }
+#pragma unroll
+  for (uint32_t s = 0; s < 3; ++s) {
+    const uint32_t off = stage_off(s);
+#pragma unroll
+    for (int i = 0; i < MT + NT; ++i) load_piece(off, i);
+    if (s < 2) {
+#pragma unroll
+      for (int i = 0; i < MT + NT; ++i) write_piece(s, i);
+    }
+  }
+  load_scales(5);
+  lds_barrier();
+  Op<EXACT> av[MT], bv[2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) read_op(av[m], lds_w[0] + (wm + 16 * m) * 128);
+  read_op(bv[0], lds_x[0] + wn * 128);
+  float f[NT], f_last = 0.0f;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) f[n] = ws[0] * lds_s[0][wn + 16 * n + r][0];
+
+  // The sums of two products stay in flight while the ones before them are
+  // scaled into the accumulators, across steps too.
+  constexpr int kLag = 2;
+  float4_t p[kLag];
+#pragma unroll
+  for (int i = 0; i < kLag; ++i) p[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t s = 0; s < kb; ++s) {
+    const uint8_t* xb = lds_x[s & 1] + wn * 128;
+    const uint8_t* xnext = lds_x[(s + 1) & 1] + wn * 128;
+    const uint8_t* wnext = lds_w[(s + 1) & 1] + wm * 128;
+    const float sw_next = ws[min(s + 1, kb - 1)];
+    const uint32_t off = stage_off(s + 3);
+    float f_next[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n < NT - 1) {
+        read_op(bv[(n + 1) & 1], xb + (n + 1) * 16 * 128);
+      } else {
+        // every wave holds its operands of this step, so its buffers can take
+        // the step after next, and the next step's data has arrived
+        lds_barrier();
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int i = n * MT + m;
+        const float4_t now = dot128<EXACT>(av[m], bv[n & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n == NT - 1) {
+          read_op(av[m], wnext + m * 16 * 128);
+#pragma unroll
+          for (int k = m; k < MT + NT; k += MT) {
+            write_piece(s, k);
+            load_piece(off, k);
+          }
+#pragma unroll
+          for (int k = m; k < NT; k += MT) f_next[k] = lds_s[((s + 1) >> 2) & 1][wn + 16 * k + r][(s + 1) & 3];
+          if (m == MT - 1) {
+            read_op(bv[0], xnext);
+            write_scales(s + 5);
+            load_scales(s + 6);
+          }
+        }
+        {
+          const int j = i - kLag, jn = j >= 0 ? j / MT : NT - 1, jm = j >= 0 ? j % MT : MT + j;
+          const float fj = j >= 0 ? f[jn] : f_last;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[jm][jn][c] = fmaf(fj, p[i % kLag][c], acc[jm][jn][c]);
+        }
+        p[i % kLag] = now;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    f_last = f[NT - 1];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) f[n] = sw_next * f_next[n];
+  }
+#pragma unroll
+  for (int i = 0; i < kLag; ++i) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      acc[MT - kLag + i][NT - 1][c] = fmaf(f_last, p[i][c], acc[MT - kLag + i][NT - 1][c]);
+  }
+  // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
+  // token's rows leave in whole pieces.
+  lds_barrier();
+  constexpr int kPitch = 16 * MT + 4;  // fp32 a token
+  static_assert(4 * 16 * kPitch * 4 <= (int)sizeof(lds_w), "a wave's 16 tokens fit");
+  float* out = reinterpret_cast<float*>(&lds_w[0][0]) + wave * 16 * kPitch;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) *reinterpret_cast<float4_t*>(out + r * kPitch + 16 * m + 4 * g) = acc[m][n];
+    wave_lds_fence();
+    store_tokens<16 * MT>(a, out, kPitch, t0 + wn + 16 * n, r0 + wm, lane);
+    wave_lds_fence();
+  }
+}
+
 }  // namespace
 
 hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t* q, float* scales, hipStream_t s) {
@@ -186,6 +453,13 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x,
   a.T = T;
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
+  if (T > 64) {
+    const int tr = io.y_kind == kOutF32 ? 128 : 256, tk = 192;
+    const dim3 grid((unsigned)((w.rows + tr - 1) / tr) * ((T + tk - 1) / tk));
+    if (io.y_kind == kOutF32) hipLaunchKernelGGL((vq_fp8_tile_kernel<true, 4, 6>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((vq_fp8_tile_kernel<false, 8, 6>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)((w.rows + 15) / 16) * ((T + 15) / 16));
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<8>), grid, dim3(512), 0, s, a);
   return hipGetLastError();

@@ -10,13 +10,6 @@ constexpr int kFp8Block = 128;       // columns (and weight rows) that share a s
 constexpr float kFp8Max = 448.0f;    // largest e4m3 value
 constexpr uint32_t kFp8Nan = 0x7fu;
 
-// fp32 rounded to nearest even as bf16 bits (NaN stays NaN).
-__device__ __forceinline__ uint16_t bf16_bits(float v) {
-  const uint32_t u = __float_as_uint(v);
-  const bool nan = (u & 0x7fffffffu) > 0x7f800000u;
-  return (uint16_t)(nan ? (u >> 16) | 0x40u : (u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
-
 // Maximum over the 16 lanes of a DPP row, in every lane of it (rotations by
 // 1, 2, 4 and 8).
 __device__ __forceinline__ float row16_max(float v) {

@@ -77,12 +77,6 @@ __device__ __forceinline__ float load1(const void* p, int64_t i, int kind) {
   return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
 }
 
-__device__ __forceinline__ void store1(void* p, int64_t i, float v, int kind) {
-  if (kind == kOutF32) static_cast<float*>(p)[i] = v;
-  else if (kind == kOutF16) static_cast<_Float16*>(p)[i] = (_Float16)v;
-  else static_cast<uint16_t*>(p)[i] = bf16_bits(v);
-}
-
 __device__ __forceinline__ void store8(void* p, int64_t i, const float* x, int kind) {
   if (kind == kOutF32) {
     u32x4* q = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
@@ -94,7 +88,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float* x, int k
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (kind == kOutF16) w[k] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)x[2 * k], (_Float16)x[2 * k + 1]});
-    else w[k] = (uint32_t)bf16_bits(x[2 * k]) | (uint32_t)bf16_bits(x[2 * k + 1]) << 16;
+    else w[k] = (uint32_t)f32_to_bf16_bits(x[2 * k]) | (uint32_t)f32_to_bf16_bits(x[2 * k + 1]) << 16;
   }
   *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = u32x4{w[0], w[1], w[2], w[3]};
 }
@@ -131,7 +125,7 @@ struct RowMap {
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (in(ch, j)) store1(p, at + col(ch, j), x[j], kind);
+        if (in(ch, j)) store_out(p, at + col(ch, j), x[j], kind);
       }
     }
   }
