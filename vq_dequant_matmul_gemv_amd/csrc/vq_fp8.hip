@@ -7,6 +7,7 @@
 #include "vq_kernels.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace vqmi {
 
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args a) {
 
 
 // ---------------------------------------------------------------------------
-// product, many tokens: four waves of 16*MT rows x 16*NT tokens a block
+// product, many tokens: WM x WN waves of 16*MT rows x 16*NT tokens a block
 // ---------------------------------------------------------------------------
 typedef int int8v __attribute__((ext_vector_type(8)));
 
@@ -247,9 +248,13 @@ __device__ __forceinline__ float4_t dot128(const Op<EXACT>& a, const Op<EXACT>& 
   return p;
 }
 
-template <bool EXACT, int MT, int NT>
-__global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
-  constexpr int kTileRows = 32 * MT, kTileTokens = 32 * NT;
+template <bool EXACT, int WM, int WN, int MT, int NT>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(Fp8Args a) {
+  constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
+  constexpr int kLoadRows = 8 * kWaves;  // rows the block loads at once
+  constexpr int kWLoads = kTileRows / kLoadRows, kXLoads = kTileTokens / kLoadRows, kLoads = kWLoads + kXLoads;
+  static_assert(kTileRows % kLoadRows == 0 && kTileTokens % kLoadRows == 0, "whole loads");
+  static_assert(128 % (16 * MT) == 0, "a wave's rows share their scales");
   static_assert(kTileTokens <= 256 && NT % 2 == 0, "scales of at most 256 tokens; the token operands alternate");
   __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
   __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
   const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * cols, (uint64_t)min(kTileRows, a.rows - r0) * cols);
   const rsrc_t xr = make_rsrc(a.x + (int64_t)t0 * cols, (uint64_t)min(kTileTokens, a.T - t0) * cols);
   const rsrc_t sr = make_rsrc(a.xs + (int64_t)t0 * kb, (uint64_t)min(kTileTokens, a.T - t0) * kb * 4);
-  const int wm = (wave >> 1) * 16 * MT, wn = (wave & 1) * 16 * NT;  // the wave's rows and tokens
+  const int wm = wave / WN * 16 * MT, wn = wave % WN * 16 * NT;  // the wave's rows and tokens
   // rows past the end multiply zeros: any block of scales will do
   const float* ws = a.ws + (int64_t)min((r0 + wm) / kFp8Block, (a.rows - 1) / kFp8Block) * kb;
 
@@ -283,28 +288,28 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
   // and steps past the end arrive as zeros.
   const uint32_t ld_piece = (lane & 7) * 16, ld_row = wave * 8 + (lane >> 3);
   const uint32_t ld_dst = ld_row * 128 + (ld_piece ^ ((lane >> 3) * 16));
-  u32x4 stage[MT + NT];
+  u32x4 stage[kLoads];
   float stage_s;
   auto stage_off = [&](uint32_t s) {
     const uint32_t c = s * kFp8Block + ld_piece;
     return c < cols ? ld_row * cols + c : kOutOfRange;
   };
   auto load_piece = [&](uint32_t off, int i) {
-    stage[i] = i < MT ? buf_load_b128(wr, off + i * 32 * cols) : buf_load_b128(xr, off + (i - MT) * 32 * cols);
+    stage[i] = i < kWLoads ? buf_load_b128(wr, off + i * kLoadRows * cols)
+                           : buf_load_b128(xr, off + (i - kWLoads) * kLoadRows * cols);
   };
   auto write_piece = [&](uint32_t s, int i) {
-    uint8_t* to = i < MT ? lds_w[s & 1] + i * 4096 : lds_x[s & 1] + (i - MT) * 4096;
+    uint8_t* to = i < kWLoads ? lds_w[s & 1] + i * kLoadRows * 128 : lds_x[s & 1] + (i - kWLoads) * kLoadRows * 128;
     *reinterpret_cast<u32x4*>(to + ld_dst) = stage[i];
   };
   // Scales of the four steps from v & ~3 on, for the quarter v % 4 of the
-  // tokens (four lanes a token).
+  // tokens (four lanes a token; every four waves load the same).
+  const uint32_t sc_tok = (wave & 3) * 16 + (lane >> 2);
   auto load_scales = [&](uint32_t v) {
-    const uint32_t tok = (v & 3) * 64 + wave * 16 + (lane >> 2), k = (v & ~3u) + (lane & 3);
+    const uint32_t tok = (v & 3) * 64 + sc_tok, k = (v & ~3u) + (lane & 3);
     stage_s = __uint_as_float(buf_load_b32(sr, k < kb && tok < kTileTokens ? (tok * kb + k) * 4 : kOutOfRange));
   };
-  auto write_scales = [&](uint32_t v) {
-    lds_s[(v >> 2) & 1][(v & 3) * 64 + wave * 16 + (lane >> 2)][lane & 3] = stage_s;
-  };
+  auto write_scales = [&](uint32_t v) { lds_s[(v >> 2) & 1][(v & 3) * 64 + sc_tok][lane & 3] = stage_s; };
   const int r = lane & 15, g = lane >> 4;
   const uint32_t f_lo = r * 128 + ((g ^ (r & 7)) * 16), f_hi = r * 128 + (((g + 4) ^ (r & 7)) * 16);
   auto read_op = [&](Op<EXACT>& o, const uint8_t* base) {
@@ -317,21 +322,21 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // Steps 0 and 1 with the scales of their group (and a quarter of the next)
-  // in LDS, step 2 in registers.
+  // Step 0 with the scales of its group (and a quarter of the next) in LDS,
+  // step 1 in registers.
 #pragma unroll
   for (uint32_t v = 0; v < 5; ++v) {
     load_scales(v);
     write_scales(v);
   }
 #pragma unroll
-  for (uint32_t s = 0; s < 3; ++s) {
+  for (uint32_t s = 0; s < 2; ++s) {
     const uint32_t off = stage_off(s);
 #pragma unroll
-    for (int i = 0; i < MT + NT; ++i) load_piece(off, i);
-    if (s < 2) {
+    for (int i = 0; i < kLoads; ++i) load_piece(off, i);
+    if (s < 1) {
 #pragma unroll
-      for (int i = 0; i < MT + NT; ++i) write_piece(s, i);
+      for (int i = 0; i < kLoads; ++i) write_piece(s, i);
     }
   }
   load_scales(5);
@@ -355,15 +360,15 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
     const uint8_t* xnext = lds_x[(s + 1) & 1] + wn * 128;
     const uint8_t* wnext = lds_w[(s + 1) & 1] + wm * 128;
     const float sw_next = ws[min(s + 1, kb - 1)];
-    const uint32_t off = stage_off(s + 3);
+    const uint32_t off = stage_off(s + 2);
     float f_next[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n < NT - 1) {
         read_op(bv[(n + 1) & 1], xb + (n + 1) * 16 * 128);
       } else {
-        // every wave holds its operands of this step, so its buffers can take
-        // the step after next, and the next step's data has arrived
+        // every wave holds its operands of this step, so the next one's pieces
+        // in LDS are complete and this one's buffers free
         lds_barrier();
       }
 #pragma unroll
@@ -371,13 +376,18 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
         const int i = n * MT + m;
         const float4_t now = dot128<EXACT>(av[m], bv[n & 1]);
         __builtin_amdgcn_sched_barrier(0);
-        if (n == NT - 1) {
-          read_op(av[m], wnext + m * 16 * 128);
+        // the next step's pieces go to LDS, spread over the step, and the ones
+        // after them are loaded in their place
+        constexpr int kSlots = (NT - 1) * MT;
 #pragma unroll
-          for (int k = m; k < MT + NT; k += MT) {
-            write_piece(s, k);
+        for (int k = 0; k < kLoads; ++k) {
+          if (k * kSlots / kLoads == i) {
+            write_piece(s + 1, k);
             load_piece(off, k);
           }
+        }
+        if (n == NT - 1) {
+          read_op(av[m], wnext + m * 16 * 128);
 #pragma unroll
           for (int k = m; k < NT; k += MT) f_next[k] = lds_s[((s + 1) >> 2) & 1][wn + 16 * k + r][(s + 1) & 3];
           if (m == MT - 1) {
@@ -410,7 +420,7 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
   // token's rows leave in whole pieces.
   lds_barrier();
   constexpr int kPitch = 16 * MT + 4;  // fp32 a token
-  static_assert(4 * 16 * kPitch * 4 <= (int)sizeof(lds_w), "a wave's 16 tokens fit");
+  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds_w), "every wave's 16 tokens fit");
   float* out = reinterpret_cast<float*>(&lds_w[0][0]) + wave * 16 * kPitch;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -420,6 +430,14 @@ __global__ __launch_bounds__(256, 1) void vq_fp8_tile_kernel(Fp8Args a) {
     store_tokens<16 * MT>(a, out, kPitch, t0 + wn + 16 * n, r0 + wm, lane);
     wave_lds_fence();
   }
+}
+
+template <bool EXACT, int WM, int WN, int MT, int NT>
+hipError_t run_tile(const Fp8Args& a, hipStream_t s) {
+  constexpr int kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
+  const dim3 grid((unsigned)((a.rows + kTileRows - 1) / kTileRows) * ((a.T + kTileTokens - 1) / kTileTokens));
+  hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT>), grid, dim3(64 * WM * WN), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -454,11 +472,11 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x,
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
   if (T > 64) {
-    const int tr = io.y_kind == kOutF32 ? 128 : 256, tk = 192;
-    const dim3 grid((unsigned)((w.rows + tr - 1) / tr) * ((T + tk - 1) / tk));
-    if (io.y_kind == kOutF32) hipLaunchKernelGGL((vq_fp8_tile_kernel<true, 4, 6>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((vq_fp8_tile_kernel<false, 8, 6>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    if (io.y_kind == kOutF32) return run_tile<true, 4, 2, 2, 6>(a, s);
+    static const int cfg = getenv("FP8CFG") ? atoi(getenv("FP8CFG")) : 0;
+    if (cfg == 0) return run_tile<false, 4, 2, 4, 6>(a, s);
+    if (cfg == 1) return run_tile<false, 4, 2, 4, 8>(a, s);
+    return run_tile<false, 2, 2, 8, 6>(a, s);
   }
   const dim3 grid((unsigned)((w.rows + 15) / 16) * ((T + 15) / 16));
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<8>), grid, dim3(512), 0, s, a);
