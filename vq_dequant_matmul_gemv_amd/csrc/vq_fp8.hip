@@ -248,14 +248,14 @@ __device__ __forceinline__ float4_t dot128(const Op<EXACT>& a, const Op<EXACT>& 
   return p;
 }
 
-template <bool EXACT, int WM, int WN, int MT, int NT>
+template <bool EXACT, int WM, int WN, int MT, int NT, int AHEAD>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(Fp8Args a) {
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
   constexpr int kLoadRows = 8 * kWaves;  // rows the block loads at once
   constexpr int kWLoads = kTileRows / kLoadRows, kXLoads = kTileTokens / kLoadRows, kLoads = kWLoads + kXLoads;
   static_assert(kTileRows % kLoadRows == 0 && kTileTokens % kLoadRows == 0, "whole loads");
   static_assert(128 % (16 * MT) == 0, "a wave's rows share their scales");
-  static_assert(kTileTokens <= 256 && NT % 2 == 0, "scales of at most 256 tokens; the token operands alternate");
+  static_assert(kTileTokens <= 256 && NT % (AHEAD + 1) == 0, "scales of at most 256 tokens; a ring of operands");
   __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
   __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
   __shared__ __align__(1024) float lds_s[2][256][4];  // x scales of four steps, twice
@@ -341,10 +341,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   }
   load_scales(5);
   lds_barrier();
-  Op<EXACT> av[MT], bv[2];
+  constexpr int kRing = AHEAD + 1;  // token operands: the current one and the next AHEAD
+  Op<EXACT> av[MT], bv[kRing];
 #pragma unroll
   for (int m = 0; m < MT; ++m) read_op(av[m], lds_w[0] + (wm + 16 * m) * 128);
-  read_op(bv[0], lds_x[0] + wn * 128);
+#pragma unroll
+  for (int n = 0; n < AHEAD; ++n) read_op(bv[n], lds_x[0] + (wn + n * 16) * 128);
   float f[NT], f_last = 0.0f;
 #pragma unroll
   for (int n = 0; n < NT; ++n) f[n] = ws[0] * lds_s[0][wn + 16 * n + r][0];
@@ -364,21 +366,19 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
     float f_next[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (n < NT - 1) {
-        read_op(bv[(n + 1) & 1], xb + (n + 1) * 16 * 128);
-      } else {
-        // every wave holds its operands of this step, so the next one's pieces
-        // in LDS are complete and this one's buffers free
-        lds_barrier();
-      }
+      // every wave has issued its last reads of this step before the barrier
+      // waits for them, so behind it the next step's pieces in LDS are complete
+      // and this one's buffers free
+      if (n == NT - AHEAD) lds_barrier();
+      read_op(bv[(n + AHEAD) % kRing], (n + AHEAD < NT ? xb : xnext) + (n + AHEAD) % NT * 16 * 128);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int i = n * MT + m;
-        const float4_t now = dot128<EXACT>(av[m], bv[n & 1]);
+        const float4_t now = dot128<EXACT>(av[m], bv[n % kRing]);
         __builtin_amdgcn_sched_barrier(0);
         // the next step's pieces go to LDS, spread over the step, and the ones
         // after them are loaded in their place
-        constexpr int kSlots = (NT - 1) * MT;
+        constexpr int kSlots = (NT - AHEAD) * MT;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
           if (k * kSlots / kLoads == i) {
@@ -391,7 +391,6 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
 #pragma unroll
           for (int k = m; k < NT; k += MT) f_next[k] = lds_s[((s + 1) >> 2) & 1][wn + 16 * k + r][(s + 1) & 3];
           if (m == MT - 1) {
-            read_op(bv[0], xnext);
             write_scales(s + 5);
             load_scales(s + 6);
           }
@@ -432,11 +431,11 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   }
 }
 
-template <bool EXACT, int WM, int WN, int MT, int NT>
+template <bool EXACT, int WM, int WN, int MT, int NT, int AHEAD>
 hipError_t run_tile(const Fp8Args& a, hipStream_t s) {
   constexpr int kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
   const dim3 grid((unsigned)((a.rows + kTileRows - 1) / kTileRows) * ((a.T + kTileTokens - 1) / kTileTokens));
-  hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT>), grid, dim3(64 * WM * WN), 0, s, a);
+  hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT, AHEAD>), grid, dim3(64 * WM * WN), 0, s, a);
   return hipGetLastError();
 }
 
@@ -472,11 +471,11 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x,
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
   if (T > 64) {
-    if (io.y_kind == kOutF32) return run_tile<true, 4, 2, 2, 6>(a, s);
+    if (io.y_kind == kOutF32) return run_tile<true, 4, 2, 2, 6, 1>(a, s);
     static const int cfg = getenv("FP8CFG") ? atoi(getenv("FP8CFG")) : 0;
-    if (cfg == 0) return run_tile<false, 4, 2, 4, 6>(a, s);
-    if (cfg == 1) return run_tile<false, 4, 2, 4, 8>(a, s);
-    return run_tile<false, 2, 2, 8, 6>(a, s);
+    if (cfg == 0) return run_tile<false, 4, 2, 4, 6, 2>(a, s);
+    if (cfg == 1) return run_tile<false, 4, 2, 4, 8, 1>(a, s);
+    return run_tile<false, 2, 2, 8, 6, 2>(a, s);
   }
   const dim3 grid((unsigned)((w.rows + 15) / 16) * ((T + 15) / 16));
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<8>), grid, dim3(512), 0, s, a);
