@@ -176,9 +176,15 @@ def workspace_bytes(T: int, top_k: int, num_experts: int) -> int:
 # torch-facing wrappers
 # --------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream):
@@ -272,12 +278,17 @@ def dequant(w: VQTensor, expert: int = 0, out=None, stream=None):
     return out
 
 
+_DTYPE_CODES = {}
+
+
 def _dtype_code(dt):
-    torch = _torch()
-    codes = {torch.float32: VQ_DTYPE_F32, torch.float16: VQ_DTYPE_F16, torch.bfloat16: VQ_DTYPE_BF16}
-    if dt not in codes:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: VQ_DTYPE_F32, torch.float16: VQ_DTYPE_F16,
+                             torch.bfloat16: VQ_DTYPE_BF16})
+    if dt not in _DTYPE_CODES:
         raise ValueError(f"unsupported dtype {dt}")
-    return codes[dt]
+    return _DTYPE_CODES[dt]
 
 
 def _io(x, y_dtype, epilogue, route_weights):
@@ -449,27 +460,21 @@ SCORES = {"softmax": VQ_SCORE_SOFTMAX, "sigmoid": VQ_SCORE_SIGMOID}
 GROUP_SCORES = {"max": VQ_GROUP_MAX, "top2": VQ_GROUP_TOP2}
 
 
-def _on_device(device, stream, call, *shapes):
-    """Allocate an output for each (shape, dtype) that is not a tensor already,
-    on the stream the work goes to, then run call(outputs, raw stream) with
-    `device` current."""
+def _elsewhere(device, stream):
+    """The context a call has to enter first: the given stream's, or that of
+    tensors on another GPU than the current one.  None where the current
+    device and stream are the ones to use."""
     torch = _torch()
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream on {stream.device}, tensors on {device}")
-        with torch.cuda.stream(stream):   # makes the stream's device current too
-            return _run_alloc(torch, device, stream, call, shapes)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _run_alloc(torch, device, torch.cuda.current_stream(device), call, shapes)
-    return _run_alloc(torch, device, torch.cuda.current_stream(device), call, shapes)
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else None
 
 
-def _run_alloc(torch, device, stream, call, shapes):
-    outs = [s if isinstance(s, torch.Tensor) else None if s is None else
-            torch.empty(s[0], dtype=s[1], device=device) for s in shapes]
-    check(call(outs, stream.cuda_stream))
-    return outs
+def _raw_stream(device) -> int:
+    """Handle of the device's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 @dataclass
@@ -502,24 +507,29 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
     T, k = logits.shape[0], r.top_k
     dev = logits.device
     _dev_check(logits)
+    bias = None
     if r.bias is not None:
         if r.bias.dtype != torch.float32 or tuple(r.bias.shape) != (r.num_experts,):
             raise ValueError(f"bias must be fp32 [{r.num_experts}]")
         _dev_check(r.bias, device=dev)
+        bias = r.bias.data_ptr()
     for t, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
         if t is not None:
             _check_out(t, dt, (T, k), name)
             _dev_check(t, device=dev)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return moe_route(router, logits, ids, weights)
+    if ids is None:
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
     cr = CRouter(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
-                 GROUP_SCORES[r.group_score], int(r.renormalize), r.scale, 0,
-                 None if r.bias is None else r.bias.data_ptr())
-
-    def call(outs, st):
-        return LIB.vq_moe_route(ctypes.byref(cr), logits.data_ptr(), T, outs[0].data_ptr(), outs[1].data_ptr(), st)
-
-    shape = (T, max(k, 0))
-    return tuple(_on_device(dev, stream, call, ids if ids is not None else (shape, torch.int32),
-                            weights if weights is not None else (shape, torch.float32)))
+                 GROUP_SCORES[r.group_score], int(r.renormalize), r.scale, 0, bias)
+    check(LIB.vq_moe_route(ctypes.byref(cr), logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
+                           _raw_stream(dev)))
+    return ids, weights
 
 
 # --------------------------------------------------------------------------
@@ -571,13 +581,17 @@ def fp8_quant(x, q=None, scales=None, stream=None):
     if scales is not None:
         _check_out(scales, torch.float32, sshape, "scales")
         _dev_check(scales, device=dev)
-    code = _dtype_code(x.dtype)
-
-    def call(outs, st):
-        return LIB.vq_fp8_quant(x.data_ptr(), code, T, cols, outs[0].data_ptr(), outs[1].data_ptr(), st)
-
-    return tuple(_on_device(dev, stream, call, q if q is not None else ((T, cols), torch.float8_e4m3fn),
-                            scales if scales is not None else (sshape, torch.float32)))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fp8_quant(x, q, scales)
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+    check(LIB.vq_fp8_quant(x.data_ptr(), _dtype_code(x.dtype), T, cols, q.data_ptr(), scales.data_ptr(),
+                           _raw_stream(dev)))
+    return q, scales
 
 
 def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_dtype=None, epilogue=None):
@@ -603,17 +617,22 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
         _dev_check(y, device=dev)
     if workspace is not None:
         _dev_check(workspace, device=dev)
-    need = LIB.vq_fp8_workspace_bytes(rows, cols, T)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fp8_gemm(w, x, x_scales, y, workspace, None, y_dtype, epilogue)
+    if y is None:
+        y = torch.empty(yshape, dtype=y_dtype, device=dev)
+    if workspace is None:
+        need = LIB.vq_fp8_workspace_bytes(rows, cols, T)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     io = CIo(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, None)
-
-    def call(outs, st):
-        ws = outs[1]
-        return LIB.vq_fp8_gemm(ctypes.byref(cs), ctypes.byref(io), x.data_ptr(), x_scales.data_ptr(), T,
-                               outs[0].data_ptr(), None if ws is None else ws.data_ptr(),
-                               0 if ws is None else ws.numel() * ws.element_size(), st)
-
-    return _on_device(dev, stream, call, y if y is not None else (yshape, y_dtype),
-                      workspace if workspace is not None or need == 0 else ((need,), torch.uint8))[0]
+    check(LIB.vq_fp8_gemm(ctypes.byref(cs), ctypes.byref(io), x.data_ptr(), x_scales.data_ptr(), T, y.data_ptr(),
+                          None if workspace is None else workspace.data_ptr(),
+                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                          _raw_stream(dev)))
+    return y
 
 
 # --------------------------------------------------------------------------
@@ -646,55 +665,58 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
         raise ValueError("norm needs a block or a residual")
     if first.dim() != 2:
         raise ValueError("block and residual must be [T][cols]")
-    T, cols = first.shape
+    shape = T, cols = first.shape
     dev = first.device
-    v_dtype = (residual if residual is not None else block).dtype
+    v_dtype = first.dtype if residual is None else residual.dtype
     if h_dtype is None:
         h_dtype = h.dtype if h is not None else pre_weight.dtype if pre_weight is not None else None
     e4m3 = h_dtype == torch.float8_e4m3fn
     if h_dtype is None and not store_residual:
         raise ValueError("norm has nothing to compute: neither v nor h is wanted")
-    given = [t for t in (block, residual, post_weight, pre_weight, gate) if t is not None]
-    _dev_check(*given, device=dev)
-    for t in (block, residual):
-        if t is not None and tuple(t.shape) != (T, cols):
+    _dev_check(first)
+    if block is not None and residual is not None:
+        _dev_check(residual, device=dev)
+        if residual.shape != shape:
             raise ValueError("block and residual must have the same shape [T][cols]")
-    w_dtype = None
+    w_dtype = kind = None
     for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (gate, "gate")):
         if t is None:
             continue
-        if name != "gate" and tuple(t.shape) != (cols,):
-            raise ValueError(f"{name} must be [{cols}]")
+        _dev_check(t, device=dev)
         if w_dtype is not None and t.dtype != w_dtype:
             raise ValueError("post_weight, pre_weight and gate must have one dtype")
         w_dtype = t.dtype
+        if name == "gate":
+            kind = {(cols,): VQ_GATE_CHANNEL, (T, 1): VQ_GATE_TOKEN, (T, cols): VQ_GATE_FULL}.get(tuple(t.shape))
+            if kind is None:
+                raise ValueError(f"gate must be [{cols}], [{T}][1] or [{T}][{cols}]")
+        elif t.dim() != 1 or t.shape[0] != cols:
+            raise ValueError(f"{name} must be [{cols}]")
     if gate_act not in GATE_ACTS:
         raise ValueError(f"gate_act must be None or one of {sorted(k for k in GATE_ACTS if k)}")
-    kind = VQ_GATE_NONE
-    if gate is not None:
-        kinds = {(cols,): VQ_GATE_CHANNEL, (T, 1): VQ_GATE_TOKEN, (T, cols): VQ_GATE_FULL}
-        if tuple(gate.shape) not in kinds:
-            raise ValueError(f"gate must be [{cols}], [{T}][1] or [{T}][{cols}]")
-        kind = kinds[tuple(gate.shape)]
-    sshape = (T, _blocks(cols))
-    for t, dt, shape, name in ((residual_out, v_dtype, (T, cols), "residual_out"), (h, h_dtype, (T, cols), "h"),
-                               (h_scales, torch.float32, sshape, "h_scales")):
+    for t, dt, want, name in ((residual_out, v_dtype, shape, "residual_out"), (h, h_dtype, shape, "h"),
+                              (h_scales, torch.float32, (T, _blocks(cols)), "h_scales")):
         if t is not None:
-            _check_out(t, dt, shape, name)
+            _check_out(t, dt, want, name)
             _dev_check(t, device=dev)
-    spec = CNormSpec(cols, _dtype_code((block if block is not None else first).dtype), _dtype_code(v_dtype),
-                     _dtype_code(w_dtype or torch.float32),
-                     VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind,
-                     GATE_ACTS[gate_act] if gate is not None else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset,
-                     *(None if t is None else t.data_ptr() for t in (post_weight, pre_weight, gate)))
-
-    def call(outs, st):
-        return LIB.vq_norm(ctypes.byref(spec), None if block is None else block.data_ptr(),
-                           None if residual is None else residual.data_ptr(), T,
-                           *(None if o is None else o.data_ptr() for o in outs), st)
-
-    return tuple(_on_device(
-        dev, stream, call,
-        residual_out if residual_out is not None else ((T, cols), v_dtype) if store_residual else None,
-        h if h is not None else ((T, cols), h_dtype) if h_dtype is not None else None,
-        h_scales if h_scales is not None else (sshape, torch.float32) if e4m3 else None))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return norm(block, residual, post_weight=post_weight, pre_weight=pre_weight, gate=gate,
+                        gate_act=gate_act, alpha=alpha, beta=beta, weight_offset=weight_offset, eps=eps,
+                        h_dtype=h_dtype, residual_out=residual_out, h=h, h_scales=h_scales,
+                        store_residual=store_residual)
+    if residual_out is None and store_residual:
+        residual_out = torch.empty_like(first, dtype=v_dtype)
+    if h is None and h_dtype is not None:
+        h = torch.empty_like(first, dtype=h_dtype)
+    if h_scales is None and e4m3:
+        h_scales = torch.empty((T, _blocks(cols)), dtype=torch.float32, device=dev)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    spec = CNormSpec(cols, _dtype_code(first.dtype), _dtype_code(v_dtype), _dtype_code(w_dtype or torch.float32),
+                     VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind or VQ_GATE_NONE,
+                     GATE_ACTS[gate_act] if kind else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset,
+                     ptr(post_weight), ptr(pre_weight), ptr(gate))
+    check(LIB.vq_norm(ctypes.byref(spec), ptr(block), ptr(residual), T, ptr(residual_out), ptr(h), ptr(h_scales),
+                      _raw_stream(dev)))
+    return residual_out, h, h_scales
