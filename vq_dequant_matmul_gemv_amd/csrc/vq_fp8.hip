@@ -7,6 +7,8 @@
 #include "vq_kernels.h"
 
 #include <algorithm>
+#include <cmath>
+#include <cstdio>
 #include <cstdlib>
 
 namespace vqmi {
@@ -64,6 +66,8 @@ struct Fp8Args {
   void* y;
   int rows, cols, kb, T;
   int y_kind, swiglu;
+  float* part;      // split columns: fp32 sums [gridDim.y][T][rows] in place of y
+  int split_steps;  // column blocks a split (the last one may have fewer)
 };
 
 // One wave's LDS writes before its later reads of other lanes' values (LDS
@@ -102,6 +106,17 @@ __device__ __forceinline__ void store_run(void* y, int64_t i, const float* v, in
   uint16_t* p = static_cast<uint16_t*>(y) + i;
   if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
   else *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+}
+
+// The arguments of one split of the columns: its sums go to their own plane of
+// the workspace, as they are.
+__device__ __forceinline__ Fp8Args split_args(Fp8Args a) {
+  if (a.part) {
+    a.y = a.part + (int64_t)blockIdx.y * a.T * a.rows;
+    a.y_kind = kOutF32;
+    a.swiglu = 0;
+  }
+  return a;
 }
 
 // Stores 16 tokens from t0 on of ROWS rows from r0 on (a multiple of 16) that
@@ -180,38 +195,89 @@ __device__ __forceinline__ float4_t dot128_f16(const Frag& a, const Frag& b) {
   return p;
 }
 
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args a) {
-  __shared__ float4_t part[WAVES][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+// NT x 16 tokens a block; a wave takes every WAVES-th block of 128 columns and
+// keeps DEPTH of them in flight.  The products of the scales of a chunk of
+// kChunk column blocks are set up in LDS first, so the loop waits for
+// nothing but its operands.
+constexpr int kScaleSteps = 256;
+
+template <int WAVES, int NT, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args) {
+  const Fp8Args a = split_args(args);
+  constexpr int kThreads = 64 * WAVES, kTok = 16 * NT;
+  constexpr int kChunk = kScaleSteps / NT;  // column blocks per chunk: 16 KiB of scales
+  __shared__ float f[kChunk][kTok];
+  __shared__ float4_t part[WAVES][NT][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const unsigned row_tiles = (a.rows + 15) / 16;  // row tiles run fastest: they share the tokens
-  const int r0 = (blockIdx.x % row_tiles) * 16, t0 = (blockIdx.x / row_tiles) * 16;
+  const int r0 = (blockIdx.x % row_tiles) * 16, t0 = (blockIdx.x / row_tiles) * kTok;
   const int r = lane & 15;
   const uint32_t cols = a.cols;
+  const int kb = a.kb;
   const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * cols, (uint64_t)min(16, a.rows - r0) * cols);
-  const rsrc_t xr = make_rsrc(a.x + (int64_t)t0 * cols, (uint64_t)min(16, a.T - t0) * cols);
-  const float* ws = a.ws + (int64_t)(r0 / kFp8Block) * a.kb;
-  const float* xs = a.xs + (int64_t)min(t0 + r, a.T - 1) * a.kb;
-  float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = wave; k < a.kb; k += WAVES) {
+  const rsrc_t xr = make_rsrc(a.x + (int64_t)t0 * cols, (uint64_t)min(kTok, a.T - t0) * cols);
+  const rsrc_t sr = make_rsrc(a.xs + (int64_t)t0 * kb, (uint64_t)min(kTok, a.T - t0) * kb * 4);
+  const rsrc_t wsr = make_rsrc(a.ws + (int64_t)(r0 / kFp8Block) * kb, (uint64_t)kb * 4);
+  float4_t acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  Frag aw[DEPTH], bx[DEPTH][NT];
+  auto load = [&](int j, int k) {  // steps past the end: zeros
     const uint32_t c = k * kFp8Block + (lane >> 4) * 16;
-    const Frag av = load_frag(wr, r * cols, c, cols);
-    const Frag bv = load_frag(xr, r * cols, c, cols);
-    const float s = ws[k] * xs[k];
-    const float4_t p = dot128_f16(av, bv);
+    aw[j] = load_frag(wr, r * cols, c, cols);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, p[i], acc[i]);
+    for (int n = 0; n < NT; ++n) bx[j][n] = load_frag(xr, (16 * n + r) * cols, c, cols);
+  };
+  const int k_first = blockIdx.y * a.split_steps, k_end = min(kb, k_first + a.split_steps);
+  for (int k0 = k_first; k0 < k_end; k0 += kChunk) {
+    const int steps = min(kChunk, k_end - k0);
+    if (k0 > k_first) __syncthreads();
+    // a thread's scale products: token-major reads (the steps of a token lie
+    // side by side), step-major in LDS
+    constexpr int kPer = kChunk * kTok / kThreads;
+    float sx[kPer], sw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = threadIdx.x + i * kThreads, t = e / kChunk, k = e % kChunk;
+      const uint32_t ok = k < steps ? 0u : kOutOfRange;
+      sx[i] = __uint_as_float(buf_load_b32(sr, ok | (uint32_t)(t * kb + k0 + k) * 4));
+      sw[i] = __uint_as_float(buf_load_b32(wsr, ok | (uint32_t)(k0 + k) * 4));
+    }
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) load(j, wave + j * WAVES < steps ? k0 + wave + j * WAVES : kb);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      f[e % kChunk][e / kChunk] = sx[i] * sw[i];
+    }
+    lds_barrier();
+    for (int k = wave; k < steps; k += DEPTH * WAVES) {
+#pragma unroll
+      for (int j = 0; j < DEPTH; ++j) {
+        // no branches: the loads in flight are counted through the loop
+        const int kj = k + j * WAVES, next = kj + DEPTH * WAVES;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4_t p = dot128_f16(aw[j], bx[j][n]);
+          const float s = kj < steps ? f[min(kj, steps - 1)][16 * n + r] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, p[i], acc[n][i]);
+        }
+        load(j, next < steps ? k0 + next : kb);
+      }
+    }
   }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) acc += part[w][lane];
-  const int t = t0 + r;
-  float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+  for (int n = 0; n < NT; ++n) part[wave][n][lane] = acc[n];
+  __syncthreads();
+  if (wave >= NT) return;  // wave n joins token tile n
+  float4_t sum = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) sum += part[w][wave][lane];
+  const int t = t0 + 16 * wave + r;
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
   if (t < a.T) store_rows4(a, t, r0 + (lane >> 4) * 4, v);
 }
-
 
 // ---------------------------------------------------------------------------
 // product, many tokens: WM x WN waves of 16*MT rows x 16*NT tokens a block
@@ -249,7 +315,8 @@ __device__ __forceinline__ float4_t dot128(const Op<EXACT>& a, const Op<EXACT>& 
 }
 
 template <bool EXACT, int WM, int WN, int MT, int NT, int AHEAD>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(Fp8Args a) {
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(Fp8Args args) {
+  const Fp8Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
   constexpr int kLoadRows = 8 * kWaves;  // rows the block loads at once
   constexpr int kWLoads = kTileRows / kLoadRows, kXLoads = kTileTokens / kLoadRows, kLoads = kWLoads + kXLoads;
@@ -288,11 +355,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   // and steps past the end arrive as zeros.
   const uint32_t ld_piece = (lane & 7) * 16, ld_row = wave * 8 + (lane >> 3);
   const uint32_t ld_dst = ld_row * 128 + (ld_piece ^ ((lane >> 3) * 16));
+  // steps of this split: s0 is a multiple of four
+  const uint32_t s0 = blockIdx.y * a.split_steps, s1 = min(kb, s0 + a.split_steps);
   u32x4 stage[kLoads];
   float stage_s;
   auto stage_off = [&](uint32_t s) {
     const uint32_t c = s * kFp8Block + ld_piece;
-    return c < cols ? ld_row * cols + c : kOutOfRange;
+    return s < s1 && c < cols ? ld_row * cols + c : kOutOfRange;
   };
   auto load_piece = [&](uint32_t off, int i) {
     stage[i] = i < kWLoads ? buf_load_b128(wr, off + i * kLoadRows * cols)
@@ -322,16 +391,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // Step 0 with the scales of its group (and a quarter of the next) in LDS,
-  // step 1 in registers.
+  // The first step with the scales of its group (and a quarter of the next) in
+  // LDS, the second in registers.
 #pragma unroll
   for (uint32_t v = 0; v < 5; ++v) {
-    load_scales(v);
-    write_scales(v);
+    load_scales(s0 + v);
+    write_scales(s0 + v);
   }
 #pragma unroll
   for (uint32_t s = 0; s < 2; ++s) {
-    const uint32_t off = stage_off(s);
+    const uint32_t off = stage_off(s0 + s);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) load_piece(off, i);
     if (s < 1) {
@@ -339,7 +408,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
       for (int i = 0; i < kLoads; ++i) write_piece(s, i);
     }
   }
-  load_scales(5);
+  load_scales(s0 + 5);
   lds_barrier();
   constexpr int kRing = AHEAD + 1;  // token operands: the current one and the next AHEAD
   Op<EXACT> av[MT], bv[kRing];
@@ -349,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   for (int n = 0; n < AHEAD; ++n) read_op(bv[n], lds_x[0] + (wn + n * 16) * 128);
   float f[NT], f_last = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) f[n] = ws[0] * lds_s[0][wn + 16 * n + r][0];
+  for (int n = 0; n < NT; ++n) f[n] = ws[s0] * lds_s[(s0 >> 2) & 1][wn + 16 * n + r][0];
 
   // The sums of two products stay in flight while the ones before them are
   // scaled into the accumulators, across steps too.
@@ -357,7 +426,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   float4_t p[kLag];
 #pragma unroll
   for (int i = 0; i < kLag; ++i) p[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (uint32_t s = 0; s < kb; ++s) {
+  for (uint32_t s = s0; s < s1; ++s) {
     const uint8_t* xb = lds_x[s & 1] + wn * 128;
     const uint8_t* xnext = lds_x[(s + 1) & 1] + wn * 128;
     const uint8_t* wnext = lds_w[(s + 1) & 1] + wm * 128;
@@ -431,12 +500,161 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   }
 }
 
+// ---------------------------------------------------------------------------
+// joining the splits: y = the sum of the planes, in their order
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void vq_fp8_join_kernel(Fp8Args a, int splits) {
+  const int64_t n = (int64_t)a.T * a.rows, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (n % 4 == 0 && (!a.swiglu || a.rows % 2 == 0)) {
+    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(a.part + s * n + i);
+    // pairs of rows never straddle a token: rows are even under SwiGLU
+    if (a.swiglu) {
+      store_out(a.y, i / 2, silu_mul(v[0], v[1]), a.y_kind);
+      store_out(a.y, i / 2 + 1, silu_mul(v[2], v[3]), a.y_kind);
+    } else {
+      const float o[4] = {v[0], v[1], v[2], v[3]};
+      store_run<4>(a.y, i, o, a.y_kind, true, 4);
+    }
+    return;
+  }
+  for (int64_t k = i; k < min(n, i + 4); k += a.swiglu ? 2 : 1) {
+    float v = 0.0f, u = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+      v += a.part[s * n + k];
+      if (a.swiglu) u += a.part[s * n + k + 1];
+    }
+    store_out(a.y, a.swiglu ? k / 2 : k, a.swiglu ? silu_mul(v, u) : v, a.y_kind);
+  }
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
 template <bool EXACT, int WM, int WN, int MT, int NT, int AHEAD>
-hipError_t run_tile(const Fp8Args& a, hipStream_t s) {
-  constexpr int kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
-  const dim3 grid((unsigned)((a.rows + kTileRows - 1) / kTileRows) * ((a.T + kTileTokens - 1) / kTileTokens));
+void run_tile(const Fp8Args& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
   hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT, AHEAD>), grid, dim3(64 * WM * WN), 0, s, a);
-  return hipGetLastError();
+}
+
+template <int WAVES, int NT, int DEPTH>
+void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, 16 * NT), splits);
+  hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+}
+
+// The kernels of the product and a time model of each (us), fitted to 9400
+// measured calls (1 to 2048 tokens, 64 to 17408 rows, 256 to 17408 columns, 1
+// to 24 splits; the fit's error is 8-11 % rms, and the model's choice takes
+// 2.5 % longer than the best one on average):
+//   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
+//   and, split, 2 + join * (bytes of the planes, written and read, in MB)
+// with steps the column blocks a wave runs through, rounds of 256 blocks, and
+// bytes the weight once, y, and `x_share` of the tokens' reads by every row
+// tile (MB; bw in TB/s).
+struct Fp8Kernel {
+  int rows, tokens;        // of a block
+  int k_waves;             // waves that split a block's columns
+  int min_T, max_T;        // tokens it is considered for
+  bool f32, f16;           // outputs it serves: fp32, 16-bit
+  float base, latency, rate, bw, join, unit, x_share;
+  void (*run)(const Fp8Args&, int, hipStream_t);
+};
+constexpr int kAnyT = 1 << 30;
+const Fp8Kernel kFp8Kernels[] = {
+    // few tokens, columns split over a block's waves (fp16 instructions)
+    {16, 16, 8, 1, 16, true, true, 4.059f, 0.740f, 0.239f, 5.130f, 0.597f, 1.171f, 0.509f, run_skinny<8, 1, 1>},
+    {16, 32, 8, 17, 32, true, true, 4.210f, 1.367f, 0.000f, 4.190f, 0.598f, 1.889f, 0.393f, run_skinny<8, 2, 1>},
+    {16, 64, 8, 17, 512, true, true, 3.705f, 2.108f, 0.996f, 6.735f, 0.367f, 2.233f, 0.951f, run_skinny<8, 4, 1>},
+    // tiles on fp16 instructions: exact products for an fp32 y
+    {128, 32, 1, 1, 256, true, false, 4.731f, 0.609f, 0.352f, 5.125f, 0.229f, 0.518f, 0.215f,
+     run_tile<true, 4, 1, 2, 2, 1>},
+    {128, 64, 1, 1, 256, true, false, 4.986f, 0.826f, 0.491f, 5.798f, 0.210f, 1.108f, 0.290f,
+     run_tile<true, 4, 1, 2, 4, 1>},
+    {128, 192, 1, 32, kAnyT, true, false, 5.683f, 1.163f, 1.299f, 3.543f, 0.210f, 1.173f, 0.708f,
+     run_tile<true, 4, 2, 2, 6, 1>},
+    // tiles on e4m3 instructions: for a 16-bit y
+    {128, 32, 1, 1, 512, false, true, 4.678f, 0.418f, 0.239f, 5.367f, 0.176f, 0.417f, 0.990f,
+     run_tile<false, 4, 1, 2, 2, 1>},
+    {128, 64, 1, 1, 512, false, true, 4.724f, 0.438f, 0.304f, 5.821f, 0.157f, 1.276f, 0.831f,
+     run_tile<false, 4, 1, 2, 4, 1>},
+    {128, 192, 1, 32, kAnyT, false, true, 4.428f, 0.517f, 0.625f, 5.679f, 0.171f, 3.419f, 0.793f,
+     run_tile<false, 4, 2, 2, 6, 1>},
+    {256, 192, 1, 32, kAnyT, false, true, 7.232f, 0.887f, 0.778f, 6.958f, 0.156f, 4.162f, 1.572f,
+     run_tile<false, 4, 2, 4, 6, 2>},
+    {256, 256, 1, 32, kAnyT, false, true, 10.987f, 1.284f, 0.476f, 9.736f, 0.141f, 3.187f, 2.477f,
+     run_tile<false, 4, 2, 4, 8, 1>},
+};
+constexpr int kNumFp8Kernels = sizeof(kFp8Kernels) / sizeof(kFp8Kernels[0]);
+constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
+
+struct Fp8Plan {
+  int rows = 0, cols = 0, T = 0, exact = 0;  // what it is for
+  int kernel = 0, splits = 1, split_steps = 0;
+  size_t workspace() const { return splits > 1 ? (size_t)splits * T * rows * sizeof(float) : 0; }
+};
+
+// Column blocks per split (the tiles' groups of scales: whole fours) and the
+// splits that leaves.
+void set_splits(Fp8Plan& p, int splits) {
+  const int kb = ceil_div(p.cols, kFp8Block), q = kFp8Kernels[p.kernel].k_waves > 1 ? 1 : 4;
+  p.split_steps = ceil_div(ceil_div(kb, splits), q) * q;
+  p.splits = ceil_div(kb, p.split_steps);
+}
+
+float plan_time(const Fp8Plan& p) {
+  const Fp8Kernel& k = kFp8Kernels[p.kernel];
+  const float steps = (float)ceil_div(p.split_steps, k.k_waves);
+  const float load_steps = (float)p.split_steps / k.k_waves;
+  const int64_t units = (int64_t)ceil_div(p.rows, k.rows) * ceil_div(p.T, k.tokens) * p.splits;
+  const float out = (float)p.T * p.rows;
+  const float bytes = ((float)p.rows * p.cols + 4.0f * out + k.x_share * (float)p.T * p.cols * p.rows / k.rows) * 1e-6f;
+  const float a = k.latency * steps, b = (float)((units + 255) / 256) * (k.rate * load_steps + k.unit), c = bytes / k.bw;
+  const float t = k.base + std::sqrt(std::sqrt(a * a * a * a + b * b * b * b + c * c * c * c));
+  return p.splits > 1 ? t + 2.0f + k.join * p.splits * out * 8e-6f : t;
+}
+
+Fp8Plan make_plan(int rows, int cols, int T, bool exact) {
+  Fp8Plan best;
+  float best_t = 0.0f;
+  for (int i = 0; i < kNumFp8Kernels; ++i) {
+    const Fp8Kernel& k = kFp8Kernels[i];
+    if (T < k.min_T || T > k.max_T || !(exact ? k.f32 : k.f16)) continue;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
+      Fp8Plan p;
+      p.rows = rows, p.cols = cols, p.T = T, p.exact = exact, p.kernel = i;
+      set_splits(p, s);
+      if (s > 1 && (p.splits != s || p.workspace() > kMaxPlanBytes)) continue;
+      const float t = plan_time(p);
+      if (best.rows == 0 || t < best_t) best = p, best_t = t;
+    }
+  }
+  return best;
+}
+
+// VQMI_FP8_PLAN = "kernel,splits" (a row of the table) forces the choice, for
+// tests; a kernel that does not serve the output type is passed over.
+bool forced_plan(Fp8Plan& p) {
+  const char* e = getenv("VQMI_FP8_PLAN");
+  int k = 0, s = 0;
+  if (!e || sscanf(e, "%d,%d", &k, &s) != 2 || k < 0 || k >= kNumFp8Kernels || s < 1 || s > 64) return false;
+  if (!(p.exact ? kFp8Kernels[k].f32 : kFp8Kernels[k].f16)) return false;
+  p.kernel = k;
+  set_splits(p, s);
+  return true;
+}
+
+Fp8Plan fp8_plan(int rows, int cols, int T, bool exact) {
+  Fp8Plan p;
+  p.rows = rows, p.cols = cols, p.T = T, p.exact = exact;
+  if (forced_plan(p)) return p;
+  // the plans this thread made last (choosing takes a microsecond or two, and
+  // a call asks for its workspace first)
+  static thread_local Fp8Plan last[64];
+  Fp8Plan& slot = last[((unsigned)rows * 31u + (unsigned)cols * 7u + (unsigned)T * 2u + (unsigned)exact) % 64u];
+  if (slot.rows != rows || slot.cols != cols || slot.T != T || slot.exact != (int)exact)
+    slot = make_plan(rows, cols, T, exact);
+  return slot;
 }
 
 }  // namespace
@@ -451,13 +669,12 @@ hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t*
 }
 
 size_t fp8_workspace_bytes(int rows, int cols, int T) {
-  (void)rows; (void)cols; (void)T;
-  return 0;
+  return std::max(fp8_plan(rows, cols, T, false).workspace(), fp8_plan(rows, cols, T, true).workspace());
 }
 
 hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x, const float* xs, int T, void* y,
                            void* workspace, hipStream_t s) {
-  (void)workspace;
+  const Fp8Plan p = fp8_plan(w.rows, w.cols, T, io.y_kind == kOutF32);
   Fp8Args a{};
   a.w = w.values;
   a.ws = w.scales;
@@ -466,19 +683,17 @@ hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x,
   a.y = y;
   a.rows = w.rows;
   a.cols = w.cols;
-  a.kb = (w.cols + kFp8Block - 1) / kFp8Block;
+  a.kb = ceil_div(w.cols, kFp8Block);
   a.T = T;
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
-  if (T > 64) {
-    if (io.y_kind == kOutF32) return run_tile<true, 4, 2, 2, 6, 1>(a, s);
-    static const int cfg = getenv("FP8CFG") ? atoi(getenv("FP8CFG")) : 0;
-    if (cfg == 0) return run_tile<false, 4, 2, 4, 6, 2>(a, s);
-    if (cfg == 1) return run_tile<false, 4, 2, 4, 8, 1>(a, s);
-    return run_tile<false, 2, 2, 8, 6, 2>(a, s);
-  }
-  const dim3 grid((unsigned)((w.rows + 15) / 16) * ((T + 15) / 16));
-  hipLaunchKernelGGL((vq_fp8_skinny_kernel<8>), grid, dim3(512), 0, s, a);
+  a.part = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.split_steps = p.split_steps;
+  kFp8Kernels[p.kernel].run(a, p.splits, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(vq_fp8_join_kernel, dim3((unsigned)ceil_div((int64_t)T * w.rows, 1024)), dim3(256), 0, s, a,
+                     p.splits);
   return hipGetLastError();
 }
 
