@@ -100,8 +100,7 @@ __device__ __forceinline__ void store_run(void* y, int64_t i, const float* v, in
   uint32_t w[N / 2];
 #pragma unroll
   for (int k = 0; k < N / 2; ++k) {
-    w[k] = kind == kOutF16 ? __builtin_bit_cast(uint32_t, half2_t{(_Float16)v[2 * k], (_Float16)v[2 * k + 1]})
-                           : (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16;
+    w[k] = pack16(v[2 * k], v[2 * k + 1], kind == kOutF16);
   }
   uint16_t* p = static_cast<uint16_t*>(y) + i;
   if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};

@@ -10,6 +10,14 @@ constexpr int kFp8Block = 128;       // columns (and weight rows) that share a s
 constexpr float kFp8Max = 448.0f;    // largest e4m3 value
 constexpr uint32_t kFp8Nan = 0x7fu;
 
+// Two fp32 values as fp16 (or bf16) bits, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
+  if (f16) return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float float2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf16x2));
+}
+
 // Maximum over the 16 lanes of a DPP row, in every lane of it (rotations by
 // 1, 2, 4 and 8).
 __device__ __forceinline__ float row16_max(float v) {

@@ -5,14 +5,13 @@
 //   v = beta * residual + alpha * act(gate) * u
 //   h = v * rsqrt(mean(v^2) + eps) * (pre_weight + offset)
 //
-// The row stays in registers between its one read and its writes: up to 32
-// values a thread, 64, 256 or 1024 threads a row.  All arithmetic and both
+// The row stays in registers between its one read and its writes: 8 to 32
+// values a thread, a wave to 16 waves a row.  All arithmetic and both
 // sums of squares are fp32; v and h are rounded once, on their stores (h
 // comes from the unrounded v).
 #include "vq_fp8_device.h"
 #include "vq_kernels.h"
 
-#include <algorithm>
 
 namespace vqmi {
 
@@ -33,40 +32,31 @@ struct NormArgs {
   float alpha, beta, eps, offset, inv_cols;
 };
 
-// Eight values as they lie in memory: 16 bytes, or 32 for fp32.
+// Eight values as they lie in memory: 32 bytes of fp32 (WIDE) or 16 of fp16 or
+// bf16.
+template <bool WIDE>
 struct Raw8 {
-  u32x4 a, b;
+  u32x4 q[WIDE ? 2 : 1];
 };
 
-__device__ __forceinline__ Raw8 load_raw8(const void* p, int64_t i, int kind) {
-  Raw8 r{};
-  if (kind == kOutF32) {
-    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
-    r.a = q[0];
-    r.b = q[1];
-  } else {
-    r.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
-  }
-  return r;
-}
-
-__device__ __forceinline__ void raw_to_float(const Raw8& r, int kind, float* x) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  if (kind == kOutF32) {
+template <bool WIDE>
+__device__ __forceinline__ void to_float(const Raw8<WIDE>& r, int kind, float* x) {
+  if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.q[i / 4][i % 4]);
   } else if (kind == kOutF16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const half2_t h = __builtin_bit_cast(half2_t, w[i]);
+      const uint32_t w = r.q[0][i];
+      const half2_t h = __builtin_bit_cast(half2_t, w);
       x[2 * i] = (float)h.x;
       x[2 * i + 1] = (float)h.y;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      x[2 * i] = __uint_as_float(r.q[0][i] << 16);
+      x[2 * i + 1] = __uint_as_float(r.q[0][i] & 0xffff0000u);
     }
   }
 }
@@ -86,110 +76,117 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float* x, int k
   }
   uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (kind == kOutF16) w[k] = __builtin_bit_cast(uint32_t, half2_t{(_Float16)x[2 * k], (_Float16)x[2 * k + 1]});
-    else w[k] = (uint32_t)f32_to_bf16_bits(x[2 * k]) | (uint32_t)f32_to_bf16_bits(x[2 * k + 1]) << 16;
-  }
+  for (int k = 0; k < 4; ++k) w[k] = pack16(x[2 * k], x[2 * k + 1], kind == kOutF16);
   *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// exp(x) within two units: the product's rounding error goes into the result.
+__device__ __forceinline__ float exp_near(float x) {
+  const float t = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -t) + x * 1.925963033e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return e < INFINITY && e > 0.0f ? fmaf(e, lo * 0.693147181f, e) : e;
+}
+
 __device__ __forceinline__ float gate_act(float g, int act) {
-  if (act == kGateSigmoid) return 1.0f / (1.0f + expf(-g));
-  if (act == kGateTanh) return tanhf(g);
+  if (act == kGateSigmoid) return 1.0f / (1.0f + exp_near(-g));
+  if (act == kGateTanh) {
+    // near zero the odd series to x^11 (the rest below 2^-28 at 0.3)
+    const float a = fabsf(g), q = g * g;
+    float p = fmaf(q, -8.8632355e-3f, 2.1869489e-2f);
+    p = fmaf(q, p, -5.3968254e-2f);
+    p = fmaf(q, p, 1.3333333e-1f);
+    p = fmaf(q, p, -3.3333333e-1f);
+    const float small = fmaf(g * q, p, g), big = copysignf(1.0f - 2.0f / (1.0f + exp_near(2.0f * a)), g);
+    return a < 0.3f ? small : (a >= 0.3f ? big : g);  // NaN stays
+  }
   return g;
 }
 
-// VEC 8: a thread's values are runs of 8 columns, 16-byte loads (cols a
-// multiple of 8).  VEC 1: any cols, one column at a time.
-template <int VEC, int TPR, int CH>
+// Chunk c of a thread's row.  VEC 8: runs of 8 columns, 16-byte loads (cols a
+// multiple of 8).  VEC 1: any cols, one column at a time, converted as loaded.
+template <int VEC>
 struct RowMap {
-  int tid, cols;
-  __device__ __forceinline__ int col(int ch, int j) const {
-    return VEC == 8 ? (ch * TPR + tid) * 8 + j : (ch * 8 + j) * TPR + tid;
+  int tid, threads, cols;  // threads: of a row
+  __device__ __forceinline__ int col(int c, int j) const {
+    return VEC == 8 ? (c * threads + tid) * 8 + j : (c * 8 + j) * threads + tid;
   }
-  __device__ __forceinline__ bool in(int ch, int j) const { return col(ch, VEC == 8 ? 0 : j) < cols; }
-  // chunk ch's eight values of the row or vector that starts at `at`
-  __device__ __forceinline__ void load(const void* p, int64_t at, int kind, int ch, float* x) const {
+  __device__ __forceinline__ bool in(int c, int j) const { return col(c, VEC == 8 ? 0 : j) < cols; }
+  // The eight values of the row (or vector) that starts at `at`; zeros past the
+  // last column.
+  template <bool WIDE>
+  __device__ __forceinline__ void load(Raw8<WIDE>& r, const void* p, int64_t at, int kind, int c) const {
     if constexpr (VEC == 8) {
-      Raw8 r{};
-      if (in(ch, 0)) r = load_raw8(p, at + col(ch, 0), kind);
-      raw_to_float(r, kind, x);
-    } else {
+      const char* q = static_cast<const char*>(p) + (at + col(c, 0)) * (WIDE ? 4 : 2);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = in(ch, j) ? load1(p, at + col(ch, j), kind) : 0.0f;
+      for (int i = 0; i < (WIDE ? 2 : 1); ++i)
+        r.q[i] = in(c, 0) ? reinterpret_cast<const u32x4*>(q)[i] : u32x4{0u, 0u, 0u, 0u};
+    } else {
+      static_assert(VEC == 8 || WIDE, "single columns are loaded as floats");
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        r.q[j / 4][j % 4] = in(c, j) ? __float_as_uint(load1(p, at + col(c, j), kind)) : 0u;
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t at, int kind, int ch, const float* x) const {
+  __device__ __forceinline__ void store(void* p, int64_t at, int kind, int c, const float* x) const {
     if constexpr (VEC == 8) {
-      if (in(ch, 0)) store8(p, at + col(ch, 0), x, kind);
+      if (in(c, 0)) store8(p, at + col(c, 0), x, kind);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (in(ch, j)) store_out(p, at + col(ch, j), x[j], kind);
+        if (in(c, j)) store_out(p, at + col(c, j), x[j], kind);
       }
     }
   }
 };
 
-// Sum over the TPR threads of a row, in every one of them.
-template <int TPR>
+// Sum over the threads of a row (ONE: one wave, else the block's up to 16
+// waves), in every one of them.
+template <bool ONE>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (TPR > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  if constexpr (!ONE) {
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    if (lane == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
+    v = (lane & 15) < waves ? red[lane & 15] : 0.0f;
 #pragma unroll
-    for (int w = 0; w < TPR / 64; ++w) v += red[w];
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   }
   return v;
 }
 
-template <int VEC, int TPR, int CH>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void vq_norm_kernel(NormArgs a) {
+// BW, RW, WW: block, residual and weights are fp32.
+template <int VEC, int CH, bool ONE, bool BW, bool RW, bool WW>
+__global__ __launch_bounds__(ONE ? 256 : 1024) void vq_norm_kernel(NormArgs a) {
   __shared__ float red[2][16];
-  constexpr int kRows = TPR == 64 ? 4 : 1;  // rows per block
-  const int tid = threadIdx.x % TPR;
-  const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  // With eight values a thread (few rows in flight) the weights are loaded up
+  // front too, so one memory latency covers every input.
+  constexpr bool kEarly = CH == 1;
+  const int tid = ONE ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t t = ONE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
   if (t >= a.T) return;  // whole waves, and only where a row is one wave
-  const RowMap<VEC, TPR, CH> m{tid, a.cols};
+  const RowMap<VEC> m{tid, ONE ? 64 : (int)blockDim.x, a.cols};
   const int64_t at = t * a.cols;
+  Raw8<BW> rb[CH];
+  Raw8<RW> rr[CH];
+  Raw8<WW> rw, rp;
+  if (a.block) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) m.load(rb[c], a.block, at, a.block_kind, c);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) m.load(rr[c], a.residual, at, a.res_kind, c);
+  }
+  if (kEarly && a.post_w) m.load(rw, a.post_w, 0, a.w_kind, 0);
+  if (kEarly && a.pre_w) m.load(rp, a.pre_w, 0, a.w_kind, 0);
+  float g1 = a.alpha;
+  if (a.gate_kind == kGateToken) g1 *= gate_act(load1(a.gate, t, a.w_kind), a.gate_act);
   float v[CH][8];
   if (a.block) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) m.load(a.block, at, a.block_kind, c, v[c]);
-    if (a.post_w) {
-      float s = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(v[c][j], v[c][j], s);
-      }
-      const float r = 1.0f / sqrtf(row_sum<TPR>(s, red[0]) * a.inv_cols + a.eps);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float w[8];
-        m.load(a.post_w, 0, a.w_kind, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] *= r * (w[j] + a.offset);
-      }
-    }
-    float g1 = a.alpha;
-    if (a.gate_kind == kGateToken) g1 *= gate_act(load1(a.gate, t, a.w_kind), a.gate_act);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-      if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
-        m.load(a.gate, a.gate_kind == kGateFull ? at : 0, a.w_kind, c, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = gate_act(g[j], a.gate_act);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] *= g1 * g[j];
-    }
+    for (int c = 0; c < CH; ++c) to_float(rb[c], a.block_kind, v[c]);
   } else {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -197,13 +194,47 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void vq_norm_kernel(NormArgs
       for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
     }
   }
+  if (a.post_w) {
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(v[c][j], v[c][j], s);
+    }
+    g1 *= 1.0f / sqrtf(row_sum<ONE>(s, red[0]) * a.inv_cols + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[8];
+      if (!kEarly) m.load(rw, a.post_w, 0, a.w_kind, c);
+      to_float(rw, a.w_kind, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] *= w[j] + a.offset;
+    }
+  }
+  if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      Raw8<WW> rg;
+      float g[8];
+      m.load(rg, a.gate, a.gate_kind == kGateFull ? at : 0, a.w_kind, c);
+      to_float(rg, a.w_kind, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] *= gate_act(g[j], a.gate_act);
+    }
+  }
   if (a.residual) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float x[8];
-      m.load(a.residual, at, a.res_kind, c, x);
+      to_float(rr[c], a.res_kind, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = fmaf(a.beta, x[j], v[c][j]);
+      for (int j = 0; j < 8; ++j) v[c][j] = fmaf(a.beta, x[j], v[c][j] * g1);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] *= g1;
     }
   }
   if (a.v_out) {
@@ -211,27 +242,26 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void vq_norm_kernel(NormArgs
     for (int c = 0; c < CH; ++c) m.store(a.v_out, at, a.res_kind, c, v[c]);
   }
   if (!a.h) return;
+  // past the last column v is zero, but for a post norm of infinities
   float s = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (m.in(c, j)) s = fmaf(v[c][j], v[c][j], s);
-    }
+    for (int j = 0; j < 8; ++j) s = m.in(c, j) ? fmaf(v[c][j], v[c][j], s) : s;
   }
-  const float r = 1.0f / sqrtf(row_sum<TPR>(s, red[1]) * a.inv_cols + a.eps);
+  const float r = 1.0f / sqrtf(row_sum<ONE>(s, red[1]) * a.inv_cols + a.eps);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
     if (a.pre_w) {
-      m.load(a.pre_w, 0, a.w_kind, c, w);
+      float w[8];
+      if (!kEarly) m.load(rp, a.pre_w, 0, a.w_kind, c);
+      to_float(rp, a.w_kind, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] += a.offset;
+      for (int j = 0; j < 8; ++j) v[c][j] *= r * (w[j] + a.offset);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] *= r;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[c][j] *= r * w[j];
     if (VEC == 8 && a.h_kind == kNormE4m3) {
       // 16 lanes side by side hold a block of 128 columns
       float amax = 0.0f;
@@ -249,23 +279,42 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void vq_norm_kernel(NormArgs
   }
 }
 
-template <int VEC, int TPR>
-hipError_t run_ch(const NormArgs& a, hipStream_t s) {
-  constexpr int kRows = TPR == 64 ? 4 : 1;
-  const dim3 grid((unsigned)((a.T + kRows - 1) / kRows)), block(TPR == 64 ? 256 : TPR);
-  const int ch = (a.cols + TPR * 8 - 1) / (TPR * 8);
-  if (ch <= 1) hipLaunchKernelGGL((vq_norm_kernel<VEC, TPR, 1>), grid, block, 0, s, a);
-  else if (ch <= 2) hipLaunchKernelGGL((vq_norm_kernel<VEC, TPR, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((vq_norm_kernel<VEC, TPR, 4>), grid, block, 0, s, a);
-  return hipGetLastError();
+template <int VEC, int CH, bool ONE, bool BW, bool RW, bool WW>
+void run(const NormArgs& a, hipStream_t s) {
+  // whole waves for the row's pieces of 8, split over CH chunks
+  const int pieces = (a.cols + 7) / 8, threads = ONE ? 256 : ((pieces + CH - 1) / CH + 63) / 64 * 64;
+  const unsigned blocks = ONE ? ((unsigned)a.T + 3) / 4 : (unsigned)a.T;
+  hipLaunchKernelGGL((vq_norm_kernel<VEC, CH, ONE, BW, RW, WW>), dim3(blocks), dim3(threads), 0, s, a);
 }
 
-template <int VEC>
-hipError_t run_norm(const NormArgs& a, hipStream_t s) {
-  // one wave a row for short rows, up to 32 values a thread for the others
-  if (a.cols <= 64 * 8) return run_ch<VEC, 64>(a, s);
-  if (a.cols <= 256 * 32) return run_ch<VEC, 256>(a, s);
-  return run_ch<VEC, 1024>(a, s);
+template <int CH, bool ONE>
+void run_types(const NormArgs& a, hipStream_t s) {
+  const int w = (a.block && a.block_kind == kOutF32 ? 4 : 0) | (a.residual && a.res_kind == kOutF32 ? 2 : 0) |
+                (a.w_kind == kOutF32 ? 1 : 0);
+  switch (w) {
+    case 0: return run<8, CH, ONE, false, false, false>(a, s);
+    case 1: return run<8, CH, ONE, false, false, true>(a, s);
+    case 2: return run<8, CH, ONE, false, true, false>(a, s);
+    case 3: return run<8, CH, ONE, false, true, true>(a, s);
+    case 4: return run<8, CH, ONE, true, false, false>(a, s);
+    case 5: return run<8, CH, ONE, true, false, true>(a, s);
+    case 6: return run<8, CH, ONE, true, true, false>(a, s);
+    default: return run<8, CH, ONE, true, true, true>(a, s);
+  }
+}
+
+void run_norm(const NormArgs& a, hipStream_t s) {
+  if (a.cols % 8 != 0) return run<1, 4, false, true, true, true>(a, s);  // single columns: off the tuned path
+  const int pieces = a.cols / 8;
+  if (pieces <= 64) return run_types<1, true>(a, s);
+  // 8 values a thread while that many threads run at once, then 16: fewer
+  // reductions a value (4096 x 5120 bf16: 41.8 against 49.6 us, 8192 x 2048:
+  // 31.6 against 33.2; 512 x 5120: 10.2 against 9.7, one row of 5120: 6.2
+  // against 5.0; 24 values: 42.4 at 4096 x 5120)
+  const bool many = (int64_t)a.T * a.cols >= (int64_t)8 << 20;
+  if (pieces <= 1024 && !many) return run_types<1, false>(a, s);
+  if (pieces <= 2048) return run_types<2, false>(a, s);
+  return run_types<4, false>(a, s);
 }
 
 }  // namespace
@@ -295,7 +344,8 @@ hipError_t launch_norm(const NormSpec& n, const void* block, const void* residua
   a.eps = n.eps;
   a.offset = n.offset;
   a.inv_cols = 1.0f / (float)n.cols;
-  return n.cols % 8 == 0 ? run_norm<8>(a, s) : run_norm<1>(a, s);
+  run_norm(a, s);
+  return hipGetLastError();
 }
 
 }  // namespace vqmi
