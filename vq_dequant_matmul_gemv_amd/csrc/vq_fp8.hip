@@ -38,20 +38,24 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, uint8_t* q, float* scales, uint32_t T,
                                                            uint32_t cols, uint32_t kb) {
   const uint32_t b = blockIdx.x * 16u + (threadIdx.x >> 4);  // block of 128 columns, row by row
-  if (b >= T * kb) return;                                   // whole DPP rows
   const uint32_t t = b / kb, k = b - t * kb;
   const uint32_t c = k * kFp8Block + (threadIdx.x & 15u) * 8u;
-  float v[8] = {};
-  const bool in = c < cols;  // cols is a multiple of 16
+  const bool in = t < T && c < cols;  // cols is a multiple of 16
   const int64_t at = (int64_t)t * cols + c;
-  if (in) unpack8<BF16>(*reinterpret_cast<const u32x4*>(x + at), v);
-  float amax = 0.0f;
+  u32x4 raw = {0u, 0u, 0u, 0u};
+  if (in) raw = *reinterpret_cast<const u32x4*>(x + at);
+  // the largest magnitude from the 16-bit patterns, two at a time
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m2 = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(v[i]));
-  amax = row16_max(amax);
-  const float s = fp8_scale(amax);
-  if (in) *reinterpret_cast<u32x2*>(q + at) = fp8_pack8(v, s, fp8_lift(amax));
-  if ((threadIdx.x & 15u) == 0) scales[b] = s;
+  for (int i = 0; i < 4; ++i) m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, raw[i] & 0x7fff7fffu));
+  const uint32_t m = max((uint32_t)m2.x, (uint32_t)m2.y);
+  const uint32_t top = BF16 ? m << 16 : __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)m));
+  float v[8], s;
+  unpack8<BF16>(raw, v);
+  const u32x2 codes = fp8_quantize8(v, top, &s);
+  if (in) *reinterpret_cast<u32x2*>(q + at) = codes;
+  if (t < T && (threadIdx.x & 15u) == 0) scales[b] = s;
 }
 
 // ---------------------------------------------------------------------------

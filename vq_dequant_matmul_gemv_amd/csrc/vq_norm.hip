@@ -264,13 +264,14 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void vq_norm_kernel(NormArgs a) {
     }
     if (VEC == 8 && a.h_kind == kNormE4m3) {
       // 16 lanes side by side hold a block of 128 columns
-      float amax = 0.0f;
+      if (!m.in(c, 0)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, m.in(c, 0) ? finite_abs(v[c][j]) : 0.0f);
-      amax = row16_max(amax);
-      const float sc = fp8_scale(amax);
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
+      }
+      float sc;
+      const u32x2 q = fp8_quantize8(v[c], abs_max8(v[c]), &sc);
       if (m.in(c, 0)) {
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.h) + at + m.col(c, 0)) = fp8_pack8(v[c], sc, fp8_lift(amax));
+        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.h) + at + m.col(c, 0)) = q;
         if ((tid & 15) == 0) a.h_scales[t * a.kb + m.col(c, 0) / kFp8Block] = sc;
       }
     } else {
