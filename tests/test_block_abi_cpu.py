@@ -244,3 +244,15 @@ def test_norm_wrapper_refuses_before_the_library(b):
         b.norm(x)
     with pytest.raises(ValueError, match="nothing to compute"):
         b.norm(x, store_residual=False)
+
+
+def test_packed_descriptors_have_the_structures_layout(b):
+    """The bytes the wrappers pass are the ctypes mirrors' (and the header's)."""
+    r = b.CRouter(256, 8, 1, 2, 8, 4, 1, 1, 2.5, 0, 0x1234567890)
+    assert bytes(r) == b._pack_router(256, 8, 1, 2, 8, 4, 1, True, 2.5, 0, 0x1234567890)
+    w = b.CFP8Tensor(0x1000, 0x2000, 7, 16, 112, 1)
+    assert bytes(w) == b._pack_fp8(0x1000, 0x2000, 7, 16, 112, 1)
+    io = b.CIo(3, 2, 1, 0, None)
+    assert bytes(io) == b._pack_io(3, 2, 1, 0, 0)
+    n = b.CNormSpec(64, 0, 1, 2, 3, 1, 2, 0, 0.5, 0.25, 1e-6, 1.0, 0x10, 0x20, 0x30)
+    assert bytes(n) == b._pack_norm(64, 0, 1, 2, 3, 1, 2, 0, 0.5, 0.25, 1e-6, 1.0, 0x10, 0x20, 0x30)

@@ -16,5 +16,6 @@ __all__ = sorted(_BINDING_NAMES | {"synth", "binding"})
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(name)

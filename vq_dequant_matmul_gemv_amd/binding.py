@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -135,11 +136,11 @@ def _load():
         "vq_moe_gemm_no_alloc": (i32, [T, P, i32, P, i32, i32, P, P]),
         "vq_encode_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "vq_encode": (i32, [P, i32, i32, i32, i32, i32, P, i32, P, i32, P, P, P, P, P, ctypes.c_size_t, P]),
-        "vq_moe_route": (i32, [ctypes.POINTER(CRouter), P, i32, P, P, P]),
+        "vq_moe_route": (i32, [P, P, i32, P, P, P]),
         "vq_fp8_quant": (i32, [P, i32, i32, i32, P, P, P]),
         "vq_fp8_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
-        "vq_fp8_gemm": (i32, [ctypes.POINTER(CFP8Tensor), IO, P, P, i32, P, P, ctypes.c_size_t, P]),
-        "vq_norm": (i32, [ctypes.POINTER(CNormSpec), P, P, i32, P, P, P, P]),
+        "vq_fp8_gemm": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
+        "vq_norm": (i32, [P, P, P, i32, P, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
     }
@@ -460,6 +461,22 @@ SCORES = {"softmax": VQ_SCORE_SOFTMAX, "sigmoid": VQ_SCORE_SIGMOID}
 GROUP_SCORES = {"max": VQ_GROUP_MAX, "top2": VQ_GROUP_TOP2}
 
 
+# Descriptors as bytes, in the layouts of CRouter, CFP8Tensor, CIo and CNormSpec
+# (packing takes a third of a ctypes structure's time).
+_pack_router = struct.Struct("<8ifiQ").pack
+_pack_fp8 = struct.Struct("<QQiiqq").pack
+_pack_io = struct.Struct("<4iQ").pack
+_pack_norm = struct.Struct("<8i4f3Q").pack
+
+
+def _placed(t, device):
+    """The tensor is contiguous on `device`."""
+    if t.device != device:
+        raise ValueError(f"tensor on {t.device}, expected {device} (the GPU of the other tensors)")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+
+
 def _elsewhere(device, stream):
     """The context a call has to enter first: the given stream's, or that of
     tensors on another GPU than the current one.  None where the current
@@ -502,21 +519,24 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
         raise ValueError(f"score must be one of {sorted(SCORES)}")
     if r.group_score not in GROUP_SCORES:
         raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}")
-    if logits.dim() != 2 or logits.shape[1] != r.num_experts:
+    shape = logits.shape
+    if len(shape) != 2 or shape[1] != r.num_experts:
         raise ValueError(f"logits must be [T][{r.num_experts}]")
-    T, k = logits.shape[0], r.top_k
-    dev = logits.device
+    T, k = shape[0], r.top_k
     _dev_check(logits)
-    bias = None
+    dev = logits.device
+    bias = 0
     if r.bias is not None:
-        if r.bias.dtype != torch.float32 or tuple(r.bias.shape) != (r.num_experts,):
+        if r.bias.dtype != torch.float32 or r.bias.shape != (r.num_experts,):
             raise ValueError(f"bias must be fp32 [{r.num_experts}]")
-        _dev_check(r.bias, device=dev)
+        _placed(r.bias, dev)
         bias = r.bias.data_ptr()
-    for t, dt, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-        if t is not None:
-            _check_out(t, dt, (T, k), name)
-            _dev_check(t, device=dev)
+    if ids is not None:
+        _check_out(ids, torch.int32, (T, k), "ids")
+        _placed(ids, dev)
+    if weights is not None:
+        _check_out(weights, torch.float32, (T, k), "weights")
+        _placed(weights, dev)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
@@ -525,9 +545,9 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
         ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-    cr = CRouter(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
-                 GROUP_SCORES[r.group_score], int(r.renormalize), r.scale, 0, bias)
-    check(LIB.vq_moe_route(ctypes.byref(cr), logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
+    cr = _pack_router(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
+                      GROUP_SCORES[r.group_score], bool(r.renormalize), r.scale, 0, bias)
+    check(LIB.vq_moe_route(cr, logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
                            _raw_stream(dev)))
     return ids, weights
 
@@ -572,15 +592,15 @@ def fp8_quant(x, q=None, scales=None, stream=None):
     if x.dtype not in (torch.float16, torch.bfloat16) or x.dim() != 2:
         raise ValueError("x must be fp16 or bf16 [T][cols]")
     T, cols = x.shape
-    dev = x.device
     _dev_check(x)
+    dev = x.device
     sshape = (T, _blocks(cols))
     if q is not None:
         _check_out(q, torch.float8_e4m3fn, (T, cols), "q")
-        _dev_check(q, device=dev)
+        _placed(q, dev)
     if scales is not None:
         _check_out(scales, torch.float32, sshape, "scales")
-        _dev_check(scales, device=dev)
+        _placed(scales, dev)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
@@ -599,24 +619,29 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
     [T][ceil(cols/128)]) through vq_fp8_gemm, decode and prefill alike;
     epilogue "swiglu" on interleaved gate/up rows gives silu(gate) * up."""
     torch = _torch()
-    cs = w.cstruct()
-    rows, cols = cs.rows, cs.cols
-    if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.dim() != 2 or x.shape[1] != cols:
+    v, ws = w.values, w.scales
+    e4m3 = (torch.float8_e4m3fn, torch.uint8)
+    if v.dtype not in e4m3 or v.dim() != 2 or ws.dtype != torch.float32:
+        raise ValueError("w must hold float8_e4m3fn (or uint8) values [rows][cols] and fp32 scales")
+    rows, cols = v.shape
+    if x.dtype not in e4m3 or x.dim() != 2 or x.shape[1] != cols:
         raise ValueError(f"x must be float8_e4m3fn (or uint8 codes) [T][{cols}]")
     T = x.shape[0]
-    if x_scales.dtype != torch.float32 or tuple(x_scales.shape) != (T, _blocks(cols)):
+    if x_scales.dtype != torch.float32 or x_scales.shape != (T, _blocks(cols)):
         raise ValueError(f"x_scales must be fp32 {(T, _blocks(cols))}")
     if epilogue not in EPILOGUES or epilogue == "combine":
         raise ValueError("epilogue must be None or 'swiglu'")
     y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
     yshape = (T, rows // 2 if epilogue == "swiglu" else rows)
-    dev = w.device
-    _dev_check(x, x_scales, device=dev)
+    _dev_check(v)
+    dev = v.device
+    for t in (ws, x, x_scales):
+        _placed(t, dev)
     if y is not None:
         _check_out(y, y_dtype, yshape)
-        _dev_check(y, device=dev)
+        _placed(y, dev)
     if workspace is not None:
-        _dev_check(workspace, device=dev)
+        _placed(workspace, dev)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
@@ -627,11 +652,11 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
         need = LIB.vq_fp8_workspace_bytes(rows, cols, T)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    io = CIo(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, None)
-    check(LIB.vq_fp8_gemm(ctypes.byref(cs), ctypes.byref(io), x.data_ptr(), x_scales.data_ptr(), T, y.data_ptr(),
-                          None if workspace is None else workspace.data_ptr(),
-                          0 if workspace is None else workspace.numel() * workspace.element_size(),
-                          _raw_stream(dev)))
+    wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
+    check(LIB.vq_fp8_gemm(_pack_fp8(v.data_ptr(), ws.data_ptr(), rows, cols, rows * cols, ws.numel()),
+                          _pack_io(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, 0), x.data_ptr(),
+                          x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(dev)))
     return y
 
 
@@ -675,30 +700,43 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
         raise ValueError("norm has nothing to compute: neither v nor h is wanted")
     _dev_check(first)
     if block is not None and residual is not None:
-        _dev_check(residual, device=dev)
+        _placed(residual, dev)
         if residual.shape != shape:
             raise ValueError("block and residual must have the same shape [T][cols]")
-    w_dtype = kind = None
-    for t, name in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (gate, "gate")):
-        if t is None:
-            continue
-        _dev_check(t, device=dev)
-        if w_dtype is not None and t.dtype != w_dtype:
+    post = pre = gates = kind = 0
+    w_dtype = None
+    if post_weight is not None:
+        _placed(post_weight, dev)
+        if post_weight.shape != (cols,):
+            raise ValueError(f"post_weight must be [{cols}]")
+        w_dtype, post = post_weight.dtype, post_weight.data_ptr()
+    if pre_weight is not None:
+        _placed(pre_weight, dev)
+        if pre_weight.shape != (cols,):
+            raise ValueError(f"pre_weight must be [{cols}]")
+        if w_dtype is not None and pre_weight.dtype != w_dtype:
             raise ValueError("post_weight, pre_weight and gate must have one dtype")
-        w_dtype = t.dtype
-        if name == "gate":
-            kind = {(cols,): VQ_GATE_CHANNEL, (T, 1): VQ_GATE_TOKEN, (T, cols): VQ_GATE_FULL}.get(tuple(t.shape))
-            if kind is None:
-                raise ValueError(f"gate must be [{cols}], [{T}][1] or [{T}][{cols}]")
-        elif t.dim() != 1 or t.shape[0] != cols:
-            raise ValueError(f"{name} must be [{cols}]")
+        w_dtype, pre = pre_weight.dtype, pre_weight.data_ptr()
+    if gate is not None:
+        _placed(gate, dev)
+        if w_dtype is not None and gate.dtype != w_dtype:
+            raise ValueError("post_weight, pre_weight and gate must have one dtype")
+        kind = (VQ_GATE_FULL if gate.shape == shape else VQ_GATE_CHANNEL if gate.shape == (cols,) else
+                VQ_GATE_TOKEN if gate.shape == (T, 1) else 0)
+        if kind == 0:
+            raise ValueError(f"gate must be [{cols}], [{T}][1] or [{T}][{cols}]")
+        w_dtype, gates = gate.dtype, gate.data_ptr()
     if gate_act not in GATE_ACTS:
         raise ValueError(f"gate_act must be None or one of {sorted(k for k in GATE_ACTS if k)}")
-    for t, dt, want, name in ((residual_out, v_dtype, shape, "residual_out"), (h, h_dtype, shape, "h"),
-                              (h_scales, torch.float32, (T, _blocks(cols)), "h_scales")):
-        if t is not None:
-            _check_out(t, dt, want, name)
-            _dev_check(t, device=dev)
+    if residual_out is not None:
+        _check_out(residual_out, v_dtype, shape, "residual_out")
+        _placed(residual_out, dev)
+    if h is not None:
+        _check_out(h, h_dtype, shape, "h")
+        _placed(h, dev)
+    if h_scales is not None:
+        _check_out(h_scales, torch.float32, (T, _blocks(cols)), "h_scales")
+        _placed(h_scales, dev)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
@@ -713,10 +751,8 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
     if h_scales is None and e4m3:
         h_scales = torch.empty((T, _blocks(cols)), dtype=torch.float32, device=dev)
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    spec = CNormSpec(cols, _dtype_code(first.dtype), _dtype_code(v_dtype), _dtype_code(w_dtype or torch.float32),
-                     VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind or VQ_GATE_NONE,
-                     GATE_ACTS[gate_act] if kind else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset,
-                     ptr(post_weight), ptr(pre_weight), ptr(gate))
-    check(LIB.vq_norm(ctypes.byref(spec), ptr(block), ptr(residual), T, ptr(residual_out), ptr(h), ptr(h_scales),
-                      _raw_stream(dev)))
+    spec = _pack_norm(cols, _dtype_code(first.dtype), _dtype_code(v_dtype), _dtype_code(w_dtype or torch.float32),
+                      VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind,
+                      GATE_ACTS[gate_act] if kind else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset, post, pre, gates)
+    check(LIB.vq_norm(spec, ptr(block), ptr(residual), T, ptr(residual_out), ptr(h), ptr(h_scales), _raw_stream(dev)))
     return residual_out, h, h_scales
