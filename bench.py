@@ -287,7 +287,8 @@ def configs_report(only=""):
     dev = torch.device("cuda", 0)
     from vq_dequant_matmul_gemv_amd.profsum import source_digest
     out = [f"command: {REPORT_CMD}", f"kernel source digest: {source_digest()}",
-           f"encoder source digest: {source_digest('encoder')}", "",
+           f"encoder source digest: {source_digest('encoder')}",
+           f"block operators' source digest: {source_digest('block')}", "",
            "vq_gemv hands token counts above its measured crossover to the MFMA kernel (the rows with",
            "larger T under vq_gemv time that kernel); vq_gemm always runs the MFMA kernel.", "",
            "| workload | tensor | call | T | per call us (median, p10, p90) | GB/s | % of 8 TB/s | TFLOP/s | % of 2.5 PF |",
@@ -595,6 +596,59 @@ def configs_report(only=""):
         for (d, b) in ((2, 9), (4, 11), (4, 14), (8, 14)):
             spec = S(17408, 5120, d, b, 64)
             dense(nx, f"17408x5120 d{d}/K{1 << b}", spec, [1], [2048], (nx, d, b))
+    def block_rows(wl):
+        """The operators around the products, as a feed-forward block calls
+        them (rotating inputs); bytes: every input read and output written
+        once."""
+        f16, bf16, f32, e4m3 = torch.float16, torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+        def rand(*shape, dtype=f32):
+            return torch.randn(shape, device=dev).to(dtype)
+
+        for T, kw, what in ((1, dict(), "softmax, top-8 of 256"), (16384, dict(), "softmax, top-8 of 256"),
+                            (16384, dict(score="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5),
+                             "sigmoid + bias, 4 of 8 groups, top-8 of 256")):
+            r = binding.Router(256, 8, bias=0.05 * rand(256) if kw else None, **kw)
+            xs = [rand(T, 256) for _ in range(4)]
+            ids, w = binding.moe_route(r, xs[0])
+            us = timed([(lambda x=xs[i % 4]: binding.moe_route(r, x, ids, w)) for i in range(16)])
+            row(wl, what, "vq_moe_route", T, us, T * (256 * 4 + 64), 10.0 * T * 256)
+        for T, cols, dt in ((4, 17408, bf16), (4096, 5120, f16)):
+            xs = [rand(T, cols, dtype=dt) for _ in range(6)]
+            q, sc = binding.fp8_quant(xs[0])
+            us = timed([(lambda x=xs[i % 6]: binding.fp8_quant(x, q, sc)) for i in range(12)])
+            row(wl, f"{T}x{cols}", "vq_fp8_quant", T, us, 3 * T * cols, 2.0 * T * cols)
+        for T, rows, cols, ydt, epi in ((1, 17408, 5120, bf16, None), (16, 5120, 17408, f32, None),
+                                        (64, 5120, 5120, bf16, None), (197, 1001, 2000, f32, None),
+                                        (2048, 17408, 5120, bf16, "swiglu"), (2048, 17408, 5120, f32, None),
+                                        (4096, 8192, 8192, bf16, None)):
+            n = int(max(1, min(8, 700e6 // (rows * cols))))
+            ws = [binding.FP8Tensor(*_e4m3_weight(torch, rand(rows, cols))) for _ in range(n)]
+            q, sc = binding.fp8_quant(rand(T, cols, dtype=bf16))
+            y = torch.empty((T, rows // 2 if epi else rows), dtype=ydt, device=dev)
+            need = binding.LIB.vq_fp8_workspace_bytes(rows, cols, T)
+            wsp = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            us = timed([(lambda w=ws[i % n]: binding.fp8_gemm(w, q, sc, y, wsp, epilogue=epi)) for i in range(16)])
+            row(wl, f"{rows}x{cols} {str(ydt)[6:]} y{' swiglu' if epi else ''}", "vq_fp8_gemm", T, us,
+                T * cols + rows * cols + y.numel() * y.element_size(), 2.0 * T * rows * cols)
+            del ws
+        for T, cols, bdt, hdt in ((1, 5120, f32, bf16), (333, 2000, f16, e4m3), (4096, 5120, bf16, bf16),
+                                  (4096, 5120, f32, e4m3)):
+            n = int(max(1, min(6, 800e6 // (T * cols * 8))))
+            bl, res = [rand(T, cols, dtype=bdt) for _ in range(n)], [rand(T, cols, dtype=bf16) for _ in range(n)]
+            w, g = rand(cols, dtype=bf16), rand(T, 1, dtype=bf16)
+
+            def call(i, out=(None, None, None)):
+                return binding.norm(bl[i % n], res[i % n], post_weight=w, pre_weight=w, gate=g, gate_act="sigmoid",
+                                    alpha=0.5, h_dtype=hdt, residual_out=out[0], h=out[1], h_scales=out[2])
+            o = call(0)
+            us = timed([(lambda i=i: call(i, o)) for i in range(12)])
+            row(wl, f"{cols} columns, {str(bdt)[6:]} block, bf16 residual, {str(hdt)[6:]} h, token gate", "vq_norm", T,
+                us, T * cols * (bl[0].element_size() + 4 + o[1].element_size()), 12.0 * T * cols)
+        torch.cuda.empty_cache()
+
+    if keep("block"):
+        block_rows("block operators")
     if keep("encoder"):
         encode_row(1024, 4096, 4, 8, 64, 16384, 10)
     if only:
@@ -617,6 +671,16 @@ def configs_report(only=""):
                    f"{2.0 * M * K * N / us[0] / 1e6:.1f} TFLOP/s")
         del a, b
     print("\n".join(out), flush=True)
+
+
+def _e4m3_weight(torch, w):
+    """(values, scales) of a weight whose sizes need not be whole blocks."""
+    rows, cols = w.shape
+    b = torch.nn.functional.pad(w, (0, -cols % 128, 0, -rows % 128))
+    b = b.view(b.shape[0] // 128, 128, b.shape[1] // 128, 128)
+    s = b.abs().amax((1, 3), keepdim=True) / 448.0
+    q = (b / s).clamp(-448, 448).reshape(b.shape[0] * 128, -1)[:rows, :cols]
+    return q.contiguous().to(torch.float8_e4m3fn), s[:, 0, :, 0].contiguous()
 
 
 def main():

@@ -7,6 +7,7 @@
 // whole must be refused with an explanation, never read as if it were.
 
 #include "vq.h"
+#include "vq_block_kernels.h"
 #include "vq_kernels.h"
 
 #include <hip/hip_runtime.h>

@@ -4,7 +4,7 @@
 //   quantize  s[t][b] = fl32(max |x| over the block / 448), q = e4m3(x / s)
 //   product   y[t][r] = sum_b s_x[t][b] * s_w[r / 128][b] * sum_{c in b} x[t][c] * w[r][c]
 #include "vq_fp8_device.h"
-#include "vq_kernels.h"
+#include "vq_block_kernels.h"
 
 #include <algorithm>
 #include <cmath>

@@ -10,7 +10,7 @@
 // sums of squares are fp32; v and h are rounded once, on their stores (h
 // comes from the unrounded v).
 #include "vq_fp8_device.h"
-#include "vq_kernels.h"
+#include "vq_block_kernels.h"
 
 
 namespace vqmi {

@@ -23,7 +23,7 @@
 // depends on lie closer than twice that bound the wave starts over with
 // scores in 64 bits (about 1 token in 100 on random sigmoid scores).
 #include "vq_device.h"
-#include "vq_kernels.h"
+#include "vq_block_kernels.h"
 
 #include <cfloat>
 

@@ -13,7 +13,8 @@ profiles/.
 Only the library's kernels (and, for the copy calibration, the copy kernel)
 are listed.  The kernel source digest printed with each summary lets a reader
 see whether the kernels have changed since the counters were taken (the
-matmul kernels and the encoder have digests of their own).
+matmul kernels, the encoder and the operators around the products have digests
+of their own).
 """
 
 from __future__ import annotations
@@ -30,21 +31,28 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 ENCODER_SOURCES = ("vq_encode.hip",)
+BLOCK_SOURCES = ("vq_block_kernels.h", "vq_fp8.hip", "vq_fp8_device.h", "vq_norm.hip", "vq_router.hip")
 
 
 def source_digest(part: str = "matmul") -> str:
     """sha256 over kernel sources, 12 hex chars: "matmul" = every csrc/*.hip
-    and csrc/*.h except the encoder's, "encoder" = the encoder's source and
-    the shared headers.  The C-ABI wrapper and the public header are left
+    and csrc/*.h except the encoder's and the block operators', "encoder" =
+    the encoder's source and the shared headers, "block" = the operators
+    around the products and the shared headers.  The C-ABI wrapper and the public header are left
     out: they launch the kernels but do not change what a launch does on the
     GPU."""
     h = hashlib.sha256()
     files = sorted(glob.glob(os.path.join(HERE, "csrc", "*.hip")) +
                    glob.glob(os.path.join(HERE, "csrc", "*.h")))
-    if part == "matmul":
-        files = [f for f in files if os.path.basename(f) not in ENCODER_SOURCES]
+    name = os.path.basename
+    if part == "block":
+        files = [f for f in files if name(f) in BLOCK_SOURCES or f.endswith(".h")]
     else:
-        files = [f for f in files if os.path.basename(f) in ENCODER_SOURCES or f.endswith(".h")]
+        files = [f for f in files if name(f) not in BLOCK_SOURCES]
+    if part == "matmul":
+        files = [f for f in files if name(f) not in ENCODER_SOURCES]
+    elif part == "encoder":
+        files = [f for f in files if name(f) in ENCODER_SOURCES or f.endswith(".h")]
     for f in files:
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
