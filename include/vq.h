@@ -449,9 +449,15 @@ vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, 
  * Product of e4m3 activations with an e4m3 weight:
  *   y[t][r] = sum_b x_scales[t][b] * scales[r / 128][b] *
  *             sum over the 128 columns of block b of x[t][c] * w[r][c],
- * the products exact, all sums in fp32.  Any T (decode and prefill shapes
- * run different kernels with the same result contract); the same call gives
- * the same bits every time.
+ * all sums held in fp32.  An fp32 y is made of exact products (fp16 matrix
+ * instructions); for a 16-bit y the e4m3 instructions are used where they are
+ * faster, which cut every product of a group of eight columns below 2^-13 of
+ * the group's largest one (a relative error of 1.6e-5 on normal inputs, well
+ * below the type's rounding).  Any T: decode and prefill shapes run different
+ * kernels, and few output tiles are split along the columns into planes of
+ * the workspace and joined in order, as a time model of the call rates best.
+ * The same call gives the same bits every time.  The environment variable
+ * VQMI_FP8_PLAN = "kernel,splits" forces the choice (for tests).
  *   io: y_dtype and epilogue (NONE or SWIGLU on interleaved gate/up rows: y
  *     has rows / 2 values per token) as for vq_gemm_ex; x_dtype must be
  *     VQ_DTYPE_E4M3.  NULL: fp32 y, no epilogue.

@@ -243,7 +243,7 @@ def test_empty_batch():
 
 # ---- every kernel and split, whatever the planner would choose -------------
 
-KERNELS = 11
+KERNELS = 12
 
 
 @pytest.mark.parametrize("kernel", range(KERNELS))

@@ -546,10 +546,11 @@ void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 9400
+// The kernels of the product and a time model of each (us), fitted to 9700
 // measured calls (1 to 2048 tokens, 64 to 17408 rows, 256 to 17408 columns, 1
-// to 24 splits; the fit's error is 8-11 % rms, and the model's choice takes
-// 2.5 % longer than the best one on average):
+// to 24 splits), the faster ones of a shape weighing more; the fit's error is
+// 9-13 % rms, and the model's choice takes 2.5 % longer than the best one on
+// average:
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
 // with steps the column blocks a wave runs through, rounds of 256 blocks, and
@@ -566,26 +567,28 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 8, 1, 16, true, true, 4.059f, 0.740f, 0.239f, 5.130f, 0.597f, 1.171f, 0.509f, run_skinny<8, 1, 1>},
-    {16, 32, 8, 17, 32, true, true, 4.210f, 1.367f, 0.000f, 4.190f, 0.598f, 1.889f, 0.393f, run_skinny<8, 2, 1>},
-    {16, 64, 8, 17, 512, true, true, 3.705f, 2.108f, 0.996f, 6.735f, 0.367f, 2.233f, 0.951f, run_skinny<8, 4, 1>},
+    {16, 16, 8, 1, 16, true, true, 3.886f, 0.676f, 0.430f, 5.712f, 1.405f, 0.860f, 0.523f, run_skinny<8, 1, 1>},
+    {16, 32, 8, 17, 32, true, true, 4.388f, 1.244f, 0.781f, 7.323f, 0.984f, 0.944f, 0.728f, run_skinny<8, 2, 1>},
+    {16, 64, 8, 17, 512, true, true, 4.126f, 1.855f, 1.242f, 19.374f, 0.668f, 1.487f, 2.731f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
-    {128, 32, 1, 1, 256, true, false, 4.731f, 0.609f, 0.352f, 5.125f, 0.229f, 0.518f, 0.215f,
+    {128, 32, 1, 1, 256, true, false, 3.688f, 0.700f, 0.330f, 5.076f, 0.218f, 1.040f, 0.603f,
      run_tile<true, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 256, true, false, 4.986f, 0.826f, 0.491f, 5.798f, 0.210f, 1.108f, 0.290f,
+    {128, 64, 1, 1, 256, true, false, 4.035f, 0.906f, 0.468f, 5.306f, 0.207f, 1.505f, 0.304f,
      run_tile<true, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, true, false, 5.683f, 1.163f, 1.299f, 3.543f, 0.210f, 1.173f, 0.708f,
+    {128, 192, 1, 32, kAnyT, true, false, 6.061f, 1.247f, 1.336f, 3.528f, 0.238f, 0.000f, 0.636f,
      run_tile<true, 4, 2, 2, 6, 1>},
+    {256, 128, 1, 32, kAnyT, true, false, 5.362f, 1.407f, 1.330f, 10.227f, 0.166f, 4.689f, 4.243f,
+     run_tile<true, 4, 2, 4, 4, 1>},
     // tiles on e4m3 instructions: for a 16-bit y
-    {128, 32, 1, 1, 512, false, true, 4.678f, 0.418f, 0.239f, 5.367f, 0.176f, 0.417f, 0.990f,
+    {128, 32, 1, 1, 512, false, true, 3.902f, 0.466f, 0.231f, 5.177f, 0.217f, 0.378f, 0.872f,
      run_tile<false, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 512, false, true, 4.724f, 0.438f, 0.304f, 5.821f, 0.157f, 1.276f, 0.831f,
+    {128, 64, 1, 1, 512, false, true, 4.133f, 0.489f, 0.306f, 5.306f, 0.173f, 0.871f, 0.622f,
      run_tile<false, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, false, true, 4.428f, 0.517f, 0.625f, 5.679f, 0.171f, 3.419f, 0.793f,
+    {128, 192, 1, 32, kAnyT, false, true, 4.091f, 0.004f, 0.725f, 6.074f, 0.188f, 2.251f, 0.657f,
      run_tile<false, 4, 2, 2, 6, 1>},
-    {256, 192, 1, 32, kAnyT, false, true, 7.232f, 0.887f, 0.778f, 6.958f, 0.156f, 4.162f, 1.572f,
+    {256, 192, 1, 32, kAnyT, false, true, 6.141f, 0.902f, 0.869f, 6.997f, 0.150f, 3.605f, 1.471f,
      run_tile<false, 4, 2, 4, 6, 2>},
-    {256, 256, 1, 32, kAnyT, false, true, 10.987f, 1.284f, 0.476f, 9.736f, 0.141f, 3.187f, 2.477f,
+    {256, 256, 1, 32, kAnyT, false, true, 6.947f, 1.383f, 0.768f, 9.877f, 0.140f, 6.100f, 2.207f,
      run_tile<false, 4, 2, 4, 8, 1>},
 };
 constexpr int kNumFp8Kernels = sizeof(kFp8Kernels) / sizeof(kFp8Kernels[0]);

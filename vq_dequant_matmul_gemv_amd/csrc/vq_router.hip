@@ -190,7 +190,7 @@ __device__ __forceinline__ void store_slot(const RouterArgs& a, int64_t t, int l
     if (a.sigmoid) {
       const float c = a.renorm ? fminf(top, 0.0f) : 0.0f;
       w = (l <= 0.0f ? expf(l - c) : 1.0f) / (1.0f + expf(-fabsf(l)));
-      if (l < -709.0f) w = 0.0f;
+      if (l < -709.78f) w = 0.0f;
     } else {
       w = a.renorm ? expf(l - top) : expf(l - m) * inv_z;
       if (l - m < -745.0f) w = 0.0f;
