@@ -82,7 +82,23 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) * u, silu(g) = g / (1 + exp(-g)), by the instructions for 2^x and
+// 1 / x (within a unit each).  PRECISE, for an fp32 y: with e = exp(-|g|),
+// g / (1 + e), or g * e / (1 + e) for a negative g, so that nothing overflows,
+// and the exponent's product with log2(e) carried in two parts (one rounded
+// product would cost |g| units): 6 units in all.  Else, for 16 bits, the one
+// product, whose |g| units of 2^-24 are far below a half unit of 16 bits.
+// (35.7 million of them behind the tile kernel at 2048 tokens, 17408 rows:
+// expf() and a division 16 us, the precise form 10, the other 8.)
+template <bool PRECISE>
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.69314718f;
+  if constexpr (!PRECISE) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g)) * u;
+  const float a = fminf(fabsf(g), 128.0f);  // 2^-184 is 0 already; a NaN stays in g
+  const float t = a * kLog2e, low = fmaf(a, kLog2eLow, fmaf(a, kLog2e, -t));
+  const float p = __builtin_amdgcn_exp2f(-t), e = fmaf(p, -kLn2 * low, p);
+  return g * (g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
 
 // N consecutive outputs of one token, the first at y[i]; `whole`: i is a
 // multiple of N and all N exist.
@@ -125,7 +141,7 @@ __device__ __forceinline__ Fp8Args split_args(Fp8Args a) {
 // Stores 16 tokens from t0 on of ROWS rows from r0 on (a multiple of 16) that
 // lie in LDS, `pitch` floats a token; 8 rows a lane, with whole pieces of y
 // where its rows allow them.
-template <int ROWS>
+template <int ROWS, bool PRECISE>
 __device__ __forceinline__ void store_tokens(const Fp8Args& a, const float* lds, int pitch, int t0, int r0, int lane) {
   constexpr int kLanes = ROWS / 8, kPer = 64 / kLanes;  // lanes a token, tokens at once
   const int row = r0 + lane % kLanes * 8, n = a.rows - row;
@@ -137,8 +153,8 @@ __device__ __forceinline__ void store_tokens(const Fp8Args& a, const float* lds,
     const float4_t lo = *reinterpret_cast<const float4_t*>(lds + k * pitch + row - r0);
     const float4_t hi = *reinterpret_cast<const float4_t*>(lds + k * pitch + row - r0 + 4);
     if (a.swiglu) {
-      const float v[4] = {silu_mul(lo[0], lo[1]), silu_mul(lo[2], lo[3]), silu_mul(hi[0], hi[1]),
-                          silu_mul(hi[2], hi[3])};
+      const float v[4] = {silu_mul<PRECISE>(lo[0], lo[1]), silu_mul<PRECISE>(lo[2], lo[3]),
+                          silu_mul<PRECISE>(hi[0], hi[1]), silu_mul<PRECISE>(hi[2], hi[3])};
       store_run<4>(a.y, (int64_t)t * (a.rows / 2) + row / 2, v, a.y_kind, a.rows % 8 == 0, n / 2);
     } else {
       const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -153,7 +169,7 @@ __device__ __forceinline__ void store_rows4(const Fp8Args& a, int t, int row, co
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       if (row + 2 * p < a.rows)
-        store_out(a.y, (int64_t)t * (a.rows / 2) + row / 2 + p, silu_mul(v[2 * p], v[2 * p + 1]), a.y_kind);
+        store_out(a.y, (int64_t)t * (a.rows / 2) + row / 2 + p, silu_mul<true>(v[2 * p], v[2 * p + 1]), a.y_kind);
     }
   } else {
 #pragma unroll
@@ -498,7 +514,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
 #pragma unroll
     for (int m = 0; m < MT; ++m) *reinterpret_cast<float4_t*>(out + r * kPitch + 16 * m + 4 * g) = acc[m][n];
     wave_lds_fence();
-    store_tokens<16 * MT>(a, out, kPitch, t0 + wn + 16 * n, r0 + wm, lane);
+    store_tokens<16 * MT, EXACT>(a, out, kPitch, t0 + wn + 16 * n, r0 + wm, lane);
     wave_lds_fence();
   }
 }
@@ -514,8 +530,8 @@ __global__ __launch_bounds__(256) void vq_fp8_join_kernel(Fp8Args a, int splits)
     for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(a.part + s * n + i);
     // pairs of rows never straddle a token: rows are even under SwiGLU
     if (a.swiglu) {
-      store_out(a.y, i / 2, silu_mul(v[0], v[1]), a.y_kind);
-      store_out(a.y, i / 2 + 1, silu_mul(v[2], v[3]), a.y_kind);
+      store_out(a.y, i / 2, silu_mul<true>(v[0], v[1]), a.y_kind);
+      store_out(a.y, i / 2 + 1, silu_mul<true>(v[2], v[3]), a.y_kind);
     } else {
       const float o[4] = {v[0], v[1], v[2], v[3]};
       store_run<4>(a.y, i, o, a.y_kind, true, 4);
@@ -528,7 +544,7 @@ __global__ __launch_bounds__(256) void vq_fp8_join_kernel(Fp8Args a, int splits)
       v += a.part[s * n + k];
       if (a.swiglu) u += a.part[s * n + k + 1];
     }
-    store_out(a.y, a.swiglu ? k / 2 : k, a.swiglu ? silu_mul(v, u) : v, a.y_kind);
+    store_out(a.y, a.swiglu ? k / 2 : k, a.swiglu ? silu_mul<true>(v, u) : v, a.y_kind);
   }
 }
 
@@ -546,11 +562,11 @@ void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 9700
-// measured calls (1 to 2048 tokens, 64 to 17408 rows, 256 to 17408 columns, 1
+// The kernels of the product and a time model of each (us), fitted to 12200
+// measured calls (1 to 4096 tokens, 64 to 34816 rows, 256 to 17408 columns, 1
 // to 24 splits), the faster ones of a shape weighing more; the fit's error is
-// 9-13 % rms, and the model's choice takes 2.5 % longer than the best one on
-// average:
+// 8-12 % rms, and the model's choice takes 1.9 % longer than the best one on
+// average, 0.2 % for products of more than 100 us:
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
 // with steps the column blocks a wave runs through, rounds of 256 blocks, and
@@ -567,28 +583,28 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 8, 1, 16, true, true, 3.886f, 0.676f, 0.430f, 5.712f, 1.405f, 0.860f, 0.523f, run_skinny<8, 1, 1>},
-    {16, 32, 8, 17, 32, true, true, 4.388f, 1.244f, 0.781f, 7.323f, 0.984f, 0.944f, 0.728f, run_skinny<8, 2, 1>},
-    {16, 64, 8, 17, 512, true, true, 4.126f, 1.855f, 1.242f, 19.374f, 0.668f, 1.487f, 2.731f, run_skinny<8, 4, 1>},
+    {16, 16, 8, 1, 16, true, true, 3.907f, 0.663f, 0.471f, 6.085f, 1.221f, 0.857f, 0.586f, run_skinny<8, 1, 1>},
+    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
+    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
-    {128, 32, 1, 1, 256, true, false, 3.688f, 0.700f, 0.330f, 5.076f, 0.218f, 1.040f, 0.603f,
+    {128, 32, 1, 1, 256, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
      run_tile<true, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 256, true, false, 4.035f, 0.906f, 0.468f, 5.306f, 0.207f, 1.505f, 0.304f,
+    {128, 64, 1, 1, 256, true, false, 4.138f, 0.890f, 0.492f, 5.733f, 0.179f, 1.538f, 0.444f,
      run_tile<true, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, true, false, 6.061f, 1.247f, 1.336f, 3.528f, 0.238f, 0.000f, 0.636f,
+    {128, 192, 1, 32, kAnyT, true, false, 6.328f, 1.224f, 1.338f, 3.770f, 0.211f, 0.000f, 0.769f,
      run_tile<true, 4, 2, 2, 6, 1>},
-    {256, 128, 1, 32, kAnyT, true, false, 5.362f, 1.407f, 1.330f, 10.227f, 0.166f, 4.689f, 4.243f,
+    {256, 128, 1, 32, kAnyT, true, false, 5.046f, 0.745f, 1.648f, 4.748f, 0.151f, 3.549f, 1.200f,
      run_tile<true, 4, 2, 4, 4, 1>},
     // tiles on e4m3 instructions: for a 16-bit y
-    {128, 32, 1, 1, 512, false, true, 3.902f, 0.466f, 0.231f, 5.177f, 0.217f, 0.378f, 0.872f,
+    {128, 32, 1, 1, 512, false, true, 3.882f, 0.474f, 0.265f, 5.141f, 0.198f, 0.439f, 0.645f,
      run_tile<false, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 512, false, true, 4.133f, 0.489f, 0.306f, 5.306f, 0.173f, 0.871f, 0.622f,
+    {128, 64, 1, 1, 512, false, true, 3.876f, 0.507f, 0.337f, 5.262f, 0.161f, 1.188f, 0.491f,
      run_tile<false, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, false, true, 4.091f, 0.004f, 0.725f, 6.074f, 0.188f, 2.251f, 0.657f,
+    {128, 192, 1, 32, kAnyT, false, true, 3.911f, 0.010f, 0.727f, 6.659f, 0.179f, 2.502f, 0.765f,
      run_tile<false, 4, 2, 2, 6, 1>},
-    {256, 192, 1, 32, kAnyT, false, true, 6.141f, 0.902f, 0.869f, 6.997f, 0.150f, 3.605f, 1.471f,
+    {256, 192, 1, 32, kAnyT, false, true, 5.601f, 0.522f, 1.027f, 6.291f, 0.145f, 3.357f, 1.200f,
      run_tile<false, 4, 2, 4, 6, 2>},
-    {256, 256, 1, 32, kAnyT, false, true, 6.947f, 1.383f, 0.768f, 9.877f, 0.140f, 6.100f, 2.207f,
+    {256, 256, 1, 32, kAnyT, false, true, 5.866f, 0.014f, 1.365f, 6.712f, 0.137f, 4.071f, 1.200f,
      run_tile<false, 4, 2, 4, 8, 1>},
 };
 constexpr int kNumFp8Kernels = sizeof(kFp8Kernels) / sizeof(kFp8Kernels[0]);
