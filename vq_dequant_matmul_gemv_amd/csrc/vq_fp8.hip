@@ -3,6 +3,10 @@
 //
 //   quantize  s[t][b] = fl32(max |x| over the block / 448), q = e4m3(x / s)
 //   product   y[t][r] = sum_b s_x[t][b] * s_w[r / 128][b] * sum_{c in b} x[t][c] * w[r][c]
+//
+// The times below are those of calls replayed from a graph over weights that
+// do not stay in the caches, on a card that copies at 5.06 TB/s and reaches
+// 3.2 PFLOP/s in the library's e4m3 product of 8192 x 8192 x 8192.
 #include "vq_fp8_device.h"
 #include "vq_block_kernels.h"
 
@@ -33,6 +37,12 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* x) {
 
 // ---------------------------------------------------------------------------
 // quantizer: 16 lanes per block of 128 columns, 8 values each
+//
+// Bound by its bytes: two read, one written and a scale per 128.  16 lanes of
+// 16 bytes make a block's maximum a matter of four DPP steps, no LDS, and its
+// loads and stores whole lines; the maximum is taken from the 16-bit patterns.
+// 4096 x 5120 in 15.0 us = 4.2 TB/s (13.2 where the input is still in the
+// caches), 4 x 17408 in 2.3 us, a launch.
 // ---------------------------------------------------------------------------
 template <bool BF16>
 __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, uint8_t* q, float* scales, uint32_t T,
@@ -59,8 +69,15 @@ __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, ui
 }
 
 // ---------------------------------------------------------------------------
-// product, few tokens: a block takes 16 rows of w and 16 tokens, its waves
-// split the blocks of 128 columns and join their sums in LDS
+// product, few tokens: a block takes 16 rows of w and 16 to 64 tokens, its
+// waves split the blocks of 128 columns and join their sums in LDS
+//
+// Bound by the weights' bytes.  Blocks of 16 rows are enough of them to fill
+// the card at 5120 rows already, and eight waves a block keep 8 KiB of a row
+// tile in flight.  One token, 17408 x 5120: 22 us = 4.1 TB/s (19.1 in a
+// plain stream of calls); 16 tokens, 5120 x 17408: 26 (22.3).  Five column
+// blocks in flight a wave, 16 waves a block and columns that start elsewhere in
+// every block took as long.
 // ---------------------------------------------------------------------------
 struct Fp8Args {
   const uint8_t* w;
@@ -215,12 +232,12 @@ __device__ __forceinline__ float4_t dot128_f16(const Frag& a, const Frag& b) {
 }
 
 // NT x 16 tokens a block; a wave takes every WAVES-th block of 128 columns and
-// keeps DEPTH of them in flight.  The products of the scales of a chunk of
+// has the next one in flight.  The products of the scales of a chunk of
 // kChunk column blocks are set up in LDS first, so the loop waits for
 // nothing but its operands.
 constexpr int kScaleSteps = 256;
 
-template <int WAVES, int NT, int DEPTH>
+template <int WAVES, int NT>
 __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args) {
   const Fp8Args a = split_args(args);
   constexpr int kThreads = 64 * WAVES, kTok = 16 * NT;
@@ -240,12 +257,12 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
   float4_t acc[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  Frag aw[DEPTH], bx[DEPTH][NT];
-  auto load = [&](int j, int k) {  // steps past the end: zeros
+  Frag aw, bx[NT];
+  auto load = [&](int k) {  // steps past the end: zeros
     const uint32_t c = k * kFp8Block + (lane >> 4) * 16;
-    aw[j] = load_frag(wr, r * cols, c, cols);
+    aw = load_frag(wr, r * cols, c, cols);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) bx[j][n] = load_frag(xr, (16 * n + r) * cols, c, cols);
+    for (int n = 0; n < NT; ++n) bx[n] = load_frag(xr, (16 * n + r) * cols, c, cols);
   };
   const int k_first = blockIdx.y * a.split_steps, k_end = min(kb, k_first + a.split_steps);
   for (int k0 = k_first; k0 < k_end; k0 += kChunk) {
@@ -262,28 +279,22 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
       sx[i] = __uint_as_float(buf_load_b32(sr, ok | (uint32_t)(t * kb + k0 + k) * 4));
       sw[i] = __uint_as_float(buf_load_b32(wsr, ok | (uint32_t)(k0 + k) * 4));
     }
-#pragma unroll
-    for (int j = 0; j < DEPTH; ++j) load(j, wave + j * WAVES < steps ? k0 + wave + j * WAVES : kb);
+    load(wave < steps ? k0 + wave : kb);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = threadIdx.x + i * kThreads;
       f[e % kChunk][e / kChunk] = sx[i] * sw[i];
     }
     lds_barrier();
-    for (int k = wave; k < steps; k += DEPTH * WAVES) {
+    for (int k = wave; k < steps; k += WAVES) {
 #pragma unroll
-      for (int j = 0; j < DEPTH; ++j) {
-        // no branches: the loads in flight are counted through the loop
-        const int kj = k + j * WAVES, next = kj + DEPTH * WAVES;
+      for (int n = 0; n < NT; ++n) {
+        const float4_t p = dot128_f16(aw, bx[n]);
+        const float s = f[k][16 * n + r];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float4_t p = dot128_f16(aw[j], bx[j][n]);
-          const float s = kj < steps ? f[min(kj, steps - 1)][16 * n + r] : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, p[i], acc[n][i]);
-        }
-        load(j, next < steps ? k0 + next : kb);
+        for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, p[i], acc[n][i]);
       }
+      load(k + WAVES < steps ? k0 + k + WAVES : kb);
     }
   }
 #pragma unroll
@@ -300,6 +311,26 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
 
 // ---------------------------------------------------------------------------
 // product, many tokens: WM x WN waves of 16*MT rows x 16*NT tokens a block
+//
+// The scales change with every 128 columns, so a product of 16 x 16 x 128 is
+// one instruction and four FMAs a lane scale it into the sums.  A large tile
+// is bound by what feeds the matrix units: of a 256 x 192 step's 1536 cycles
+// of e4m3 instructions at their peak, the LDS needs 1730 for its fragments,
+// and the FMAs and the next step's pieces share the rest of the issue slots.
+//   - 8 waves (two a SIMD: one's FMAs and LDS reads run under the other's
+//     products) take 212 us where 4 waves of 128 x 96 took 245;
+//   - operands are read two products ahead, sums scaled two products behind
+//     (212 -> 202), across steps;
+//   - global loads pass through registers into LDS, spread over the step:
+//     with loads straight to LDS the compiler waits for all of them before
+//     the next LDS read;
+//   - one barrier a step, two buffers, pieces XORed so that reads of 8 rows
+//     touch all banks.
+// 2048 tokens x 17408 x 5120 in bf16: 189 to 200 us on different cards, 1.8 to
+// 1.9 PFLOP/s (10 us more with SwiGLU; the library's e4m3 product with one scale for each whole tensor takes 205
+// there); 4096 x 8192 x 8192: 246 us, 2.23 PFLOP/s.  An fp32 y pays for exact
+// products: four fp16 instructions of 16 cycles for one e4m3 of 32, and their
+// conversions: 384 us.
 // ---------------------------------------------------------------------------
 typedef int int8v __attribute__((ext_vector_type(8)));
 
@@ -556,10 +587,10 @@ void run_tile(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT, AHEAD>), grid, dim3(64 * WM * WN), 0, s, a);
 }
 
-template <int WAVES, int NT, int DEPTH>
+template <int WAVES, int NT>
 void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, 16 * NT), splits);
-  hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+  hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
 // The kernels of the product and a time model of each (us), fitted to 12200
@@ -583,9 +614,9 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 8, 1, 16, true, true, 3.907f, 0.663f, 0.471f, 6.085f, 1.221f, 0.857f, 0.586f, run_skinny<8, 1, 1>},
-    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
-    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
+    {16, 16, 8, 1, 16, true, true, 3.907f, 0.663f, 0.471f, 6.085f, 1.221f, 0.857f, 0.586f, run_skinny<8, 1>},
+    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2>},
+    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4>},
     // tiles on fp16 instructions: exact products for an fp32 y
     {128, 32, 1, 1, 256, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
      run_tile<true, 4, 1, 2, 2, 1>},
