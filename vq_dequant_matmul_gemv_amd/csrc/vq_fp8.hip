@@ -327,10 +327,10 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
 //   - one barrier a step, two buffers, pieces XORed so that reads of 8 rows
 //     touch all banks.
 // 2048 tokens x 17408 x 5120 in bf16: 189 to 200 us on different cards, 1.8 to
-// 1.9 PFLOP/s (10 us more with SwiGLU; the library's e4m3 product with one scale for each whole tensor takes 205
-// there); 4096 x 8192 x 8192: 246 us, 2.23 PFLOP/s.  An fp32 y pays for exact
-// products: four fp16 instructions of 16 cycles for one e4m3 of 32, and their
-// conversions: 384 us.
+// 1.9 PFLOP/s (10 us more with SwiGLU; the library's e4m3 product with one
+// scale for each whole tensor takes 205 there); 4096 x 8192 x 8192: 246 us,
+// 2.23 PFLOP/s.  An fp32 y pays for exact products: four fp16 instructions of
+// 16 cycles for one e4m3 of 32, and their conversions: 384 us.
 // ---------------------------------------------------------------------------
 typedef int int8v __attribute__((ext_vector_type(8)));
 
@@ -558,7 +558,14 @@ __global__ __launch_bounds__(256) void vq_fp8_join_kernel(Fp8Args a, int splits)
   if (i >= n) return;
   if (n % 4 == 0 && (!a.swiglu || a.rows % 2 == 0)) {
     float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(a.part + s * n + i);
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float4_t p[8];  // eight planes in flight
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        p[s] = *reinterpret_cast<const float4_t*>(a.part + min(s0 + s, splits - 1) * n + i);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) v += s0 + s < splits ? p[s] : float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     // pairs of rows never straddle a token: rows are even under SwiGLU
     if (a.swiglu) {
       store_out(a.y, i / 2, silu_mul<true>(v[0], v[1]), a.y_kind);

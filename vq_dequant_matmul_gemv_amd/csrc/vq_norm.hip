@@ -9,9 +9,15 @@
 // values a thread, a wave to 16 waves a row.  All arithmetic and both
 // sums of squares are fp32; v and h are rounded once, on their stores (h
 // comes from the unrounded v).
+//
+// Bound by its bytes: 4096 x 5120 in bf16, both norms, v and h stored, takes
+// 36 to 38 us = 4.4 to 4.7 TB/s, where a plain copy reaches 5.06; 333 x 2000 to
+// e4m3 5.3, one token of 5120 4.5, twice a launch.  A row a block, without a
+// loop over rows: persistent blocks with the next row in flight and the weights
+// held took 63 to 98, as the registers cost more rows in flight than that put
+// back.
 #include "vq_fp8_device.h"
 #include "vq_block_kernels.h"
-
 
 namespace vqmi {
 
