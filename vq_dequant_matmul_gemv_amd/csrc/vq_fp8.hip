@@ -313,10 +313,11 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
 // product, many tokens: WM x WN waves of 16*MT rows x 16*NT tokens a block
 //
 // The scales change with every 128 columns, so a product of 16 x 16 x 128 is
-// one instruction and four FMAs a lane scale it into the sums.  A large tile
-// is bound by what feeds the matrix units: of a 256 x 192 step's 1536 cycles
-// of e4m3 instructions at their peak, the LDS needs 1730 for its fragments,
-// and the FMAs and the next step's pieces share the rest of the issue slots.
+// one instruction and four FMAs a lane scale it into the sums.  Of a 256 x 192
+// step the e4m3 instructions are 1536 cycles at their peak, 1940 with the FMAs
+// and addresses; LDS is busy for 1400 (reads at 249 bytes a cycle, writes at
+// 80), and a block alone takes 2360.  With every compute unit busy the clock
+// falls to 1.85 GHz: what moves fewer bytes for a product gains twice.
 //   - 8 waves (two a SIMD: one's FMAs and LDS reads run under the other's
 //     products) take 212 us where 4 waves of 128 x 96 took 245;
 //   - operands are read two products ahead, sums scaled two products behind
