@@ -161,3 +161,49 @@ def test_empty_batch_and_other_stream_and_capture():
         torch.cuda.synchronize()
         ri, rw = binding.moe_route(r, buf)
         assert torch.equal(gi, ri) and torch.equal(gw, rw)
+
+
+# ---- keys close to each other, and sums that cancel ------------------------
+
+@pytest.mark.parametrize("E,k,T", [(64, 6, 33), (160, 16, 21), (256, 8, 40), (256, 32, 9), (512, 64, 5), (20, 20, 7)])
+@pytest.mark.parametrize("cluster", [2, 3, 9])
+def test_clusters_of_close_keys(E, k, T, cluster):
+    """Sigmoid scores plus a bias in clusters of neighbours far closer than an
+    fp32 score's error, exact ties among them: at the edge of the chosen and
+    inside, with clusters that fit the chosen and the next one and that do not."""
+    import torch
+    g = synth.rng("route-cluster", E, k, cluster)
+    n = -(-E // cluster)
+    x = np.repeat(g.normal(size=(T, n)), cluster, axis=1)[:, :E].astype(np.float32)
+    x = np.nextafter(x, np.where(g.random((T, E)) < 0.5, np.float32(9), np.float32(-9)).astype(np.float32))
+    b = np.zeros(E, dtype=np.float32)
+    b[g.random(E) < 0.1] = np.float32(2.0 ** -30)
+    order = g.permutation(E)
+    _check(torch.from_numpy(np.ascontiguousarray(x[:, order])), k, torch.from_numpy(b), score="sigmoid")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [10.0, 200.0, 1000.0, 3e6, 3e38])
+def test_group_sums_that_cancel(score, big):
+    """Two experts of a group with biases of nearly opposite size: the group's
+    sum is small, its keys' rounding errors are not."""
+    import torch
+    E, groups, T = 64, 16, 1200
+    g = synth.rng("route-cancel", score, str(big))
+    b = np.full(E, -big, dtype=np.float32)
+    b[0::4] = big
+    b[1::4] = -big
+    b[2::4] = -big * 1.5 if big < 1e38 else -big
+    x = torch.from_numpy((0.01 * g.normal(size=(T, E))).astype(np.float32))
+    _check(x, 5, torch.from_numpy(b), score=score, groups=groups, top_groups=5, group_score="top2")
+
+
+@pytest.mark.parametrize("T", [8191, 8192, 8195])
+@pytest.mark.parametrize("kw", [dict(), dict(score="sigmoid", groups=8, top_groups=3, group_score="top2")])
+def test_many_tokens(T, kw):
+    """Both sides of the token count at which a token takes fewer lanes."""
+    import torch
+    g = synth.rng("route-many", T)
+    x = _logits(T, 144, torch.bfloat16, ("many", T), masked=True)
+    b = torch.from_numpy((0.05 * g.normal(size=144)).astype(np.float32)) if kw else None
+    _check(x, 6, b, **kw)

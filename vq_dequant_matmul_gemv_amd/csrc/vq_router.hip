@@ -19,17 +19,20 @@
 //
 // Which keys are larger has to be right, not nearly right: logits are compared
 // as they are; scores (with a bias, or summed over a group's best two) are
-// formed in fp32 first, whose error is bounded, and where two that the choice
-// depends on lie closer than twice that bound the wave starts over with
-// scores in 64 bits (about 1 token in 1000 on random sigmoid scores with 256
-// experts, where scores in 64 bits throughout take 37 us).
+// formed in fp32 first, whose error is bounded.  Where two that the choice
+// depends on lie closer than twice that bound (about 1 token in 1000 on random
+// sigmoid scores with 256 experts), 64 bits decide: among the chosen and the
+// next one where that is all that is open, else over the whole token again.
+// (Scores in 64 bits throughout take 37 us where this takes 19.)
 //
-// 16384 tokens x 256 experts: 13.2 us (softmax, top 8), 24 us (sigmoid with a
-// bias, 4 of 8 groups by their two best, top 8); one token 4.6 us.  The bytes
+// 16384 tokens x 256 experts: 10.6 us (softmax, top 8), 19 us (sigmoid with a
+// bias, 4 of 8 groups by their two best, top 8); one token 4.7 us.  The bytes
 // would take 3.5: it is bound by the vector instructions of the choices, about
-// 60 for each of the top_k + 1, and ends with 5 us of the tokens done again.
-// Few lanes with several experts each share a choice's lane exchanges among
-// the wave's tokens: 33 us with a token a wave, 24 with two.
+// 60 for each of the top_k + 1.  Few lanes with several experts each share a
+// choice's lane exchanges among the wave's tokens: 33 us with a token a wave,
+// 24 with two, 19 with four and the close ones put in order by one exponential
+// a lane (5 us less than a token's full 64-bit pass, which the last wave of a
+// launch used to end with: 2048 grouped tokens 10 to 12 -> 7.8).
 #include "vq_device.h"
 #include "vq_block_kernels.h"
 
@@ -349,13 +352,15 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
       inv_z = z > 0.0f ? 1.0f / z : 0.0f;
     }
   }
-  // Keys in fp32.  Scores are off by less than 2^-22 (sigmoid: the argument's
-  // rounding |l| e^-|l| 1.5 * 2^-24, the exponential's and the reciprocal's
-  // unit) or 2^-18 (softmax: the same and a sum of at most 1024 terms), and a
-  // sum with a bias or a second score by half a unit more.
-  const float slack = sigmoid ? 0x1p-21f : 0x1p-17f;
-  auto margin = [&](float v) { return fmaf(fabsf(v), 0x1p-21f, slack); };
-  bool close = false;
+  // Keys in fp32.  A sigmoid is off by less than 2^-22: s (1 - s) times the
+  // exponential's relative error of 1.22 |l| 2^-24 (argument) and 2^-23 makes
+  // 0.77 * 2^-24, the sum below the reciprocal 2^-24, the reciprocal 2^-23.  A
+  // softmax (the same and a sum of at most 1024 terms) is off by less than
+  // 2^-18.  The sum with a bias adds 2^-24 of itself, so two keys near v are
+  // certainly in order when they differ by more than margin(v).
+  const float slack = sigmoid ? 0x1p-21f : 0x1p-17f;  // twice a score's error
+  auto margin = [&](float v) { return fmaf(fabsf(v), 0x1.2p-23f, slack); };
+  bool close = false;  // the whole token again in 64 bits
   float p[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) p[i] = l[i];
@@ -423,10 +428,18 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
       for (int h = 0; h < a.groups; ++h) against(h);
     }
     const bool stays = s > -INFINITY && rank < a.top_groups;
-    if (need_p) {  // the worst group that stays against the best that does not
+    if (need_p) {
+      // the worst group that stays against the best that does not; a group's
+      // sum is off by its two keys' errors (they may cancel) and its own
       const float in = order_value(lanes_min<LPT>(stays ? order_key(s) : order_key(INFINITY)));
       const float out = order_value(lanes_max<LPT>(stays ? order_key(-INFINITY) : order_key(s)));
-      close = in < INFINITY && in - out <= 2.0f * margin(in);
+      if (a.top2) {
+        const float both = s > -INFINITY ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
+        const float mag = __uint_as_float(lanes_max<LPT>(__float_as_uint(both)));
+        close = in - out <= fmaf(mag, 0x1.2p-22f, 2.0f * slack) || !(mag < 0x1p126f);
+      } else {
+        close = in < INFINITY && in - out <= margin(in);
+      }
     }
     keep = __ballot(stays) >> first;
   }
@@ -446,9 +459,10 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
       left = left == 0 ? a.group_size : left;
     }
   }
-  int my_id = -1;
-  float last = INFINITY;
-  const int rounds = a.bias ? a.top_k + 1 : a.top_k;  // with a bias also the best one left out
+  int my_id = -1;  // with a bias also the best one left out, in lane top_k
+  float last = INFINITY, last2 = INFINITY;
+  bool mixed = false;  // two neighbours among them are close
+  const int rounds = a.bias ? a.top_k + 1 : a.top_k;
   for (int j = 0; j < rounds; ++j) {
     uint32_t best = key[0];
 #pragma unroll
@@ -462,20 +476,49 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
     for (int i = 0; i < PL; ++i) key[i] = (uint32_t)(e0 + i) == id ? 0u : key[i];
     if (a.bias && top != 0u) {
       const float v = order_value(top);
-      close = close || last - v <= margin(v);
+      mixed = mixed || last - v <= margin(v);
+      last2 = last;
       last = v;
     }
-    if (lane == j && j < a.top_k && top != 0u) my_id = (int)id;
+    if (lane == j && top != 0u) my_id = (int)id;
   }
-  const uint64_t near = __ballot(close);
-  const bool again = (near >> first & (LPT == 64 ? ~0ull : (1ull << (LPT & 63)) - 1)) != 0;
+  // Where the last one in is clear of the second one left out, the chosen are
+  // among those found: 64 bits put them in order, one a lane.
+  const bool sort = a.bias && sigmoid && a.top_k < LPT;
+  if (!sort) close = close || mixed;
+  if (__builtin_expect(__ballot(mixed && !close) != 0ull, 0)) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < PL; ++i) best = max(best, key[i]);
+    const uint32_t top = lanes_max<LPT>(best);
+    const float v = order_value(top);
+    close = close || (mixed && top != 0u && last2 - v <= margin(v));
+    const float lc = my_id >= 0 ? logit_at<DT>(a.logits, t * E + my_id) : 0.0f;
+    const double pc = my_id >= 0 ? 1.0 / (1.0 + exp(-(double)in_play(lc, 0.0f))) + (double)a.bias[my_id] : -INFINITY;
+    int rank = 0;
+    for (int j = 0; j <= a.top_k; ++j) {
+      const double po = __shfl(pc, first + j, 64);
+      const int io = __shfl(my_id, first + j, 64);
+      rank += io >= 0 && (po > pc || (po == pc && io < my_id)) ? 1 : 0;
+    }
+    int* order = reinterpret_cast<int*>(lds[wave]) + first;
+    order[lane] = -1;
+    wave_lds_fence();
+    if (my_id >= 0) order[rank] = my_id;  // rank <= top_k < LPT
+    wave_lds_fence();
+    if (mixed) my_id = order[lane];
+    wave_lds_fence();
+  }
+  if (lane >= a.top_k) my_id = -1;
+  constexpr uint64_t kTokenLanes = LPT == 64 ? ~0ull : (1ull << (LPT & 63)) - 1;
+  const uint64_t again = __ballot(close);
   const float my_l = my_id >= 0 ? in_play(logit_at<DT>(a.logits, t * E + my_id), 0.0f) : -INFINITY;
-  store_slot<LPT>(a, t, lane, my_id, my_l, m, inv_z, t_mine < a.T && !again);
-  if (near != 0ull) {
+  store_slot<LPT>(a, t, lane, my_id, my_l, m, inv_z, t_mine < a.T && (again >> first & kTokenLanes) == 0);
+  if (__builtin_expect(again != 0ull, 0)) {
 #pragma unroll 1
     for (int k = 0; k < kTokens; ++k) {
-      const uint64_t mine = near >> (k * LPT) & (LPT == 64 ? ~0ull : (1ull << (LPT & 63)) - 1);
-      if (mine != 0ull && t0 + k < a.T) route_token64<(LPT * PL + 63) / 64, DT>(a, lds[wave], t0 + k, lane64);
+      if ((again >> (k * LPT) & kTokenLanes) != 0 && t0 + k < a.T)
+        route_token64<(LPT * PL + 63) / 64, DT>(a, lds[wave], t0 + k, lane64);
     }
   }
 }
@@ -495,8 +538,8 @@ hipError_t run_lanes(const RouterArgs& a, int pl, int dtype, hipStream_t s) {
   if (pl <= 1) return run_router<LPT, 1>(a, dtype, s);
   if (pl <= 2) return run_router<LPT, 2>(a, dtype, s);
   if (pl <= 4) return run_router<LPT, 4>(a, dtype, s);
-  if (pl <= 8 || LPT < 64) return run_router<LPT, 8>(a, dtype, s);
-  return run_router<64, 16>(a, dtype, s);
+  if (pl <= 8 || LPT == 32) return run_router<LPT, 8>(a, dtype, s);
+  return run_router<LPT == 32 ? 64 : LPT, 16>(a, dtype, s);
 }
 
 }  // namespace
@@ -520,10 +563,16 @@ hipError_t launch_router(const RouterSpec& r, const void* logits, int T, int32_t
   while (a.groups_pow2 < r.groups) a.groups_pow2 <<= 1;
   a.renorm = r.renorm;
   a.scale = r.scale;
-  // lanes of a token: up to 8 experts a lane (16 above 512 experts), a lane at
-  // least for every group and every slot
+  // Lanes of a token: up to 8 experts a lane (16 above 512 experts), a lane at
+  // least for every group and every slot (and the first one left out).  From
+  // 8192 tokens on, where four a wave still fill the card, 129 to 256 experts
+  // take 16 lanes of 16 (us, 32 lanes of 8 -> 16 of 16): softmax 12.0 -> 10.1
+  // at 16384 tokens, 7.3 -> 6.6 at 8192, 5.6 -> 5.8 at 4096, 4.4 -> 5.3 at one;
+  // grouped sigmoid 23.6 -> 21.8, 15.7 -> 15.8, 12.8 -> 12.3 and 6.2 -> 7.7.
+  const int slots = r.top_k + (r.bias ? 1 : 0);
   int lpt = 16;
-  while (lpt < 64 && (lpt * 8 < r.num_experts || lpt < r.groups || lpt < r.top_k)) lpt <<= 1;
+  while (lpt < 64 && (lpt * (lpt == 16 && T >= 8192 ? 16 : 8) < r.num_experts || lpt < r.groups || lpt < slots))
+    lpt <<= 1;
   int pl = 1;
   while (pl * lpt < r.num_experts) pl <<= 1;
   const int piece = pl * (r.logits_kind == kOutF32 ? 4 : 2), align = piece < 16 ? piece : 16;
