@@ -385,7 +385,7 @@ vq_status vq_encode(const float *w, int32_t rows, int32_t cols, int32_t d, int32
  * or above top_groups * num_experts / groups; groups outside [1, 64] or not a
  * divisor of num_experts; top_groups outside [1, groups]; an unknown score,
  * group_score or logits_dtype; renormalize not 0 or 1; a scale that is not
- * finite; reserved not 0; T * num_experts above 2^40 or T above 2^30.
+ * finite; reserved not 0; T above 2^25.
  */
 typedef enum { VQ_SCORE_SOFTMAX = 0, VQ_SCORE_SIGMOID = 1 } vq_score;
 typedef enum { VQ_GROUP_MAX = 0, VQ_GROUP_TOP2 = 1 } vq_group_score;
@@ -440,7 +440,7 @@ typedef struct vq_fp8_tensor {
  *   x: device [T][cols] of x_dtype (F16 or BF16), 16-byte aligned;
  *   q: device [T][cols] e4m3, 16-byte aligned; scales: device
  *   [T][ceil(cols/128)] fp32, 4-byte aligned.  cols as for vq_fp8_tensor;
- *   T >= 0 (0 enqueues nothing), T * ceil(cols/128) < 2^31.
+ *   T >= 0 (0 enqueues nothing), T * ceil(cols/128) < 2^28.
  */
 vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t *q, float *scales,
                        void *stream);
@@ -499,8 +499,8 @@ vq_status vq_fp8_gemm(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x,
  *             h_scales [T][ceil(cols/128)] fp32); NULL: not computed.  Not
  *             both outputs NULL.  No other buffers may overlap.
  * Pointers of [T][cols] and [cols] data 16-byte aligned, the others to their
- * element.  T >= 0 (0 enqueues nothing), T <= 2^30.  One launch, no workspace;
- * the same inputs give the same bits.
+ * element.  T >= 0 (0 enqueues nothing), T * ceil(cols/512) < 2^26.  One
+ * launch, no workspace; the same inputs give the same bits.
  * Errors (VQ_ERR_SHAPE): cols outside [1, 32768], or not a multiple of 16 for
  * an E4M3 h; an unknown dtype, gate or gate_act; a gate_act without a gate; a
  * post norm or gate without a block; eps negative or not finite; alpha, beta

@@ -256,3 +256,15 @@ def test_packed_descriptors_have_the_structures_layout(b):
     assert bytes(io) == b._pack_io(3, 2, 1, 0, 0)
     n = b.CNormSpec(64, 0, 1, 2, 3, 1, 2, 0, 0.5, 0.25, 1e-6, 1.0, 0x10, 0x20, 0x30)
     assert bytes(n) == b._pack_norm(64, 0, 1, 2, 3, 1, 2, 0, 0.5, 0.25, 1e-6, 1.0, 0x10, 0x20, 0x30)
+
+
+# ---- launches of 2^32 threads and more are refused -------------------------
+
+def test_calls_too_large_for_a_launch_are_refused(b):
+    assert _route(b, T=(1 << 25) + 1) == "VQ_ERR_SHAPE"
+    assert _status(b, b.LIB.vq_fp8_quant(0x10000, 1, 1 << 28, 128, 0x20000, 0x30000, None)) == "VQ_ERR_SHAPE"
+    assert _status(b, b.LIB.vq_fp8_quant(0x10000, 1, 1 << 27, 256, 0x20000, 0x30000, None)) == "VQ_ERR_SHAPE"
+    for T, cols in [(1 << 26, 8), (1 << 25, 513), (1 << 20, 32768)]:
+        spec = b.CNormSpec(cols=cols, block_dtype=0, residual_dtype=0, weight_dtype=0, h_dtype=0, gate=0, gate_act=0,
+                           reserved=0, alpha=1.0, beta=1.0, eps=1e-6, weight_offset=0.0)
+        assert _status(b, b.LIB.vq_norm(ctypes.byref(spec), 0x10000, 0, T, 0, 0x20000, None, None)) == "VQ_ERR_SHAPE"

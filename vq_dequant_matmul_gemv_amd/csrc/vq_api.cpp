@@ -433,8 +433,8 @@ vq_status vq_moe_route(const vq_router* r, const void* logits, int32_t T, int32_
     return fail(VQ_ERR_SHAPE, "vq_moe_route: renormalize=%d must be 0 or 1", r->renormalize);
   if (!std::isfinite(r->scale)) return fail(VQ_ERR_SHAPE, "vq_moe_route: scale is not finite");
   if (r->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_moe_route: reserved must be 0");
-  if (T < 0 || T > (1 << 30) || (int64_t)T * E > ((int64_t)1 << 40))
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: T=%d out of range", T);
+  // (a launch holds fewer than 2^32 threads, here and below)
+  if (T < 0 || T > (1 << 25)) return fail(VQ_ERR_SHAPE, "vq_moe_route: T=%d outside [0, 2^25]", T);
   if (T == 0) return VQ_OK;
   if (!logits || !expert_ids || !route_weights)
     return fail(VQ_ERR_NULL, "vq_moe_route: a required pointer is NULL (logits=%p expert_ids=%p route_weights=%p)",
@@ -468,7 +468,7 @@ vq_status vq_fp8_quant(const void* x, int32_t x_dtype, int32_t T, int32_t cols, 
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: x_dtype=%d: x must be VQ_DTYPE_F16 or VQ_DTYPE_BF16", x_dtype);
   if (!fp8_cols_ok(cols))
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: cols=%d must be a multiple of 16 in [16, 2^20]", cols);
-  if (T < 0 || (int64_t)T * ((cols + 127) / 128) >= (int64_t)1 << 31)
+  if (T < 0 || (int64_t)T * ((cols + 127) / 128) >= (int64_t)1 << 28)
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: T=%d out of range for cols=%d", T, cols);
   if (T == 0) return VQ_OK;
   vq_status st = check_xy(x, q, "q");
@@ -567,7 +567,8 @@ vq_status vq_norm(const vq_norm_spec* n, const void* block, const void* residual
   if (!std::isfinite(n->alpha) || !std::isfinite(n->beta) || !std::isfinite(n->weight_offset))
     return fail(VQ_ERR_SHAPE, "vq_norm: alpha, beta and weight_offset must be finite");
   if (n->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_norm: reserved must be 0");
-  if (T < 0 || T > (1 << 30)) return fail(VQ_ERR_SHAPE, "vq_norm: T=%d outside [0, 2^30]", T);
+  if (T < 0 || (int64_t)T * ((n->cols + 511) / 512) >= (int64_t)1 << 26)
+    return fail(VQ_ERR_SHAPE, "vq_norm: T=%d out of range for cols=%d", T, n->cols);
   if (T == 0) return VQ_OK;
   if (!block && !residual) return fail(VQ_ERR_NULL, "vq_norm: block and residual are both NULL");
   if (!residual_out && !h) return fail(VQ_ERR_NULL, "vq_norm: residual_out and h are both NULL");

@@ -681,6 +681,8 @@ Fp8Plan make_plan(int rows, int cols, int T, bool exact) {
   for (int i = 0; i < kNumFp8Kernels; ++i) {
     const Fp8Kernel& k = kFp8Kernels[i];
     if (T < k.min_T || T > k.max_T || !(exact ? k.f32 : k.f16)) continue;
+    // a launch holds fewer than 2^32 threads, a block up to 512
+    if ((int64_t)ceil_div(rows, k.rows) * ceil_div(T, k.tokens) >= 1 << 22) continue;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
       Fp8Plan p;
       p.rows = rows, p.cols = cols, p.T = T, p.exact = exact, p.kernel = i;
