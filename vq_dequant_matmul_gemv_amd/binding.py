@@ -469,19 +469,39 @@ _pack_io = struct.Struct("<4iQ").pack
 _pack_norm = struct.Struct("<8i4f3Q").pack
 
 
-def _placed(t, device):
-    """The tensor is contiguous on `device`."""
-    if t.device != device:
-        raise ValueError(f"tensor on {t.device}, expected {device} (the GPU of the other tensors)")
+def _placed(t, index):
+    """The tensor is contiguous on GPU `index`."""
+    if t.get_device() != index:
+        raise ValueError(f"tensor on {t.device}, expected cuda:{index} (the GPU of the other tensors)")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
+
+
+def _gpu(t):
+    """Index of the GPU the tensor is on; it is contiguous there."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must live on the GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return index
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(T, cols, dtype, device):
+    """An uninitialised [T][cols] (empty_strided takes a quarter less time than
+    empty, which parses its sizes)."""
+    return _TORCH.empty_strided((T, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _elsewhere(device, stream):
     """The context a call has to enter first: the given stream's, or that of
     tensors on another GPU than the current one.  None where the current
     device and stream are the ones to use."""
-    torch = _torch()
+    torch = _TORCH
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream on {stream.device}, tensors on {device}")
@@ -489,9 +509,9 @@ def _elsewhere(device, stream):
     return torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else None
 
 
-def _raw_stream(device) -> int:
-    """Handle of the device's current stream."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+def _raw_stream(index) -> int:
+    """Handle of the GPU's current stream."""
+    return _TORCH._C._cuda_getCurrentRawStream(index)
 
 
 @dataclass
@@ -523,32 +543,32 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
     if len(shape) != 2 or shape[1] != r.num_experts:
         raise ValueError(f"logits must be [T][{r.num_experts}]")
     T, k = shape[0], r.top_k
-    _dev_check(logits)
+    gpu = _gpu(logits)
     dev = logits.device
     bias = 0
     if r.bias is not None:
         if r.bias.dtype != torch.float32 or r.bias.shape != (r.num_experts,):
             raise ValueError(f"bias must be fp32 [{r.num_experts}]")
-        _placed(r.bias, dev)
+        _placed(r.bias, gpu)
         bias = r.bias.data_ptr()
     if ids is not None:
         _check_out(ids, torch.int32, (T, k), "ids")
-        _placed(ids, dev)
+        _placed(ids, gpu)
     if weights is not None:
         _check_out(weights, torch.float32, (T, k), "weights")
-        _placed(weights, dev)
+        _placed(weights, gpu)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
             return moe_route(router, logits, ids, weights)
     if ids is None:
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        ids = _rows(T, max(k, 0), torch.int32, dev)
     if weights is None:
-        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        weights = _rows(T, max(k, 0), torch.float32, dev)
     cr = _pack_router(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
                       GROUP_SCORES[r.group_score], bool(r.renormalize), r.scale, 0, bias)
     check(LIB.vq_moe_route(cr, logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
-                           _raw_stream(dev)))
+                           _raw_stream(gpu)))
     return ids, weights
 
 
@@ -592,25 +612,25 @@ def fp8_quant(x, q=None, scales=None, stream=None):
     if x.dtype not in (torch.float16, torch.bfloat16) or x.dim() != 2:
         raise ValueError("x must be fp16 or bf16 [T][cols]")
     T, cols = x.shape
-    _dev_check(x)
+    gpu = _gpu(x)
     dev = x.device
     sshape = (T, _blocks(cols))
     if q is not None:
         _check_out(q, torch.float8_e4m3fn, (T, cols), "q")
-        _placed(q, dev)
+        _placed(q, gpu)
     if scales is not None:
         _check_out(scales, torch.float32, sshape, "scales")
-        _placed(scales, dev)
+        _placed(scales, gpu)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
             return fp8_quant(x, q, scales)
     if q is None:
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        q = _rows(T, cols, torch.float8_e4m3fn, dev)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+        scales = _rows(*sshape, torch.float32, dev)
     check(LIB.vq_fp8_quant(x.data_ptr(), _dtype_code(x.dtype), T, cols, q.data_ptr(), scales.data_ptr(),
-                           _raw_stream(dev)))
+                           _raw_stream(gpu)))
     return q, scales
 
 
@@ -633,21 +653,21 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
         raise ValueError("epilogue must be None or 'swiglu'")
     y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
     yshape = (T, rows // 2 if epilogue == "swiglu" else rows)
-    _dev_check(v)
+    gpu = _gpu(v)
     dev = v.device
     for t in (ws, x, x_scales):
-        _placed(t, dev)
+        _placed(t, gpu)
     if y is not None:
         _check_out(y, y_dtype, yshape)
-        _placed(y, dev)
+        _placed(y, gpu)
     if workspace is not None:
-        _placed(workspace, dev)
+        _placed(workspace, gpu)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
             return fp8_gemm(w, x, x_scales, y, workspace, None, y_dtype, epilogue)
     if y is None:
-        y = torch.empty(yshape, dtype=y_dtype, device=dev)
+        y = _rows(*yshape, y_dtype, dev)
     if workspace is None:
         need = LIB.vq_fp8_workspace_bytes(rows, cols, T)
         if need:
@@ -656,7 +676,7 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
                                                         workspace.numel() * workspace.element_size())
     check(LIB.vq_fp8_gemm(_pack_fp8(v.data_ptr(), ws.data_ptr(), rows, cols, rows * cols, ws.numel()),
                           _pack_io(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, 0), x.data_ptr(),
-                          x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(dev)))
+                          x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(gpu)))
     return y
 
 
@@ -698,27 +718,27 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
     e4m3 = h_dtype == torch.float8_e4m3fn
     if h_dtype is None and not store_residual:
         raise ValueError("norm has nothing to compute: neither v nor h is wanted")
-    _dev_check(first)
+    gpu = _gpu(first)
     if block is not None and residual is not None:
-        _placed(residual, dev)
+        _placed(residual, gpu)
         if residual.shape != shape:
             raise ValueError("block and residual must have the same shape [T][cols]")
     post = pre = gates = kind = 0
     w_dtype = None
     if post_weight is not None:
-        _placed(post_weight, dev)
+        _placed(post_weight, gpu)
         if post_weight.shape != (cols,):
             raise ValueError(f"post_weight must be [{cols}]")
         w_dtype, post = post_weight.dtype, post_weight.data_ptr()
     if pre_weight is not None:
-        _placed(pre_weight, dev)
+        _placed(pre_weight, gpu)
         if pre_weight.shape != (cols,):
             raise ValueError(f"pre_weight must be [{cols}]")
         if w_dtype is not None and pre_weight.dtype != w_dtype:
             raise ValueError("post_weight, pre_weight and gate must have one dtype")
         w_dtype, pre = pre_weight.dtype, pre_weight.data_ptr()
     if gate is not None:
-        _placed(gate, dev)
+        _placed(gate, gpu)
         if w_dtype is not None and gate.dtype != w_dtype:
             raise ValueError("post_weight, pre_weight and gate must have one dtype")
         kind = (VQ_GATE_FULL if gate.shape == shape else VQ_GATE_CHANNEL if gate.shape == (cols,) else
@@ -730,13 +750,13 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
         raise ValueError(f"gate_act must be None or one of {sorted(k for k in GATE_ACTS if k)}")
     if residual_out is not None:
         _check_out(residual_out, v_dtype, shape, "residual_out")
-        _placed(residual_out, dev)
+        _placed(residual_out, gpu)
     if h is not None:
         _check_out(h, h_dtype, shape, "h")
-        _placed(h, dev)
+        _placed(h, gpu)
     if h_scales is not None:
         _check_out(h_scales, torch.float32, (T, _blocks(cols)), "h_scales")
-        _placed(h_scales, dev)
+        _placed(h_scales, gpu)
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
@@ -745,14 +765,14 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
                         h_dtype=h_dtype, residual_out=residual_out, h=h, h_scales=h_scales,
                         store_residual=store_residual)
     if residual_out is None and store_residual:
-        residual_out = torch.empty_like(first, dtype=v_dtype)
+        residual_out = _rows(T, cols, v_dtype, dev)
     if h is None and h_dtype is not None:
-        h = torch.empty_like(first, dtype=h_dtype)
+        h = _rows(T, cols, h_dtype, dev)
     if h_scales is None and e4m3:
-        h_scales = torch.empty((T, _blocks(cols)), dtype=torch.float32, device=dev)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        h_scales = _rows(T, _blocks(cols), torch.float32, dev)
     spec = _pack_norm(cols, _dtype_code(first.dtype), _dtype_code(v_dtype), _dtype_code(w_dtype or torch.float32),
                       VQ_DTYPE_E4M3 if e4m3 else _dtype_code(h_dtype or torch.float32), kind,
                       GATE_ACTS[gate_act] if kind else VQ_ACT_NONE, 0, alpha, beta, eps, weight_offset, post, pre, gates)
-    check(LIB.vq_norm(spec, ptr(block), ptr(residual), T, ptr(residual_out), ptr(h), ptr(h_scales), _raw_stream(dev)))
+    check(LIB.vq_norm(spec, _address(block), _address(residual), T, _address(residual_out), _address(h),
+                      _address(h_scales), _raw_stream(gpu)))
     return residual_out, h, h_scales
