@@ -207,3 +207,14 @@ def test_many_tokens(T, kw):
     x = _logits(T, 144, torch.bfloat16, ("many", T), masked=True)
     b = torch.from_numpy((0.05 * g.normal(size=144)).astype(np.float32)) if kw else None
     _check(x, 6, b, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("score,bias", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+def test_many_tokens_with_groups_of_whole_lanes(dtype, score, bias):
+    import torch
+    g = synth.rng("route-many-whole", dtype)
+    x = _logits(8209, 256, _dt(dtype), ("many-whole", dtype), masked=True)
+    b = torch.from_numpy((0.05 * g.normal(size=256)).astype(np.float32)) if bias else None
+    _check(x, 8, b, score=score, groups=8, top_groups=4, group_score="top2", scale=2.5)
+    _check(x, 16, b, score=score, groups=16, top_groups=5, renormalize=False)

@@ -74,10 +74,11 @@ __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, ui
 //
 // Bound by the weights' bytes.  Blocks of 16 rows are enough of them to fill
 // the card at 5120 rows already, and eight waves a block keep 8 KiB of a row
-// tile in flight.  One token, 17408 x 5120: 22 us = 4.1 TB/s (19.1 in a
-// plain stream of calls); 16 tokens, 5120 x 17408: 26 (22.3).  Five column
-// blocks in flight a wave, 16 waves a block and columns that start elsewhere in
-// every block took as long.
+// tile in flight.  One token, 17408 x 5120: 22 to 23 us = 3.9 TB/s (19.3 in a
+// plain stream of calls on the same weights).  Five column blocks in flight a
+// wave, 16 waves a block and columns that start elsewhere in every block took
+// as long.  From a few tokens on a 128 x 32 tile with the columns split may be
+// faster (16 tokens, 5120 x 17408: 24.4 against 31).
 // ---------------------------------------------------------------------------
 struct Fp8Args {
   const uint8_t* w;

@@ -25,8 +25,9 @@
 // next one where that is all that is open, else over the whole token again.
 // (Scores in 64 bits throughout take 37 us where this takes 19.)
 //
-// 16384 tokens x 256 experts: 10.6 us (softmax, top 8), 19 us (sigmoid with a
-// bias, 4 of 8 groups by their two best, top 8); one token 4.7 us.  The bytes
+// 16384 tokens x 256 experts: 10.6 us (softmax, top 8, bf16; 11.8 in fp32), 19
+// to 20 us (sigmoid with a bias, 4 of 8 groups by their two best, top 8, fp32);
+// one token 4.7 us.  The bytes
 // would take 3.5: it is bound by the vector instructions of the choices, about
 // 60 for each of the top_k + 1.  Few lanes with several experts each share a
 // choice's lane exchanges among the wave's tokens: 33 us with a token a wave,

@@ -140,7 +140,8 @@ def main():
     ap.add_argument("--copy", action="store_true", help="also list torch's copy kernel")
     a = ap.parse_args()
     lines = [f"command: {a.cmd}", f"kernel source digest: {source_digest()}",
-             f"encoder source digest: {source_digest('encoder')}", ""]
+             f"encoder source digest: {source_digest('encoder')}",
+             f"block operators' source digest: {source_digest('block')}", ""]
     lines += trace(a.dir, a.copy) if a.mode == "trace" else pmc(a.dir, a.copy)
     print("\n".join(lines))
 
