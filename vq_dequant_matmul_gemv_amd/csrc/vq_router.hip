@@ -25,8 +25,8 @@
 // next one where that is all that is open, else over the whole token again.
 // (Scores in 64 bits throughout take 37 us where this takes 19.)
 //
-// 16384 tokens x 256 experts: 10.6 us (softmax, top 8, bf16; 11.8 in fp32), 19
-// to 20 us (sigmoid with a bias, 4 of 8 groups by their two best, top 8, fp32);
+// 16384 tokens x 256 experts: 10.4 us (softmax, top 8, bf16; 11.6 in fp32), 18
+// to 19 us (sigmoid with a bias, 4 of 8 groups by their two best, top 8, fp32);
 // one token 4.7 us.  The bytes
 // would take 3.5: it is bound by the vector instructions of the choices, about
 // 60 for each of the top_k + 1.  Few lanes with several experts each share a
@@ -379,7 +379,9 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
     }
   }
   uint64_t keep = ~0ull;
+  bool stays = true;
   const int lpg = LPT / a.groups_pow2;  // lanes that share a group's score
+  const bool whole = a.group_size == lpg * PL;  // a group is whole lanes
   if (a.groups > 1) {
     const int g = lane / lpg;
     float m1 = -INFINITY, m2 = -INFINITY;
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
       m2 = fmaxf(m2, fminf(m1, v));
       m1 = fmaxf(m1, v);
     };
-    if (a.group_size == lpg * PL) {  // a group is whole lanes
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < PL; ++i) add(p[i]);
     } else {
@@ -428,7 +430,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
     } else {
       for (int h = 0; h < a.groups; ++h) against(h);
     }
-    const bool stays = s > -INFINITY && rank < a.top_groups;
+    stays = s > -INFINITY && rank < a.top_groups;
     if (need_p) {
       // the worst group that stays against the best that does not; a group's
       // sum is off by its two keys' errors (they may cancel) and its own
@@ -450,7 +452,10 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
     const float v = a.bias ? p[i] : l[i];
     key[i] = l[i] > -INFINITY ? order_key(v) : 0u;
   }
-  if (a.groups > 1) {
+  if (a.groups > 1 && whole) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) key[i] = stays ? key[i] : 0u;
+  } else if (a.groups > 1) {
     int ge = e0 / a.group_size, left = (ge + 1) * a.group_size - e0;  // e0's group, experts left in it
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
