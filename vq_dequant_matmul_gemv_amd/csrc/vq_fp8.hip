@@ -73,12 +73,14 @@ __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, ui
 // waves split the blocks of 128 columns and join their sums in LDS
 //
 // Bound by the weights' bytes.  Blocks of 16 rows are enough of them to fill
-// the card at 5120 rows already, and eight waves a block keep 8 KiB of a row
-// tile in flight.  One token, 17408 x 5120: 22 to 23 us = 3.9 TB/s (19.3 in a
-// plain stream of calls on the same weights).  Five column blocks in flight a
-// wave, 16 waves a block and columns that start elsewhere in every block took
-// as long.  From a few tokens on a 128 x 32 tile with the columns split may be
-// faster (16 tokens, 5120 x 17408: 24.4 against 31).
+// the card at 5120 rows already.  Up to 16 tokens four waves a block with two
+// column blocks in flight each (64 registers: every block of 17408 rows is on
+// the card at once), else eight waves with one.  One token, 17408 x 5120: 22 us
+// = 4.1 TB/s (19 in a plain stream of calls on the same weights), 34816 x 5120:
+// 37.  Eight waves took 22.5 and 39, five column blocks in flight 24, and 16
+// waves a block or columns that start elsewhere in every block were no faster.
+// From a few tokens on a 128 x 32 tile with the columns split may be faster (16
+// tokens, 5120 x 17408: 24.4 against 31).
 // ---------------------------------------------------------------------------
 struct Fp8Args {
   const uint8_t* w;
@@ -233,12 +235,12 @@ __device__ __forceinline__ float4_t dot128_f16(const Frag& a, const Frag& b) {
 }
 
 // NT x 16 tokens a block; a wave takes every WAVES-th block of 128 columns and
-// has the next one in flight.  The products of the scales of a chunk of
+// has DEPTH of them in flight.  The products of the scales of a chunk of
 // kChunk column blocks are set up in LDS first, so the loop waits for
 // nothing but its operands.
 constexpr int kScaleSteps = 256;
 
-template <int WAVES, int NT>
+template <int WAVES, int NT, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args) {
   const Fp8Args a = split_args(args);
   constexpr int kThreads = 64 * WAVES, kTok = 16 * NT;
@@ -258,12 +260,12 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
   float4_t acc[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  Frag aw, bx[NT];
-  auto load = [&](int k) {  // steps past the end: zeros
+  Frag aw[DEPTH], bx[DEPTH][NT];
+  auto load = [&](int j, int k) {  // steps past the end: zeros
     const uint32_t c = k * kFp8Block + (lane >> 4) * 16;
-    aw = load_frag(wr, r * cols, c, cols);
+    aw[j] = load_frag(wr, r * cols, c, cols);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) bx[n] = load_frag(xr, (16 * n + r) * cols, c, cols);
+    for (int n = 0; n < NT; ++n) bx[j][n] = load_frag(xr, (16 * n + r) * cols, c, cols);
   };
   const int k_first = blockIdx.y * a.split_steps, k_end = min(kb, k_first + a.split_steps);
   for (int k0 = k_first; k0 < k_end; k0 += kChunk) {
@@ -280,22 +282,28 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
       sx[i] = __uint_as_float(buf_load_b32(sr, ok | (uint32_t)(t * kb + k0 + k) * 4));
       sw[i] = __uint_as_float(buf_load_b32(wsr, ok | (uint32_t)(k0 + k) * 4));
     }
-    load(wave < steps ? k0 + wave : kb);
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) load(j, wave + j * WAVES < steps ? k0 + wave + j * WAVES : kb);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = threadIdx.x + i * kThreads;
       f[e % kChunk][e / kChunk] = sx[i] * sw[i];
     }
     lds_barrier();
-    for (int k = wave; k < steps; k += WAVES) {
+    for (int k = wave; k < steps; k += DEPTH * WAVES) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4_t p = dot128_f16(aw, bx[n]);
-        const float s = f[k][16 * n + r];
+      for (int j = 0; j < DEPTH; ++j) {
+        // no branches: the loads in flight are counted through the loop
+        const int kj = k + j * WAVES, next = kj + DEPTH * WAVES;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, p[i], acc[n][i]);
+        for (int n = 0; n < NT; ++n) {
+          const float4_t p = dot128_f16(aw[j], bx[j][n]);
+          const float s = DEPTH == 1 || kj < steps ? f[min(kj, kChunk - 1)][16 * n + r] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s, p[i], acc[n][i]);
+        }
+        load(j, next < steps ? k0 + next : kb);
       }
-      load(k + WAVES < steps ? k0 + k + WAVES : kb);
     }
   }
 #pragma unroll
@@ -596,13 +604,13 @@ void run_tile(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_tile_kernel<EXACT, WM, WN, MT, NT, AHEAD>), grid, dim3(64 * WM * WN), 0, s, a);
 }
 
-template <int WAVES, int NT>
+template <int WAVES, int NT, int DEPTH>
 void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, 16 * NT), splits);
-  hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT>), grid, dim3(64 * WAVES), 0, s, a);
+  hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 12200
+// The kernels of the product and a time model of each (us), fitted to 13600
 // measured calls (1 to 4096 tokens, 64 to 34816 rows, 256 to 17408 columns, 1
 // to 24 splits), the faster ones of a shape weighing more; the fit's error is
 // 8-12 % rms, and the model's choice takes 1.9 % longer than the best one on
@@ -623,9 +631,9 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 8, 1, 16, true, true, 3.907f, 0.663f, 0.471f, 6.085f, 1.221f, 0.857f, 0.586f, run_skinny<8, 1>},
-    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2>},
-    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4>},
+    {16, 16, 4, 1, 16, true, true, 3.878f, 0.332f, 0.227f, 6.215f, 0.479f, 0.648f, 0.661f, run_skinny<4, 1, 2>},
+    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
+    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
     {128, 32, 1, 1, 256, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
      run_tile<true, 4, 1, 2, 2, 1>},
