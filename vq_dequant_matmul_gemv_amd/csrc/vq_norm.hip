@@ -128,18 +128,41 @@ struct RowMap {
         r.q[i] = in(c, 0) ? reinterpret_cast<const u32x4*>(q)[i] : u32x4{0u, 0u, 0u, 0u};
     } else {
       static_assert(VEC == 8 || WIDE, "single columns are loaded as floats");
+      // no branch between the loads, so that all of them are in flight
+      uint32_t x[8];
+      if (kind == kOutF32) {
+        const uint32_t* q = static_cast<const uint32_t*>(p) + at;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        r.q[j / 4][j % 4] = in(c, j) ? __float_as_uint(load1(p, at + col(c, j), kind)) : 0u;
+        for (int j = 0; j < 8; ++j) x[j] = q[min(col(c, j), cols - 1)];
+      } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = q[min(col(c, j), cols - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[j] = kind == kOutF16 ? __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)x[j])) : x[j] << 16;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r.q[j / 4][j % 4] = in(c, j) ? x[j] : 0u;
     }
   }
   __device__ __forceinline__ void store(void* p, int64_t at, int kind, int c, const float* x) const {
     if constexpr (VEC == 8) {
       if (in(c, 0)) store8(p, at + col(c, 0), x, kind);
     } else {
+      if (kind == kOutF32) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (in(c, j)) store_out(p, at + col(c, j), x[j], kind);
+        for (int j = 0; j < 8; ++j) {
+          if (in(c, j)) static_cast<float*>(p)[at + col(c, j)] = x[j];
+        }
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack16(x[2 * k], x[2 * k + 1], kind == kOutF16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (in(c, j)) static_cast<uint16_t*>(p)[at + col(c, j)] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
       }
     }
   }
@@ -311,8 +334,14 @@ void run_types(const NormArgs& a, hipStream_t s) {
 }
 
 void run_norm(const NormArgs& a, hipStream_t s) {
-  if (a.cols % 8 != 0) return run<1, 4, false, true, true, true>(a, s);  // single columns: off the tuned path
-  const int pieces = a.cols / 8;
+  const int pieces = (a.cols + 7) / 8;
+  // single columns, coalesced over the threads (1 x 5119: 5.6 us, 4096 x 5119:
+  // 72; with a branch on the type at every load they took 25 and 152)
+  if (a.cols % 8 != 0) {
+    if (pieces <= 1024) return run<1, 1, false, true, true, true>(a, s);
+    if (pieces <= 2048) return run<1, 2, false, true, true, true>(a, s);
+    return run<1, 4, false, true, true, true>(a, s);
+  }
   if (pieces <= 64) return run_types<1, true>(a, s);
   // 8 values a thread while that many threads run at once, then 16: fewer
   // reductions a value (4096 x 5120 bf16: 41.8 against 49.6 us, 8192 x 2048:
