@@ -14,6 +14,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
+#include <type_traits>
 
 namespace vqmi {
 
@@ -120,17 +121,9 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * (g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-// N consecutive outputs of one token, the first at y[i]; `whole`: i is a
-// multiple of N and all N exist.
+// N consecutive outputs, the first at y[i] (a multiple of N).
 template <int N>
-__device__ __forceinline__ void store_run(void* y, int64_t i, const float* v, int kind, bool whole, int n) {
-  if (!whole) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (k < n) store_out(y, i + k, v[k], kind);
-    }
-    return;
-  }
+__device__ __forceinline__ void store_run(void* y, int64_t i, const float* v, int kind) {
   if (kind == kOutF32) {
 #pragma unroll
     for (int k = 0; k < N; k += 4)
@@ -159,13 +152,37 @@ __device__ __forceinline__ Fp8Args split_args(Fp8Args a) {
 }
 
 // Stores 16 tokens from t0 on of ROWS rows from r0 on (a multiple of 16) that
-// lie in LDS, `pitch` floats a token; 8 rows a lane, with whole pieces of y
-// where its rows allow them.
+// lie in LDS, `pitch` floats a token; 8 rows a lane in whole pieces of y where
+// its rows allow them.
 template <int ROWS, bool PRECISE>
 __device__ __forceinline__ void store_tokens(const Fp8Args& a, const float* lds, int pitch, int t0, int r0, int lane) {
+  if (a.rows % 8 != 0) {  // one value a lane: a token's rows still leave side by side
+    auto single = [&](auto swiglu) {
+      constexpr int kPairs = swiglu.value ? 2 : 1, kOut = ROWS / kPairs;
+      const int rows = a.rows / kPairs, o0 = r0 / kPairs;
+      for (int base = 0; base < 16 * kOut; base += 4 * 64) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = base + 64 * i + lane, k = e / kOut, o = e % kOut;
+          const float* f = lds + k * pitch + kPairs * o;
+          if constexpr (swiglu.value) v[i] = silu_mul<PRECISE>(f[0], f[1]);
+          else v[i] = f[0];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = base + 64 * i + lane, k = e / kOut, o = e % kOut;
+          if (t0 + k < a.T && o0 + o < rows) store_out(a.y, (int64_t)(t0 + k) * rows + o0 + o, v[i], a.y_kind);
+        }
+      }
+    };
+    if (a.swiglu) single(std::true_type{});
+    else single(std::false_type{});
+    return;
+  }
   constexpr int kLanes = ROWS / 8, kPer = 64 / kLanes;  // lanes a token, tokens at once
-  const int row = r0 + lane % kLanes * 8, n = a.rows - row;
-  if (n <= 0) return;
+  const int row = r0 + lane % kLanes * 8;
+  if (row >= a.rows) return;
 #pragma unroll 1
   for (int k = lane / kLanes; k < 16; k += kPer) {
     const int t = t0 + k;
@@ -175,10 +192,10 @@ __device__ __forceinline__ void store_tokens(const Fp8Args& a, const float* lds,
     if (a.swiglu) {
       const float v[4] = {silu_mul<PRECISE>(lo[0], lo[1]), silu_mul<PRECISE>(lo[2], lo[3]),
                           silu_mul<PRECISE>(hi[0], hi[1]), silu_mul<PRECISE>(hi[2], hi[3])};
-      store_run<4>(a.y, (int64_t)t * (a.rows / 2) + row / 2, v, a.y_kind, a.rows % 8 == 0, n / 2);
+      store_run<4>(a.y, (int64_t)t * (a.rows / 2) + row / 2, v, a.y_kind);
     } else {
       const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      store_run<8>(a.y, (int64_t)t * a.rows + row, v, a.y_kind, a.rows % 8 == 0, n);
+      store_run<8>(a.y, (int64_t)t * a.rows + row, v, a.y_kind);
     }
   }
 }
@@ -582,7 +599,7 @@ __global__ __launch_bounds__(256) void vq_fp8_join_kernel(Fp8Args a, int splits)
       store_out(a.y, i / 2 + 1, silu_mul<true>(v[2], v[3]), a.y_kind);
     } else {
       const float o[4] = {v[0], v[1], v[2], v[3]};
-      store_run<4>(a.y, i, o, a.y_kind, true, 4);
+      store_run<4>(a.y, i, o, a.y_kind);
     }
     return;
   }

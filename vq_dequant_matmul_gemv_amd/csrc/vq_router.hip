@@ -355,11 +355,14 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
   }
   // Keys in fp32.  A sigmoid is off by less than 2^-22: s (1 - s) times the
   // exponential's relative error of 1.22 |l| 2^-24 (argument) and 2^-23 makes
-  // 0.77 * 2^-24, the sum below the reciprocal 2^-24, the reciprocal 2^-23.  A
-  // softmax (the same and a sum of at most 1024 terms) is off by less than
-  // 2^-18.  The sum with a bias adds 2^-24 of itself, so two keys near v are
-  // certainly in order when they differ by more than margin(v).
-  const float slack = sigmoid ? 0x1p-21f : 0x1p-17f;  // twice a score's error
+  // 0.77 * 2^-24, the sum below the reciprocal 2^-24, the reciprocal 2^-23.
+  // The softmax's sum Z = sum e^-x is off by less than 33 * 2^-24 of itself:
+  // 1.22 * 2^-24 times the mean of x (at most the entropy's log 1024), 2^-23
+  // and 22 additions; so a score is off by less than 39 * 2^-24 < 2^-18 of the
+  // largest possible one, 1 / Z.  The sum with a bias adds 2^-24 of itself, so
+  // two keys near v are certainly in order when they differ by more than
+  // margin(v).
+  const float slack = sigmoid ? 0x1p-21f : inv_z * 0x1p-17f;  // twice a score's error
   auto margin = [&](float v) { return fmaf(fabsf(v), 0x1.2p-23f, slack); };
   bool close = false;  // the whole token again in 64 bits
   float p[PL];
