@@ -650,20 +650,20 @@ const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
     {16, 16, 4, 1, 16, true, true, 3.878f, 0.332f, 0.227f, 6.215f, 0.479f, 0.648f, 0.661f, run_skinny<4, 1, 2>},
     {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
-    {16, 64, 8, 17, 512, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
+    {16, 64, 8, 17, kAnyT, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
-    {128, 32, 1, 1, 256, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
+    {128, 32, 1, 1, kAnyT, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
      run_tile<true, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 256, true, false, 4.138f, 0.890f, 0.492f, 5.733f, 0.179f, 1.538f, 0.444f,
+    {128, 64, 1, 1, kAnyT, true, false, 4.138f, 0.890f, 0.492f, 5.733f, 0.179f, 1.538f, 0.444f,
      run_tile<true, 4, 1, 2, 4, 1>},
     {128, 192, 1, 32, kAnyT, true, false, 6.328f, 1.224f, 1.338f, 3.770f, 0.211f, 0.000f, 0.769f,
      run_tile<true, 4, 2, 2, 6, 1>},
     {256, 128, 1, 32, kAnyT, true, false, 5.046f, 0.745f, 1.648f, 4.748f, 0.151f, 3.549f, 1.200f,
      run_tile<true, 4, 2, 4, 4, 1>},
     // tiles on e4m3 instructions: for a 16-bit y
-    {128, 32, 1, 1, 512, false, true, 3.882f, 0.474f, 0.265f, 5.141f, 0.198f, 0.439f, 0.645f,
+    {128, 32, 1, 1, kAnyT, false, true, 3.882f, 0.474f, 0.265f, 5.141f, 0.198f, 0.439f, 0.645f,
      run_tile<false, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, 512, false, true, 3.876f, 0.507f, 0.337f, 5.262f, 0.161f, 1.188f, 0.491f,
+    {128, 64, 1, 1, kAnyT, false, true, 3.876f, 0.507f, 0.337f, 5.262f, 0.161f, 1.188f, 0.491f,
      run_tile<false, 4, 1, 2, 4, 1>},
     {128, 192, 1, 32, kAnyT, false, true, 3.911f, 0.010f, 0.727f, 6.659f, 0.179f, 2.502f, 0.765f,
      run_tile<false, 4, 2, 2, 6, 1>},
