@@ -648,8 +648,8 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 4, 1, 16, true, true, 3.878f, 0.332f, 0.227f, 6.215f, 0.479f, 0.648f, 0.661f, run_skinny<4, 1, 2>},
-    {16, 32, 8, 17, 32, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
+    {16, 16, 4, 1, kAnyT, true, true, 3.878f, 0.332f, 0.227f, 6.215f, 0.479f, 0.648f, 0.661f, run_skinny<4, 1, 2>},
+    {16, 32, 8, 17, kAnyT, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
     {16, 64, 8, 17, kAnyT, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
     {128, 32, 1, 1, kAnyT, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
