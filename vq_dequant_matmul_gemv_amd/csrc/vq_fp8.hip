@@ -627,10 +627,10 @@ void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 13600
-// measured calls (1 to 4096 tokens, 64 to 34816 rows, 256 to 17408 columns, 1
+// The kernels of the product and a time model of each (us), fitted to 21200
+// measured calls (1 to 4096 tokens, 32 to 34816 rows, 256 to 17408 columns, 1
 // to 24 splits), the faster ones of a shape weighing more; the fit's error is
-// 8-12 % rms, and the model's choice takes 1.9 % longer than the best one on
+// 6-13 % rms, and the model's choice takes 1.7 % longer than the best one on
 // average, 0.2 % for products of more than 100 us:
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
@@ -648,28 +648,28 @@ struct Fp8Kernel {
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
     // few tokens, columns split over a block's waves (fp16 instructions)
-    {16, 16, 4, 1, kAnyT, true, true, 3.878f, 0.332f, 0.227f, 6.215f, 0.479f, 0.648f, 0.661f, run_skinny<4, 1, 2>},
-    {16, 32, 8, 17, kAnyT, true, true, 4.364f, 1.243f, 0.838f, 7.969f, 0.827f, 0.957f, 0.886f, run_skinny<8, 2, 1>},
-    {16, 64, 8, 17, kAnyT, true, true, 4.062f, 1.893f, 1.180f, 8.000f, 0.634f, 1.566f, 1.068f, run_skinny<8, 4, 1>},
+    {16, 16, 4, 1, kAnyT, true, true, 4.200f, 0.347f, 0.265f, 7.268f, 0.422f, 0.685f, 1.200f, run_skinny<4, 1, 2>},
+    {16, 32, 8, 17, kAnyT, true, true, 4.055f, 1.362f, 0.648f, 7.871f, 0.241f, 1.700f, 1.200f, run_skinny<8, 2, 1>},
+    {16, 64, 8, 17, kAnyT, true, true, 3.886f, 1.965f, 1.025f, 8.000f, 0.321f, 2.192f, 1.162f, run_skinny<8, 4, 1>},
     // tiles on fp16 instructions: exact products for an fp32 y
-    {128, 32, 1, 1, kAnyT, true, false, 3.780f, 0.698f, 0.348f, 5.065f, 0.204f, 0.966f, 0.221f,
+    {128, 32, 1, 1, kAnyT, true, false, 4.034f, 0.682f, 0.349f, 5.276f, 0.169f, 1.087f, 0.650f,
      run_tile<true, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, kAnyT, true, false, 4.138f, 0.890f, 0.492f, 5.733f, 0.179f, 1.538f, 0.444f,
+    {128, 64, 1, 1, kAnyT, true, false, 4.195f, 0.909f, 0.504f, 6.366f, 0.148f, 1.736f, 1.200f,
      run_tile<true, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, true, false, 6.328f, 1.224f, 1.338f, 3.770f, 0.211f, 0.000f, 0.769f,
+    {128, 192, 1, 32, kAnyT, true, false, 5.953f, 1.008f, 1.368f, 3.543f, 0.181f, 1.149f, 0.665f,
      run_tile<true, 4, 2, 2, 6, 1>},
-    {256, 128, 1, 32, kAnyT, true, false, 5.046f, 0.745f, 1.648f, 4.748f, 0.151f, 3.549f, 1.200f,
+    {256, 128, 1, 32, kAnyT, true, false, 4.851f, 0.691f, 1.628f, 4.558f, 0.139f, 3.888f, 1.200f,
      run_tile<true, 4, 2, 4, 4, 1>},
     // tiles on e4m3 instructions: for a 16-bit y
-    {128, 32, 1, 1, kAnyT, false, true, 3.882f, 0.474f, 0.265f, 5.141f, 0.198f, 0.439f, 0.645f,
+    {128, 32, 1, 1, kAnyT, false, true, 4.105f, 0.469f, 0.236f, 5.226f, 0.169f, 0.857f, 0.814f,
      run_tile<false, 4, 1, 2, 2, 1>},
-    {128, 64, 1, 1, kAnyT, false, true, 3.876f, 0.507f, 0.337f, 5.262f, 0.161f, 1.188f, 0.491f,
+    {128, 64, 1, 1, kAnyT, false, true, 4.169f, 0.510f, 0.300f, 5.329f, 0.155f, 1.299f, 0.674f,
      run_tile<false, 4, 1, 2, 4, 1>},
-    {128, 192, 1, 32, kAnyT, false, true, 3.911f, 0.010f, 0.727f, 6.659f, 0.179f, 2.502f, 0.765f,
+    {128, 192, 1, 32, kAnyT, false, true, 3.997f, 0.003f, 0.713f, 5.712f, 0.173f, 2.684f, 0.615f,
      run_tile<false, 4, 2, 2, 6, 1>},
-    {256, 192, 1, 32, kAnyT, false, true, 5.601f, 0.522f, 1.027f, 6.291f, 0.145f, 3.357f, 1.200f,
+    {256, 192, 1, 32, kAnyT, false, true, 6.537f, 0.000f, 1.026f, 6.435f, 0.151f, 2.174f, 1.200f,
      run_tile<false, 4, 2, 4, 6, 2>},
-    {256, 256, 1, 32, kAnyT, false, true, 5.866f, 0.014f, 1.365f, 6.712f, 0.137f, 4.071f, 1.200f,
+    {256, 256, 1, 32, kAnyT, false, true, 7.251f, 0.010f, 1.357f, 6.978f, 0.144f, 2.308f, 1.200f,
      run_tile<false, 4, 2, 4, 8, 1>},
 };
 constexpr int kNumFp8Kernels = sizeof(kFp8Kernels) / sizeof(kFp8Kernels[0]);
