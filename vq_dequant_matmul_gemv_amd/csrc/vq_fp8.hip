@@ -74,14 +74,15 @@ __global__ __launch_bounds__(256) void vq_fp8_quant_kernel(const uint16_t* x, ui
 // waves split the blocks of 128 columns and join their sums in LDS
 //
 // Bound by the weights' bytes.  Blocks of 16 rows are enough of them to fill
-// the card at 5120 rows already.  Up to 16 tokens four waves a block with two
-// column blocks in flight each (64 registers: every block of 17408 rows is on
-// the card at once), else eight waves with one.  One token, 17408 x 5120: 22 us
-// = 4.1 TB/s (19 in a plain stream of calls on the same weights), 34816 x 5120:
-// 37.  Eight waves took 22.5 and 39, five column blocks in flight 24, and 16
-// waves a block or columns that start elsewhere in every block were no faster.
-// From a few tokens on a 128 x 32 tile with the columns split may be faster (16
-// tokens, 5120 x 17408: 24.4 against 31).
+// the card at 5120 rows already.  With 16 tokens a block takes four waves with
+// two column blocks in flight each (64 registers: every block of 17408 rows is
+// on the card at once), with 32 or 64 eight waves with one.  One token, 17408 x
+// 5120: 22 us = 4.1 TB/s (18 in a plain stream of calls on the same weights),
+// 34816 x 5120: 37.  At 16, eight waves took 22.5 and 39, five column blocks in
+// flight 24, and 16 waves a block or columns that start elsewhere in every
+// block were no faster.  From a few tokens on a 128 x 32 tile with the columns
+// split may be faster (16 tokens, 5120 x 17408: 24.4 against 31), and few rows
+// with many tokens may do better here (991 tokens, 29 rows: 6.9 against 12.5).
 // ---------------------------------------------------------------------------
 struct Fp8Args {
   const uint8_t* w;
@@ -647,7 +648,7 @@ struct Fp8Kernel {
 };
 constexpr int kAnyT = 1 << 30;
 const Fp8Kernel kFp8Kernels[] = {
-    // few tokens, columns split over a block's waves (fp16 instructions)
+    // columns split over a block's waves (fp16 instructions): few tokens or few rows
     {16, 16, 4, 1, kAnyT, true, true, 4.200f, 0.347f, 0.265f, 7.268f, 0.422f, 0.685f, 1.200f, run_skinny<4, 1, 2>},
     {16, 32, 8, 17, kAnyT, true, true, 4.055f, 1.362f, 0.648f, 7.871f, 0.241f, 1.700f, 1.200f, run_skinny<8, 2, 1>},
     {16, 64, 8, 17, kAnyT, true, true, 3.886f, 1.965f, 1.025f, 8.000f, 0.321f, 2.192f, 1.162f, run_skinny<8, 4, 1>},
