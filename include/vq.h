@@ -449,29 +449,41 @@ vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, 
  * Product of e4m3 activations with an e4m3 weight:
  *   y[t][r] = sum_b x_scales[t][b] * scales[r / 128][b] *
  *             sum over the 128 columns of block b of x[t][c] * w[r][c],
- * all sums held in fp32.  An fp32 y is made of exact products (fp16 matrix
- * instructions); for a 16-bit y the e4m3 instructions are used where they are
- * faster, which cut every product of a group of eight columns below 2^-13 of
- * the group's largest one (a relative error of 1.6e-5 on normal inputs, well
- * below the type's rounding).  Any T: decode and prefill shapes run different
+ * exact products (the fp16 matrix instructions hold them), all sums in fp32,
+ * rounded to y's type once.  Any T: decode and prefill shapes run different
  * kernels, and few output tiles are split along the columns into planes of
  * the workspace and joined in order, as a time model of the call rates best.
- * The same call gives the same bits every time.  The environment variable
+ * The same call gives the same bits every time; the order of the fp32 sums,
+ * and with it a row's last bits, depends on T.  The environment variable
  * VQMI_FP8_PLAN = "kernel,splits" forces the choice (for tests).
  *   io: y_dtype and epilogue (NONE or SWIGLU on interleaved gate/up rows: y
  *     has rows / 2 values per token) as for vq_gemm_ex; x_dtype must be
  *     VQ_DTYPE_E4M3.  NULL: fp32 y, no epilogue.
  *   x: device [T][cols] e4m3, 16-byte aligned; x_scales: device
  *     [T][ceil(cols/128)] fp32, 4-byte aligned; y: device, 16-byte aligned.
- *   workspace: device, >= vq_fp8_workspace_bytes(rows, cols, T) bytes, 16-byte
- *     aligned, owned by the caller (may be NULL where that is 0); contents on
+ *   workspace: device, >= vq_fp8_workspace_bytes(rows, cols, T) bytes (enough
+ *     for both calls, any y type and epilogue), 16-byte aligned, owned by the caller (may be NULL where that is 0); contents on
  *     entry are ignored and on return are undefined.  Calls that overlap in
  *     time need separate workspaces.
  * T >= 0 (0 enqueues nothing), T <= 2^24, rows <= 2^24.
+ *
+ * vq_fp8_gemm_fast: the same call for a 16-bit y (io with y_dtype F16 or BF16;
+ * VQ_ERR_SHAPE otherwise) that may use the e4m3 matrix instructions, which do
+ * twice the operations a second.  They cut every product of eight consecutive
+ * columns (8j to 8j + 7) 13 bits below the leading bit of the eight's largest
+ * product, so that y[t][r] is off by up to
+ *   sum_b x_scales[t][b] * scales[r / 128][b] *
+ *   sum over the eights of block b of 7 * 2^-13 * max |x[t][c] * w[r][c]|
+ * more than vq_fp8_gemm's: 1.6e-5 of y's norm on normal inputs, but without a
+ * limit relative to an output whose large products cancel.  Whether a call
+ * uses them depends on T, rows and cols (a few tokens or rows are summed
+ * exactly), so a token's accuracy depends on the batch it is in.
  */
 size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T);
 vq_status vq_fp8_gemm(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x, const float *x_scales, int32_t T,
                       void *y, void *workspace, size_t workspace_bytes, void *stream);
+vq_status vq_fp8_gemm_fast(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x, const float *x_scales,
+                           int32_t T, void *y, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * The norms before and after a block, fused with its gate and the scaled

@@ -268,3 +268,20 @@ def test_calls_too_large_for_a_launch_are_refused(b):
         spec = b.CNormSpec(cols=cols, block_dtype=0, residual_dtype=0, weight_dtype=0, h_dtype=0, gate=0, gate_act=0,
                            reserved=0, alpha=1.0, beta=1.0, eps=1e-6, weight_offset=0.0)
         assert _status(b, b.LIB.vq_norm(ctypes.byref(spec), 0x10000, 0, T, 0, 0x20000, None, None)) == "VQ_ERR_SHAPE"
+
+
+# ---- the product with the e4m3 instructions allowed ------------------------
+
+def test_fast_fp8_gemm_refuses_an_fp32_y_and_what_the_exact_one_refuses(b):
+    w = b.CFP8Tensor(values=0x10000, scales=0x20000, rows=300, cols=272, value_bytes=300 * 272, scale_elems=9)
+
+    def call(io, T=4, x=0x40000):
+        i = None if io is None else ctypes.byref(b.CIo(*io))
+        return _status(b, b.LIB.vq_fp8_gemm_fast(ctypes.byref(w), i, x, 0x50000, T, 0x60000, 0x70000, 1 << 40, None))
+
+    assert call(None) == "VQ_ERR_SHAPE" and b"F16 or BF16" in b.LIB.vq_last_error()
+    assert call((3, 0, 0, 0, None)) == "VQ_ERR_SHAPE"
+    assert call((3, 2, 2, 0, None)) == "VQ_ERR_SHAPE"                       # COMBINE
+    assert call((3, 1, 0, 0, None), x=0x40008) == "VQ_ERR_ALIGN"
+    assert call((3, 1, 0, 0, None), T=-1) == "VQ_ERR_SHAPE" and b"vq_fp8_gemm_fast" in b.LIB.vq_last_error()
+    assert call((3, 2, 1, 0, None), T=0) == "VQ_OK"

@@ -140,6 +140,7 @@ def _load():
         "vq_fp8_quant": (i32, [P, i32, i32, i32, P, P, P]),
         "vq_fp8_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
         "vq_fp8_gemm": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
+        "vq_fp8_gemm_fast": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
         "vq_norm": (i32, [P, P, P, i32, P, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
@@ -156,7 +157,8 @@ LIB = _load()
 EXPORTED = ("vq_words_per_row", "vq_dequant", "vq_gemv", "vq_gemm", "vq_moe_gemv", "vq_gemv_ex",
             "vq_gemm_ex", "vq_moe_gemv_ex", "vq_moe_gemm_ex",
             "vq_moe_workspace_bytes", "vq_moe_gemm", "vq_moe_gemm_no_alloc", "vq_encode_workspace_bytes",
-            "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm", "vq_norm",
+            "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm",
+            "vq_fp8_gemm_fast", "vq_norm",
             "vq_last_error", "vq_status_name")
 
 
@@ -634,10 +636,13 @@ def fp8_quant(x, q=None, scales=None, stream=None):
     return q, scales
 
 
-def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_dtype=None, epilogue=None):
+def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_dtype=None, epilogue=None,
+             fast=False):
     """y = x W^T of e4m3 activations (values [T][cols], scales
     [T][ceil(cols/128)]) through vq_fp8_gemm, decode and prefill alike;
-    epilogue "swiglu" on interleaved gate/up rows gives silu(gate) * up."""
+    epilogue "swiglu" on interleaved gate/up rows gives silu(gate) * up.
+    fast, for a 16-bit y: vq_fp8_gemm_fast, whose products of large batches are
+    cut 13 bits below the largest of eight (see include/vq.h)."""
     torch = _torch()
     v, ws = w.values, w.scales
     e4m3 = (torch.float8_e4m3fn, torch.uint8)
@@ -665,7 +670,7 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
-            return fp8_gemm(w, x, x_scales, y, workspace, None, y_dtype, epilogue)
+            return fp8_gemm(w, x, x_scales, y, workspace, None, y_dtype, epilogue, fast)
     if y is None:
         y = _rows(*yshape, y_dtype, dev)
     if workspace is None:
@@ -674,9 +679,10 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
                                                         workspace.numel() * workspace.element_size())
-    check(LIB.vq_fp8_gemm(_pack_fp8(v.data_ptr(), ws.data_ptr(), rows, cols, rows * cols, ws.numel()),
-                          _pack_io(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, 0), x.data_ptr(),
-                          x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(gpu)))
+    call = LIB.vq_fp8_gemm_fast if fast else LIB.vq_fp8_gemm
+    check(call(_pack_fp8(v.data_ptr(), ws.data_ptr(), rows, cols, rows * cols, ws.numel()),
+               _pack_io(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, 0), x.data_ptr(),
+               x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(gpu)))
     return y
 
 

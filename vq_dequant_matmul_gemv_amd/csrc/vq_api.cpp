@@ -479,69 +479,84 @@ vq_status vq_fp8_quant(const void* x, int32_t x_dtype, int32_t T, int32_t cols, 
                     "vq_fp8_quant launch");
 }
 
-static vq_status check_fp8_sizes(int32_t rows, int32_t cols, int32_t T) {
-  if (rows < 1 || rows > (1 << 24)) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: rows=%d outside [1, 2^24]", rows);
+static vq_status check_fp8_sizes(const char* fn, int32_t rows, int32_t cols, int32_t T) {
+  if (rows < 1 || rows > (1 << 24)) return fail(VQ_ERR_SHAPE, "%s: rows=%d outside [1, 2^24]", fn, rows);
   if (!fp8_cols_ok(cols))
-    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: cols=%d must be a multiple of 16 in [16, 2^20]", cols);
-  if (T < 0 || T > (1 << 24)) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: T=%d outside [0, 2^24]", T);
+    return fail(VQ_ERR_SHAPE, "%s: cols=%d must be a multiple of 16 in [16, 2^20]", fn, cols);
+  if (T < 0 || T > (1 << 24)) return fail(VQ_ERR_SHAPE, "%s: T=%d outside [0, 2^24]", fn, T);
   if ((int64_t)((rows + 15) / 16) * ((T + 15) / 16) > (1 << 30))
-    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: T=%d x %d rows makes too many tiles", T, rows);
+    return fail(VQ_ERR_SHAPE, "%s: T=%d x %d rows makes too many tiles", fn, T, rows);
   return VQ_OK;
 }
 
 size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T) {
-  if (check_fp8_sizes(rows, cols, T) != VQ_OK) return 0;
+  if (check_fp8_sizes("vq_fp8_workspace_bytes", rows, cols, T) != VQ_OK) return 0;
   return T == 0 ? 0 : vqmi::fp8_workspace_bytes(rows, cols, T);
 }
 
-vq_status vq_fp8_gemm(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x, const float* x_scales, int32_t T,
-                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!w) return fail(VQ_ERR_NULL, "vq_fp8_gemm: tensor descriptor is NULL");
+// vq_fp8_gemm and vq_fp8_gemm_fast
+static vq_status fp8_product(bool fast, const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x,
+                             const float* x_scales, int32_t T, void* y, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const char* const fn = fast ? "vq_fp8_gemm_fast" : "vq_fp8_gemm";
+  if (!w) return fail(VQ_ERR_NULL, "%s: tensor descriptor is NULL", fn);
   if (!w->values || !w->scales)
-    return fail(VQ_ERR_NULL, "vq_fp8_gemm: tensor has a NULL pointer (values=%p scales=%p)", (const void*)w->values,
+    return fail(VQ_ERR_NULL, "%s: tensor has a NULL pointer (values=%p scales=%p)", fn, (const void*)w->values,
                 (const void*)w->scales);
-  vq_status st = check_fp8_sizes(w->rows, w->cols, T);
+  vq_status st = check_fp8_sizes(fn, w->rows, w->cols, T);
   if (st != VQ_OK) return st;
   if (w->value_bytes != (int64_t)w->rows * w->cols)
-    return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: values hold %lld bytes but rows*cols = %lld", (long long)w->value_bytes,
+    return fail(VQ_ERR_SHAPE, "%s: values hold %lld bytes but rows*cols = %lld", fn, (long long)w->value_bytes,
                 (long long)w->rows * w->cols);
   const int64_t want = (int64_t)((w->rows + 127) / 128) * ((w->cols + 127) / 128);
   if (w->scale_elems != want)
     return fail(VQ_ERR_SHAPE,
-                "vq_fp8_gemm: scales hold %lld values but a %d x %d weight has %lld blocks of 128 x 128: sliced, or "
-                "of another layout",
-                (long long)w->scale_elems, w->rows, w->cols, (long long)want);
-  if (!aligned(w->values, 16)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: values are not 16-byte aligned");
-  if (!aligned(w->scales, 4)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: scales are not 4-byte aligned");
+                "%s: scales hold %lld values but a %d x %d weight has %lld blocks of 128 x 128: sliced, or of another "
+                "layout",
+                fn, (long long)w->scale_elems, w->rows, w->cols, (long long)want);
+  if (!aligned(w->values, 16)) return fail(VQ_ERR_ALIGN, "%s: values are not 16-byte aligned", fn);
+  if (!aligned(w->scales, 4)) return fail(VQ_ERR_ALIGN, "%s: scales are not 4-byte aligned", fn);
   vqmi::IoSpec ios{};
   if (io) {
     if (io->x_dtype != VQ_DTYPE_E4M3)
-      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->x_dtype=%d: x must be VQ_DTYPE_E4M3", io->x_dtype);
+      return fail(VQ_ERR_SHAPE, "%s: io->x_dtype=%d: x must be VQ_DTYPE_E4M3", fn, io->x_dtype);
     if (io->y_dtype != VQ_DTYPE_F32 && io->y_dtype != VQ_DTYPE_F16 && io->y_dtype != VQ_DTYPE_BF16)
-      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->y_dtype=%d must be F32, F16 or BF16", io->y_dtype);
+      return fail(VQ_ERR_SHAPE, "%s: io->y_dtype=%d must be F32, F16 or BF16", fn, io->y_dtype);
     if (io->epilogue != VQ_EPILOGUE_NONE && io->epilogue != VQ_EPILOGUE_SWIGLU)
-      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->epilogue=%d: NONE or SWIGLU", io->epilogue);
-    if (io->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: io->reserved must be 0");
+      return fail(VQ_ERR_SHAPE, "%s: io->epilogue=%d: NONE or SWIGLU", fn, io->epilogue);
+    if (io->reserved != 0) return fail(VQ_ERR_SHAPE, "%s: io->reserved must be 0", fn);
     if (io->epilogue == VQ_EPILOGUE_SWIGLU && w->rows % 2 != 0)
-      return fail(VQ_ERR_SHAPE, "vq_fp8_gemm: SWIGLU needs interleaved (gate, up) row pairs: rows=%d is odd", w->rows);
+      return fail(VQ_ERR_SHAPE, "%s: SWIGLU needs interleaved (gate, up) row pairs: rows=%d is odd", fn, w->rows);
     ios.y_kind = dtype_kind(io->y_dtype);
     ios.epi = io->epilogue == VQ_EPILOGUE_SWIGLU ? vqmi::kEpiSwiglu : vqmi::kEpiNone;
   }
+  if (fast && ios.y_kind == vqmi::kOutF32)
+    return fail(VQ_ERR_SHAPE, "%s: y must be F16 or BF16 (vq_fp8_gemm serves F32)", fn);
   if (T == 0) return VQ_OK;
   st = check_xy(x, y, "y");
   if (st != VQ_OK) return st;
-  if (!x_scales) return fail(VQ_ERR_NULL, "vq_fp8_gemm: x_scales is NULL");
-  if (!aligned(x_scales, 4)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: x_scales is not 4-byte aligned");
+  if (!x_scales) return fail(VQ_ERR_NULL, "%s: x_scales is NULL", fn);
+  if (!aligned(x_scales, 4)) return fail(VQ_ERR_ALIGN, "%s: x_scales is not 4-byte aligned", fn);
   const size_t need = vqmi::fp8_workspace_bytes(w->rows, w->cols, T);
   if (need > 0) {
-    if (!workspace) return fail(VQ_ERR_WORKSPACE, "vq_fp8_gemm: workspace is NULL (need %zu bytes)", need);
+    if (!workspace) return fail(VQ_ERR_WORKSPACE, "%s: workspace is NULL (need %zu bytes)", fn, need);
     if (workspace_bytes < need)
-      return fail(VQ_ERR_WORKSPACE, "vq_fp8_gemm: workspace has %zu bytes, need %zu", workspace_bytes, need);
-    if (!aligned(workspace, 16)) return fail(VQ_ERR_ALIGN, "vq_fp8_gemm: workspace is not 16-byte aligned");
+      return fail(VQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, need %zu", fn, workspace_bytes, need);
+    if (!aligned(workspace, 16)) return fail(VQ_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
   }
   const vqmi::Fp8View v{w->values, w->scales, w->rows, w->cols};
-  return hip_status(vqmi::launch_fp8_gemm(v, ios, x, x_scales, T, y, workspace, (hipStream_t)stream),
-                    "vq_fp8_gemm launch");
+  return hip_status(vqmi::launch_fp8_gemm(v, ios, fast, x, x_scales, T, y, workspace, (hipStream_t)stream),
+                    fast ? "vq_fp8_gemm_fast launch" : "vq_fp8_gemm launch");
+}
+
+vq_status vq_fp8_gemm(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x, const float* x_scales, int32_t T,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_product(false, w, io, x, x_scales, T, y, workspace, workspace_bytes, stream);
+}
+
+vq_status vq_fp8_gemm_fast(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x, const float* x_scales,
+                           int32_t T, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_product(true, w, io, x, x_scales, T, y, workspace, workspace_bytes, stream);
 }
 
 vq_status vq_norm(const vq_norm_spec* n, const void* block, const void* residual, int32_t T, void* residual_out,

@@ -24,8 +24,9 @@ struct Fp8View {
 };
 hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t* q, float* scales, hipStream_t s);
 size_t fp8_workspace_bytes(int rows, int cols, int T);
-hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const uint8_t* x, const float* xs, int T, void* y,
-                           void* workspace, hipStream_t s);
+// fast: the e4m3 matrix instructions may be used
+hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, bool fast, const uint8_t* x, const float* xs, int T,
+                           void* y, void* workspace, hipStream_t s);
 
 // Norms before and after a block with its gate and residual (vq_norm.hip).
 enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
