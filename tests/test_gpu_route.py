@@ -218,3 +218,27 @@ def test_many_tokens_with_groups_of_whole_lanes(dtype, score, bias):
     b = torch.from_numpy((0.05 * g.normal(size=256)).astype(np.float32)) if bias else None
     _check(x, 8, b, score=score, groups=8, top_groups=4, group_score="top2", scale=2.5)
     _check(x, 16, b, score=score, groups=16, top_groups=5, renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,T", [(8, 2, 3), (96, 8, 21), (32, 8, 8200), (256, 8, 9), (120, 12, 5)])
+def test_groups_masked_by_the_lowest_bias(score, E, groups, T):
+    """A bias of fp32's lowest value on whole groups: their two best sum to
+    below every fp32 number, and they stay in play behind the others."""
+    import torch
+    g = synth.rng("route-lowest", E, groups)
+    size = E // groups
+    low = torch.finfo(torch.float32).min
+    b = torch.from_numpy((0.05 * g.normal(size=E)).astype(np.float32))
+    b[size:2 * size] = low                     # one whole group
+    b[(groups - 1) * size:] = 0.75 * low       # another, a little less low
+    if groups > 4:
+        b[2 * size + 1:3 * size] = low         # one with a single ordinary expert
+    x = torch.from_numpy((1.5 * g.normal(size=(T, E))).astype(np.float32))
+    if T > 8191:                               # many tokens: four a wave; the groups behind the first two are low
+        b[2 * size:] = low
+        return _check(x, 2 * size + 6, b, score=score, groups=groups, top_groups=groups - 1, group_score="top2")
+    for top_groups in (groups, groups - 1):
+        k = min(64, top_groups * size)
+        for gs in ("top2", "max"):
+            _check(x, k, b, score=score, groups=groups, top_groups=top_groups, group_score=gs)

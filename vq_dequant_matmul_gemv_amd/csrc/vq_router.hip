@@ -436,11 +436,13 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
     stays = s > -INFINITY && rank < a.top_groups;
     if (need_p) {
       // the worst group that stays against the best that does not; a group's
-      // sum is off by its two keys' errors (they may cancel) and its own
+      // sum is off by its two keys' errors (they may cancel) and its own, and
+      // sums that may leave fp32 (a group is then not even known to be in play)
+      // are left to the 64-bit pass
       const float in = order_value(lanes_min<LPT>(stays ? order_key(s) : order_key(INFINITY)));
       const float out = order_value(lanes_max<LPT>(stays ? order_key(-INFINITY) : order_key(s)));
       if (a.top2) {
-        const float both = s > -INFINITY ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
+        const float both = m1 > -INFINITY ? fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f) : 0.0f;
         const float mag = __uint_as_float(lanes_max<LPT>(__float_as_uint(both)));
         close = in - out <= fmaf(mag, 0x1.2p-22f, 2.0f * slack) || !(mag < 0x1p126f);
       } else {
