@@ -440,7 +440,7 @@ typedef struct vq_fp8_tensor {
  *   x: device [T][cols] of x_dtype (F16 or BF16), 16-byte aligned;
  *   q: device [T][cols] e4m3, 16-byte aligned; scales: device
  *   [T][ceil(cols/128)] fp32, 4-byte aligned.  cols as for vq_fp8_tensor;
- *   T >= 0 (0 enqueues nothing), T * ceil(cols/128) < 2^28.
+ *   T >= 0 (0 enqueues nothing), T * ceil(cols/128) <= 2^28 - 16.
  */
 vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t *q, float *scales,
                        void *stream);
@@ -511,8 +511,8 @@ vq_status vq_fp8_gemm_fast(const vq_fp8_tensor *w, const vq_io *io, const uint8_
  *             h_scales [T][ceil(cols/128)] fp32); NULL: not computed.  Not
  *             both outputs NULL.  No other buffers may overlap.
  * Pointers of [T][cols] and [cols] data 16-byte aligned, the others to their
- * element.  T >= 0 (0 enqueues nothing), T * ceil(cols/512) < 2^26.  One
- * launch, no workspace; the same inputs give the same bits.
+ * element.  T >= 0 (0 enqueues nothing), T * ceil(cols/512) <= 2^26 - 4.
+ * One launch, no workspace; the same inputs give the same bits.
  * Errors (VQ_ERR_SHAPE): cols outside [1, 32768], or not a multiple of 16 for
  * an E4M3 h; an unknown dtype, gate or gate_act; a gate_act without a gate; a
  * post norm or gate without a block; eps negative or not finite; alpha, beta

@@ -285,3 +285,26 @@ def test_fast_fp8_gemm_refuses_an_fp32_y_and_what_the_exact_one_refuses(b):
     assert call((3, 1, 0, 0, None), x=0x40008) == "VQ_ERR_ALIGN"
     assert call((3, 1, 0, 0, None), T=-1) == "VQ_ERR_SHAPE" and b"vq_fp8_gemm_fast" in b.LIB.vq_last_error()
     assert call((3, 2, 1, 0, None), T=0) == "VQ_OK"
+
+
+def test_the_largest_sizes_taken_and_the_first_ones_refused(b):
+    """Grids round up to whole blocks and still hold fewer than 2^32 threads.  A
+    size that is taken fails on the NULL outputs behind it: nothing is launched."""
+    def route(T):
+        return _route(b, T=T, ids=0)
+
+    def quant(T, cols):
+        return _quant(b, T=T, cols=cols, q=0)
+
+    def norm(T, cols):
+        return _norm(b, T=T, cols=cols, v=0, h=0)
+
+    for call, taken, refused in [(route, [(1 << 25,)], [((1 << 25) + 1,)]),
+                                 (quant, [((1 << 28) - 16, 16), ((1 << 27) - 8, 256), ((1 << 28) // 3 - 6, 384)],
+                                  [((1 << 28) - 15, 16), ((1 << 28) - 1, 128), ((1 << 27) - 7, 256)]),
+                                 (norm, [((1 << 26) - 4, 8), ((1 << 26) - 4, 511), ((1 << 25) - 2, 513), ((1 << 20) - 1, 32768)],
+                                  [((1 << 26) - 3, 8), ((1 << 26) - 1, 512), ((1 << 25) - 1, 513), (1 << 20, 32768)])]:
+        for a in taken:
+            assert call(*a) == "VQ_ERR_NULL", (a, b.LIB.vq_last_error())
+        for a in refused:
+            assert call(*a) == "VQ_ERR_SHAPE", (a, b.LIB.vq_last_error())

@@ -468,7 +468,8 @@ vq_status vq_fp8_quant(const void* x, int32_t x_dtype, int32_t T, int32_t cols, 
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: x_dtype=%d: x must be VQ_DTYPE_F16 or VQ_DTYPE_BF16", x_dtype);
   if (!fp8_cols_ok(cols))
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: cols=%d must be a multiple of 16 in [16, 2^20]", cols);
-  if (T < 0 || (int64_t)T * ((cols + 127) / 128) >= (int64_t)1 << 28)
+  // 16 lanes a block of columns, 256 threads a launched block
+  if (T < 0 || (int64_t)T * ((cols + 127) / 128) > ((int64_t)1 << 28) - 16)
     return fail(VQ_ERR_SHAPE, "vq_fp8_quant: T=%d out of range for cols=%d", T, cols);
   if (T == 0) return VQ_OK;
   vq_status st = check_xy(x, q, "q");
@@ -582,7 +583,8 @@ vq_status vq_norm(const vq_norm_spec* n, const void* block, const void* residual
   if (!std::isfinite(n->alpha) || !std::isfinite(n->beta) || !std::isfinite(n->weight_offset))
     return fail(VQ_ERR_SHAPE, "vq_norm: alpha, beta and weight_offset must be finite");
   if (n->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_norm: reserved must be 0");
-  if (T < 0 || (int64_t)T * ((n->cols + 511) / 512) >= (int64_t)1 << 26)
+  // a wave for 512 columns at most, and whole blocks of four rows of one wave
+  if (T < 0 || (int64_t)T * ((n->cols + 511) / 512) > ((int64_t)1 << 26) - 4)
     return fail(VQ_ERR_SHAPE, "vq_norm: T=%d out of range for cols=%d", T, n->cols);
   if (T == 0) return VQ_OK;
   if (!block && !residual) return fail(VQ_ERR_NULL, "vq_norm: block and residual are both NULL");
