@@ -308,3 +308,19 @@ def test_the_largest_sizes_taken_and_the_first_ones_refused(b):
             assert call(*a) == "VQ_ERR_NULL", (a, b.LIB.vq_last_error())
         for a in refused:
             assert call(*a) == "VQ_ERR_SHAPE", (a, b.LIB.vq_last_error())
+
+
+def test_weight_scales_of_another_layout_are_refused(b):
+    """[cols/128][rows/128] holds as many values as [rows/128][cols/128]: the
+    shape tells them apart, before a GPU is needed."""
+    import torch
+    v = torch.zeros(256, 640, dtype=torch.uint8)
+    x, xs = torch.zeros(3, 640, dtype=torch.uint8), torch.ones(3, 5)
+    for scales in (torch.ones(5, 2), torch.ones(10), torch.ones(2, 5, 1), torch.ones(2, 4), torch.ones(2, 5).half()):
+        w = b.FP8Tensor(v, scales)
+        with pytest.raises(ValueError, match="w.scales must be"):
+            b.fp8_gemm(w, x, xs)
+        with pytest.raises(ValueError, match="w.scales must be"):
+            w.cstruct()
+    with pytest.raises(ValueError, match="GPU"):                 # the right shape gets as far as the device
+        b.fp8_gemm(b.FP8Tensor(v, torch.ones(2, 5)), x, xs)

@@ -596,15 +596,24 @@ class FP8Tensor:
     def device(self):
         return self.values.device
 
-    def cstruct(self) -> CFP8Tensor:
+    def checked(self):
+        """(rows, cols, index of the GPU both tensors are on), after the checks
+        of their types, shapes and places."""
         torch = _torch()
         v, s = self.values, self.scales
-        _dev_check(v, s, device=v.device)
         if v.dtype not in (torch.float8_e4m3fn, torch.uint8) or v.dim() != 2:
-            raise ValueError("values must be float8_e4m3fn (or uint8 codes) [rows][cols]")
-        if s.dtype != torch.float32:
-            raise ValueError("scales must be fp32")
-        return CFP8Tensor(v.data_ptr(), s.data_ptr(), v.shape[0], v.shape[1], v.numel(), s.numel())
+            raise ValueError("w.values must be float8_e4m3fn (or uint8 codes) [rows][cols]")
+        rows, cols = v.shape
+        if s.dtype != torch.float32 or s.shape != (_blocks(rows), _blocks(cols)):
+            raise ValueError(f"w.scales must be fp32 {(_blocks(rows), _blocks(cols))} (one value for each 128 x 128 "
+                             f"block), got {s.dtype} {tuple(s.shape)}")
+        gpu = _gpu(v)
+        _placed(s, gpu)
+        return rows, cols, gpu
+
+    def cstruct(self) -> CFP8Tensor:
+        rows, cols, _ = self.checked()
+        return CFP8Tensor(self.values.data_ptr(), self.scales.data_ptr(), rows, cols, rows * cols, self.scales.numel())
 
 
 def fp8_quant(x, q=None, scales=None, stream=None):
@@ -644,12 +653,9 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
     fast, for a 16-bit y: vq_fp8_gemm_fast, whose products of large batches are
     cut 13 bits below the largest of eight (see include/vq.h)."""
     torch = _torch()
+    rows, cols, gpu = w.checked()
     v, ws = w.values, w.scales
-    e4m3 = (torch.float8_e4m3fn, torch.uint8)
-    if v.dtype not in e4m3 or v.dim() != 2 or ws.dtype != torch.float32:
-        raise ValueError("w must hold float8_e4m3fn (or uint8) values [rows][cols] and fp32 scales")
-    rows, cols = v.shape
-    if x.dtype not in e4m3 or x.dim() != 2 or x.shape[1] != cols:
+    if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.dim() != 2 or x.shape[1] != cols:
         raise ValueError(f"x must be float8_e4m3fn (or uint8 codes) [T][{cols}]")
     T = x.shape[0]
     if x_scales.dtype != torch.float32 or x_scales.shape != (T, _blocks(cols)):
@@ -658,10 +664,9 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
         raise ValueError("epilogue must be None or 'swiglu'")
     y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
     yshape = (T, rows // 2 if epilogue == "swiglu" else rows)
-    gpu = _gpu(v)
     dev = v.device
-    for t in (ws, x, x_scales):
-        _placed(t, gpu)
+    _placed(x, gpu)
+    _placed(x_scales, gpu)
     if y is not None:
         _check_out(y, y_dtype, yshape)
         _placed(y, gpu)
