@@ -465,7 +465,8 @@ vq_status vq_fp8_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, 
  *     for both calls, any y type and epilogue), 16-byte aligned, owned by the caller (may be NULL where that is 0); contents on
  *     entry are ignored and on return are undefined.  Calls that overlap in
  *     time need separate workspaces.
- * T >= 0 (0 enqueues nothing), T <= 2^24, rows <= 2^24.
+ * T >= 0 (0 enqueues nothing), T <= 2^24, rows <= 2^24, and a launch holds
+ * ceil(rows/256) * ceil(T/128) < 2^22 tiles (more: VQ_ERR_SHAPE).
  *
  * vq_fp8_gemm_fast: the same call for a 16-bit y (io with y_dtype F16 or BF16;
  * VQ_ERR_SHAPE otherwise) that may use the e4m3 matrix instructions, which do

@@ -324,3 +324,41 @@ def test_weight_scales_of_another_layout_are_refused(b):
             w.cstruct()
     with pytest.raises(ValueError, match="GPU"):                 # the right shape gets as far as the device
         b.fp8_gemm(b.FP8Tensor(v, torch.ones(2, 5)), x, xs)
+
+
+# ---- the product's plan -----------------------------------------------------
+
+@pytest.mark.parametrize("T,rows", [(1 << 14, 1 << 24), (1 << 24, 1 << 14), ((1 << 14) - 128 + 1, 1 << 23 | 1)])
+def test_sizes_no_kernel_holds_in_one_launch_are_refused(b, T, rows):
+    """Up to 2^30 tiles of 16 x 16 pass the first check; where the largest tiles
+    still make 2^22 of them there is no plan, and nothing may run in its place."""
+    for call in (b.LIB.vq_fp8_gemm, b.LIB.vq_fp8_gemm_fast):
+        w = b.CFP8Tensor(values=0x10000, scales=0x20000, rows=rows, cols=16, value_bytes=rows * 16,
+                         scale_elems=-(-rows // 128))
+        if call is b.LIB.vq_fp8_gemm_fast and T < 1 << 14:
+            continue                             # 256 x 256 tiles: half as many
+        io = b.CIo(3, 2, 0, 0, None)
+        # the NULL x behind the check keeps a size that is taken from being launched
+        st = _status(b, call(ctypes.byref(w), ctypes.byref(io), 0, 0x50000, T, 0x60000, 0x70000, 1 << 40, None))
+        assert st == "VQ_ERR_SHAPE" and b"too many tiles" in b.LIB.vq_last_error()
+
+
+def test_a_forced_plan_keeps_the_planners_limits(b, monkeypatch):
+    """VQMI_FP8_PLAN with more planes than the planner would ever ask for (512
+    MiB) is passed over; one within them is taken, and a stated workspace is what
+    the call wants."""
+    free = b.LIB.vq_fp8_workspace_bytes(17408, 5120, 4096)
+    assert free <= 512 << 20
+    monkeypatch.setenv("VQMI_FP8_PLAN", "3,8")
+    assert b.LIB.vq_fp8_workspace_bytes(17408, 5120, 4096) == free
+    need = b.LIB.vq_fp8_workspace_bytes(640, 5120, 64)
+    assert need >= 5 * 640 * 64 * 4          # 40 column blocks in parts of whole fours: 5 of 8
+    kw = dict(T=64, rows=640, cols=5120)
+    assert _fp8(b, ws_bytes=need - 1, **kw) == "VQ_ERR_WORKSPACE"
+    assert _fp8(b, ws=0x70008, ws_bytes=need, **kw) == "VQ_ERR_ALIGN"
+
+
+def test_some_shapes_need_a_workspace(b):
+    """So that the workspace checks above are made at all."""
+    for T, rows, cols in [(64, 512, 17408), (40, 640, 17408), (16, 5120, 17408)]:
+        assert b.LIB.vq_fp8_workspace_bytes(rows, cols, T) > 0

@@ -492,7 +492,7 @@ static vq_status check_fp8_sizes(const char* fn, int32_t rows, int32_t cols, int
 
 size_t vq_fp8_workspace_bytes(int32_t rows, int32_t cols, int32_t T) {
   if (check_fp8_sizes("vq_fp8_workspace_bytes", rows, cols, T) != VQ_OK) return 0;
-  return T == 0 ? 0 : vqmi::fp8_workspace_bytes(rows, cols, T);
+  return T == 0 ? 0 : vqmi::fp8_plans(rows, cols, T).workspace();
 }
 
 // vq_fp8_gemm and vq_fp8_gemm_fast
@@ -534,11 +534,14 @@ static vq_status fp8_product(bool fast, const vq_fp8_tensor* w, const vq_io* io,
   if (fast && ios.y_kind == vqmi::kOutF32)
     return fail(VQ_ERR_SHAPE, "%s: y must be F16 or BF16 (vq_fp8_gemm serves F32)", fn);
   if (T == 0) return VQ_OK;
+  const vqmi::Fp8Plans plans = vqmi::fp8_plans(w->rows, w->cols, T);
+  const vqmi::Fp8Plan& plan = fast ? plans.fast : plans.exact;
+  if (plan.kernel < 0) return fail(VQ_ERR_SHAPE, "%s: T=%d x %d rows makes too many tiles", fn, T, w->rows);
   st = check_xy(x, y, "y");
   if (st != VQ_OK) return st;
   if (!x_scales) return fail(VQ_ERR_NULL, "%s: x_scales is NULL", fn);
   if (!aligned(x_scales, 4)) return fail(VQ_ERR_ALIGN, "%s: x_scales is not 4-byte aligned", fn);
-  const size_t need = vqmi::fp8_workspace_bytes(w->rows, w->cols, T);
+  const size_t need = plans.workspace();
   if (need > 0) {
     if (!workspace) return fail(VQ_ERR_WORKSPACE, "%s: workspace is NULL (need %zu bytes)", fn, need);
     if (workspace_bytes < need)
@@ -546,7 +549,7 @@ static vq_status fp8_product(bool fast, const vq_fp8_tensor* w, const vq_io* io,
     if (!aligned(workspace, 16)) return fail(VQ_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
   }
   const vqmi::Fp8View v{w->values, w->scales, w->rows, w->cols};
-  return hip_status(vqmi::launch_fp8_gemm(v, ios, fast, x, x_scales, T, y, workspace, (hipStream_t)stream),
+  return hip_status(vqmi::launch_fp8_gemm(v, ios, plan, x, x_scales, T, y, workspace, (hipStream_t)stream),
                     fast ? "vq_fp8_gemm_fast launch" : "vq_fp8_gemm launch");
 }
 

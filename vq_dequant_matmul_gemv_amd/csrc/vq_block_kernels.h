@@ -23,10 +23,21 @@ struct Fp8View {
   int rows, cols;
 };
 hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t* q, float* scales, hipStream_t s);
-size_t fp8_workspace_bytes(int rows, int cols, int T);
-// fast: the e4m3 matrix instructions may be used
-hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, bool fast, const uint8_t* x, const float* xs, int T,
-                           void* y, void* workspace, hipStream_t s);
+// How a product runs: a kernel of vq_fp8.hip's table and the columns' splits.
+struct Fp8Plan {
+  int kernel = -1;  // -1: no kernel holds these sizes in one launch
+  int splits = 1, split_steps = 0;
+  size_t workspace = 0;
+};
+// The plans of vq_fp8_gemm and vq_fp8_gemm_fast for these sizes.  A call looks
+// them up once and runs what it has checked its workspace for.
+struct Fp8Plans {
+  Fp8Plan exact, fast;
+  size_t workspace() const { return exact.workspace > fast.workspace ? exact.workspace : fast.workspace; }
+};
+Fp8Plans fp8_plans(int rows, int cols, int T);
+hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const Fp8Plan& p, const uint8_t* x, const float* xs,
+                           int T, void* y, void* workspace, hipStream_t s);
 
 // Norms before and after a block with its gate and residual (vq_norm.hip).
 enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };

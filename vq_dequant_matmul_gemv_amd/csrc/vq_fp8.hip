@@ -10,7 +10,6 @@
 #include "vq_fp8_device.h"
 #include "vq_block_kernels.h"
 
-#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -678,75 +677,68 @@ const Fp8Kernel kFp8Kernels[] = {
 constexpr int kNumFp8Kernels = sizeof(kFp8Kernels) / sizeof(kFp8Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
 
-struct Fp8Plan {
-  int rows = 0, cols = 0, T = 0, fast = 0;  // what it is for
-  int kernel = 0, splits = 1, split_steps = 0;
-  size_t workspace() const { return splits > 1 ? (size_t)splits * T * rows * sizeof(float) : 0; }
+// Sizes a plan is for.
+struct Fp8Call {
+  int rows, cols, T;
+  bool fast;
+  bool operator==(const Fp8Call& o) const {
+    return rows == o.rows && cols == o.cols && T == o.T && fast == o.fast;
+  }
 };
 
-// Column blocks per split (the tiles' groups of scales: whole fours) and the
-// splits that leaves.
-void set_splits(Fp8Plan& p, int splits) {
-  const int kb = ceil_div(p.cols, kFp8Block), q = kFp8Kernels[p.kernel].k_waves > 1 ? 1 : 4;
-  p.split_steps = ceil_div(ceil_div(kb, splits), q) * q;
-  p.splits = ceil_div(kb, p.split_steps);
+// The call by kernel i with its columns in up to `splits` parts of whole column
+// blocks (the tiles' groups of scales: whole fours).  False where the kernel
+// does not serve the call, or the launch (fewer than 2^32 threads, a block up
+// to 512) or the planes grow too large.
+bool set_plan(const Fp8Call& c, int i, int splits, Fp8Plan* p) {
+  const Fp8Kernel& k = kFp8Kernels[i];
+  if (!(c.fast ? k.fast : k.exact)) return false;
+  if ((int64_t)ceil_div(c.rows, k.rows) * ceil_div(c.T, k.tokens) >= 1 << 22) return false;
+  const int kb = ceil_div(c.cols, kFp8Block), q = k.k_waves > 1 ? 1 : 4;
+  p->kernel = i;
+  p->split_steps = ceil_div(ceil_div(kb, splits), q) * q;
+  p->splits = ceil_div(kb, p->split_steps);
+  p->workspace = p->splits > 1 ? (size_t)p->splits * c.T * c.rows * sizeof(float) : 0;
+  return p->workspace <= kMaxPlanBytes;
 }
 
-float plan_time(const Fp8Plan& p) {
+float plan_time(const Fp8Call& c, const Fp8Plan& p) {
   const Fp8Kernel& k = kFp8Kernels[p.kernel];
   const float steps = (float)ceil_div(p.split_steps, k.k_waves);
   const float load_steps = (float)p.split_steps / k.k_waves;
-  const int64_t units = (int64_t)ceil_div(p.rows, k.rows) * ceil_div(p.T, k.tokens) * p.splits;
-  const float out = (float)p.T * p.rows;
-  const float bytes = ((float)p.rows * p.cols + 4.0f * out + k.x_share * (float)p.T * p.cols * p.rows / k.rows) * 1e-6f;
-  const float a = k.latency * steps, b = (float)((units + 255) / 256) * (k.rate * load_steps + k.unit), c = bytes / k.bw;
-  const float t = k.base + std::sqrt(std::sqrt(a * a * a * a + b * b * b * b + c * c * c * c));
+  const int64_t units = (int64_t)ceil_div(c.rows, k.rows) * ceil_div(c.T, k.tokens) * p.splits;
+  const float out = (float)c.T * c.rows;
+  const float bytes = ((float)c.rows * c.cols + 4.0f * out + k.x_share * (float)c.T * c.cols * c.rows / k.rows) * 1e-6f;
+  const float a = k.latency * steps, b = (float)((units + 255) / 256) * (k.rate * load_steps + k.unit), e = bytes / k.bw;
+  const float t = k.base + std::sqrt(std::sqrt(a * a * a * a + b * b * b * b + e * e * e * e));
   return p.splits > 1 ? t + 2.0f + k.join * p.splits * out * 8e-6f : t;
 }
 
-Fp8Plan make_plan(int rows, int cols, int T, bool fast) {
+Fp8Plan make_plan(const Fp8Call& c) {
   Fp8Plan best;
   float best_t = 0.0f;
   for (int i = 0; i < kNumFp8Kernels; ++i) {
-    const Fp8Kernel& k = kFp8Kernels[i];
-    if (T < k.min_T || T > k.max_T || !(fast ? k.fast : k.exact)) continue;
-    // a launch holds fewer than 2^32 threads, a block up to 512
-    if ((int64_t)ceil_div(rows, k.rows) * ceil_div(T, k.tokens) >= 1 << 22) continue;
+    if (c.T < kFp8Kernels[i].min_T || c.T > kFp8Kernels[i].max_T) continue;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
       Fp8Plan p;
-      p.rows = rows, p.cols = cols, p.T = T, p.fast = fast, p.kernel = i;
-      set_splits(p, s);
-      if (s > 1 && (p.splits != s || p.workspace() > kMaxPlanBytes)) continue;
-      const float t = plan_time(p);
-      if (best.rows == 0 || t < best_t) best = p, best_t = t;
+      if (!set_plan(c, i, s, &p) || p.splits != s) continue;
+      const float t = plan_time(c, p);
+      if (best.kernel < 0 || t < best_t) best = p, best_t = t;
     }
   }
   return best;
 }
 
-// VQMI_FP8_PLAN = "kernel,splits" (a row of the table) forces the choice, for
-// tests; a kernel that does not serve the call is passed over.
-bool forced_plan(Fp8Plan& p) {
-  const char* e = getenv("VQMI_FP8_PLAN");
-  int k = 0, s = 0;
-  if (!e || sscanf(e, "%d,%d", &k, &s) != 2 || k < 0 || k >= kNumFp8Kernels || s < 1 || s > 64) return false;
-  if (!(p.fast ? kFp8Kernels[k].fast : kFp8Kernels[k].exact)) return false;
-  p.kernel = k;
-  set_splits(p, s);
-  return true;
-}
-
-Fp8Plan fp8_plan(int rows, int cols, int T, bool fast) {
-  Fp8Plan p;
-  p.rows = rows, p.cols = cols, p.T = T, p.fast = fast;
-  if (forced_plan(p)) return p;
-  // the plans this thread made last (choosing takes a microsecond or two, and
-  // a call asks for its workspace first)
-  static thread_local Fp8Plan last[64];
-  Fp8Plan& slot = last[((unsigned)rows * 31u + (unsigned)cols * 7u + (unsigned)T * 2u + (unsigned)fast) % 64u];
-  if (slot.rows != rows || slot.cols != cols || slot.T != T || slot.fast != (int)fast)
-    slot = make_plan(rows, cols, T, fast);
-  return slot;
+Fp8Plan cached_plan(const Fp8Call& c) {
+  // the plans this thread made last (choosing takes a microsecond or two)
+  struct Slot {
+    Fp8Call call{};  // no rows: empty
+    Fp8Plan plan;
+  };
+  static thread_local Slot last[64];
+  Slot& slot = last[((unsigned)c.rows * 31u + (unsigned)c.cols * 7u + (unsigned)c.T * 2u + (unsigned)c.fast) % 64u];
+  if (!(slot.call == c)) slot.plan = make_plan(c), slot.call = c;
+  return slot.plan;
 }
 
 }  // namespace
@@ -760,13 +752,23 @@ hipError_t launch_fp8_quant(const void* x, int x_bf16, int T, int cols, uint8_t*
   return hipGetLastError();
 }
 
-size_t fp8_workspace_bytes(int rows, int cols, int T) {
-  return std::max(fp8_plan(rows, cols, T, false).workspace(), fp8_plan(rows, cols, T, true).workspace());
+// VQMI_FP8_PLAN = "kernel,splits" (a row of the table) forces the choice, for
+// tests; a kernel or split that set_plan refuses is passed over.
+Fp8Plans fp8_plans(int rows, int cols, int T) {
+  const char* e = getenv("VQMI_FP8_PLAN");
+  int k = 0, splits = 0;
+  const bool forced = e && sscanf(e, "%d,%d", &k, &splits) == 2 && k >= 0 && k < kNumFp8Kernels && splits >= 1 &&
+                      splits <= 64;
+  auto plan = [&](bool fast) {
+    const Fp8Call c{rows, cols, T, fast};
+    Fp8Plan p;
+    return forced && set_plan(c, k, splits, &p) ? p : cached_plan(c);
+  };
+  return {plan(false), plan(true)};
 }
 
-hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, bool fast, const uint8_t* x, const float* xs, int T,
-                           void* y, void* workspace, hipStream_t s) {
-  const Fp8Plan p = fp8_plan(w.rows, w.cols, T, fast);
+hipError_t launch_fp8_gemm(const Fp8View& w, const IoSpec& io, const Fp8Plan& p, const uint8_t* x, const float* xs,
+                           int T, void* y, void* workspace, hipStream_t s) {
   Fp8Args a{};
   a.w = w.values;
   a.ws = w.scales;
