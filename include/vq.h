@@ -432,7 +432,7 @@ typedef struct vq_fp8_tensor {
 
 /*
  * Quantize activations: for each token and 128 columns,
- *   scale = max |x| / 448 rounded to fp32 (1 for a block of zeros),
+ *   scale = max |x| / 448 rounded to fp32 (1 where that is 0),
  *   q = the e4m3 value nearest to x / scale (ties to even; exact, no double
  *       rounding), at most 448 in magnitude.
  * NaN and infinite x become NaN codes and do not count for the scale, so they

@@ -95,7 +95,8 @@ def fp8_quant(x):
     for b in range(scales.shape[1]):
         part = x[:, b * BLOCK:(b + 1) * BLOCK]
         amax = np.where(np.isfinite(part), np.abs(part), 0.0).max(axis=1)
-        s = np.where(amax > 0, amax / 448.0, 1.0).astype(np.float32)
+        s = (amax / 448.0).astype(np.float32)
+        s = np.where(s > 0, s, np.float32(1.0))
         scales[:, b] = s
         # the float64 quotient of an fp16/bf16 value and an fp32 scale lies on
         # a tie (5 bits) only if it is one: x = tie * s has at most 29 bits

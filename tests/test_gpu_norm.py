@@ -196,3 +196,22 @@ def test_only_one_output_and_empty_batch():
     assert only[0] is None and torch.equal(only[1], h)
     e = binding.norm(torch.zeros(0, 16, device="cuda"), h_dtype=torch.float8_e4m3fn)
     assert e[0].shape == (0, 16) and e[1].shape == (0, 16) and e[2].shape == (0, 1)
+
+
+def test_e4m3_output_of_the_smallest_values():
+    """Rows from fp32's smallest number to its smallest normal ones: the codes
+    and scales of the unrounded h (as the fp32 output shows it), a scale of one
+    where h / 448 rounds to nothing."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = synth.rng("norm", "smallest")
+    x = g.normal(size=(96, 144)) * 10.0 ** np.linspace(-45.5, -36, 96)[:, None]
+    x = torch.from_numpy(x.astype(np.float32)).cuda()
+    x[:, ::5] = 0
+    kw = dict(eps=1.0, store_residual=False)       # h = x but for its rounding
+    h = binding.norm(None, x, h_dtype=torch.float32, **kw)[1].double().cpu().numpy()
+    _, q, s = binding.norm(None, x, h_dtype=torch.float8_e4m3fn, **kw)
+    rq, rs = O.fp8_quant(h)
+    assert (rs == 1).any() and (rs < 1).any()
+    assert np.array_equal(s.cpu().numpy(), rs)
+    assert np.array_equal(q.view(torch.uint8).cpu().numpy(), rq)

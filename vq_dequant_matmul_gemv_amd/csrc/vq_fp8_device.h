@@ -31,8 +31,12 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 }
 
 // The scale of a block whose largest finite magnitude is amax: amax / 448
-// rounded to nearest (1 for a block of zeros).
-__device__ __forceinline__ float fp8_scale(float amax) { return amax > 0.0f ? __fdiv_rn(amax, kFp8Max) : 1.0f; }
+// rounded to nearest, or 1 where that is 0 (a block of zeros, or of values up
+// to 3e-43, which the e4m3 codes of x / 1 take as zeros too).
+__device__ __forceinline__ float fp8_scale(float amax) {
+  const float s = __fdiv_rn(amax, kFp8Max);
+  return s > 0.0f ? s : 1.0f;
+}
 
 // x / s on its way to the nearest e4m3 value: the fp32 quotient with its last
 // bit set where it is not exact ("rounded to odd"), so that the conversion's
