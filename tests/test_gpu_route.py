@@ -242,3 +242,17 @@ def test_groups_masked_by_the_lowest_bias(score, E, groups, T):
         k = min(64, top_groups * size)
         for gs in ("top2", "max"):
             _check(x, k, b, score=score, groups=groups, top_groups=top_groups, group_score=gs)
+
+
+def test_a_slot_count_out_of_range_allocates_nothing():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    x = torch.zeros(4096, 64, device="cuda")
+    binding.moe_route(binding.Router(64, 8), x)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for k in (65, 1 << 20, 1 << 30, 0, -1):
+        with pytest.raises(binding.VQError, match="top_k"):
+            binding.moe_route(binding.Router(64, k), x)
+    assert torch.cuda.max_memory_allocated() - before <= 1 << 20

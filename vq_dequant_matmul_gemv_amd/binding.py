@@ -563,10 +563,11 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
     if away is not None:
         with away:
             return moe_route(router, logits, ids, weights)
+    slots = k if 0 <= k <= 64 else 0  # the library refuses any other k: nothing is allocated for it
     if ids is None:
-        ids = _rows(T, max(k, 0), torch.int32, dev)
+        ids = _rows(T, slots, torch.int32, dev)
     if weights is None:
-        weights = _rows(T, max(k, 0), torch.float32, dev)
+        weights = _rows(T, slots, torch.float32, dev)
     cr = _pack_router(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
                       GROUP_SCORES[r.group_score], bool(r.renormalize), r.scale, 0, bias)
     check(LIB.vq_moe_route(cr, logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
