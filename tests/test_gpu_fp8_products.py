@@ -8,7 +8,7 @@ import pytest
 
 from oracle import block_oracle as O
 from tests.helpers import announce
-from tests.test_gpu_fp8 import _eps, _operands, _torch_dt
+from tests.test_gpu_fp8 import _eps, _operands, _product_check, _torch_dt
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,47 @@ def test_fast_swiglu_captured_and_on_another_stream(monkeypatch):
             assert torch.equal(y, g) and torch.equal(y, other) and torch.equal(y, binding.fp8_gemm(w, x, s, **kw))
     with pytest.raises(binding.VQError, match="F16 or BF16"):
         binding.fp8_gemm(w, x, s, fast=True)
+
+
+# ---- many tokens on the few-token kernels, and the planner's splits ----------
+
+@pytest.mark.parametrize("kernel", range(3))
+@pytest.mark.parametrize("splits", [1, 3])
+def test_few_token_kernels_on_many_tokens(kernel, splits, monkeypatch):
+    """The planner takes them for any number of tokens where rows are few."""
+    monkeypatch.setenv("VQMI_FP8_PLAN", f"{kernel},{splits}")
+    for T, R, C, dtype, epi in [(257, 34, 1200, "float32", None), (500, 18, 2000, "bfloat16", "swiglu"),
+                                (1030, 29, 640, "float16", None)]:
+        _product_check(_operands(T, R, C, ("many", T, R, C)), dtype, epi)
+        e = _run(_operands(T, R, C, ("many", T, R, C), 0.2), "float32")
+        assert _norm_error(e, O.fp8_product(*_operands(T, R, C, ("many", T, R, C), 0.2))[0]) <= SUMS + 2.0 ** -19
+
+
+@pytest.mark.parametrize("T,R,C", [(991, 29, 4400), (300, 64, 17408), (89, 290, 1280), (1012, 453, 160), (868, 175, 1008)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_rows_and_many_tokens_as_planned(T, R, C, dtype):
+    ops = _operands(T, R, C, ("planned", T, R, C), 0.2)
+    _product_check(ops, dtype)
+    assert _norm_error(_run(ops, dtype), O.fp8_product(*ops)[0]) <= SUMS + (ops[1].shape[1] + 4) * 2.0 ** -24 + (
+        _eps(_torch_dt(dtype)) if dtype != "float32" else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("T,R,C", [(40, 640, 17408), (16, 5120, 17408), (64, 512, 17408)])
+def test_planned_splits_within_the_fp32_bound(T, R, C):
+    """Shapes the planner splits, on a poisoned workspace of the stated size:
+    elementwise the bound of exact products summed in fp32 (128 roundings of
+    2^-23 a block, the blocks, planes and scales 2^-24 each), and the 2-norm."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    need = binding.LIB.vq_fp8_workspace_bytes(R, C, T)
+    assert need > 0
+    xc, xs, wc, ws = ops = _operands(T, R, C, ("planned-split", T), 0.2)
+    w = binding.FP8Tensor(torch.from_numpy(wc).cuda(), torch.from_numpy(ws).cuda())
+    buf = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    y = binding.fp8_gemm(w, torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), workspace=buf[:need])
+    torch.cuda.synchronize()
+    assert torch.all(buf[need:] == 0xff).item()
+    got = y.double().cpu().numpy()
+    ref, mag = O.fp8_product(*ops)
+    assert np.all(np.abs(got - ref) <= mag * (128 * 2.0 ** -23 + (xs.shape[1] + 24 + 4) * 2.0 ** -24) + 2.0 ** -24 * np.abs(ref))
+    assert _norm_error(got, ref) <= SUMS + (xs.shape[1] + 28) * 2.0 ** -24
