@@ -7,6 +7,7 @@
 // The times below are those of calls replayed from a graph over weights that
 // do not stay in the caches, on a card that copies at 5.06 TB/s and reaches
 // 3.2 PFLOP/s in the library's e4m3 product of 8192 x 8192 x 8192.
+#include "vq_block_device.h"
 #include "vq_fp8_device.h"
 #include "vq_block_kernels.h"
 
@@ -95,20 +96,14 @@ struct Fp8Args {
   int split_steps;  // column blocks a split (the last one may have fewer)
 };
 
-// One wave's LDS writes before its later reads of other lanes' values (LDS
-// runs a wave's accesses in order: only the compiler is held back).
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // silu(g) * u, silu(g) = g / (1 + exp(-g)), by the instructions for 2^x and
 // 1 / x (within a unit each).  PRECISE, for an fp32 y: with e = exp(-|g|),
 // g / (1 + e), or g * e / (1 + e) for a negative g, so that nothing overflows,
 // and the exponent's product with log2(e) carried in two parts (one rounded
-// product would cost |g| units): 6 units in all.  Else, for 16 bits, the one
-// product, whose |g| units of 2^-24 are far below a half unit of 16 bits.
+// product would cost |g| units): 6 units in all, down to g = -87.3, where silu
+// is -1.1e-36 and e falls below the normal numbers: 0 from there on.  Else, for
+// 16 bits, the one product, whose |g| units of 2^-24 are far below a half unit
+// of 16 bits.
 // (35.7 million of them behind the tile kernel at 2048 tokens, 17408 rows:
 // expf() and a division 16 us, the precise form 10, the other 8.)
 template <bool PRECISE>
@@ -354,12 +349,12 @@ __global__ __launch_bounds__(64 * WAVES) void vq_fp8_skinny_kernel(Fp8Args args)
 //     the next LDS read;
 //   - one barrier a step, two buffers, pieces XORed so that reads of 8 rows
 //     touch all banks.
-// 2048 tokens x 17408 x 5120 in bf16: 189 to 200 us on different cards, 1.8 to
-// 1.9 PFLOP/s (10 us more with SwiGLU; the library's e4m3 product with one
-// scale for each whole tensor takes 205 there); 4096 x 8192 x 8192: 246 us,
-// 2.23 PFLOP/s.  Those are the e4m3 instructions (vq_fp8_gemm_fast).  Exact
-// products cost four fp16 instructions of 16 cycles for one e4m3 of 32, and
-// their conversions: 384 us with an fp32 y.
+// 2048 tokens x 17408 x 5120 in bf16: 182 to 201 us on different cards, 1.8 to
+// 2.0 PFLOP/s, with SwiGLU (half the outputs) the same; 4096 x 8192 x 8192: 230
+// to 249 us, 2.2 to 2.4 PFLOP/s.  Those are the e4m3 instructions
+// (vq_fp8_gemm_fast).  Exact products cost four fp16 instructions of 16 cycles
+// for one e4m3 of 32, and their conversions: 370 to 384 us there for any y, and
+// 499 at 4096 x 8192 x 8192 (1.0 and 1.1 PFLOP/s).
 // ---------------------------------------------------------------------------
 typedef int int8v __attribute__((ext_vector_type(8)));
 
@@ -629,11 +624,13 @@ void run_skinny(const Fp8Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_fp8_skinny_kernel<WAVES, NT, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 21200
+// The kernels of the product and a time model of each (us), fitted to 21180
 // measured calls (1 to 4096 tokens, 32 to 34816 rows, 256 to 17408 columns, 1
 // to 24 splits), the faster ones of a shape weighing more; the fit's error is
-// 6-13 % rms, and the model's choice takes 1.7 % longer than the best one on
-// average, 0.2 % for products of more than 100 us:
+// 6-13 % rms.  The model's choice takes 1.7 % longer than the best one on
+// average, 0.2 to 0.3 % for products of more than 100 us; exact products with
+// a bf16 y, measured afterwards, 1.9 and 0.2 % (the calls and the fit:
+// profiles/fp8_product_calls.txt, profiles/fp8_plan_fit.py):
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
 // with steps the column blocks a wave runs through, rounds of 256 blocks, and

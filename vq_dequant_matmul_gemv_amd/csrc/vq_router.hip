@@ -34,7 +34,7 @@
 // 24 with two, 19 with four and the close ones put in order by one exponential
 // a lane (5 us less than a token's full 64-bit pass, which the last wave of a
 // launch used to end with: 2048 grouped tokens 10 to 12 -> 7.8).
-#include "vq_device.h"
+#include "vq_block_device.h"
 #include "vq_block_kernels.h"
 
 #include <cfloat>
@@ -43,7 +43,7 @@ namespace vqmi {
 
 namespace {
 
-constexpr int kRouterWaves = 4;  // tokens per block
+constexpr int kRouterWaves = 4;  // per block; a wave routes 64 / LPT tokens
 
 // Floats and doubles as unsigned integers of the same order, never 0 for a
 // number above -inf: 0 stands for "out of play".  -0 counts as +0.
@@ -110,13 +110,6 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 __device__ __forceinline__ float order_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
-// One wave's LDS writes before its later reads of other lanes' values.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 struct RouterArgs {
@@ -191,8 +184,10 @@ __device__ __forceinline__ float in_play(float l, float bias) {
 // Slot `lane` of a token's LPT lanes: stores the chosen expert (-1: none) and
 // its weight, in fp32.  Renormalised weights come from the chosen logits alone,
 // relative to the largest of them, so they hold where the scores underflow
-// (zero where a score is below the smallest 64-bit number).  m, inv_z: largest
-// logit in play and inverse sum of the softmax.
+// fp32.  Zero where the score would be zero in 64 bits: a sigmoid whose exp(-l)
+// overflows (l < -709.78, a score of 5.6e-309), a softmax whose exp(l - m) is
+// below the smallest 64-bit number.  m, inv_z: largest logit in play and
+// inverse sum of the softmax.
 template <int LPT>
 __device__ __forceinline__ void store_slot(const RouterArgs& a, int64_t t, int lane, int id, float l, float m,
                                            float inv_z, bool write) {
@@ -356,12 +351,15 @@ __global__ __launch_bounds__(64 * kRouterWaves) void vq_router_kernel(RouterArgs
   // Keys in fp32.  A sigmoid is off by less than 2^-22: s (1 - s) times the
   // exponential's relative error of 1.22 |l| 2^-24 (argument) and 2^-23 makes
   // 0.77 * 2^-24, the sum below the reciprocal 2^-24, the reciprocal 2^-23.
-  // The softmax's sum Z = sum e^-x is off by less than 33 * 2^-24 of itself:
-  // 1.22 * 2^-24 times the mean of x (at most the entropy's log 1024), 2^-23
-  // and 22 additions; so a score is off by less than 39 * 2^-24 < 2^-18 of the
-  // largest possible one, 1 / Z.  The sum with a bias adds 2^-24 of itself, so
-  // two keys near v are certainly in order when they differ by more than
-  // margin(v).
+  // The softmax's x = m - l rounds before that product: 2.22 |x| 2^-24 in the
+  // argument.  Its sum Z = sum e^-x is off by less than 40 * 2^-24 of itself:
+  // 2.22 * 2^-24 times the mean of x (at most the entropy's log 1024 = 6.94:
+  // 15.4), 2 * 2^-24 of an exponential and 22 additions.  So a score is off by
+  // less than 46 * 2^-24 of the largest possible one, 1 / Z: Z's 40, the
+  // reciprocal's and the product's 2, and its own exponential's 2.22 x e^-x <=
+  // 0.82 and 2.  The slack allows 64 * 2^-24 = 2^-18.  The sum with a bias adds
+  // 2^-24 of itself, so two keys near v are certainly in order when they differ
+  // by more than margin(v).
   const float slack = sigmoid ? 0x1p-21f : inv_z * 0x1p-17f;  // twice a score's error
   auto margin = [&](float v) { return fmaf(fabsf(v), 0x1.2p-23f, slack); };
   bool close = false;  // the whole token again in 64 bits

@@ -31,7 +31,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 ENCODER_SOURCES = ("vq_encode.hip",)
-BLOCK_SOURCES = ("vq_block_kernels.h", "vq_fp8.hip", "vq_fp8_device.h", "vq_norm.hip", "vq_router.hip")
+BLOCK_SOURCES = ("vq_block_device.h", "vq_block_kernels.h", "vq_fp8.hip", "vq_fp8_device.h", "vq_norm.hip", "vq_router.hip")
 
 
 def source_digest(part: str = "matmul") -> str:
