@@ -40,6 +40,7 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBPS = 8000.0          # MI355X HBM3E
 MFMA_F16_PEAK_TFLOPS = 2500.0   # MI355X dense fp16 MFMA
+MFMA_E4M3_PEAK_TFLOPS = 5000.0  # MI355X dense e4m3 MFMA
 
 WORKLOAD = "dense_mlp_5120x17408_d2k256"
 DECODE_T = 1
@@ -286,7 +287,7 @@ def configs_report(only=""):
 
     dev = torch.device("cuda", 0)
     from vq_dequant_matmul_gemv_amd.profsum import source_digest
-    out = [f"command: {REPORT_CMD}", f"kernel source digest: {source_digest()}",
+    out = [f"command: {REPORT_CMD} {only}".rstrip(), f"kernel source digest: {source_digest()}",
            f"encoder source digest: {source_digest('encoder')}",
            f"block operators' source digest: {source_digest('block')}", "",
            "vq_gemv hands token counts above its measured crossover to the MFMA kernel (the rows with",
@@ -318,12 +319,13 @@ def configs_report(only=""):
         del g
         return np.percentile(per, [50, 10, 90])
 
-    def row(wl, name, call, T, us, nbytes, flops):
+    def row(wl, name, call, T, us, nbytes, flops, peak=MFMA_F16_PEAK_TFLOPS):
         med = us[0]
         gbs = nbytes / med / 1e3
         tf = flops / med / 1e6
+        of = "" if peak == MFMA_F16_PEAK_TFLOPS else f" of {peak / 1e3:g} PF"
         out.append(f"| {wl} | {name} | {call} | {T} | {us[0]:.2f} ({us[1]:.2f}, {us[2]:.2f}) | {gbs:.0f} | "
-                   f"{100 * gbs / HBM_PEAK_GBPS:.1f} | {tf:.1f} | {100 * tf / MFMA_F16_PEAK_TFLOPS:.1f} |")
+                   f"{100 * gbs / HBM_PEAK_GBPS:.1f} | {tf:.1f} | {100 * tf / peak:.1f}{of} |")
         print(out[-1], file=sys.stderr, flush=True)
 
     def replicas(spec, host, nbytes, cap=2048):
@@ -605,35 +607,40 @@ def configs_report(only=""):
         def rand(*shape, dtype=f32):
             return torch.randn(shape, device=dev).to(dtype)
 
-        for T, kw, what in ((1, dict(), "softmax, top-8 of 256"), (16384, dict(), "softmax, top-8 of 256"),
-                            (16384, dict(score="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5),
-                             "sigmoid + bias, 4 of 8 groups, top-8 of 256")):
+        grouped = dict(score="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5)
+        for T, kw, what, dt in ((1, dict(), "softmax, top-8 of 256", f32), (16384, dict(), "softmax, top-8 of 256", f32),
+                                (16384, dict(), "softmax, top-8 of 256, bf16 logits", bf16),
+                                (16384, grouped, "sigmoid + bias, 4 of 8 groups, top-8 of 256", f32)):
             r = binding.Router(256, 8, bias=0.05 * rand(256) if kw else None, **kw)
-            xs = [rand(T, 256) for _ in range(4)]
+            xs = [rand(T, 256, dtype=dt) for _ in range(4)]
             ids, w = binding.moe_route(r, xs[0])
             us = timed([(lambda x=xs[i % 4]: binding.moe_route(r, x, ids, w)) for i in range(16)])
-            row(wl, what, "vq_moe_route", T, us, T * (256 * 4 + 64), 10.0 * T * 256)
+            row(wl, what, "vq_moe_route", T, us, T * (256 * xs[0].element_size() + 64), 10.0 * T * 256)
         for T, cols, dt in ((4, 17408, bf16), (4096, 5120, f16)):
             xs = [rand(T, cols, dtype=dt) for _ in range(6)]
             q, sc = binding.fp8_quant(xs[0])
             us = timed([(lambda x=xs[i % 6]: binding.fp8_quant(x, q, sc)) for i in range(12)])
             row(wl, f"{T}x{cols}", "vq_fp8_quant", T, us, 3 * T * cols, 2.0 * T * cols)
-        for T, rows, cols, ydt, epi in ((1, 17408, 5120, bf16, None), (16, 5120, 17408, f32, None),
-                                        (64, 5120, 5120, bf16, None), (197, 1001, 2000, f32, None),
-                                        (2048, 17408, 5120, bf16, "swiglu"), (2048, 17408, 5120, f32, None),
-                                        (4096, 8192, 8192, bf16, None)):
+        exact = [(1, 17408, 5120, bf16, None), (16, 5120, 17408, f32, None), (64, 5120, 5120, bf16, None),
+                 (128, 5120, 5120, bf16, None), (256, 5120, 5120, bf16, None), (197, 1001, 2000, f32, None),
+                 (300, 64, 17408, f32, None), (2048, 17408, 5120, bf16, "swiglu"), (2048, 17408, 5120, f32, None),
+                 (4096, 8192, 8192, bf16, None)]
+        e4m3_allowed = [(T, rows, cols, ydt, epi) for T, rows, cols, ydt, epi in exact if ydt == bf16 and T >= 64]
+        for T, rows, cols, ydt, epi, fast in [(*c, False) for c in exact] + [(*c, True) for c in e4m3_allowed]:
             n = int(max(1, min(8, 700e6 // (rows * cols))))
             ws = [binding.FP8Tensor(*_e4m3_weight(torch, rand(rows, cols))) for _ in range(n)]
             q, sc = binding.fp8_quant(rand(T, cols, dtype=bf16))
             y = torch.empty((T, rows // 2 if epi else rows), dtype=ydt, device=dev)
             need = binding.LIB.vq_fp8_workspace_bytes(rows, cols, T)
             wsp = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-            us = timed([(lambda w=ws[i % n]: binding.fp8_gemm(w, q, sc, y, wsp, epilogue=epi)) for i in range(16)])
-            row(wl, f"{rows}x{cols} {str(ydt)[6:]} y{' swiglu' if epi else ''}", "vq_fp8_gemm", T, us,
-                T * cols + rows * cols + y.numel() * y.element_size(), 2.0 * T * rows * cols)
+            us = timed([(lambda w=ws[i % n]: binding.fp8_gemm(w, q, sc, y, wsp, epilogue=epi, fast=fast))
+                        for i in range(16)])
+            row(wl, f"{rows}x{cols} {str(ydt)[6:]} y{' swiglu' if epi else ''}", f"vq_fp8_gemm{'_fast' * fast}", T, us,
+                T * cols + rows * cols + y.numel() * y.element_size(), 2.0 * T * rows * cols,
+                MFMA_E4M3_PEAK_TFLOPS if fast else MFMA_F16_PEAK_TFLOPS)
             del ws
         for T, cols, bdt, hdt in ((1, 5120, f32, bf16), (333, 2000, f16, e4m3), (4096, 5120, bf16, bf16),
-                                  (4096, 5120, f32, e4m3)):
+                                  (4096, 5119, bf16, bf16), (4096, 5120, f32, e4m3)):
             n = int(max(1, min(6, 800e6 // (T * cols * 8))))
             bl, res = [rand(T, cols, dtype=bdt) for _ in range(n)], [rand(T, cols, dtype=bf16) for _ in range(n)]
             w, g = rand(cols, dtype=bf16), rand(T, 1, dtype=bf16)
@@ -647,22 +654,43 @@ def configs_report(only=""):
                 us, T * cols * (bl[0].element_size() + 4 + o[1].element_size()), 12.0 * T * cols)
         torch.cuda.empty_cache()
 
+    def copy_context():
+        src = torch.empty(1 << 29, dtype=torch.float16, device=dev).normal_()
+        dst = torch.empty_like(src)
+        us = timed([lambda: dst.copy_(src)] * 8)
+        out.append(f"- plain stream (torch copy of 1 GiB fp16: 1 GiB read + 1 GiB written): {us[0]:.1f} us median = "
+                   f"{(2 << 30) / us[0] / 1e3:.0f} GB/s")
+
+    def product_context():
+        """The library's plain products at the e4m3 product's sizes."""
+        bf16, e4m3 = torch.bfloat16, torch.float8_e4m3fn
+        for M, K, N in ((8192, 8192, 8192), (2048, 5120, 17408)):
+            a, b = (torch.randn(r, K, device=dev).to(bf16) for r in (M, N))
+            one = torch.ones((), device=dev)
+            for what, us in (("bf16", timed([lambda: a @ b.t()] * 8)),
+                             ("e4m3, one scale a tensor,", timed([lambda x=a.to(e4m3), w=b.to(e4m3).t(): torch._scaled_mm(
+                                 x, w, scale_a=one, scale_b=one, out_dtype=bf16)] * 8))):
+                out.append(f"- torch {what} matmul (hipBLASLt), {M}x{K} by {N}x{K}: {us[0]:.1f} us = "
+                           f"{2.0 * M * K * N / us[0] / 1e6:.0f} TFLOP/s")
+            del a, b
+        torch.cuda.empty_cache()
+
     if keep("block"):
         block_rows("block operators")
     if keep("encoder"):
         encode_row(1024, 4096, 4, 8, 64, 16384, 10)
-    if only:
+    if only and not keep("block"):
         print("\n".join(out), flush=True)
         return
 
-    # context: a plain read and torch's fp16 GEMM on uncompressed weights
+    # context: a plain copy and torch's GEMMs on uncompressed weights
     out += ["", "context (same GPU, same run):", ""]
-    src = torch.empty(1 << 29, dtype=torch.float16, device=dev).normal_()
-    dst = torch.empty_like(src)
-    us = timed([lambda: dst.copy_(src)] * 8)
-    out.append(f"- plain stream (torch copy of 1 GiB fp16: 1 GiB read + 1 GiB written): {us[0]:.1f} us median = "
-               f"{(2 << 30) / us[0] / 1e3:.0f} GB/s")
-    del src, dst
+    copy_context()
+    if keep("block"):
+        product_context()
+    if only:
+        print("\n".join(out), flush=True)
+        return
     for (M, K, N) in ((17408, 5120, 2048), (17408, 5120, 4096), (5120, 17408, 4096)):
         a = torch.randn(M, K, device=dev, dtype=torch.float16)
         b = torch.randn(K, N, device=dev, dtype=torch.float16)
