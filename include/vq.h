@@ -33,8 +33,8 @@
  *
  * Conventions for every entry point:
  *   - Pointers named as device data point to device memory the caller owns.
- *     The library never allocates device memory; MoE-GEMM scratch comes from
- *     the caller's workspace.
+ *     The library never allocates device memory; scratch (vq_moe_gemm,
+ *     vq_encode, vq_fp8_gemm) comes from the caller's workspace.
  *   - fp16 values travel as uint16_t bit patterns.
  *   - `stream` is a hipStream_t (NULL = the default stream).  Work is enqueued
  *     on it without host synchronisation.
@@ -47,7 +47,8 @@
  *     id outside [0, num_experts) means "skip": that slot's output row is
  *     written as zeros.
  *   - Calls on one stream are ordered; the library keeps no state between
- *     calls apart from the thread-local error text.
+ *     calls apart from the thread-local error text and the thread's last plans
+ *     of vq_fp8_gemm, which depend on a call's sizes alone.
  */
 #ifndef VQMI_VQ_H
 #define VQMI_VQ_H
@@ -65,7 +66,7 @@ typedef enum {
   VQ_ERR_GEOMETRY = 2,  /* (d, log2_k, group) not supported                    */
   VQ_ERR_SHAPE = 3,     /* sizes inconsistent (see each check below)           */
   VQ_ERR_ALIGN = 4,     /* a buffer is not aligned as required                 */
-  VQ_ERR_WORKSPACE = 5, /* MoE-GEMM workspace missing or too small             */
+  VQ_ERR_WORKSPACE = 5, /* a call's workspace is missing or too small           */
   VQ_ERR_HIP = 6        /* a HIP runtime call or kernel launch failed          */
 } vq_status;
 
@@ -375,7 +376,9 @@ vq_status vq_encode(const float *w, int32_t rows, int32_t cols, int32_t d, int32
  *           the routed products) and weight 0.  Scores are compared in 64
  *           bits where they decide the choice.
  *   weight  scale * p_e, with renormalize scale * p_e / (sum of the chosen
- *           p_e; 0 where that sum is 0).
+ *           p_e; 0 where that sum is 0), in fp32.  A p_e that is 0 in 64 bits
+ *           (a sigmoid of l_e < -709.78, a softmax 745 below its largest
+ *           logit) counts as 0.
  * logits: device [T][num_experts] of logits_dtype (vq_dtype), aligned to
  * their element; expert_ids: device [T][top_k] int32 and route_weights:
  * device [T][top_k] fp32, 4-byte aligned; bias: device [num_experts] fp32,
