@@ -42,7 +42,7 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* x) {
 // Bound by its bytes: two read, one written and a scale per 128.  16 lanes of
 // 16 bytes make a block's maximum a matter of four DPP steps, no LDS, and its
 // loads and stores whole lines; the maximum is taken from the 16-bit patterns.
-// 4096 x 5120 in 15.0 us = 4.2 TB/s (13.2 where the input is still in the
+// 4096 x 5120 in 14.8 to 15.3 us = 4.1 to 4.2 TB/s (13.2 where the input is still in the
 // caches), 4 x 17408 in 2.3 us, a launch.
 // ---------------------------------------------------------------------------
 template <bool BF16>

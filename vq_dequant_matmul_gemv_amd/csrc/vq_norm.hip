@@ -336,7 +336,7 @@ void run_types(const NormArgs& a, hipStream_t s) {
 void run_norm(const NormArgs& a, hipStream_t s) {
   const int pieces = (a.cols + 7) / 8;
   // single columns, coalesced over the threads (1 x 5119: 5.6 us, 4096 x 5119:
-  // 72; with a branch on the type at every load they took 25 and 152)
+  // 72 to 75; with a branch on the type at every load they took 25 and 152)
   if (a.cols % 8 != 0) {
     if (pieces <= 1024) return run<1, 1, false, true, true, true>(a, s);
     if (pieces <= 2048) return run<1, 2, false, true, true, true>(a, s);

@@ -25,8 +25,8 @@
 // next one where that is all that is open, else over the whole token again.
 // (Scores in 64 bits throughout take 37 us where this takes 19.)
 //
-// 16384 tokens x 256 experts: 10.4 us (softmax, top 8, bf16; 11.6 in fp32), 18
-// to 19 us (sigmoid with a bias, 4 of 8 groups by their two best, top 8, fp32);
+// 16384 tokens x 256 experts: 10.6 us (softmax, top 8, bf16; 11.8 in fp32), 18
+// to 20 us (sigmoid with a bias, 4 of 8 groups by their two best, top 8, fp32);
 // one token 4.7 us.  The bytes
 // would take 3.5: it is bound by the vector instructions of the choices, about
 // 60 for each of the top_k + 1.  Few lanes with several experts each share a
