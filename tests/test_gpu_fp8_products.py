@@ -225,3 +225,20 @@ def test_planned_splits_within_the_fp32_bound(T, R, C):
     ref, mag = O.fp8_product(*ops)
     assert np.all(np.abs(got - ref) <= mag * (128 * 2.0 ** -23 + (xs.shape[1] + 24 + 4) * 2.0 ** -24) + 2.0 ** -24 * np.abs(ref))
     assert _norm_error(got, ref) <= SUMS + (xs.shape[1] + 28) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kernel", FAST[3:])
+@pytest.mark.parametrize("at", [0, 8, 56, 64, 72, 120])
+def test_fast_products_are_cut_by_their_own_eight_alone(kernel, at, monkeypatch):
+    """448 * 448 alone in one eight, 15 other eights of 20s in its block, -448 *
+    448 alone in the next block: the 20s stay whole (15 * 8 * 20 = 2400), where
+    a cut by a neighbour would take 4 of each."""
+    monkeypatch.setenv("VQMI_FP8_PLAN", f"{kernel},1")
+    T, R, C = 40, 130, 256
+    x, w = np.zeros((T, C)), np.zeros((R, C))
+    x[:, :128], w[:, :128] = 4.0, 5.0
+    x[:, at:at + 8] = 0
+    x[:, at] = x[:, 128 + at] = 448.0
+    w[:, at], w[:, 128 + at] = 448.0, -448.0
+    ops = (O.e4m3_nearest(x), _ones(T, R, C)[0], O.e4m3_nearest(w), _ones(T, R, C)[1])
+    assert np.all(_run(ops, "float16", fast=True) == 2400)
