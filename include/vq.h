@@ -34,7 +34,8 @@
  * Conventions for every entry point:
  *   - Pointers named as device data point to device memory the caller owns.
  *     The library never allocates device memory; scratch (vq_moe_gemm,
- *     vq_encode, vq_fp8_gemm) comes from the caller's workspace.
+ *     vq_encode, vq_fp8_gemm, vq_mx4_gemm, vq_mx4_moe) comes from the caller's
+ *     workspace.
  *   - fp16 values travel as uint16_t bit patterns.
  *   - `stream` is a hipStream_t (NULL = the default stream).  Work is enqueued
  *     on it without host synchronisation.
@@ -48,7 +49,7 @@
  *     written as zeros.
  *   - Calls on one stream are ordered; the library keeps no state between
  *     calls apart from the thread-local error text and the thread's last plans
- *     of vq_fp8_gemm, which depend on a call's sizes alone.
+ *     of vq_fp8_gemm and vq_mx4_gemm, which depend on a call's sizes alone.
  */
 #ifndef VQMI_VQ_H
 #define VQMI_VQ_H
@@ -150,8 +151,14 @@ typedef struct vq_tensor {
  * vq_moe_gemv_ex with cols > 20480 accept only y_dtype F32 and no SWIGLU.
  * A NULL io means the defaults.
  */
-/* E4M3: 8-bit values with block scales, for the calls that name it. */
-typedef enum { VQ_DTYPE_F32 = 0, VQ_DTYPE_F16 = 1, VQ_DTYPE_BF16 = 2, VQ_DTYPE_E4M3 = 3 } vq_dtype;
+/* E4M3 and E2M1: 8- and 4-bit values with block scales, for the calls that name them. */
+typedef enum {
+  VQ_DTYPE_F32 = 0,
+  VQ_DTYPE_F16 = 1,
+  VQ_DTYPE_BF16 = 2,
+  VQ_DTYPE_E4M3 = 3,
+  VQ_DTYPE_E2M1 = 4
+} vq_dtype;
 typedef enum { VQ_EPILOGUE_NONE = 0, VQ_EPILOGUE_SWIGLU = 1, VQ_EPILOGUE_COMBINE = 2 } vq_epilogue;
 
 typedef struct vq_io {
@@ -488,6 +495,115 @@ vq_status vq_fp8_gemm(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x,
                       void *y, void *workspace, size_t workspace_bytes, void *stream);
 vq_status vq_fp8_gemm_fast(const vq_fp8_tensor *w, const vq_io *io, const uint8_t *x, const float *x_scales,
                            int32_t T, void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Tensors in microscaled 4-bit floating point: OCP e2m1 values (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives: codes 0 to 7, plus 8 for the sign; no
+ * infinities, no NaN) with an e8m0 scale for each 32 columns (byte b stands for
+ * 2^(b - 127), 255 for NaN).  A value stands for code * scale, a block whose
+ * scale is 255 for NaN throughout.
+ *
+ * One tensor or a stack of experts: values [E][rows][cols/2], two codes a byte,
+ * the even column in the low half; scales [E][rows][cols/32].  rows >= 1; cols
+ * a positive multiple of 32, at most 2^20; num_experts >= 1 (else
+ * VQ_ERR_SHAPE).  value_bytes == E * rows * cols / 2 and scale_bytes == E *
+ * rows * cols / 32, so a short or sliced buffer is refused.  values 16-byte
+ * aligned; scales anywhere (4-byte aligned scales with cols a multiple of 128
+ * are read in whole words, which is faster).
+ * Activations: x [T][cols/2] with x_scales [T][cols/32], as vq_mx4_quant leaves
+ * them.
+ */
+typedef struct vq_mx4_tensor {
+  const uint8_t *values; /* device [E][rows][cols/2]                             */
+  const uint8_t *scales; /* device [E][rows][cols/32]                            */
+  int32_t rows;          /* output features per expert                           */
+  int32_t cols;          /* input features                                       */
+  int32_t num_experts;   /* E; 1 for a single tensor                             */
+  int32_t reserved;      /* must be 0                                            */
+  int64_t value_bytes;   /* number of bytes behind `values`                      */
+  int64_t scale_bytes;   /* number of bytes behind `scales`                      */
+} vq_mx4_tensor;
+
+/*
+ * Quantize x [T][cols] (activations, or the rows of a weight): for each row and
+ * 32 columns, with m = max |x|,
+ *   scale = 2^k, k = floor(log2(m)) - 2, at least -127; 1 where m is 0;
+ *   q = the e2m1 value nearest to x / scale (ties to the even code; exact), at
+ *       most 6 in magnitude (values above 6 * scale, where m is above it, stop
+ *       there); the sign of zeros is kept.
+ * A block that holds a NaN or an infinity gets the scale 255 and codes 0.
+ *   x: device [T][cols] of x_dtype (F32, F16 or BF16), 16-byte aligned;
+ *   q: device [T][cols/2], 16-byte aligned; scales: device [T][cols/32] bytes.
+ *   cols as for vq_mx4_tensor; T >= 0 (0 enqueues nothing), T * cols <= 2^34.
+ *
+ * vq_mx4_dequant: y[t][c] = code * scale, rounded to y_dtype (F32, F16 or BF16)
+ * once: exact in fp32 and bf16, and in fp16 where that can hold it (larger ones
+ * become infinite, smaller ones round).  y: device [T][cols], 16-byte aligned.
+ */
+vq_status vq_mx4_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t *q, uint8_t *scales,
+                       void *stream);
+vq_status vq_mx4_dequant(const uint8_t *q, const uint8_t *scales, int32_t T, int32_t cols, int32_t y_dtype, void *y,
+                         void *stream);
+
+/*
+ * Product with a 4-bit weight (num_experts == 1), y = x W^T:
+ *   io->x_dtype VQ_DTYPE_E2M1: x [T][cols/2] with x_scales [T][cols/32];
+ *   io->x_dtype F16 or BF16: x [T][cols], x_scales NULL.
+ * Products are exact, sums are in fp32 (4-bit x: the 32 products of a block sum
+ * exactly; sums below 2^-126 lose bits), y is rounded to its type once.  Any T:
+ * decode and prefill shapes run different kernels, and few output tiles may be
+ * split along the columns into planes of the workspace and joined in order, as
+ * a time model of the call rates best.  The same call gives the same bits every
+ * time; the order of the sums, and with it a row's last bits, depends on T.
+ * The environment variable VQMI_MX4_PLAN = "kernel,splits" forces the choice
+ * (for tests).
+ *   io: y_dtype F32, F16 or BF16, epilogue NONE or SWIGLU (interleaved gate/up
+ *     rows: y has rows / 2 values per token) as for vq_gemm_ex.  NULL: 4-bit x,
+ *     fp32 y, no epilogue.
+ *   x, y: device, 16-byte aligned; x_scales: device, any alignment.
+ *   workspace: device, >= vq_mx4_workspace_bytes(rows, cols, T) bytes (enough
+ *     for every x and y type and epilogue), 16-byte aligned, owned by the
+ *     caller (may be NULL where that is 0); contents on entry are ignored and
+ *     on return are undefined.  Calls that overlap in time need separate
+ *     workspaces.
+ * T >= 0 (0 enqueues nothing), T <= 2^24, rows <= 2^24, ceil(rows/16) *
+ * ceil(T/16) <= 2^30, and the call has to fit a launch (else VQ_ERR_SHAPE).
+ */
+size_t vq_mx4_workspace_bytes(int32_t rows, int32_t cols, int32_t T);
+vq_status vq_mx4_gemm(const vq_mx4_tensor *w, const vq_io *io, const void *x, const uint8_t *x_scales, int32_t T,
+                      void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens over stacks of 4-bit
+ * experts, from the router's logits to the weighted sum:
+ *   ids, weights = vq_moe_route(r, logits)
+ *   g, u = rows 2i and 2i + 1 of W_gate_up[e] x[t],  e = ids[t][s]
+ *   h[t][s][i] = silu(g) * u, kept in fp32
+ *   y[t] = sum over the slots s with ids[t][s] >= 0 of weights[t][s] *
+ *          W_down[e] h[t][s]
+ * Products are exact, sums are in fp32, y is rounded to its type once.  A token
+ * without an expert gets zeros.  Every expert's weights are read once per call
+ * (per 16 of its tokens): the call is for decode batches.  The same call gives
+ * the same bits every time; a token's last bits depend on the batch.
+ *   r: as for vq_moe_route, with num_experts those of both stacks;
+ *   gate_up: [E][2 * inter][hidden], interleaved gate and up rows; down:
+ *   [E][hidden][inter];
+ *   io: x_dtype F16 (default) or BF16, y_dtype F32 (default), F16 or BF16;
+ *   epilogue NONE;
+ *   logits: device [T][E] of r->logits_dtype, aligned to their element;
+ *   x: device [T][hidden], y: device [T][hidden], 16-byte aligned;
+ *   expert_ids: device [T][top_k] int32, route_weights: device [T][top_k]
+ *   fp32, 4-byte aligned: outputs, as vq_moe_route leaves them;
+ *   workspace: device, >= vq_mx4_moe_workspace_bytes(T, top_k, inter) bytes,
+ *   16-byte aligned, as for vq_mx4_gemm.
+ * 0 <= T <= 64 (0 enqueues nothing), T * top_k <= 1024, and T * top_k * inter
+ * <= 2^26 (else VQ_ERR_SHAPE; larger batches belong to vq_moe_route and products
+ * of their own).
+ */
+size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t inter);
+vq_status vq_mx4_moe(const vq_router *r, const vq_mx4_tensor *gate_up, const vq_mx4_tensor *down, const vq_io *io,
+                     const void *logits, const void *x, int32_t T, void *y, int32_t *expert_ids, float *route_weights,
+                     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * The norms before and after a block, fused with its gate and the scaled

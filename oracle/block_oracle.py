@@ -141,3 +141,81 @@ def norm(block=None, residual=None, *, post_weight=None, pre_weight=None, gate=N
     rms = np.sqrt((v * v).mean(axis=1, keepdims=True) + eps)
     w = 1.0 if pre_weight is None else f(pre_weight) + weight_offset
     return {"u": u * np.ones_like(v), "r": r * np.ones_like(v), "v": v, "rms": rms, "w": w, "h": v / rms * w}
+
+
+# ---------------------------------------------------------------------------
+# e2m1 with a power-of-two scale for each 32 columns
+# ---------------------------------------------------------------------------
+
+MX4_BLOCK = 32
+# value of every e2m1 code: sign, 2 exponent bits (bias 1), 1 mantissa bit
+E2M1 = np.array([(-1.0) ** (c >> 3) * ((c & 1) * 0.5 if ((c >> 1) & 3) == 0 else
+                                       (2 + (c & 1)) * 2.0 ** (((c >> 1) & 3) - 2)) for c in range(16)])
+
+
+def e2m1_nearest(v):
+    """Codes (uint8) of the e2m1 values nearest to finite float64 v, ties to
+    the even code, clamped to +-6."""
+    v = np.asarray(v, dtype=np.float64)
+    a = np.minimum(np.abs(v), 6.0)
+    grid = E2M1[:8]
+    up = np.clip(np.searchsorted(grid, a), 1, 7)
+    lo = up - 1
+    dl, du = a - grid[lo], grid[up] - a
+    code = np.where(dl < du, lo, np.where(du < dl, up, np.where(lo % 2 == 0, lo, up)))
+    return (code | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def mx4_pack(codes):
+    """Two codes a byte, the even column in the low half."""
+    return (codes[..., 0::2] | codes[..., 1::2] << 4).astype(np.uint8)
+
+
+def mx4_quant(x):
+    """(packed codes uint8 [T][C/2], scale bytes uint8 [T][C/32]) of x [T][C]."""
+    x = np.asarray(x, dtype=np.float64)
+    T, C = x.shape
+    part = x.reshape(T, C // MX4_BLOCK, MX4_BLOCK)
+    bad = ~np.isfinite(part).all(axis=2)
+    amax = np.abs(np.where(np.isfinite(part), part, 0.0)).max(axis=2)
+    k = np.where(amax > 0, np.frexp(amax)[1] - 3, 0)          # floor(log2) - 2
+    k = np.maximum(k, -127)
+    codes = e2m1_nearest(np.where(bad[..., None], 0.0, np.ldexp(np.where(bad[..., None], 0.0, part), -k[..., None])))
+    scales = np.where(bad, 255, k + 127).astype(np.uint8)
+    return mx4_pack(codes.reshape(T, C)), scales
+
+
+def mx4_values(q, s):
+    """float64 values [..][C] of packed codes [..][C/2] and scale bytes [..][C/32]."""
+    codes = np.stack([q & 15, q >> 4], axis=-1).reshape(*q.shape[:-1], -1)
+    scale = np.where(s == 255, np.nan, np.exp2(s.astype(np.float64) - 127))
+    return E2M1[codes] * np.repeat(scale, MX4_BLOCK, axis=-1)
+
+
+def swiglu(y):
+    """silu(even columns) * odd columns."""
+    a, b = y[..., 0::2], y[..., 1::2]
+    with np.errstate(over="ignore"):
+        return a / (1 + np.exp(-a)) * b
+
+
+def mx4_moe(ids, weights, x, gate_up, down):
+    """The layer's y [T][hidden] in float64, and the magnitudes its sums are of:
+    ids, weights [T][k], x [T][hidden], gate_up [E][2 * inter][hidden] and down
+    [E][hidden][inter] as values.  Returns (y, gu, gu_mag, h): per pair the
+    gate/up sums, their magnitudes' sums and the activations."""
+    T, k = ids.shape
+    gu = np.zeros((T, k, gate_up.shape[1]))
+    mag = np.zeros_like(gu)
+    h = np.zeros((T, k, gate_up.shape[1] // 2))
+    y = np.zeros((T, down.shape[1]))
+    for t in range(T):
+        for s in range(k):
+            e = ids[t, s]
+            if e < 0:
+                continue
+            gu[t, s] = gate_up[e] @ x[t]
+            mag[t, s] = np.abs(gate_up[e]) @ np.abs(x[t])
+            h[t, s] = swiglu(gu[t, s])
+            y[t] += weights[t, s] * (down[e] @ h[t, s])
+    return y, gu, mag, h

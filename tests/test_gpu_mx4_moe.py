@@ -1,0 +1,276 @@
+"""vq_mx4_moe against the routing and the 64-bit oracle: one token to 64, odd
+sizes, tokens and slots without an expert, shared experts, every type."""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as O
+from tests.helpers import announce
+from vq_dequant_matmul_gemv_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+
+def _dt(name):
+    import torch
+    return getattr(torch, name)
+
+
+class Layer:
+    def __init__(self, E, H, I, key, lo=116, hi=124):
+        import torch
+        from vq_dequant_matmul_gemv_amd import binding
+        g = synth.rng("mx4-moe", *key)
+        def stack(rows, cols):
+            return (g.integers(0, 256, (E, rows, cols // 2), dtype=np.uint8),
+                    g.integers(lo, hi + 1, (E, rows, cols // 32), dtype=np.uint8))
+        self.E, self.H, self.I = E, H, I
+        self.gu, self.dn = stack(2 * I, H), stack(H, I)
+        self.tensors = [binding.MX4Tensor(*(torch.from_numpy(t).cuda() for t in p)) for p in (self.gu, self.dn)]
+
+    def values(self):
+        return O.mx4_values(*self.gu), O.mx4_values(*self.dn)
+
+
+def _check(layer, router, logits, x, y_dtype="float32", **kw):
+    """The ids and weights are vq_moe_route's bit for bit.  With them, per pair:
+    the gate/up sums are off by at most 12 units of 2^-24 a block of 32 columns
+    and 36 (see the product's bounds), SwiGLU by the product rule and 16 units;
+    the activations enter the down products whole (three bf16 planes), 18 units
+    a block; the weighted sum over slots and the joins of the waves add 2 * top_k +
+    32 units of its magnitudes."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    T = x.shape[0]
+    announce("mx4_moe", T, layer.E, router.top_k, layer.H, layer.I, str(x.dtype), y_dtype, router)
+    dt = _dt(y_dtype)
+    buf = torch.full(((T + 1) * layer.H,), 55.0, dtype=dt, device="cuda")
+    y, ids, weights = binding.mx4_moe(router, *layer.tensors, logits, x, y=buf[:T * layer.H].view(T, layer.H), **kw)
+    torch.cuda.synchronize()
+    rid, rw = binding.moe_route(router, logits)
+    assert torch.equal(ids, rid) and torch.equal(weights, rw)
+    assert torch.all(buf[T * layer.H:] == 55.0).item()
+    gv, dv = layer.values()
+    ids, w = ids.cpu().numpy(), weights.double().cpu().numpy()
+    ref, gu, mag, h = O.mx4_moe(ids, w, x.double().cpu().numpy(), gv, dv)
+    u = 2.0 ** -24
+    e = mag * (12 * (layer.H // 32) + 36) * u
+    a, b, ea, eb = gu[..., 0::2], gu[..., 1::2], e[..., 0::2], e[..., 1::2]
+    silu = a / (1 + np.exp(-np.clip(a, -700, None)))
+    eh = 1.1 * ea * (np.abs(b) + eb) + np.abs(silu) * eb + 16 * u * np.abs(h)
+    err, total = np.zeros_like(ref), np.zeros_like(ref)
+    for t in range(T):
+        for s in range(ids.shape[1]):
+            if ids[t, s] >= 0:
+                m = np.abs(dv[ids[t, s]])
+                err[t] += np.abs(w[t, s]) * (m @ eh[t, s] + (18 * (layer.I // 32) + 4) * u * (m @ np.abs(h[t, s])))
+                total[t] += np.abs(w[t, s]) * (m @ np.abs(h[t, s]))
+    err += total * (2 * ids.shape[1] + 32) * u
+    eps = torch.finfo(dt).eps / 2
+    got = y.double().cpu().numpy()
+    tol = err + eps * (np.abs(ref) + err) + float(torch.finfo(dt).smallest_normal) * eps * 2
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], np.abs(got - ref)[bad][:4], tol[bad][:4])
+    return y
+
+
+def _inputs(T, E, H, key, dtype="bfloat16", logits="float32"):
+    import torch
+    g = synth.rng("mx4-moe-in", *key)
+    l = torch.from_numpy(1.5 * g.normal(size=(T, E)) + g.normal(size=E)).to(_dt(logits)).cuda()
+    return l, torch.from_numpy(g.normal(size=(T, H))).to(_dt(dtype)).cuda()
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 15, 16, 17, 31, 33, 47, 48, 49, 64])
+@pytest.mark.parametrize("E,k,H,I", [(8, 2, 64, 32), (16, 4, 160, 96), (40, 6, 288, 224)])
+def test_sizes(T, E, k, H, I):
+    from vq_dequant_matmul_gemv_amd import binding
+    _check(Layer(E, H, I, ("sizes", E, H)), binding.Router(E, k), *_inputs(T, E, H, ("sizes", T, E)))
+
+
+@pytest.mark.parametrize("x", ["float16", "bfloat16"])
+@pytest.mark.parametrize("y", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 20])
+def test_types(x, y, T):
+    from vq_dequant_matmul_gemv_amd import binding
+    _check(Layer(12, 256, 128, ("types",)), binding.Router(12, 3, renormalize=False),
+           *_inputs(T, 12, 256, ("types", T), x, x), y)
+
+
+@pytest.mark.parametrize("T", [1, 9, 40])
+def test_one_expert_for_all_and_every_expert_for_each(T):
+    """Sixteen tokens and more on one expert; all experts of a small layer."""
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(4, 96, 64, ("all",))
+    l, x = _inputs(T, 4, 96, ("all", T))
+    _check(layer, binding.Router(4, 4), l, x)
+    l[:, 2] = 50.0
+    _check(layer, binding.Router(4, 1), l, x)
+    _check(layer, binding.Router(4, 2, renormalize=False), l, x)
+
+
+@pytest.mark.parametrize("T,k", [(16, 64), (40, 20), (1, 64), (64, 16)])
+def test_many_slots(T, k):
+    from vq_dequant_matmul_gemv_amd import binding
+    _check(Layer(72, 64, 32, ("slots",)), binding.Router(72, k), *_inputs(T, 72, 64, ("slots", T)))
+
+
+def test_largest_router():
+    from vq_dequant_matmul_gemv_amd import binding
+    _check(Layer(1024, 64, 32, ("many",)), binding.Router(1024, 8), *_inputs(33, 1024, 64, ("many",)))
+
+
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_router_options(T):
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(32, 128, 64, ("router",))
+    l, x = _inputs(T, 32, 128, ("router", T))
+    bias = torch.linspace(-0.1, 0.1, 32, device="cuda")
+    _check(layer, binding.Router(32, 4, score="sigmoid", bias=bias, groups=8, top_groups=3, group_score="top2", scale=2.5),
+           l, x)
+    _check(layer, binding.Router(32, 4, score="sigmoid", renormalize=False), l, x)
+    _check(layer, binding.Router(32, 4, groups=4, top_groups=2, scale=-0.5), l, x)
+
+
+@pytest.mark.parametrize("T", [1, 6, 35])
+def test_tokens_and_slots_without_an_expert(T):
+    """Padded tokens (no expert in play) get zeros, fewer experts than slots
+    leave slots empty; NaN logits and the type's lowest value."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(10, 96, 96, ("masked",))
+    l, x = _inputs(T, 10, 96, ("masked", T))
+    l[:, 5] = torch.finfo(l.dtype).min
+    l[0, 3:] = -torch.inf
+    l[T // 2] = -torch.inf
+    l[-1, 1] = float("nan")
+    l[-1, 2] = float("inf")
+    y = _check(layer, binding.Router(10, 6, renormalize=False), l, x)
+    if T > 1:  # (a single token's row is also the one with the infinite logit)
+        assert torch.all(y[T // 2] == 0).item()
+    l[:] = -torch.inf
+    assert torch.all(_check(layer, binding.Router(10, 6), l, x) == 0).item()
+
+
+def test_nan_stays_in_its_token():
+    """A NaN activation spoils its token, a NaN scale of an expert the tokens
+    that chose it; others keep their bits."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(6, 96, 64, ("nan",))
+    l, x = _inputs(20, 6, 96, ("nan",))
+    r = binding.Router(6, 2)
+    ref, ids, _ = binding.mx4_moe(r, *layer.tensors, l, x)
+    bad = x.clone()
+    bad[7, 50] = float("nan")
+    y, _, _ = binding.mx4_moe(r, *layer.tensors, l, bad)
+    rest = torch.arange(20, device="cuda") != 7
+    assert torch.isnan(y[7]).all() and torch.equal(y[rest], ref[rest])
+    for t in layer.tensors:
+        keep = t.scales.clone()
+        t.scales[3] = 255
+        y, _, _ = binding.mx4_moe(r, *layer.tensors, l, x)
+        hit = (ids == 3).any(1)
+        assert hit.any() and not hit.all()
+        assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], ref[~hit])
+        t.scales.copy_(keep)
+
+
+@pytest.mark.parametrize("x", ["float16", "bfloat16"])
+def test_scales_fp16_cannot_hold_and_large_activations(x):
+    """Experts of very small and large scales; activations between the products
+    beyond 16-bit types."""
+    from vq_dequant_matmul_gemv_amd import binding
+    _check(Layer(6, 96, 64, ("low",), 60, 66), binding.Router(6, 2), *_inputs(9, 6, 96, ("low",), x))
+    _check(Layer(6, 96, 64, ("high",), 138, 150), binding.Router(6, 2), *_inputs(9, 6, 96, ("high",), x))
+
+
+@pytest.mark.parametrize("T", [1, 16, 50])
+def test_same_bits_again_other_stream_and_captured(T):
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(24, 256, 128, ("again",))
+    r = binding.Router(24, 4)
+    l, x = _inputs(T, 24, 256, ("again", T))
+    ref = binding.mx4_moe(r, *layer.tensors, l, x)
+    for a, b in zip(ref, binding.mx4_moe(r, *layer.tensors, l, x)):
+        assert torch.equal(a, b)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(binding.LIB.vq_mx4_moe_workspace_bytes(T, 4, 128), dtype=torch.uint8, device="cuda").fill_(0xff)
+    torch.cuda.synchronize()
+    y = torch.empty_like(ref[0])
+    ids, w = torch.empty_like(ref[1]), torch.empty_like(ref[2])
+    binding.mx4_moe(r, *layer.tensors, l, x, y=y, ids=ids, weights=w, workspace=ws, stream=st)
+    st.synchronize()
+    for a, b in zip(ref, (y, ids, w)):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = binding.mx4_moe(r, *layer.tensors, l, x)
+    for k in range(3):
+        nl, nx = _inputs(T, 24, 256, ("again", T, k))
+        l.copy_(nl)
+        x.copy_(nx)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, binding.mx4_moe(r, *layer.tensors, l, x)):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(24, 256, 128, ("two",))
+    r = binding.Router(24, 4)
+    ins = [_inputs(T, 24, 256, ("two", T)) for T in (3, 30)]
+    ref = [binding.mx4_moe(r, *layer.tensors, *i) for i in ins]
+    torch.cuda.synchronize()
+    got = []
+    for i in ins:
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            got.append([binding.mx4_moe(r, *layer.tensors, *i) for _ in range(4)][-1])
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_layer_between_norms():
+    """A routed block as a model runs it: norm, router product, the layer, a
+    shared 4-bit expert, the residual sum and the next norm."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    E, k, H, I, T = 16, 4, 256, 128, 11
+    layer = Layer(E, H, I, ("block",))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    res = torch.randn(T, H, device="cuda", generator=g)
+    pre = torch.ones(H, device="cuda").bfloat16()
+    gate = (0.1 * torch.randn(H, E, device="cuda", generator=g)).bfloat16()
+    shared = binding.MX4Tensor(*binding.mx4_quant(0.05 * torch.randn(H, H, device="cuda", generator=g)))
+
+    def block():
+        _, h, _ = binding.norm(None, res, pre_weight=pre, store_residual=False)
+        y, ids, w = binding.mx4_moe(binding.Router(E, k), *layer.tensors, h @ gate, h)
+        binding.norm(binding.mx4_gemm(shared, h), y, residual_out=y)
+        v, n, _ = binding.norm(y, res, pre_weight=pre)
+        return h, ids, w, y, v, n
+
+    h, ids, w, y, v, n = block()
+    torch.cuda.synchronize()
+    ref, _, _, _ = O.mx4_moe(ids.cpu().numpy(), w.double().cpu().numpy(), h.double().cpu().numpy(), *layer.values())
+    sh = O.mx4_values(shared.values.view(torch.uint8).cpu().numpy(), shared.scales.view(torch.uint8).cpu().numpy())
+    ref = ref + h.double().cpu().numpy() @ sh.T
+    scale = np.abs(ref).max()
+    assert np.abs(y.double().cpu().numpy() - ref).max() <= 1e-5 * scale
+    assert np.abs(v.double().cpu().numpy() - (ref + res.double().cpu().numpy())).max() <= 1e-5 * (scale + 5)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block()
+    for i in range(3):
+        res.copy_(torch.randn(T, H, device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, block()):
+            assert torch.equal(a, b)

@@ -27,7 +27,7 @@ class VQError(RuntimeError):
         self.message = message
 
 
-VQ_DTYPE_F32, VQ_DTYPE_F16, VQ_DTYPE_BF16, VQ_DTYPE_E4M3 = 0, 1, 2, 3
+VQ_DTYPE_F32, VQ_DTYPE_F16, VQ_DTYPE_BF16, VQ_DTYPE_E4M3, VQ_DTYPE_E2M1 = 0, 1, 2, 3, 4
 VQ_EPILOGUE_NONE, VQ_EPILOGUE_SWIGLU, VQ_EPILOGUE_COMBINE = 0, 1, 2
 EPILOGUES = {None: VQ_EPILOGUE_NONE, "none": VQ_EPILOGUE_NONE, "swiglu": VQ_EPILOGUE_SWIGLU,
              "combine": VQ_EPILOGUE_COMBINE}
@@ -70,6 +70,20 @@ class CFP8Tensor(ctypes.Structure):
         ("cols", ctypes.c_int32),
         ("value_bytes", ctypes.c_int64),
         ("scale_elems", ctypes.c_int64),
+    ]
+
+
+class CMX4Tensor(ctypes.Structure):
+    """Mirror of `vq_mx4_tensor`."""
+    _fields_ = [
+        ("values", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("value_bytes", ctypes.c_int64),
+        ("scale_bytes", ctypes.c_int64),
     ]
 
 
@@ -141,6 +155,12 @@ def _load():
         "vq_fp8_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
         "vq_fp8_gemm": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
         "vq_fp8_gemm_fast": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
+        "vq_mx4_quant": (i32, [P, i32, i32, i32, P, P, P]),
+        "vq_mx4_dequant": (i32, [P, P, i32, i32, i32, P, P]),
+        "vq_mx4_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "vq_mx4_gemm": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
+        "vq_mx4_moe_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "vq_mx4_moe": (i32, [P, P, P, P, P, P, i32, P, P, P, P, ctypes.c_size_t, P]),
         "vq_norm": (i32, [P, P, P, i32, P, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
         "vq_status_name": (ctypes.c_char_p, [i32]),
@@ -158,7 +178,8 @@ EXPORTED = ("vq_words_per_row", "vq_dequant", "vq_gemv", "vq_gemm", "vq_moe_gemv
             "vq_gemm_ex", "vq_moe_gemv_ex", "vq_moe_gemm_ex",
             "vq_moe_workspace_bytes", "vq_moe_gemm", "vq_moe_gemm_no_alloc", "vq_encode_workspace_bytes",
             "vq_encode", "vq_moe_route", "vq_fp8_quant", "vq_fp8_workspace_bytes", "vq_fp8_gemm",
-            "vq_fp8_gemm_fast", "vq_norm",
+            "vq_fp8_gemm_fast", "vq_mx4_quant", "vq_mx4_dequant", "vq_mx4_workspace_bytes", "vq_mx4_gemm",
+            "vq_mx4_moe_workspace_bytes", "vq_mx4_moe", "vq_norm",
             "vq_last_error", "vq_status_name")
 
 
@@ -463,10 +484,11 @@ SCORES = {"softmax": VQ_SCORE_SOFTMAX, "sigmoid": VQ_SCORE_SIGMOID}
 GROUP_SCORES = {"max": VQ_GROUP_MAX, "top2": VQ_GROUP_TOP2}
 
 
-# Descriptors as bytes, in the layouts of CRouter, CFP8Tensor, CIo and CNormSpec
+# Descriptors as bytes, in the layouts of CRouter, CFP8Tensor, CMX4Tensor, CIo and CNormSpec
 # (packing takes a third of a ctypes structure's time).
 _pack_router = struct.Struct("<8ifiQ").pack
 _pack_fp8 = struct.Struct("<QQiiqq").pack
+_pack_mx4 = struct.Struct("<QQ4iqq").pack
 _pack_io = struct.Struct("<4iQ").pack
 _pack_norm = struct.Struct("<8i4f3Q").pack
 
@@ -532,11 +554,10 @@ class Router:
     scale: float = 1.0
 
 
-def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
-    """Expert ids int32 [T][top_k] and route weights fp32 [T][top_k] for
-    moe_gemv / moe_gemm, from logits [T][num_experts] (fp32, fp16 or bf16)."""
-    torch = _torch()
-    r = router
+def _check_route(r, logits, ids, weights):
+    """(T, index of the GPU, address of the bias) of a router's call, after the
+    checks of its tensors."""
+    torch = _TORCH
     if r.score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
     if r.group_score not in GROUP_SCORES:
@@ -546,7 +567,6 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
         raise ValueError(f"logits must be [T][{r.num_experts}]")
     T, k = shape[0], r.top_k
     gpu = _gpu(logits)
-    dev = logits.device
     bias = 0
     if r.bias is not None:
         if r.bias.dtype != torch.float32 or r.bias.shape != (r.num_experts,):
@@ -559,19 +579,38 @@ def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
     if weights is not None:
         _check_out(weights, torch.float32, (T, k), "weights")
         _placed(weights, gpu)
-    away = _elsewhere(dev, stream)
-    if away is not None:
-        with away:
-            return moe_route(router, logits, ids, weights)
+    return T, gpu, bias
+
+
+def _route_outputs(T, k, ids, weights, dev):
+    """ids and weights, allocated where they are None."""
+    torch = _TORCH
     slots = k if 0 <= k <= 64 else 0  # the library refuses any other k: nothing is allocated for it
     if ids is None:
         ids = _rows(T, slots, torch.int32, dev)
     if weights is None:
         weights = _rows(T, slots, torch.float32, dev)
-    cr = _pack_router(r.num_experts, k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
-                      GROUP_SCORES[r.group_score], bool(r.renormalize), r.scale, 0, bias)
-    check(LIB.vq_moe_route(cr, logits.data_ptr(), T, ids.data_ptr(), weights.data_ptr(),
-                           _raw_stream(gpu)))
+    return ids, weights
+
+
+def _packed_router(r, logits, bias):
+    return _pack_router(r.num_experts, r.top_k, SCORES[r.score], _dtype_code(logits.dtype), r.groups, r.top_groups,
+                        GROUP_SCORES[r.group_score], bool(r.renormalize), r.scale, 0, bias)
+
+
+def moe_route(router: Router, logits, ids=None, weights=None, stream=None):
+    """Expert ids int32 [T][top_k] and route weights fp32 [T][top_k] for
+    moe_gemv / moe_gemm, from logits [T][num_experts] (fp32, fp16 or bf16)."""
+    _torch()
+    T, gpu, bias = _check_route(router, logits, ids, weights)
+    dev = logits.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return moe_route(router, logits, ids, weights)
+    ids, weights = _route_outputs(T, router.top_k, ids, weights, dev)
+    check(LIB.vq_moe_route(_packed_router(router, logits, bias), logits.data_ptr(), T, ids.data_ptr(),
+                           weights.data_ptr(), _raw_stream(gpu)))
     return ids, weights
 
 
@@ -690,6 +729,225 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
                _pack_io(VQ_DTYPE_E4M3, _dtype_code(y_dtype), EPILOGUES[epilogue], 0, 0), x.data_ptr(),
                x_scales.data_ptr(), T, y.data_ptr(), wptr, wbytes, _raw_stream(gpu)))
     return y
+
+
+# --------------------------------------------------------------------------
+# 4-bit tensors with a scale for each 32 columns
+# --------------------------------------------------------------------------
+
+def _mx4_bytes(t, what, scales=False):
+    """The tensor holds e2m1 codes, two a byte (or e8m0 scales), as torch's type of that name or uint8."""
+    torch = _TORCH
+    own = torch.float8_e8m0fnu if scales else torch.float4_e2m1fn_x2
+    if t.dtype not in (own, torch.uint8):
+        raise ValueError(f"{what} must be {own} or uint8, got {t.dtype}")
+
+
+@dataclass
+class MX4Tensor:
+    """Device-resident 4-bit weight or stack of experts (see `vq_mx4_tensor` in
+    include/vq.h).
+
+    values  float4_e2m1fn_x2 (or uint8), two codes a byte: [rows][cols/2] or [E][rows][cols/2]
+    scales  float8_e8m0fnu (or uint8) [rows][cols/32] or [E][rows][cols/32]
+    """
+    values: object
+    scales: object
+
+    @property
+    def device(self):
+        return self.values.device
+
+    def checked(self, name="w"):
+        """(experts, rows, cols, index of the GPU both tensors are on), after
+        the checks of their types, shapes and places."""
+        _torch()
+        v, s = self.values, self.scales
+        _mx4_bytes(v, f"{name}.values")
+        _mx4_bytes(s, f"{name}.scales", scales=True)
+        shape = v.shape
+        if len(shape) == 2:
+            experts, (rows, half) = 1, shape
+        elif len(shape) == 3:
+            experts, rows, half = shape
+        else:
+            raise ValueError(f"{name}.values must be [rows][cols/2] or [E][rows][cols/2]")
+        cols = 2 * half
+        if cols % 32 != 0 or s.shape != (*shape[:-1], cols // 32):
+            raise ValueError(f"{name}.scales must hold one byte for each 32 columns, {(*shape[:-1], cols / 32)}, got "
+                             f"{tuple(s.shape)}")
+        gpu = _gpu(v)
+        _placed(s, gpu)
+        return experts, rows, cols, gpu
+
+    def cstruct(self) -> CMX4Tensor:
+        experts, rows, cols, _ = self.checked()
+        return CMX4Tensor(self.values.data_ptr(), self.scales.data_ptr(), rows, cols, experts, 0, self.values.numel(),
+                          self.scales.numel())
+
+
+def mx4_quant(x, q=None, scales=None, stream=None):
+    """float4_e2m1fn_x2 values [T][cols/2] and float8_e8m0fnu scales
+    [T][cols/32] of fp32, fp16 or bf16 x [T][cols] (vq_mx4_quant)."""
+    torch = _torch()
+    code = _dtype_code(x.dtype)
+    if x.dim() != 2 or x.shape[1] % 32 != 0:
+        raise ValueError("x must be [T][cols] with cols a multiple of 32")
+    T, cols = x.shape
+    gpu = _gpu(x)
+    dev = x.device
+    if q is not None:
+        _mx4_bytes(q, "q")
+        _check_out(q, q.dtype, (T, cols // 2), "q")
+        _placed(q, gpu)
+    if scales is not None:
+        _mx4_bytes(scales, "scales", scales=True)
+        _check_out(scales, scales.dtype, (T, cols // 32), "scales")
+        _placed(scales, gpu)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return mx4_quant(x, q, scales)
+    if q is None:
+        q = _rows(T, cols // 2, torch.float4_e2m1fn_x2, dev)
+    if scales is None:
+        scales = _rows(T, cols // 32, torch.float8_e8m0fnu, dev)
+    check(LIB.vq_mx4_quant(x.data_ptr(), code, T, cols, q.data_ptr(), scales.data_ptr(), _raw_stream(gpu)))
+    return q, scales
+
+
+def mx4_dequant(q, scales, dtype=None, y=None, stream=None):
+    """The values [T][cols] (bf16, or fp32 or fp16) of 4-bit codes [T][cols/2]
+    and scales [T][cols/32] (vq_mx4_dequant)."""
+    torch = _torch()
+    _mx4_bytes(q, "q")
+    _mx4_bytes(scales, "scales", scales=True)
+    if q.dim() != 2 or q.shape[1] % 16 != 0:
+        raise ValueError("q must be [T][cols/2] with cols a multiple of 32")
+    T, cols = q.shape[0], 2 * q.shape[1]
+    if scales.shape != (T, cols // 32):
+        raise ValueError(f"scales must be {(T, cols // 32)}")
+    dtype = y.dtype if (y is not None and dtype is None) else (dtype or torch.bfloat16)
+    code = _dtype_code(dtype)
+    gpu = _gpu(q)
+    dev = q.device
+    _placed(scales, gpu)
+    if y is not None:
+        _check_out(y, dtype, (T, cols))
+        _placed(y, gpu)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return mx4_dequant(q, scales, dtype, y)
+    if y is None:
+        y = _rows(T, cols, dtype, dev)
+    check(LIB.vq_mx4_dequant(q.data_ptr(), scales.data_ptr(), T, cols, code, y.data_ptr(), _raw_stream(gpu)))
+    return y
+
+
+def mx4_gemm(w: MX4Tensor, x, x_scales=None, y=None, workspace=None, stream=None, y_dtype=None, epilogue=None):
+    """y = x W^T with a 4-bit weight through vq_mx4_gemm, decode and prefill
+    alike.  x: 4-bit values [T][cols/2] with x_scales [T][cols/32], or fp16 or
+    bf16 [T][cols] without; epilogue "swiglu" on interleaved gate/up rows gives
+    silu(gate) * up."""
+    torch = _torch()
+    experts, rows, cols, gpu = w.checked()
+    if experts != 1:
+        raise ValueError("mx4_gemm takes one tensor, not a stack of experts")
+    half = x.dtype == torch.float16 or x.dtype == torch.bfloat16
+    if half:
+        if x_scales is not None:
+            raise ValueError("16-bit x takes no x_scales")
+    else:
+        _mx4_bytes(x, "x (if not fp16 or bf16)")
+        if x_scales is None:
+            raise ValueError("4-bit x needs x_scales")
+        _mx4_bytes(x_scales, "x_scales", scales=True)
+    if x.dim() != 2 or x.shape[1] != (cols if half else cols // 2):
+        raise ValueError(f"x must be [T][{cols}] in 16 bits, or [T][{cols // 2}] bytes of 4-bit values")
+    T = x.shape[0]
+    if not half and x_scales.shape != (T, cols // 32):
+        raise ValueError(f"x_scales must be {(T, cols // 32)}")
+    if epilogue not in EPILOGUES or epilogue == "combine":
+        raise ValueError("epilogue must be None or 'swiglu'")
+    y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
+    yshape = (T, rows // 2 if epilogue == "swiglu" else rows)
+    dev = x.device
+    _placed(x, gpu)
+    if not half:
+        _placed(x_scales, gpu)
+    if y is not None:
+        _check_out(y, y_dtype, yshape)
+        _placed(y, gpu)
+    if workspace is not None:
+        _placed(workspace, gpu)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return mx4_gemm(w, x, x_scales, y, workspace, None, y_dtype, epilogue)
+    if y is None:
+        y = _rows(*yshape, y_dtype, dev)
+    if workspace is None:
+        need = LIB.vq_mx4_workspace_bytes(rows, cols, T)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
+    v, s = w.values, w.scales
+    check(LIB.vq_mx4_gemm(_pack_mx4(v.data_ptr(), s.data_ptr(), rows, cols, 1, 0, v.numel(), s.numel()),
+                          _pack_io(_dtype_code(x.dtype) if half else VQ_DTYPE_E2M1, _dtype_code(y_dtype),
+                                   EPILOGUES[epilogue], 0, 0),
+                          x.data_ptr(), _address(x_scales), T, y.data_ptr(), wptr, wbytes, _raw_stream(gpu)))
+    return y
+
+
+def mx4_moe(router: Router, gate_up: MX4Tensor, down: MX4Tensor, logits, x, y=None, ids=None, weights=None,
+            workspace=None, stream=None, y_dtype=None):
+    """A mixture-of-experts layer for up to 64 tokens through vq_mx4_moe: routes
+    logits [T][E], runs x [T][hidden] (fp16 or bf16) through each token's experts
+    (gate_up [E][2 * inter][hidden] with interleaved rows, SwiGLU, down
+    [E][hidden][inter]) and adds them up by their weights.  Returns (y
+    [T][hidden], ids [T][top_k], weights [T][top_k])."""
+    torch = _torch()
+    T, gpu, bias = _check_route(router, logits, ids, weights)
+    E, rows, hidden, g = gate_up.checked("gate_up")
+    E2, hidden2, inter, g2 = down.checked("down")
+    if g != gpu or g2 != gpu:
+        raise ValueError(f"experts on cuda:{g} and cuda:{g2}, logits on cuda:{gpu}")
+    if E != router.num_experts or E2 != E or hidden2 != hidden or rows != 2 * inter:
+        raise ValueError(f"gate_up {(E, rows, hidden)} and down {(E2, hidden2, inter)} must be (E, 2 * inter, hidden) "
+                         f"and (E, hidden, inter) with the router's {router.num_experts} experts")
+    if x.dtype not in (torch.float16, torch.bfloat16) or x.shape != (T, hidden):
+        raise ValueError(f"x must be fp16 or bf16 {(T, hidden)}")
+    _placed(x, gpu)
+    y_dtype = y.dtype if (y is not None and y_dtype is None) else (y_dtype or torch.float32)
+    if y is not None:
+        _check_out(y, y_dtype, (T, hidden))
+        _placed(y, gpu)
+    if workspace is not None:
+        _placed(workspace, gpu)
+    dev = x.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return mx4_moe(router, gate_up, down, logits, x, y, ids, weights, workspace, None, y_dtype)
+    ids, weights = _route_outputs(T, router.top_k, ids, weights, dev)
+    if y is None:
+        y = _rows(T, hidden, y_dtype, dev)
+    if workspace is None:
+        need = LIB.vq_mx4_moe_workspace_bytes(T, router.top_k, inter)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
+    gv, gs, dv, ds = gate_up.values, gate_up.scales, down.values, down.scales
+    check(LIB.vq_mx4_moe(_packed_router(router, logits, bias),
+                         _pack_mx4(gv.data_ptr(), gs.data_ptr(), rows, hidden, E, 0, gv.numel(), gs.numel()),
+                         _pack_mx4(dv.data_ptr(), ds.data_ptr(), hidden, inter, E, 0, dv.numel(), ds.numel()),
+                         _pack_io(_dtype_code(x.dtype), _dtype_code(y_dtype), VQ_EPILOGUE_NONE, 0, 0),
+                         logits.data_ptr(), x.data_ptr(), T, y.data_ptr(), ids.data_ptr(), weights.data_ptr(), wptr,
+                         wbytes, _raw_stream(gpu)))
+    return y, ids, weights
 
 
 # --------------------------------------------------------------------------

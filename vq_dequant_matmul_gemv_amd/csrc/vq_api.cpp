@@ -411,50 +411,64 @@ vq_status vq_encode(const float* w, int32_t rows, int32_t cols, int32_t d, int32
                     "vq_encode launch");
 }
 
+// Checks a router and its call's buffers (not T) and fills `sp`; `fn` names the
+// entry point in errors.
+static vq_status check_router(const char* fn, const vq_router* r, vqmi::RouterSpec* sp) {
+  if (!r) return fail(VQ_ERR_NULL, "%s: router descriptor is NULL", fn);
+  const int32_t E = r->num_experts;
+  if (E < 1 || E > 1024) return fail(VQ_ERR_SHAPE, "%s: num_experts=%d outside [1, 1024]", fn, E);
+  if (r->groups < 1 || r->groups > 64 || E % r->groups != 0)
+    return fail(VQ_ERR_SHAPE, "%s: groups=%d must be in [1, 64] and divide num_experts=%d", fn, r->groups, E);
+  if (r->top_groups < 1 || r->top_groups > r->groups)
+    return fail(VQ_ERR_SHAPE, "%s: top_groups=%d outside [1, groups=%d]", fn, r->top_groups, r->groups);
+  if (r->top_k < 1 || r->top_k > 64 || r->top_k > r->top_groups * (E / r->groups))
+    return fail(VQ_ERR_SHAPE, "%s: top_k=%d must be in [1, 64] and at most the %d experts of %d groups", fn, r->top_k,
+                r->top_groups * (E / r->groups), r->top_groups);
+  if (r->score != VQ_SCORE_SOFTMAX && r->score != VQ_SCORE_SIGMOID)
+    return fail(VQ_ERR_SHAPE, "%s: score=%d is not a vq_score", fn, r->score);
+  if (r->group_score != VQ_GROUP_MAX && r->group_score != VQ_GROUP_TOP2)
+    return fail(VQ_ERR_SHAPE, "%s: group_score=%d is not a vq_group_score", fn, r->group_score);
+  if (r->logits_dtype != VQ_DTYPE_F32 && r->logits_dtype != VQ_DTYPE_F16 && r->logits_dtype != VQ_DTYPE_BF16)
+    return fail(VQ_ERR_SHAPE, "%s: logits_dtype=%d is not a vq_dtype", fn, r->logits_dtype);
+  if (r->renormalize != 0 && r->renormalize != 1)
+    return fail(VQ_ERR_SHAPE, "%s: renormalize=%d must be 0 or 1", fn, r->renormalize);
+  if (!std::isfinite(r->scale)) return fail(VQ_ERR_SHAPE, "%s: scale is not finite", fn);
+  if (r->reserved != 0) return fail(VQ_ERR_SHAPE, "%s: reserved must be 0", fn);
+  sp->num_experts = E;
+  sp->top_k = r->top_k;
+  sp->sigmoid = r->score == VQ_SCORE_SIGMOID;
+  sp->logits_kind = dtype_kind(r->logits_dtype);
+  sp->groups = r->groups;
+  sp->top_groups = r->top_groups;
+  sp->top2 = r->group_score == VQ_GROUP_TOP2;
+  sp->renorm = r->renormalize;
+  sp->scale = r->scale;
+  sp->bias = r->bias;
+  return VQ_OK;
+}
+
+static vq_status check_route_buffers(const char* fn, const vqmi::RouterSpec& sp, const void* logits,
+                                     const int32_t* expert_ids, const float* route_weights) {
+  if (!logits || !expert_ids || !route_weights)
+    return fail(VQ_ERR_NULL, "%s: a required pointer is NULL (logits=%p expert_ids=%p route_weights=%p)", fn, logits,
+                (const void*)expert_ids, (const void*)route_weights);
+  if (!aligned(logits, sp.logits_kind == vqmi::kOutF32 ? 4 : 2))
+    return fail(VQ_ERR_ALIGN, "%s: logits are not aligned to their element", fn);
+  if (!aligned(expert_ids, 4) || !aligned(route_weights, 4) || !aligned(sp.bias, 4))
+    return fail(VQ_ERR_ALIGN, "%s: expert_ids, route_weights and bias need 4-byte alignment", fn);
+  return VQ_OK;
+}
+
 vq_status vq_moe_route(const vq_router* r, const void* logits, int32_t T, int32_t* expert_ids,
                        float* route_weights, void* stream) {
-  if (!r) return fail(VQ_ERR_NULL, "vq_moe_route: router descriptor is NULL");
-  const int32_t E = r->num_experts;
-  if (E < 1 || E > 1024) return fail(VQ_ERR_SHAPE, "vq_moe_route: num_experts=%d outside [1, 1024]", E);
-  if (r->groups < 1 || r->groups > 64 || E % r->groups != 0)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: groups=%d must be in [1, 64] and divide num_experts=%d", r->groups, E);
-  if (r->top_groups < 1 || r->top_groups > r->groups)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: top_groups=%d outside [1, groups=%d]", r->top_groups, r->groups);
-  if (r->top_k < 1 || r->top_k > 64 || r->top_k > r->top_groups * (E / r->groups))
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: top_k=%d must be in [1, 64] and at most the %d experts of %d groups",
-                r->top_k, r->top_groups * (E / r->groups), r->top_groups);
-  if (r->score != VQ_SCORE_SOFTMAX && r->score != VQ_SCORE_SIGMOID)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: score=%d is not a vq_score", r->score);
-  if (r->group_score != VQ_GROUP_MAX && r->group_score != VQ_GROUP_TOP2)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: group_score=%d is not a vq_group_score", r->group_score);
-  if (r->logits_dtype != VQ_DTYPE_F32 && r->logits_dtype != VQ_DTYPE_F16 && r->logits_dtype != VQ_DTYPE_BF16)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: logits_dtype=%d is not a vq_dtype", r->logits_dtype);
-  if (r->renormalize != 0 && r->renormalize != 1)
-    return fail(VQ_ERR_SHAPE, "vq_moe_route: renormalize=%d must be 0 or 1", r->renormalize);
-  if (!std::isfinite(r->scale)) return fail(VQ_ERR_SHAPE, "vq_moe_route: scale is not finite");
-  if (r->reserved != 0) return fail(VQ_ERR_SHAPE, "vq_moe_route: reserved must be 0");
+  vqmi::RouterSpec sp{};
+  vq_status st = check_router("vq_moe_route", r, &sp);
+  if (st != VQ_OK) return st;
   // (a launch holds fewer than 2^32 threads, here and below)
   if (T < 0 || T > (1 << 25)) return fail(VQ_ERR_SHAPE, "vq_moe_route: T=%d outside [0, 2^25]", T);
   if (T == 0) return VQ_OK;
-  if (!logits || !expert_ids || !route_weights)
-    return fail(VQ_ERR_NULL, "vq_moe_route: a required pointer is NULL (logits=%p expert_ids=%p route_weights=%p)",
-                logits, (const void*)expert_ids, (const void*)route_weights);
-  const int kind = dtype_kind(r->logits_dtype);
-  if (!aligned(logits, kind == vqmi::kOutF32 ? 4 : 2))
-    return fail(VQ_ERR_ALIGN, "vq_moe_route: logits are not aligned to their element");
-  if (!aligned(expert_ids, 4) || !aligned(route_weights, 4) || !aligned(r->bias, 4))
-    return fail(VQ_ERR_ALIGN, "vq_moe_route: expert_ids, route_weights and bias need 4-byte alignment");
-  vqmi::RouterSpec sp{};
-  sp.num_experts = E;
-  sp.top_k = r->top_k;
-  sp.sigmoid = r->score == VQ_SCORE_SIGMOID;
-  sp.logits_kind = kind;
-  sp.groups = r->groups;
-  sp.top_groups = r->top_groups;
-  sp.top2 = r->group_score == VQ_GROUP_TOP2;
-  sp.renorm = r->renormalize;
-  sp.scale = r->scale;
-  sp.bias = r->bias;
+  st = check_route_buffers("vq_moe_route", sp, logits, expert_ids, route_weights);
+  if (st != VQ_OK) return st;
   return hip_status(vqmi::launch_router(sp, logits, T, expert_ids, route_weights, (hipStream_t)stream),
                     "vq_moe_route launch");
 }
@@ -561,6 +575,190 @@ vq_status vq_fp8_gemm(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x,
 vq_status vq_fp8_gemm_fast(const vq_fp8_tensor* w, const vq_io* io, const uint8_t* x, const float* x_scales,
                            int32_t T, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   return fp8_product(true, w, io, x, x_scales, T, y, workspace, workspace_bytes, stream);
+}
+
+// Columns of a 4-bit tensor: whole blocks of 32.
+static bool mx4_cols_ok(int32_t cols) { return cols >= 32 && cols % 32 == 0 && cols <= (1 << 20); }
+
+static bool plain_dtype(int32_t dt) { return dt == VQ_DTYPE_F32 || dt == VQ_DTYPE_F16 || dt == VQ_DTYPE_BF16; }
+
+// T rows of vq_mx4_quant and vq_mx4_dequant: 2^34 values are 2^31 threads.
+static vq_status check_mx4_rows(const char* fn, int32_t dtype, int32_t T, int32_t cols) {
+  if (!plain_dtype(dtype)) return fail(VQ_ERR_SHAPE, "%s: dtype=%d must be F32, F16 or BF16", fn, dtype);
+  if (!mx4_cols_ok(cols)) return fail(VQ_ERR_SHAPE, "%s: cols=%d must be a multiple of 32 in [32, 2^20]", fn, cols);
+  if (T < 0 || (int64_t)T * cols > (int64_t)1 << 34)
+    return fail(VQ_ERR_SHAPE, "%s: T=%d out of range for cols=%d", fn, T, cols);
+  return VQ_OK;
+}
+
+vq_status vq_mx4_quant(const void* x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t* q, uint8_t* scales,
+                       void* stream) {
+  vq_status st = check_mx4_rows("vq_mx4_quant", x_dtype, T, cols);
+  if (st != VQ_OK || T == 0) return st;
+  st = check_xy(x, q, "q");
+  if (st != VQ_OK) return st;
+  if (!scales) return fail(VQ_ERR_NULL, "vq_mx4_quant: scales is NULL");
+  return hip_status(vqmi::launch_mx4_quant(x, dtype_kind(x_dtype), (int64_t)T * cols, q, scales, (hipStream_t)stream),
+                    "vq_mx4_quant launch");
+}
+
+vq_status vq_mx4_dequant(const uint8_t* q, const uint8_t* scales, int32_t T, int32_t cols, int32_t y_dtype, void* y,
+                         void* stream) {
+  vq_status st = check_mx4_rows("vq_mx4_dequant", y_dtype, T, cols);
+  if (st != VQ_OK || T == 0) return st;
+  if (!q || !scales || !y)
+    return fail(VQ_ERR_NULL, "vq_mx4_dequant: a required pointer is NULL (q=%p scales=%p y=%p)", (const void*)q,
+                (const void*)scales, y);
+  if (!aligned(q, 16) || !aligned(y, 16))
+    return fail(VQ_ERR_ALIGN, "vq_mx4_dequant: q and y need 16-byte alignment");
+  return hip_status(vqmi::launch_mx4_dequant(q, scales, (int64_t)T * cols, y, dtype_kind(y_dtype), (hipStream_t)stream),
+                    "vq_mx4_dequant launch");
+}
+
+// A 4-bit tensor's descriptor; `what` names it in errors.
+static vq_status check_mx4_tensor(const char* fn, const char* what, const vq_mx4_tensor* w) {
+  if (!w) return fail(VQ_ERR_NULL, "%s: %s descriptor is NULL", fn, what);
+  if (!w->values || !w->scales)
+    return fail(VQ_ERR_NULL, "%s: %s has a NULL pointer (values=%p scales=%p)", fn, what, (const void*)w->values,
+                (const void*)w->scales);
+  if (w->rows < 1 || w->rows > (1 << 24)) return fail(VQ_ERR_SHAPE, "%s: %s rows=%d outside [1, 2^24]", fn, what, w->rows);
+  if (!mx4_cols_ok(w->cols))
+    return fail(VQ_ERR_SHAPE, "%s: %s cols=%d must be a multiple of 32 in [32, 2^20]", fn, what, w->cols);
+  if (w->num_experts < 1 || w->num_experts > (1 << 16))
+    return fail(VQ_ERR_SHAPE, "%s: %s num_experts=%d outside [1, 2^16]", fn, what, w->num_experts);
+  if (w->reserved != 0) return fail(VQ_ERR_SHAPE, "%s: %s reserved must be 0", fn, what);
+  const int64_t blocks = (int64_t)w->num_experts * w->rows * (w->cols / 32);
+  if (w->value_bytes != 16 * blocks || w->scale_bytes != blocks)
+    return fail(VQ_ERR_SHAPE,
+                "%s: %s holds %lld bytes of values and %lld of scales, but %d x %d x %d take %lld and %lld: sliced, or "
+                "of another layout",
+                fn, what, (long long)w->value_bytes, (long long)w->scale_bytes, w->num_experts, w->rows, w->cols,
+                (long long)(16 * blocks), (long long)blocks);
+  if (!aligned(w->values, 16)) return fail(VQ_ERR_ALIGN, "%s: %s values are not 16-byte aligned", fn, what);
+  return VQ_OK;
+}
+
+static vq_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return VQ_OK;
+  if (!workspace) return fail(VQ_ERR_WORKSPACE, "%s: workspace is NULL (need %zu bytes)", fn, need);
+  if (bytes < need) return fail(VQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, need %zu", fn, bytes, need);
+  if (!aligned(workspace, 16)) return fail(VQ_ERR_ALIGN, "%s: workspace is not 16-byte aligned", fn);
+  return VQ_OK;
+}
+
+static vq_status check_mx4_sizes(const char* fn, int32_t rows, int32_t cols, int32_t T) {
+  if (rows < 1 || rows > (1 << 24)) return fail(VQ_ERR_SHAPE, "%s: rows=%d outside [1, 2^24]", fn, rows);
+  if (!mx4_cols_ok(cols)) return fail(VQ_ERR_SHAPE, "%s: cols=%d must be a multiple of 32 in [32, 2^20]", fn, cols);
+  if (T < 0 || T > (1 << 24)) return fail(VQ_ERR_SHAPE, "%s: T=%d outside [0, 2^24]", fn, T);
+  if ((int64_t)((rows + 15) / 16) * ((T + 15) / 16) > (1 << 30))
+    return fail(VQ_ERR_SHAPE, "%s: T=%d x %d rows makes too many tiles", fn, T, rows);
+  return VQ_OK;
+}
+
+size_t vq_mx4_workspace_bytes(int32_t rows, int32_t cols, int32_t T) {
+  if (check_mx4_sizes("vq_mx4_workspace_bytes", rows, cols, T) != VQ_OK) return 0;
+  return T == 0 ? 0 : vqmi::mx4_plans(rows, cols, T).workspace();
+}
+
+vq_status vq_mx4_gemm(const vq_mx4_tensor* w, const vq_io* io, const void* x, const uint8_t* x_scales, int32_t T,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* const fn = "vq_mx4_gemm";
+  vq_status st = check_mx4_tensor(fn, "w", w);
+  if (st != VQ_OK) return st;
+  if (w->num_experts != 1) return fail(VQ_ERR_SHAPE, "%s: num_experts=%d: one tensor", fn, w->num_experts);
+  st = check_mx4_sizes(fn, w->rows, w->cols, T);
+  if (st != VQ_OK) return st;
+  vqmi::IoSpec ios{};
+  int x_kind = vqmi::kMx4XMx4;
+  if (io) {
+    if (io->x_dtype != VQ_DTYPE_E2M1 && io->x_dtype != VQ_DTYPE_F16 && io->x_dtype != VQ_DTYPE_BF16)
+      return fail(VQ_ERR_SHAPE, "%s: io->x_dtype=%d must be E2M1, F16 or BF16", fn, io->x_dtype);
+    if (!plain_dtype(io->y_dtype))
+      return fail(VQ_ERR_SHAPE, "%s: io->y_dtype=%d must be F32, F16 or BF16", fn, io->y_dtype);
+    if (io->epilogue != VQ_EPILOGUE_NONE && io->epilogue != VQ_EPILOGUE_SWIGLU)
+      return fail(VQ_ERR_SHAPE, "%s: io->epilogue=%d: NONE or SWIGLU", fn, io->epilogue);
+    if (io->reserved != 0) return fail(VQ_ERR_SHAPE, "%s: io->reserved must be 0", fn);
+    if (io->epilogue == VQ_EPILOGUE_SWIGLU && w->rows % 2 != 0)
+      return fail(VQ_ERR_SHAPE, "%s: SWIGLU needs interleaved (gate, up) row pairs: rows=%d is odd", fn, w->rows);
+    ios.y_kind = dtype_kind(io->y_dtype);
+    ios.epi = io->epilogue == VQ_EPILOGUE_SWIGLU ? vqmi::kEpiSwiglu : vqmi::kEpiNone;
+    x_kind = io->x_dtype == VQ_DTYPE_E2M1 ? vqmi::kMx4XMx4 : io->x_dtype == VQ_DTYPE_F16 ? vqmi::kMx4XF16
+                                                                                          : vqmi::kMx4XBF16;
+  }
+  if (T == 0) return VQ_OK;
+  const vqmi::Mx4Plans plans = vqmi::mx4_plans(w->rows, w->cols, T);
+  const vqmi::Mx4Plan& plan = x_kind == vqmi::kMx4XMx4 ? plans.mx4 : plans.x16;
+  if (plan.kernel < 0) return fail(VQ_ERR_SHAPE, "%s: T=%d x %d rows makes too many tiles", fn, T, w->rows);
+  st = check_xy(x, y, "y");
+  if (st != VQ_OK) return st;
+  if (x_kind == vqmi::kMx4XMx4 && !x_scales) return fail(VQ_ERR_NULL, "%s: x_scales is NULL", fn);
+  if (x_kind != vqmi::kMx4XMx4 && x_scales) return fail(VQ_ERR_SHAPE, "%s: 16-bit x takes no x_scales", fn);
+  st = check_workspace(fn, workspace, workspace_bytes, plans.workspace());
+  if (st != VQ_OK) return st;
+  const vqmi::Mx4View v{w->values, w->scales, w->rows, w->cols};
+  return hip_status(vqmi::launch_mx4_gemm(v, ios, plan, x, x_kind, x_scales, T, y, workspace, (hipStream_t)stream),
+                    "vq_mx4_gemm launch");
+}
+
+// Sizes of a layer call that its workspace depends on.
+static vq_status check_mx4_moe_sizes(const char* fn, int32_t T, int32_t top_k, int32_t inter) {
+  if (T < 0 || T > vqmi::kMx4MoeTokens)
+    return fail(VQ_ERR_SHAPE, "%s: T=%d outside [0, %d]", fn, T, vqmi::kMx4MoeTokens);
+  if (top_k < 1 || top_k > 64 || T * top_k > vqmi::kMx4MoePairs)
+    return fail(VQ_ERR_SHAPE, "%s: T=%d x top_k=%d outside [0, %d] (top_k in [1, 64])", fn, T, top_k,
+                vqmi::kMx4MoePairs);
+  if (!mx4_cols_ok(inter) || (int64_t)T * top_k * inter > (1 << 26))
+    return fail(VQ_ERR_SHAPE, "%s: inter=%d must be a multiple of 32, T * top_k * inter at most 2^26", fn, inter);
+  return VQ_OK;
+}
+
+size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t inter) {
+  if (check_mx4_moe_sizes("vq_mx4_moe_workspace_bytes", T, top_k, inter) != VQ_OK) return 0;
+  return T == 0 ? 0 : vqmi::mx4_moe_workspace_bytes(T, top_k, inter);
+}
+
+vq_status vq_mx4_moe(const vq_router* r, const vq_mx4_tensor* gate_up, const vq_mx4_tensor* down, const vq_io* io,
+                     const void* logits, const void* x, int32_t T, void* y, int32_t* expert_ids, float* route_weights,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* const fn = "vq_mx4_moe";
+  vqmi::RouterSpec sp{};
+  vq_status st = check_router(fn, r, &sp);
+  if (st != VQ_OK) return st;
+  st = check_mx4_tensor(fn, "gate_up", gate_up);
+  if (st != VQ_OK) return st;
+  st = check_mx4_tensor(fn, "down", down);
+  if (st != VQ_OK) return st;
+  if (gate_up->num_experts != r->num_experts || down->num_experts != r->num_experts)
+    return fail(VQ_ERR_SHAPE, "%s: the router has %d experts, gate_up %d and down %d", fn, r->num_experts,
+                gate_up->num_experts, down->num_experts);
+  if (down->rows != gate_up->cols || gate_up->rows != 2 * (int64_t)down->cols)
+    return fail(VQ_ERR_SHAPE, "%s: gate_up is %d x %d, so down must be %d x %d, not %d x %d", fn, gate_up->rows,
+                gate_up->cols, gate_up->cols, gate_up->rows / 2, down->rows, down->cols);
+  st = check_mx4_moe_sizes(fn, T, r->top_k, down->cols);
+  if (st != VQ_OK) return st;
+  int x_kind = vqmi::kMx4XF16, y_kind = vqmi::kOutF32;
+  if (io) {
+    if (io->x_dtype != VQ_DTYPE_F16 && io->x_dtype != VQ_DTYPE_BF16)
+      return fail(VQ_ERR_SHAPE, "%s: io->x_dtype=%d must be F16 or BF16", fn, io->x_dtype);
+    if (!plain_dtype(io->y_dtype))
+      return fail(VQ_ERR_SHAPE, "%s: io->y_dtype=%d must be F32, F16 or BF16", fn, io->y_dtype);
+    if (io->epilogue != VQ_EPILOGUE_NONE || io->reserved != 0)
+      return fail(VQ_ERR_SHAPE, "%s: io->epilogue and io->reserved must be 0", fn);
+    x_kind = io->x_dtype == VQ_DTYPE_F16 ? vqmi::kMx4XF16 : vqmi::kMx4XBF16;
+    y_kind = dtype_kind(io->y_dtype);
+  }
+  if (T == 0) return VQ_OK;
+  st = check_route_buffers(fn, sp, logits, expert_ids, route_weights);
+  if (st != VQ_OK) return st;
+  st = check_xy(x, y, "y");
+  if (st != VQ_OK) return st;
+  st = check_workspace(fn, workspace, workspace_bytes, vqmi::mx4_moe_workspace_bytes(T, r->top_k, down->cols));
+  if (st != VQ_OK) return st;
+  const vqmi::Mx4View gu{gate_up->values, gate_up->scales, gate_up->rows, gate_up->cols};
+  const vqmi::Mx4View dn{down->values, down->scales, down->rows, down->cols};
+  return hip_status(vqmi::launch_mx4_moe(sp, gu, dn, logits, x, x_kind, T, y, y_kind, expert_ids, route_weights,
+                                         workspace, (hipStream_t)stream),
+                    "vq_mx4_moe launch");
 }
 
 vq_status vq_norm(const vq_norm_spec* n, const void* block, const void* residual, int32_t T, void* residual_out,
