@@ -284,18 +284,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_fp8_tile_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t cols = a.cols, kb = a.kb;
 
-  // XCD-aware order: blocks land on XCD (block % 8); each XCD takes a
-  // contiguous range of tiles, which run through up to 8 token tiles of one
-  // row tile before the next.
   const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
   int rt, tt;
-  {
-    const int n = row_tiles * tok_tiles, q = n / 8, r8 = n % 8, xcd = blockIdx.x % 8, j = blockIdx.x / 8;
-    const int tile = xcd * q + min(xcd, r8) + j;
-    const int g = tile / (8 * row_tiles), rem = tile - g * 8 * row_tiles, width = min(8, tok_tiles - 8 * g);
-    rt = rem / width;
-    tt = 8 * g + rem % width;
-  }
+  xcd_tile(blockIdx.x, row_tiles, tok_tiles, &rt, &tt);
   const int r0 = rt * kTileRows, t0 = tt * kTileTokens;
   const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * cols, (uint64_t)min(kTileRows, a.rows - r0) * cols);
   const rsrc_t xr = make_rsrc(a.x + (int64_t)t0 * cols, (uint64_t)min(kTileTokens, a.T - t0) * cols);

@@ -198,6 +198,211 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
   if (t < a.T) store_rows4(a, t, r0 + g * 4, v);
 }
 
+// ---------------------------------------------------------------------------
+// product, many tokens, 4-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
+// block, steps of 256 columns (8 blocks, 128 bytes a row)
+// ---------------------------------------------------------------------------
+template <bool PRECISE, int WM, int WN, int MT, int NT, int AHEAD>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(Mx4Args args) {
+  const Mx4Args a = split_args(args);
+  constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
+  constexpr int kLoadRows = 8 * kWaves;  // rows the block loads at once
+  constexpr int kWLoads = kTileRows / kLoadRows, kXLoads = kTileTokens / kLoadRows, kLoads = kWLoads + kXLoads;
+  static_assert(kTileRows % kLoadRows == 0 && kTileTokens % kLoadRows == 0, "whole loads");
+  static_assert(kTileRows + kTileTokens <= 64 * kWaves && kTileRows % 64 == 0 && kTileTokens % 32 == 0,
+                "a thread loads one row's scales, a wave those of one operand");
+  static_assert(NT % (AHEAD + 1) == 0, "a ring of operands");
+  __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
+  __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
+  __shared__ __align__(1024) u32x4 lds_s[2][64 * kWaves];  // scales of two steps, a row a thread, twice
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t blocks = a.blocks, pitch = blocks * 16;
+  const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
+  int rt, tt;
+  xcd_tile(blockIdx.x, row_tiles, tok_tiles, &rt, &tt);
+  const int r0 = rt * kTileRows, t0 = tt * kTileTokens;
+  const int rows = min(kTileRows, a.rows - r0), toks = min(kTileTokens, a.T - t0);
+  const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * pitch, (uint64_t)rows * pitch);
+  const rsrc_t xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * pitch, (uint64_t)toks * pitch);
+  const int wm = wave / WN * 16 * MT, wn = wave % WN * 16 * NT;  // the wave's rows and tokens
+
+  // A wave loads 8 rows of 128 bytes at a time, 16 bytes a lane, through
+  // registers into LDS.  The 16-byte pieces (blocks of 32 columns) of row r lie
+  // in the order piece ^ (r % 8), so the fragment reads of 8 rows touch all
+  // banks.  Columns, rows and steps past the end arrive as zeros.
+  const uint32_t ld_piece = lane & 7, ld_row = wave * 8 + (lane >> 3);
+  const uint32_t ld_dst = ld_row * 128 + ((ld_piece ^ (lane >> 3)) * 16);
+  const uint32_t b0 = blockIdx.y * a.split_blocks, b1 = min(blocks, b0 + a.split_blocks);  // b0: a multiple of 16
+  const uint32_t pairs = (b1 - b0 + 15) / 16;  // steps are taken two by two
+  u32x4 stage[kLoads];
+  auto stage_off = [&](uint32_t s) {
+    const uint32_t b = b0 + s * 8 + ld_piece;
+    return b < b1 ? ld_row * pitch + b * 16 : kOutOfRange;
+  };
+  auto load_piece = [&](uint32_t off, int i) {
+    stage[i] = i < kWLoads ? buf_load_b128(wr, off + i * kLoadRows * pitch)
+                           : buf_load_b128(xr, off + (i - kWLoads) * kLoadRows * pitch);
+  };
+  auto write_piece = [&](uint32_t s, int i) {
+    uint8_t* to = i < kWLoads ? lds_w[s & 1] + i * kLoadRows * 128 : lds_x[s & 1] + (i - kWLoads) * kLoadRows * 128;
+    *reinterpret_cast<u32x4*>(to + ld_dst) = stage[i];
+  };
+  // The 16 scales of a row's two steps, a row a thread, as the aligned words
+  // they lie in (rows of scales start at any byte; no word without a byte of
+  // the tensor's is read).  Lane group g of a fragment takes blocks 2g and 2g +
+  // 1 of a step, so dword g holds those of the first step, then those of the
+  // second.  Scales past the last column are zeros: another row's there might
+  // be NaN.
+  const bool sc_w = wave * 64 < kTileRows;  // waves load either operand's
+  const uint8_t* sc_base = sc_w ? a.ws + (int64_t)r0 * blocks : a.xs + (int64_t)t0 * blocks;
+  const uint32_t sc_skew = (uint32_t)reinterpret_cast<uintptr_t>(sc_base) & 3u, sc_rows = sc_w ? rows : toks;
+  const uint32_t sc_words = (sc_skew + sc_rows * blocks + 3) / 4;
+  const rsrc_t sr = make_rsrc(sc_base - sc_skew, (uint64_t)sc_words * 4);
+  const uint32_t sc_row = sc_w ? threadIdx.x : threadIdx.x - kTileRows;
+  const uint32_t sc_off = sc_skew + sc_row * blocks + b0;
+  const bool sc_live = sc_row < sc_rows;
+  int sc_left = (int)(b1 - b0);  // scales from the next ones to be written on
+  asm("" : "+v"(sc_left));       // in vector registers: scalar compares keep the compiler from interleaving what follows
+  uint32_t stage_s[5];
+  auto load_scales = [&](uint32_t v) VQMI_INLINE {
+    const uint32_t off = sc_live ? (sc_off + v * 16) & ~3u : kOutOfRange;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) stage_s[i] = buf_load_b32(sr, off + 4 * i);
+  };
+  auto write_scales = [&](uint32_t v) VQMI_INLINE {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int left = min(max(sc_left - 4 * i, 0), 4);  // of this word
+      w[i] = __builtin_amdgcn_alignbyte(stage_s[i + 1], stage_s[i], sc_off) & (uint32_t)((1ull << (8 * left)) - 1ull);
+    }
+    sc_left -= 16;
+    // (no branch: the compiler would move matrix instructions past it)
+    lds_s[v & 1][threadIdx.x] = u32x4{(w[0] & 0xffffu) | w[2] << 16, w[0] >> 16 | (w[2] & 0xffff0000u),
+                                      (w[1] & 0xffffu) | w[3] << 16, w[1] >> 16 | (w[3] & 0xffff0000u)};
+  };
+  const int r = lane & 15, g = lane >> 4;
+  const uint32_t f_lo = r * 128 + (((2 * g) ^ (r & 7)) * 16), f_hi = r * 128 + (((2 * g + 1) ^ (r & 7)) * 16);
+  struct Op {
+    u32x4 lo, hi;
+  };
+  auto read_lo = [&](Op& o, const uint8_t* base) { o.lo = *reinterpret_cast<const u32x4*>(base + f_lo); };
+  auto read_hi = [&](Op& o, const uint8_t* base) { o.hi = *reinterpret_cast<const u32x4*>(base + f_hi); };
+  auto read_scale = [&](uint32_t v, int row) {  // row: of the rows, then of the tokens
+    return reinterpret_cast<const uint32_t*>(&lds_s[v & 1][row + r])[g];
+  };
+
+  float4_t acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // The first step in LDS, the second in registers; the first two steps' scales
+  // in LDS, the next two's in registers.
+  load_scales(0);
+#pragma unroll
+  for (uint32_t s = 0; s < 2; ++s) {
+    const uint32_t off = stage_off(s);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_piece(off, i);
+    if (s < 1) {
+      write_scales(0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) write_piece(s, i);
+    }
+  }
+  load_scales(1);
+  lds_barrier();
+  constexpr int kRing = AHEAD + 1;  // token operands: the current one and the next AHEAD
+  Op av[MT], bv[kRing];
+  uint32_t sa[MT], sb[NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    read_lo(av[m], lds_w[0] + (wm + 16 * m) * 128);
+    read_hi(av[m], lds_w[0] + (wm + 16 * m) * 128);
+    sa[m] = read_scale(0, wm + 16 * m);
+  }
+#pragma unroll
+  for (int n = 0; n < AHEAD; ++n) {
+    read_lo(bv[n], lds_x[0] + (wn + n * 16) * 128);
+    read_hi(bv[n], lds_x[0] + (wn + n * 16) * 128);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) sb[n] = read_scale(0, kTileRows + wn + 16 * n);
+
+  auto step = [&](uint32_t v, auto parity) VQMI_INLINE {
+    constexpr int P = parity.value;
+    const uint32_t s = 2 * v + P;
+    const uint8_t* xb = lds_x[P] + wn * 128;
+    const uint8_t* xnext = lds_x[P ^ 1] + wn * 128;
+    const uint8_t* wnext = lds_w[P ^ 1] + wm * 128;
+    const uint32_t off = stage_off(s + 2);
+    uint32_t sb_next[NT];
+    static_for<NT>([&](auto nc) VQMI_INLINE {
+      constexpr int n = nc.value;
+      // every wave has issued its last reads of this step before the barrier
+      // waits for them, so behind it the next step's pieces in LDS are complete
+      // and this one's buffers free
+      if constexpr (n == NT - AHEAD) lds_barrier();
+      const uint8_t* from = (n + AHEAD < NT ? xb : xnext) + (n + AHEAD) % NT * 16 * 128;
+      read_lo(bv[(n + AHEAD) % kRing], from);
+      read_hi(bv[(n + AHEAD) % kRing], from);
+      static_for<2 * MT>([&](auto hm) VQMI_INLINE {
+        constexpr int h = hm.value / MT, m = hm.value % MT;
+        const Op& b = bv[n % kRing];
+        if constexpr (h == 0) acc[m][n] = mx4_mfma<2 * P>(av[m].lo, b.lo, acc[m][n], sa[m], sb[n]);
+        else acc[m][n] = mx4_mfma<2 * P + 1>(av[m].hi, b.hi, acc[m][n], sa[m], sb[n]);
+        __builtin_amdgcn_sched_barrier(0);
+        // the next step's pieces go to LDS, spread over the step, and the ones
+        // after them are loaded in their place
+        constexpr int kSlots = (NT - AHEAD) * MT * 2, i = n * 2 * MT + hm.value;
+        static_for<kLoads>([&](auto k) VQMI_INLINE {
+          if constexpr (k.value * kSlots / kLoads == i) {
+            write_piece(s + 1, k.value);
+            load_piece(off, k.value);
+          }
+        });
+        // the next two steps' scales: written before the odd step's barrier
+        if constexpr (P == 0 && i == 0) write_scales(v + 1);
+        if constexpr (P == 0 && i == kSlots) load_scales(v + 2);
+        if constexpr (n == NT - 1) {
+          if constexpr (h == 0) read_lo(av[m], wnext + m * 16 * 128);
+          else read_hi(av[m], wnext + m * 16 * 128);
+          if constexpr (P == 1 && h == 1) {
+            sa[m] = read_scale(v + 1, wm + 16 * m);
+#pragma unroll
+            for (int k = m; k < NT; k += MT) sb_next[k] = read_scale(v + 1, kTileRows + wn + 16 * k);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    if constexpr (P == 1) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sb[n] = sb_next[n];
+    }
+  };
+  const uint32_t steps = (b1 - b0 + 7) / 8;
+  for (uint32_t v = 0; v < pairs; ++v) {
+    step(v, std::integral_constant<int, 0>{});
+    if (2 * v + 1 < steps) step(v, std::integral_constant<int, 1>{});
+  }
+  // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
+  // token's rows leave in whole pieces.
+  lds_barrier();
+  constexpr int kPitch = 16 * MT + 4;  // fp32 a token
+  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds_w), "every wave's 16 tokens fit");
+  float* out = reinterpret_cast<float*>(&lds_w[0][0]) + wave * 16 * kPitch;
+  static_for<NT>([&](auto n) VQMI_INLINE {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) *reinterpret_cast<float4_t*>(out + r * kPitch + 16 * m + 4 * g) = acc[m][n.value];
+    wave_lds_fence();
+    store_tokens<16 * MT, PRECISE>(a, out, kPitch, t0 + wn + 16 * n.value, r0 + wm, lane);
+    wave_lds_fence();
+  });
+}
+
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <int XK, int WAVES, int NT, int PCS, int DEPTH>
@@ -206,8 +411,17 @@ void run_skinny(const Mx4Args& a, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, NT, PCS, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
+template <int WM, int WN, int MT, int NT, int AHEAD>
+void run_tile(const Mx4Args& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
+  const dim3 block(64 * WM * WN);
+  if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
+}
+
 template <int XK>
 void run_kind(const Mx4Args& a, hipStream_t s) {
+  if (XK == kMx4XMx4 && a.T > 128) return run_tile<4, 2, 4, 8, 1>(a, 1, s);
   if (a.T <= 16) return run_skinny<XK, 4, 1, 2, 2>(a, 1, s);
   if (a.T <= 32) return run_skinny<XK, 4, 2, 1, 2>(a, 1, s);
   run_skinny<XK, 4, 4, 1, 2>(a, 1, s);
