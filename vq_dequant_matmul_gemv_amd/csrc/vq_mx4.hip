@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256) void vq_mx4_dequant_kernel(const uint32_t* q, 
 }
 
 // ---------------------------------------------------------------------------
-// product, few tokens: a block takes 16 rows of w and 16 * NT tokens, its waves
+// product, few tokens: a block takes 16 rows of w and up to 16 tokens, its waves
 // split the columns and join their sums in LDS
 // ---------------------------------------------------------------------------
 struct Mx4Args {
@@ -122,7 +122,6 @@ struct Mx4Args {
   void* y;
   int rows, blocks, T;  // blocks: of 32 columns
   int y_kind, swiglu;
-  int whole_w, whole_x;  // rows of scales lie on multiples of 4 bytes
   float* part;           // split columns: fp32 sums [gridDim.y][T][rows] in place of y
   int split_blocks;      // blocks of columns a split (the last one may have fewer)
 };
@@ -138,64 +137,61 @@ __device__ __forceinline__ Mx4Args split_args(Mx4Args a) {
   return a;
 }
 
-template <int XK, int WAVES, int NT, int PCS, int DEPTH>
+template <int XK, int WAVES, int NL, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
-  constexpr int kTok = 16 * NT, kStep = 4 * PCS;  // tokens; blocks of columns a step
-  __shared__ float4_t part[WAVES][NT][64];
+  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
+  constexpr int kTok = Stream::Slot::kRows;
+  __shared__ typename Stream::Slot slots[WAVES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const unsigned row_tiles = (a.rows + 15) / 16;  // row tiles run fastest: they share the tokens
   const int r0 = (blockIdx.x % row_tiles) * 16, t0 = (blockIdx.x / row_tiles) * kTok;
   const int r = lane & 15, g = lane >> 4;
   const uint32_t blocks = a.blocks;
   const int rows = min(16, a.rows - r0), toks = min(kTok, a.T - t0);
-  const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
-  const rsrc_t wsr = make_rsrc(a.ws + (int64_t)r0 * blocks, (uint64_t)rows * blocks);
-  constexpr int kXBlock = XK == kMx4XMx4 ? 16 : 64;  // bytes of a block of activations
-  const rsrc_t xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * kXBlock,
-                              (uint64_t)toks * blocks * kXBlock);
-  const rsrc_t xsr = make_rsrc(XK == kMx4XMx4 ? a.xs + (int64_t)t0 * blocks : nullptr, (uint64_t)toks * blocks);
-  const uint32_t wrow = r < rows ? (uint32_t)r : kOutOfRange;
-  uint32_t xrow[NT];
+  Stream st;
+  st.slot = slots + wave;
+  st.first = blockIdx.y * a.split_blocks;
+  st.end = min(blocks, st.first + a.split_blocks);
+  st.wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
+  st.xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * Stream::kXBlock,
+                    (uint64_t)toks * blocks * Stream::kXBlock);
+  st.plane = 0;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const uint32_t t = 16 * n + r;
-    xrow[n] = t < (uint32_t)toks ? (XK == kMx4XMx4 ? t : t * blocks * kXBlock) : kOutOfRange;
-  }
-  float4_t acc[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  Mx4Step<XK, PCS, NT> st[DEPTH];
-  const uint32_t b_first = blockIdx.y * a.split_blocks, b_end = min(blocks, b_first + a.split_blocks);
-  auto load = [&](int j, uint32_t k) {  // steps past the end: zeros
-    const uint32_t b = b_first + k * kStep + g * PCS;
-    mx4_load(st[j].w, wr, wsr, wrow, b, b_end, blocks, a.whole_w);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (XK == kMx4XMx4) mx4_load(st[j].x[n], xr, xsr, xrow[n], b, b_end, blocks, a.whole_x);
-      else mx4_load_x(st[j].x[n], xr, xrow[n], 0u, b, b_end);
-    }
-  };
-  const uint32_t steps = (b_end - b_first + kStep - 1) / kStep;
-#pragma unroll
-  for (int j = 0; j < DEPTH; ++j) load(j, wave + j * WAVES);
-  for (uint32_t k = wave; k < steps; k += DEPTH * WAVES) {
-#pragma unroll
-    for (int j = 0; j < DEPTH; ++j) {  // no branches: the loads in flight are counted through the loop
-      st[j].dot(acc);
-      load(j, k + (j + DEPTH) * WAVES);
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int row = mx4_w_row(i, lane);
+    st.woff[i] = row < rows ? row * blocks * 16 : kOutOfRange;
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) part[wave][n][lane] = acc[n];
+  for (int i = 0; i < NL; ++i) {
+    const int row = mx4_x_row<XK>(i, lane);
+    st.xoff[i] = row < toks ? row * blocks * Stream::kXBlock : kOutOfRange;
+  }
+  st.column = r & (kTok - 1);
+  const Mx4Scales ws(a.ws + (int64_t)r0 * blocks, rows * blocks);
+  const int srow = mx4_s_row(lane);
+  st.wsr = ws.rsrc;
+  st.wsoff = srow < rows ? ws.word(srow * blocks + st.first, lane) : kOutOfRange;
+  st.ws_skew = ws.skew(r * blocks + st.first);
+  if constexpr (XK == kMx4XMx4) {
+    const Mx4Scales xs(a.xs + (int64_t)t0 * blocks, toks * blocks);
+    st.xsr = xs.rsrc;
+    st.xsoff = srow < toks ? xs.word(srow * blocks + st.first, lane) : kOutOfRange;
+    st.xs_skew = xs.skew(st.column * blocks + st.first);
+  }
+  float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+  st.run(acc, wave, WAVES, lane);
+  __syncthreads();  // the slots are free: the waves' sums go there
+  float4_t* part = reinterpret_cast<float4_t*>(slots);
+  part[wave * 64 + lane] = acc[0] + acc[1];
   __syncthreads();
-  if (wave >= NT) return;  // wave n joins token tile n
-  float4_t sum = part[0][wave][lane];
+  if (wave != 0) return;
+  float4_t sum = part[lane];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) sum += part[w][wave][lane];
-  const int t = t0 + 16 * wave + r;
+  for (int w = 1; w < WAVES; ++w) sum += part[w * 64 + lane];
+  const int t = t0 + r;
   const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-  if (t < a.T) store_rows4(a, t, r0 + g * 4, v);
+  if (r < toks) store_rows4(a, t, r0 + g * 4, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -405,10 +401,11 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <int XK, int WAVES, int NT, int PCS, int DEPTH>
+template <int XK, int WAVES, int NL, int DEPTH>
 void run_skinny(const Mx4Args& a, int splits, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, 16 * NT), splits);
-  hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, NT, PCS, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+  constexpr int kTok = Mx4Slot<XK, 1, NL>::kRows;
+  const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, kTok), splits);
+  hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
 template <int WM, int WN, int MT, int NT, int AHEAD>
@@ -421,10 +418,16 @@ void run_tile(const Mx4Args& a, int splits, hipStream_t s) {
 
 template <int XK>
 void run_kind(const Mx4Args& a, hipStream_t s) {
-  if (XK == kMx4XMx4 && a.T > 128) return run_tile<4, 2, 4, 8, 1>(a, 1, s);
-  if (a.T <= 16) return run_skinny<XK, 4, 1, 2, 2>(a, 1, s);
-  if (a.T <= 32) return run_skinny<XK, 4, 2, 1, 2>(a, 1, s);
-  run_skinny<XK, 4, 4, 1, 2>(a, 1, s);
+  if constexpr (XK == kMx4XMx4) {
+    if (a.T > 128) return run_tile<4, 2, 4, 8, 1>(a, 1, s);
+    if (a.T <= 8) return run_skinny<XK, 4, 1, 3>(a, 1, s);
+    return run_skinny<XK, 4, 2, 3>(a, 1, s);
+  } else {
+    if (a.T <= 2) return run_skinny<XK, 4, 1, 3>(a, 1, s);
+    if (a.T <= 4) return run_skinny<XK, 4, 2, 3>(a, 1, s);
+    if (a.T <= 8) return run_skinny<XK, 4, 4, 2>(a, 1, s);
+    return run_skinny<XK, 4, 8, 2>(a, 1, s);
+  }
 }
 
 }  // namespace
@@ -452,7 +455,7 @@ hipError_t launch_mx4_dequant(const uint8_t* q, const uint8_t* scales, int64_t v
 
 Mx4Plans mx4_plans(int rows, int cols, int T) {
   Mx4Plan p;
-  const int64_t tiles = (int64_t)ceil_div(rows, 16) * ceil_div(T, T <= 16 ? 16 : T <= 32 ? 32 : 64);
+  const int64_t tiles = (int64_t)ceil_div(rows, 16) * ceil_div(T, 16);
   p.kernel = tiles < (1 << 24) ? 0 : -1;
   return {p, p};
 }
@@ -470,9 +473,6 @@ hipError_t launch_mx4_gemm(const Mx4View& w, const IoSpec& io, const Mx4Plan& p,
   a.T = T;
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
-  auto whole = [&](const uint8_t* q) { return a.blocks % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
-  a.whole_w = whole(w.scales);
-  a.whole_x = whole(xs);
   a.split_blocks = a.blocks;
   if (x_kind == kMx4XMx4) run_kind<kMx4XMx4>(a, s);
   else if (x_kind == kMx4XF16) run_kind<kMx4XF16>(a, s);

@@ -3,11 +3,15 @@
 // product and the mixture-of-experts layer.
 //
 // A wave's operands.  Lane l stands for row (or token) l % 16 of 16 and holds,
-// for each step of 128 * PCS columns, PCS whole blocks of 32 columns: blocks
-// PCS * (l / 16) to PCS * (l / 16) + PCS - 1 of the step.  So its values are
-// 16 * PCS consecutive bytes and its scales PCS consecutive bytes, which the
-// matrix instructions take byte by byte from one register; both operands are
+// for each step of 256 columns, blocks 2 * (l / 16) and 2 * (l / 16) + 1 of the
+// step's eight: 32 consecutive bytes of values and two of scales, which the
+// matrix instructions take byte by byte from one register.  Both operands are
 // laid out the same way, so columns meet their own.
+//
+// Memory holds rows side by side, and a wave that reads 16 bytes of 16 rows at
+// once moves a quarter of what whole lines would: so values are loaded a row's
+// 128 bytes by 8 lanes and change places in LDS, in a slot that only the wave
+// itself uses (no barriers; LDS runs a wave's accesses in order).
 //
 // Two kinds of products.
 //   4-bit x 4-bit: one 16 x 16 x 128 instruction per block of a lane, with
@@ -70,70 +74,10 @@ __device__ __forceinline__ float mx4_scale(uint32_t scales) {
   return __uint_as_float((J < 3 ? scales >> (8 * J) & 0xffu : scales >> 24) << 23);
 }
 
-// The PCS scale bytes within [104, 140] (2^-23 to 2^13), where e2m1 values times
+// Both scale bytes within [104, 140] (2^-23 to 2^13), where e2m1 values times
 // the scale are fp16 values.
-template <int PCS>
 __device__ __forceinline__ bool mx4_scales_fit_half(uint32_t s) {
-  bool ok = true;
-#pragma unroll
-  for (int j = 0; j < PCS; ++j) ok = ok && (s >> (8 * j) & 0xffu) - 104u <= 36u;
-  return ok;
-}
-
-// PCS blocks of a lane: codes and scale bytes.  Blocks past the last column (or
-// a row past the last: `row` is kOutOfRange) arrive as zeros with a scale of 1.
-template <int PCS>
-struct Mx4Frag {
-  u32x4 q[PCS];
-  uint32_t s;
-};
-// Row `row` of buffers with `pitch` blocks a row, blocks from `block` on that
-// come before `end`; whole: scales a row and `end` are multiples of PCS, and the
-// scales lie on a multiple of PCS bytes.
-template <int PCS>
-__device__ __forceinline__ void mx4_load(Mx4Frag<PCS>& f, rsrc_t qr, rsrc_t sr, uint32_t row, uint32_t block,
-                                         uint32_t end, uint32_t pitch, bool whole) {
-  const bool live = row != kOutOfRange;
-  const uint32_t at = row * pitch + block;
-#pragma unroll
-  for (int j = 0; j < PCS; ++j) f.q[j] = buf_load_b128(qr, live && block + j < end ? (at + j) * 16u : kOutOfRange);
-  if (whole) {  // then `end` is a multiple of PCS: a lane's blocks are all there or none is
-    const bool in = live && block < end;
-    const uint32_t off = in ? at : kOutOfRange;
-    uint32_t s;
-    if constexpr (PCS == 4) s = buf_load_b32(sr, off);
-    else if constexpr (PCS == 2) s = buf_load_b16(sr, off);
-    else s = __builtin_amdgcn_raw_buffer_load_b8(sr, off, 0, 0);
-    f.s = in ? s : 0x7f7f7f7fu;
-  } else {
-    f.s = 0u;
-#pragma unroll
-    for (int j = 0; j < PCS; ++j) {
-      const bool in = live && block + j < end;
-      const uint32_t s = __builtin_amdgcn_raw_buffer_load_b8(sr, in ? at + j : kOutOfRange, 0, 0);
-      f.s |= (in ? s : 0x7fu) << (8 * j);
-    }
-  }
-}
-
-// A lane's 32 * PCS values of 16-bit activations, PLANES of them; `row`: the
-// byte offset of the token's row (kOutOfRange: zeros).
-template <int PCS, int PLANES>
-struct Mx4XFrag {
-  u32x4 v[PLANES][PCS][4];
-};
-template <int PCS, int PLANES>
-__device__ __forceinline__ void mx4_load_x(Mx4XFrag<PCS, PLANES>& f, rsrc_t xr, uint32_t row, uint32_t plane_bytes,
-                                           uint32_t block, uint32_t end) {
-#pragma unroll
-  for (int p = 0; p < PLANES; ++p) {
-#pragma unroll
-    for (int j = 0; j < PCS; ++j) {
-      const uint32_t off = block + j < end && row != kOutOfRange ? row + p * plane_bytes + (block + j) * 64u : kOutOfRange;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f.v[p][j][i] = buf_load_b128(xr, off + (off == kOutOfRange ? 0u : 16u * i));
-    }
-  }
+  return (s & 0xffu) - 104u <= 36u && (s >> 8 & 0xffu) - 104u <= 36u;
 }
 
 // Eight fp16 values as two bf16 parts whose sum they are.
@@ -158,73 +102,172 @@ __device__ __forceinline__ void mx4_split_half(u32x4 x, bf16x8_t* hi, bf16x8_t* 
   *lo = __builtin_bit_cast(bf16x8_t, u32x4{l[0], l[1], l[2], l[3]});
 }
 
-// acc[n] += 16 rows times 16 tokens of tile n over block J of every lane.
-template <int XK, int J, int NT, int PCS, int PLANES>
-__device__ __forceinline__ void mx4_dot16(const Mx4Frag<PCS>& w, const Mx4XFrag<PCS, PLANES>* x, float4_t* acc,
-                                          bool fit_half) {
-  const float s = mx4_scale<J>(w.s);
+// Eight of a row's values times eight of a token's, over a step's four lane
+// groups: 16 rows x 16 tokens x 32 columns.  x: 16-bit values, or (bf16) the
+// planes whose sum they are.
+template <int XK>
+__device__ __forceinline__ float4_t mx4_mfma16(uint32_t codes, float scale, u32x4 x, float4_t acc, bool fit_half) {
+  if constexpr (XK == kMx4XF16) {
+    if (fit_half)
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(mx4_half(codes, scale), __builtin_bit_cast(half8_t, x), acc, 0, 0, 0);
+    const bf16x8_t a = mx4_bf16(codes, scale);
+    bf16x8_t hi, lo;
+    mx4_split_half(x, &hi, &lo);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, acc, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx4_bf16(codes, scale), __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// a wave's stream over the columns: 16 rows of w, up to 16 rows of activations
+//
+// XK: what the activations are; PL: planes of them; NL: load instructions for a
+// step's rows of a plane (8 rows each of 4-bit values, 2 of 16-bit ones);
+// DEPTH: steps in flight.
+// ---------------------------------------------------------------------------
+template <int XK, int PL, int NL>
+struct Mx4Slot {
+  static constexpr int kRows = NL * (XK == kMx4XMx4 ? 8 : 2);  // rows of activations
+  u32x4 w[16 * 8];
+  u32x4 x[PL][NL * 64];
+  uint32_t ws[16 * 4], xs[XK == kMx4XMx4 ? 16 * 4 : 1];  // scales: the words they lie in
+};
+
+// The row a lane loads for: of w's values by instruction i, of scales, and of
+// the activations by instruction i.
+__device__ __forceinline__ int mx4_w_row(int i, int lane) { return 8 * i + (lane >> 3); }
+__device__ __forceinline__ int mx4_s_row(int lane) { return lane >> 2; }
+template <int XK>
+__device__ __forceinline__ int mx4_x_row(int i, int lane) {
+  return XK == kMx4XMx4 ? 8 * i + (lane >> 3) : 2 * i + (lane >> 5);
+}
+
+// Rows of scales, which may start at any byte: a step's eight lie in three
+// aligned words at most, the first of them `skew` bytes before the row's.  No
+// word without a byte of the tensor's is read.
+struct Mx4Scales {
+  rsrc_t rsrc;
+  uint32_t base_skew;
+  __device__ __forceinline__ Mx4Scales(const uint8_t* base, uint32_t bytes)
+      : rsrc(make_rsrc(base - (reinterpret_cast<uintptr_t>(base) & 3u),
+                       ((reinterpret_cast<uintptr_t>(base) & 3u) + (uint64_t)bytes + 3) & ~(uint64_t)3)),
+        base_skew((uint32_t)reinterpret_cast<uintptr_t>(base) & 3u) {}
+  // The lane's word of scales from byte `at` of the tensor on.
+  __device__ __forceinline__ uint32_t word(uint32_t at, int lane) const {
+    return (lane & 3) < 3 ? ((base_skew + at) & ~3u) + 4 * (lane & 3) : kOutOfRange;
+  }
+  __device__ __forceinline__ uint32_t skew(uint32_t at) const { return (base_skew + at) & 3u; }
+};
+
+template <int XK, int PL, int NL, int DEPTH>
+struct Mx4Stream {
+  typedef Mx4Slot<XK, PL, NL> Slot;
+  static constexpr uint32_t kXBlock = XK == kMx4XMx4 ? 16 : 64;  // bytes of a block of activations
+  rsrc_t wr, xr, wsr, xsr;
+  uint32_t woff[2], xoff[NL], wsoff, xsoff;  // byte offsets of the lane's rows; kOutOfRange: no such row
+  uint32_t plane;                            // bytes from one plane of activations to the next
+  uint32_t first, end;                       // blocks of columns: the first one, and behind the last
+  uint32_t ws_skew, xs_skew;                 // of the rows that the lane multiplies
+  int column;                                // the row of activations that the lane multiplies
+  Slot* slot;
+  u32x4 w[DEPTH][2], x[DEPTH][PL][NL];
+  uint32_t ws[DEPTH], xs[DEPTH];
+
+  __device__ __forceinline__ void load(int j, uint32_t k, int lane) {  // step k; past the end: zeros
+    const uint32_t b = first + k * 8;
+    const bool in_w = b + (lane & 7) < end;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (XK == kMx4XF16) {
-      if (fit_half) {
-        const half8_t a = mx4_half(w.q[J][i], s);
+    for (int i = 0; i < 2; ++i) w[j][i] = buf_load_b128(wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
+    ws[j] = buf_load_b32(wsr, wsoff + k * 8);
+    const uint32_t piece = XK == kMx4XMx4 ? lane & 7 : lane & 31;  // of 16 bytes
+    const bool in_x = b + (XK == kMx4XMx4 ? piece : piece / 4) < end;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, x[n].v[0][J][i]), acc[n], 0, 0, 0);
-      } else {
-        const bf16x8_t a = mx4_bf16(w.q[J][i], s);
+    for (int p = 0; p < PL; ++p) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          bf16x8_t hi, lo;
-          mx4_split_half(x[n].v[0][J][i], &hi, &lo);
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, acc[n], 0, 0, 0);
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, acc[n], 0, 0, 0);
-        }
+      for (int i = 0; i < NL; ++i)
+        x[j][p][i] = buf_load_b128(xr, in_x ? xoff[i] + p * plane + b * kXBlock + piece * 16 : kOutOfRange);
+    }
+    if constexpr (XK == kMx4XMx4) xs[j] = buf_load_b32(xsr, xsoff + k * 8);
+  }
+
+  // The loaded step into LDS.  16-byte pieces change places within a row (4-bit:
+  // piece ^ row % 8 of 8, 16-bit: piece ^ row of 32), so reads of 16 rows touch
+  // all banks.
+  __device__ __forceinline__ void put(int j, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) slot->w[mx4_w_row(i, lane) * 8 + ((lane & 7) ^ (lane >> 3))] = w[j][i];
+    slot->ws[lane] = ws[j];
+#pragma unroll
+    for (int p = 0; p < PL; ++p) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int row = mx4_x_row<XK>(i, lane);
+        if constexpr (XK == kMx4XMx4) slot->x[p][row * 8 + ((lane & 7) ^ (lane >> 3))] = x[j][p][i];
+        else slot->x[p][row * 32 + ((lane & 31) ^ row)] = x[j][p][i];
       }
+    }
+    if constexpr (XK == kMx4XMx4) slot->xs[lane] = xs[j];
+  }
+
+  // The two scales of the lane's blocks of a step: those past the last column
+  // (another row's) are 1, as NaN there would spoil the sum.
+  __device__ __forceinline__ uint32_t scales(const uint32_t* words, int row, uint32_t skew, uint32_t k, int lane) const {
+    const uint32_t g2 = 2 * (lane >> 4), b = first + k * 8 + g2;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(words + 4 * row) + skew + g2;
+    return (b < end ? p[0] : 127u) | (b + 1 < end ? p[1] : 127u) << 8;
+  }
+
+  // acc[0] + acc[1] += step k, which is in LDS.
+  __device__ __forceinline__ void dot(float4_t* acc, uint32_t k, int lane) const {
+    const int r = lane & 15, g = lane >> 4, n = column;
+    const uint32_t s_w = scales(slot->ws, r, ws_skew, k, lane);
+    u32x4 q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) q[h] = slot->w[r * 8 + ((2 * g + h) ^ (r & 7))];
+    if constexpr (XK == kMx4XMx4) {
+      const uint32_t s_x = scales(slot->xs, n, xs_skew, k, lane);
+      u32x4 v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = slot->x[0][n * 8 + ((2 * g + h) ^ (n & 7))];
+      acc[0] = mx4_mfma<0>(q[0], v[0], acc[0], s_w, s_x);
+      acc[1] = mx4_mfma<1>(q[1], v[1], acc[1], s_w, s_x);
     } else {
-      const bf16x8_t a = mx4_bf16(w.q[J][i], s);
+      const bool fit = XK == kMx4XF16 && __ballot(!mx4_scales_fit_half(s_w)) == 0ull;
+      const float s[2] = {mx4_scale<0>(s_w), mx4_scale<1>(s_w)};
 #pragma unroll
-      for (int p = PLANES - 1; p >= 0; --p) {
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[n].v[p][J][i]), acc[n], 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int p = PL - 1; p >= 0; --p) {
+            const u32x4 v = slot->x[p][n * 32 + ((8 * g + 4 * h + i) ^ n)];
+            acc[i & 1] = mx4_mfma16<XK>(c[i], s[h], v, acc[i & 1], fit);
+          }
+        }
       }
     }
   }
-}
 
-// The same over all of a lane's blocks.
-template <int XK, int NT, int PCS, int PLANES>
-__device__ __forceinline__ void mx4_dot16s(const Mx4Frag<PCS>& w, const Mx4XFrag<PCS, PLANES>* x, float4_t* acc,
-                                           bool fit_half) {
-  mx4_dot16<XK, 0, NT>(w, x, acc, fit_half);
-  if constexpr (PCS > 1) mx4_dot16<XK, 1, NT>(w, x, acc, fit_half);
-  if constexpr (PCS > 2) {
-    mx4_dot16<XK, 2, NT>(w, x, acc, fit_half);
-    mx4_dot16<XK, 3, NT>(w, x, acc, fit_half);
-  }
-}
-
-// A step's operands: 16 rows of w and NT tiles of 16 tokens.
-template <int XK, int PCS, int NT>
-struct Mx4Step {
-  typedef std::conditional_t<XK == kMx4XMx4, Mx4Frag<PCS>, Mx4XFrag<PCS, 1>> X;
-  Mx4Frag<PCS> w;
-  X x[NT];
-
-  __device__ __forceinline__ void dot(float4_t* acc) const {
-    if constexpr (XK == kMx4XMx4) {
+  // acc[0] + acc[1] += steps `from`, from + stride, ...
+  __device__ __forceinline__ void run(float4_t* acc, uint32_t from, uint32_t stride, int lane) {
+    const uint32_t steps = (end - first + 7) / 8;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        acc[n] = mx4_mfma<0>(w.q[0], x[n].q[0], acc[n], w.s, x[n].s);
-        if constexpr (PCS > 1) acc[n] = mx4_mfma<1>(w.q[1], x[n].q[1], acc[n], w.s, x[n].s);
-        if constexpr (PCS > 2) {
-          acc[n] = mx4_mfma<2>(w.q[2], x[n].q[2], acc[n], w.s, x[n].s);
-          acc[n] = mx4_mfma<3>(w.q[3], x[n].q[3], acc[n], w.s, x[n].s);
+    for (int j = 0; j < DEPTH; ++j) load(j, from + j * stride, lane);
+    for (uint32_t k = from; k < steps; k += DEPTH * stride) {
+#pragma unroll
+      for (int j = 0; j < DEPTH; ++j) {
+        const uint32_t kj = k + j * stride;
+        if (kj < steps) {
+          put(j, lane);
+          load(j, kj + DEPTH * stride, lane);
+          wave_lds_fence();
+          dot(acc, kj, lane);
+          wave_lds_fence();
         }
       }
-    } else {
-      mx4_dot16s<XK, NT>(w, x, acc, XK == kMx4XF16 && __ballot(!mx4_scales_fit_half<PCS>(w.s)) == 0ull);
     }
   }
 };

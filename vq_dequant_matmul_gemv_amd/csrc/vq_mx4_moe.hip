@@ -27,7 +27,6 @@ struct MoeArgs {
   int T, top_k, pairs;
   int hidden_blocks, inter_blocks;  // blocks of 32 columns
   int y_kind;
-  int whole_gu, whole_dn;
 };
 
 // fp32 as three bf16 values whose sum it is: its 24 bits, 8 at a time.
@@ -44,14 +43,16 @@ __device__ __forceinline__ void split_planes(float v, uint32_t* p) {
 }
 
 // Gate and up: a block takes 16 rows of the expert of pair blockIdx.y, if that
-// pair is the expert's first, for all pairs of the expert.
-template <int XK, int WAVES, int PCS, int DEPTH>
+// pair is the expert's first, for all pairs of the expert, kRows at a time; its
+// waves split the columns and join their sums in LDS.
+template <int XK, int WAVES, int NL, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_up_kernel(MoeArgs a) {
-  constexpr int kStep = 4 * PCS;
-  __shared__ float4_t part[WAVES][64];
+  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
+  constexpr int kRows = Stream::Slot::kRows;
+  __shared__ typename Stream::Slot slots[WAVES];
   __shared__ uint16_t members[kMx4MoePairs];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int pair = blockIdx.y, e = a.ids[pair];
+  const int pair = blockIdx.y, e = __builtin_amdgcn_readfirstlane(a.ids[pair]);
   int count = 0;
   bool lead = e >= 0;
   for (int base = 0; base < a.pairs; base += 64) {
@@ -68,128 +69,135 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_up_kernel(MoeArgs a) {
   const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16;
   const uint32_t blocks = a.hidden_blocks;
   const int64_t row0 = (int64_t)e * a.inter_blocks * 64 + r0;  // 2 * inter rows an expert
-  const rsrc_t wr = make_rsrc(a.gu + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
-  const rsrc_t wsr = make_rsrc(a.gus + row0 * blocks, (uint64_t)16 * blocks);
-  const rsrc_t xr = make_rsrc(a.x, (uint64_t)a.T * blocks * 64);
-  const uint32_t steps = (blocks + kStep - 1) / kStep;
-  for (int m0 = 0; m0 < count; m0 += 16) {
-    const int mine = m0 + r < count ? members[m0 + r] : -1;
-    const uint32_t xrow = mine >= 0 ? (uint32_t)(mine / a.top_k) * blocks * 64u : kOutOfRange;
-    Mx4Step<XK, PCS, 1> st[DEPTH];
-    float4_t acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-    auto load = [&](int j, uint32_t k) {
-      const uint32_t b = k * kStep + g * PCS;
-      mx4_load(st[j].w, wr, wsr, r, b, blocks, blocks, a.whole_gu);
-      mx4_load_x(st[j].x[0], xr, xrow, 0u, b, blocks);
-    };
+  Stream st;
+  st.slot = slots + wave;
+  st.first = 0;
+  st.end = blocks;
+  st.wr = make_rsrc(a.gu + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+  st.xr = make_rsrc(a.x, (uint64_t)a.T * blocks * 64);
+  st.plane = 0;
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) load(j, wave + j * WAVES);
-    for (uint32_t k = wave; k < steps; k += DEPTH * WAVES) {
+  for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
+  const Mx4Scales ws(a.gus + row0 * blocks, 16 * blocks);
+  st.wsr = ws.rsrc;
+  st.wsoff = ws.word(mx4_s_row(lane) * blocks, lane);
+  st.ws_skew = ws.skew(r * blocks);
+  st.column = r & (kRows - 1);
+  for (int m0 = 0; m0 < count; m0 += kRows) {
 #pragma unroll
-      for (int j = 0; j < DEPTH; ++j) {
-        st[j].dot(acc);
-        load(j, k + (j + DEPTH) * WAVES);
-      }
+    for (int i = 0; i < NL; ++i) {
+      const int row = m0 + mx4_x_row<XK>(i, lane);
+      st.xoff[i] = row < count ? (uint32_t)(members[row] / a.top_k) * blocks * 64u : kOutOfRange;
     }
-    if (m0 > 0) __syncthreads();  // the sums of the members before have been read
-    part[wave][lane] = acc[0];
+    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    st.run(acc, wave, WAVES, lane);
+    __syncthreads();  // the slots are free: the waves' sums go there
+    float4_t* part = reinterpret_cast<float4_t*>(slots);
+    part[wave * 64 + lane] = acc[0] + acc[1];
     __syncthreads();
-    if (wave == 0 && mine >= 0) {
-      float4_t s = part[0][lane];
+    if (wave == 0 && r < kRows && m0 + r < count) {
+      float4_t s = part[lane];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) s += part[w][lane];
+      for (int w = 1; w < WAVES; ++w) s += part[w * 64 + lane];
       uint32_t lo[kMx4Planes], hi[kMx4Planes];
       split_planes(silu_mul<true>(s[0], s[1]), lo);
       split_planes(silu_mul<true>(s[2], s[3]), hi);
       const int64_t inter = (int64_t)a.inter_blocks * 32;
-      uint16_t* out = a.h + mine * inter + r0 / 2 + 2 * g;
+      uint16_t* out = a.h + members[m0 + r] * inter + r0 / 2 + 2 * g;
 #pragma unroll
       for (int p = 0; p < kMx4Planes; ++p)
         *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
     }
+    if (m0 + kRows < count) __syncthreads();
   }
 }
 
 // Down: a block takes 16 output rows for all tokens, its waves the experts in
-// turn.  The columns of a wave's products are the tokens themselves, 16 a tile:
-// those that did not choose the expert multiply zeros and leave the sum as it
-// is.
-template <int WAVES, int NT, int PCS>
+// turn, for the pairs of an expert, kRows at a time.  A wave adds up its
+// experts' weighted products per token in LDS, in the order of the pairs; the
+// waves' sums are joined in their order.
+template <int WAVES, int NL, int DEPTH, int TOKENS>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) {
-  constexpr int kStep = 4 * PCS;
-  __shared__ float4_t part[WAVES][NT][64];
+  typedef Mx4Stream<kMx4XPlanes, kMx4Planes, NL, DEPTH> Stream;
+  constexpr int kRows = Stream::Slot::kRows;
+  __shared__ typename Stream::Slot slots[WAVES];
+  __shared__ float4_t sums[WAVES][TOKENS][4];  // 16 rows a token
   __shared__ int32_t ids[kMx4MoePairs];
+  __shared__ uint16_t members[WAVES][TOKENS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16;
   for (int p = threadIdx.x; p < a.pairs; p += 64 * WAVES) ids[p] = a.ids[p];
+  for (int i = lane; i < TOKENS * 4; i += 64) sums[wave][i / 4][i % 4] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
   const uint32_t blocks = a.inter_blocks;
-  const uint32_t plane = (uint32_t)a.pairs * blocks * 64u;  // bytes
-  const rsrc_t hr = make_rsrc(a.h, (uint64_t)kMx4Planes * plane);
-  const uint32_t steps = (blocks + kStep - 1) / kStep;
-  float4_t acc[NT];
+  Stream st;
+  st.slot = slots + wave;
+  st.first = 0;
+  st.end = blocks;
+  st.plane = (uint32_t)a.pairs * blocks * 64u;
+  st.xr = make_rsrc(a.h, (uint64_t)kMx4Planes * st.plane);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
+  st.column = r & (kRows - 1);
   int turn = 0;  // experts seen
   for (int base = 0; base < a.pairs; base += 64) {
     uint64_t todo = __ballot(base + lane < a.pairs && a.leads[min(base + lane, a.pairs - 1)] != 0);
     for (; todo != 0ull; todo &= todo - 1, ++turn) {
       if (turn % WAVES != wave) continue;
       const int e = __builtin_amdgcn_readfirstlane(ids[base + __builtin_ctzll(todo)]);
-      int mine[NT];
-      uint32_t xrow[NT];
-      bool any[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int t = 16 * n + r;
-        mine[n] = -1;
-        for (int s = 0; s < a.top_k; ++s) {
-          const int p = t * a.top_k + s;
-          if (t < a.T && ids[p] == e) mine[n] = p;
-        }
-        xrow[n] = mine[n] >= 0 ? (uint32_t)mine[n] * blocks * 64u : kOutOfRange;
-        any[n] = __ballot(mine[n] >= 0) != 0ull;
+      int mine = -1;  // the pair of token `lane`
+      for (int s = 0; s < a.top_k; ++s) {
+        const int p = lane * a.top_k + s;
+        if (lane < a.T && ids[p] == e) mine = p;
       }
+      const uint64_t m = __ballot(mine >= 0);
+      const int count = __popcll(m);
+      if (mine >= 0) members[wave][__popcll(m & ((1ull << lane) - 1))] = (uint16_t)mine;
+      wave_lds_fence();
       const int64_t row0 = (int64_t)e * a.hidden_blocks * 32 + r0;
-      const rsrc_t wr = make_rsrc(a.dn + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
-      const rsrc_t wsr = make_rsrc(a.dns + row0 * blocks, (uint64_t)16 * blocks);
-      float4_t d[NT];
+      st.wr = make_rsrc(a.dn + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+      const Mx4Scales ws(a.dns + row0 * blocks, 16 * blocks);
+      st.wsr = ws.rsrc;
+      st.wsoff = ws.word(mx4_s_row(lane) * blocks, lane);
+      st.ws_skew = ws.skew(r * blocks);
+      for (int m0 = 0; m0 < count; m0 += kRows) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) d[n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      for (uint32_t k = 0; k < steps; ++k) {
-        const uint32_t b = k * kStep + g * PCS;
-        Mx4Frag<PCS> w;
-        mx4_load(w, wr, wsr, r, b, blocks, blocks, a.whole_dn);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (!any[n]) continue;
-          Mx4XFrag<PCS, kMx4Planes> x;
-          mx4_load_x(x, hr, xrow[n], plane, b, blocks);
-          mx4_dot16s<kMx4XPlanes, 1>(w, &x, &d[n], false);
+        for (int i = 0; i < NL; ++i) {
+          const int row = m0 + mx4_x_row<kMx4XPlanes>(i, lane);
+          st.xoff[i] = row < count ? (uint32_t)members[wave][row] * blocks * 64u : kOutOfRange;
         }
-      }
+        const bool live = r < kRows && m0 + r < count;
+        const int pair = live ? members[wave][m0 + r] : 0;
+        const float f = a.weights[pair];
+        float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        st.run(acc, 0, 1, lane);
+        if (live) {
+          float4_t* s = &sums[wave][pair / a.top_k][g];
+          const float4_t d = acc[0] + acc[1];
+          float4_t o = *s;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (mine[n] < 0) continue;
-        const float f = a.weights[mine[n]];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f, d[n][i], acc[n][i]);
+          for (int i = 0; i < 4; ++i) o[i] = fmaf(f, d[i], o[i]);
+          *s = o;
+        }
+        wave_lds_fence();
       }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) part[wave][n][lane] = acc[n];
   __syncthreads();
-  for (int n = wave; n < NT; n += WAVES) {  // a wave joins a tile of tokens
-    float4_t s = part[0][n][lane];
+  for (int i = threadIdx.x; i < a.T * 4; i += 64 * WAVES) {
+    const int t = i / 4, q = i % 4;
+    float4_t s = sums[0][t][q];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += part[w][n][lane];
-    const int t = 16 * n + r;
-    if (t >= a.T) continue;
-    const int64_t at = (int64_t)t * a.hidden_blocks * 32 + r0 + 4 * g;
+    for (int w = 1; w < WAVES; ++w) s += sums[w][t][q];
     const float v[4] = {s[0], s[1], s[2], s[3]};
-    store_run<4>(a.y, at, v, a.y_kind);
+    store_run<4>(a.y, (int64_t)t * a.hidden_blocks * 32 + r0 + 4 * q, v, a.y_kind);
   }
+}
+
+template <int XK, int NL>
+void run_up(const MoeArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.inter_blocks * 4, (unsigned)a.pairs);
+  hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 4, NL, 3>), grid, dim3(256), 0, s, a);
 }
 
 constexpr size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -223,18 +231,13 @@ hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4
   a.hidden_blocks = gate_up.cols / kMx4Block;
   a.inter_blocks = down.cols / kMx4Block;
   a.y_kind = y_kind;
-  auto whole = [](const uint8_t* q, int blocks) { return blocks % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
-  a.whole_gu = whole(gate_up.scales, a.hidden_blocks);
-  a.whole_dn = whole(down.scales, a.inter_blocks);
-  const dim3 up((unsigned)a.inter_blocks * 4, (unsigned)a.pairs);
-  if (x_kind == kMx4XF16) hipLaunchKernelGGL((vq_mx4_moe_up_kernel<kMx4XF16, 4, 2, 2>), up, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((vq_mx4_moe_up_kernel<kMx4XBF16, 4, 2, 2>), up, dim3(256), 0, s, a);
+  if (x_kind == kMx4XF16) T <= 4 ? run_up<kMx4XF16, 1>(a, s) : run_up<kMx4XF16, 2>(a, s);
+  else T <= 4 ? run_up<kMx4XBF16, 1>(a, s) : run_up<kMx4XBF16, 2>(a, s);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)a.hidden_blocks * 2);
-  if (T <= 16) hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 1, 2>), grid, dim3(512), 0, s, a);
-  else if (T <= 32) hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2, 2>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 4, 2>), grid, dim3(512), 0, s, a);
+  if (T <= 16) hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 1, 2, 16>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 1, 2, 64>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
