@@ -153,7 +153,8 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
   st.slot = slots + wave;
   st.first = blockIdx.y * a.split_blocks;
   st.end = min(blocks, st.first + a.split_blocks);
-  st.wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
+  typename Stream::Source src;
+  src.wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
   st.xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * Stream::kXBlock,
                     (uint64_t)toks * blocks * Stream::kXBlock);
   st.plane = 0;
@@ -165,14 +166,14 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int row = mx4_x_row<XK>(i, lane);
-    st.xoff[i] = row < toks ? row * blocks * Stream::kXBlock : kOutOfRange;
+    src.xoff[i] = row < toks ? row * blocks * Stream::kXBlock : kOutOfRange;
   }
   st.column = r & (kTok - 1);
   const Mx4Scales ws(a.ws + (int64_t)r0 * blocks, rows * blocks);
   const int srow = mx4_s_row(lane);
-  st.wsr = ws.rsrc;
-  st.wsoff = srow < rows ? ws.word(srow * blocks + st.first, lane) : kOutOfRange;
-  st.ws_skew = ws.skew(r * blocks + st.first);
+  src.wsr = ws.rsrc;
+  src.wsoff = srow < rows ? ws.word(srow * blocks + st.first, lane) : kOutOfRange;
+  src.ws_skew = ws.skew(r * blocks + st.first);
   if constexpr (XK == kMx4XMx4) {
     const Mx4Scales xs(a.xs + (int64_t)t0 * blocks, toks * blocks);
     st.xsr = xs.rsrc;
@@ -180,7 +181,12 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
     st.xs_skew = xs.skew(st.column * blocks + st.first);
   }
   float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  st.run(acc, wave, WAVES, lane);
+  st.start(src, wave, WAVES, lane);
+  typename Stream::Source none = src;
+  none.wr = none.wsr = make_rsrc(a.w, 0);  // nothing follows
+#pragma unroll
+  for (int i = 0; i < NL; ++i) none.xoff[i] = kOutOfRange;
+  st.run(acc, src, none, wave, WAVES, lane);
   __syncthreads();  // the slots are free: the waves' sums go there
   float4_t* part = reinterpret_cast<float4_t*>(slots);
   part[wave * 64 + lane] = acc[0] + acc[1];

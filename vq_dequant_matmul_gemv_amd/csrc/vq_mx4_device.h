@@ -161,33 +161,41 @@ struct Mx4Scales {
   __device__ __forceinline__ uint32_t skew(uint32_t at) const { return (base_skew + at) & 3u; }
 };
 
+// What a wave loads its steps from: 16 rows of w and rows of activations.
+template <int NL>
+struct Mx4Source {
+  rsrc_t wr, wsr;               // values and scales of the rows
+  uint32_t wsoff, xoff[NL];     // byte offsets of the lane's rows; kOutOfRange: no such row
+  uint32_t ws_skew;             // of the row that the lane multiplies
+};
+
 template <int XK, int PL, int NL, int DEPTH>
 struct Mx4Stream {
   typedef Mx4Slot<XK, PL, NL> Slot;
+  typedef Mx4Source<NL> Source;
   static constexpr uint32_t kXBlock = XK == kMx4XMx4 ? 16 : 64;  // bytes of a block of activations
-  rsrc_t wr, xr, wsr, xsr;
-  uint32_t woff[2], xoff[NL], wsoff, xsoff;  // byte offsets of the lane's rows; kOutOfRange: no such row
-  uint32_t plane;                            // bytes from one plane of activations to the next
-  uint32_t first, end;                       // blocks of columns: the first one, and behind the last
-  uint32_t ws_skew, xs_skew;                 // of the rows that the lane multiplies
-  int column;                                // the row of activations that the lane multiplies
+  rsrc_t xr, xsr;
+  uint32_t woff[2], xsoff, xs_skew;
+  uint32_t plane;       // bytes from one plane of activations to the next
+  uint32_t first, end;  // blocks of columns: the first one, and behind the last
+  int column;           // the row of activations that the lane multiplies
   Slot* slot;
   u32x4 w[DEPTH][2], x[DEPTH][PL][NL];
   uint32_t ws[DEPTH], xs[DEPTH];
 
-  __device__ __forceinline__ void load(int j, uint32_t k, int lane) {  // step k; past the end: zeros
+  __device__ __forceinline__ void load(int j, const Source& src, uint32_t k, int lane) {  // step k; past the end: zeros
     const uint32_t b = first + k * 8;
     const bool in_w = b + (lane & 7) < end;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[j][i] = buf_load_b128(wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
-    ws[j] = buf_load_b32(wsr, wsoff + k * 8);
+    for (int i = 0; i < 2; ++i) w[j][i] = buf_load_b128(src.wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
+    ws[j] = buf_load_b32(src.wsr, src.wsoff + k * 8);
     const uint32_t piece = XK == kMx4XMx4 ? lane & 7 : lane & 31;  // of 16 bytes
     const bool in_x = b + (XK == kMx4XMx4 ? piece : piece / 4) < end;
 #pragma unroll
     for (int p = 0; p < PL; ++p) {
 #pragma unroll
       for (int i = 0; i < NL; ++i)
-        x[j][p][i] = buf_load_b128(xr, in_x ? xoff[i] + p * plane + b * kXBlock + piece * 16 : kOutOfRange);
+        x[j][p][i] = buf_load_b128(xr, in_x ? src.xoff[i] + p * plane + b * kXBlock + piece * 16 : kOutOfRange);
     }
     if constexpr (XK == kMx4XMx4) xs[j] = buf_load_b32(xsr, xsoff + k * 8);
   }
@@ -220,7 +228,7 @@ struct Mx4Stream {
   }
 
   // acc[0] + acc[1] += step k, which is in LDS.
-  __device__ __forceinline__ void dot(float4_t* acc, uint32_t k, int lane) const {
+  __device__ __forceinline__ void dot(float4_t* acc, uint32_t ws_skew, uint32_t k, int lane) const {
     const int r = lane & 15, g = lane >> 4, n = column;
     const uint32_t s_w = scales(slot->ws, r, ws_skew, k, lane);
     u32x4 q[2];
@@ -251,22 +259,31 @@ struct Mx4Stream {
     }
   }
 
-  // acc[0] + acc[1] += steps `from`, from + stride, ...
-  __device__ __forceinline__ void run(float4_t* acc, uint32_t from, uint32_t stride, int lane) {
+  // Steps a wave takes of each source: whole rounds of the ring.
+  __device__ __forceinline__ uint32_t turns(uint32_t stride) const {
     const uint32_t steps = (end - first + 7) / 8;
+    return (steps + stride * DEPTH - 1) / (stride * DEPTH) * DEPTH;
+  }
+  __device__ __forceinline__ void start(const Source& src, uint32_t from, uint32_t stride, int lane) {
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) load(j, from + j * stride, lane);
-    for (uint32_t k = from; k < steps; k += DEPTH * stride) {
+    for (int j = 0; j < DEPTH; ++j) load(j, src, from + j * stride, lane);
+  }
+  // acc[0] + acc[1] += steps `from`, from + stride, ... of `cur`, whose first
+  // ones are on their way (start, or the call before); those of `next` are when
+  // it returns.
+  __device__ __forceinline__ void run(float4_t* acc, const Source& cur, const Source& next, uint32_t from,
+                                      uint32_t stride, int lane) {
+    const uint32_t steps = (end - first + 7) / 8, n = turns(stride);
+    for (uint32_t s = 0; s < n; s += DEPTH) {
 #pragma unroll
       for (int j = 0; j < DEPTH; ++j) {
-        const uint32_t kj = k + j * stride;
-        if (kj < steps) {
-          put(j, lane);
-          load(j, kj + DEPTH * stride, lane);
-          wave_lds_fence();
-          dot(acc, kj, lane);
-          wave_lds_fence();
-        }
+        const uint32_t k = from + (s + j) * stride;
+        put(j, lane);
+        if (s + DEPTH < n) load(j, cur, k + DEPTH * stride, lane);
+        else load(j, next, from + j * stride, lane);
+        wave_lds_fence();
+        if (k < steps) dot(acc, cur.ws_skew, k, lane);
+        wave_lds_fence();
       }
     }
   }

@@ -22,9 +22,8 @@ struct MoeArgs {
   void* y;
   const int32_t* ids;
   const float* weights;
-  int32_t* leads;  // [pairs]: 1 where a pair is its expert's first
   uint16_t* h;     // [kMx4Planes][pairs][inter]
-  int T, top_k, pairs;
+  int T, top_k, pairs, experts;
   int hidden_blocks, inter_blocks;  // blocks of 32 columns
   int y_kind;
 };
@@ -42,79 +41,168 @@ __device__ __forceinline__ void split_planes(float v, uint32_t* p) {
   p[2] = finite ? __float_as_uint(last) >> 16 : 0u;
 }
 
-// Gate and up: a block takes 16 rows of the expert of pair blockIdx.y, if that
-// pair is the expert's first, for all pairs of the expert, kRows at a time; its
-// waves split the columns and join their sums in LDS.
-template <int XK, int WAVES, int NL, int DEPTH>
-__global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_up_kernel(MoeArgs a) {
-  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
-  constexpr int kRows = Stream::Slot::kRows;
-  __shared__ typename Stream::Slot slots[WAVES];
-  __shared__ uint16_t members[kMx4MoePairs];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int pair = blockIdx.y, e = __builtin_amdgcn_readfirstlane(a.ids[pair]);
-  int count = 0;
-  bool lead = e >= 0;
-  for (int base = 0; base < a.pairs; base += 64) {
-    const int q = base + lane;
-    const bool mine = q < a.pairs && a.ids[q] == e;
-    const uint64_t m = __ballot(mine);
-    if (__ballot(mine && q < pair) != 0ull) lead = false;
-    if (wave == 0 && mine) members[count + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)q;
-    count += __popcll(m);
+// The pairs of a call grouped by expert, in LDS: every block works them out for
+// itself (about 1 us, less than another launch).
+struct Groups {
+  uint32_t first[kMx4MoeExperts];  // an expert's first pair
+  uint16_t ids[kMx4MoePairs];      // kNone: no expert
+  uint16_t leads[kMx4MoePairs];    // the experts' first pairs, in order
+  int count;                       // of experts that are hit
+  static constexpr uint16_t kNone = 0xffffu;
+};
+
+template <int THREADS>
+__device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
+  const bool one = a.T == 1;  // a token's experts are distinct
+  for (int p = threadIdx.x; p < a.pairs; p += THREADS) s.ids[p] = (uint16_t)a.ids[p];
+  if (!one) {
+    for (int e = threadIdx.x; e < a.experts; e += THREADS) s.first[e] = ~0u;
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.pairs; p += THREADS)
+      if (s.ids[p] != Groups::kNone) atomicMin(&s.first[s.ids[p]], (uint32_t)p);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.leads[pair] = lead ? 1 : 0;
-  if (!lead) return;
   __syncthreads();
-  const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16;
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int n = 0;
+    for (int base = 0; base < a.pairs; base += 64) {
+      const int p = base + lane;
+      const uint16_t e = p < a.pairs ? s.ids[p] : Groups::kNone;
+      const bool lead = e != Groups::kNone && (one || s.first[e] == (uint32_t)p);
+      const uint64_t m = __ballot(lead);
+      if (lead) s.leads[n + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)p;
+      n += __popcll(m);
+    }
+    if (lane == 0) s.count = n;
+  }
+  __syncthreads();
+}
+
+// The pairs of expert e: lane t looks for token t's.  Writes them in the order
+// of the tokens to `members` (the wave's own) and returns how many there are.
+__device__ __forceinline__ int find_members(const Groups& s, const MoeArgs& a, int e, uint16_t* members, int lane) {
+  int mine = -1;
+  for (int k = 0; k < a.top_k; ++k) {
+    const int p = lane * a.top_k + k;
+    if (lane < a.T && s.ids[p] == e) mine = p;
+  }
+  const uint64_t m = __ballot(mine >= 0);
+  wave_lds_fence();
+  if (mine >= 0) members[__popcll(m & ((1ull << lane) - 1))] = (uint16_t)mine;
+  wave_lds_fence();
+  return __popcll(m);
+}
+
+// A wave's (or block's) work: 16 rows of an expert and up to kRows of its
+// pairs.  `index` runs through experts (slowly) and tiles of rows (fast).
+template <int NL>
+struct MoeItem {
+  Mx4Source<NL> src;
+  int index, m0, count;  // count: the expert's pairs, m0: the first of them taken here
+  int r0, pair;          // first row; the lane's column's pair, or -1
+};
+
+template <typename Stream, int NL>
+__device__ __forceinline__ void set_item(MoeItem<NL>& it, int e, const uint8_t* w, const uint8_t* ws, int64_t row0,
+                                         uint32_t blocks, const uint16_t* members, int top_k_or_one, int lane) {
+  it.src.wr = make_rsrc(w + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+  const Mx4Scales sc(ws + row0 * blocks, 16 * blocks);
+  it.src.wsr = sc.rsrc;
+  it.src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
+  it.src.ws_skew = sc.skew((lane & 15) * blocks);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int row = it.m0 + mx4_x_row<kMx4XBF16>(i, lane);
+    it.src.xoff[i] = row < it.count ? (uint32_t)(members[min(row, 63)] / top_k_or_one) * blocks * 64u : kOutOfRange;
+  }
+  const int c = lane & 15;
+  it.pair = c < Stream::Slot::kRows && it.m0 + c < it.count ? members[min(it.m0 + c, 63)] : -1;
+}
+
+// No further work: loads of nothing.
+template <int NL>
+__device__ __forceinline__ void set_none(MoeItem<NL>& it, const void* any) {
+  it.src.wr = it.src.wsr = make_rsrc(any, 0);
+  it.src.wsoff = kOutOfRange;
+  it.src.ws_skew = 0;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) it.src.xoff[i] = kOutOfRange;
+  it.pair = -1;
+}
+
+// Gate and up.  KW waves split the columns of an item (KW = 1: each wave has
+// items of its own); the loads of the next item are under way while one is
+// multiplied.
+template <int XK, int KW, int NL, int DEPTH>
+__global__ __launch_bounds__(256) void vq_mx4_moe_up_kernel(MoeArgs a) {
+  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
+  constexpr int kRows = Stream::Slot::kRows, kWaves = 4;
+  __shared__ typename Stream::Slot slots[kWaves];
+  __shared__ float4_t part[KW > 1 ? kWaves : 1][64];
+  __shared__ Groups groups;
+  __shared__ uint16_t members[kWaves][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  group_pairs<64 * kWaves>(groups, a);
   const uint32_t blocks = a.hidden_blocks;
-  const int64_t row0 = (int64_t)e * a.inter_blocks * 64 + r0;  // 2 * inter rows an expert
+  const int tiles = a.inter_blocks * 4, items = __builtin_amdgcn_readfirstlane(groups.count) * tiles;
+  const int stride = KW > 1 ? gridDim.x : gridDim.x * kWaves;
   Stream st;
   st.slot = slots + wave;
   st.first = 0;
   st.end = blocks;
-  st.wr = make_rsrc(a.gu + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
   st.xr = make_rsrc(a.x, (uint64_t)a.T * blocks * 64);
   st.plane = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
-  const Mx4Scales ws(a.gus + row0 * blocks, 16 * blocks);
-  st.wsr = ws.rsrc;
-  st.wsoff = ws.word(mx4_s_row(lane) * blocks, lane);
-  st.ws_skew = ws.skew(r * blocks);
   st.column = r & (kRows - 1);
-  for (int m0 = 0; m0 < count; m0 += kRows) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = m0 + mx4_x_row<XK>(i, lane);
-      st.xoff[i] = row < count ? (uint32_t)(members[row] / a.top_k) * blocks * 64u : kOutOfRange;
-    }
+  auto set = [&](MoeItem<NL>& it) VQMI_INLINE {  // at it.index, its pairs from it.m0 on (0: to be found)
+    if (it.index >= items) return set_none(it, a.x);
+    const int e = __builtin_amdgcn_readfirstlane(groups.ids[groups.leads[it.index / tiles]]);
+    if (it.m0 == 0) it.count = find_members(groups, a, e, members[wave], lane);
+    it.r0 = it.index % tiles * 16;
+    set_item<Stream>(it, e, a.gu, a.gus, (int64_t)e * a.inter_blocks * 64 + it.r0, blocks, members[wave], a.top_k, lane);
+  };
+  MoeItem<NL> cur, next;
+  cur.index = KW > 1 ? blockIdx.x : blockIdx.x * kWaves + wave;
+  cur.m0 = cur.count = 0;
+  set(cur);
+  const uint32_t from = KW > 1 ? wave : 0;
+  st.start(cur.src, from, KW, lane);
+  while (cur.index < items) {
+    next.index = cur.index;
+    next.count = cur.count;
+    next.m0 = cur.m0 + kRows;
+    if (next.m0 >= cur.count) next.index += stride, next.m0 = 0;
+    set(next);
     float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    st.run(acc, wave, WAVES, lane);
-    __syncthreads();  // the slots are free: the waves' sums go there
-    float4_t* part = reinterpret_cast<float4_t*>(slots);
-    part[wave * 64 + lane] = acc[0] + acc[1];
-    __syncthreads();
-    if (wave == 0 && r < kRows && m0 + r < count) {
-      float4_t s = part[lane];
+    st.run(acc, cur.src, next.src, from, KW, lane);
+    float4_t s = acc[0] + acc[1];
+    if constexpr (KW > 1) {
+      part[wave][lane] = s;
+      lds_barrier();
+      s = part[0][lane];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) s += part[w * 64 + lane];
+      for (int w = 1; w < KW; ++w) s += part[w][lane];
+      lds_barrier();
+    }
+    if ((KW == 1 || wave == 0) && cur.pair >= 0) {
       uint32_t lo[kMx4Planes], hi[kMx4Planes];
       split_planes(silu_mul<true>(s[0], s[1]), lo);
       split_planes(silu_mul<true>(s[2], s[3]), hi);
       const int64_t inter = (int64_t)a.inter_blocks * 32;
-      uint16_t* out = a.h + members[m0 + r] * inter + r0 / 2 + 2 * g;
+      uint16_t* out = a.h + cur.pair * inter + cur.r0 / 2 + 2 * g;
 #pragma unroll
       for (int p = 0; p < kMx4Planes; ++p)
         *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
     }
-    if (m0 + kRows < count) __syncthreads();
+    cur = next;
   }
 }
 
 // Down: a block takes 16 output rows for all tokens, its waves the experts in
 // turn, for the pairs of an expert, kRows at a time.  A wave adds up its
-// experts' weighted products per token in LDS, in the order of the pairs; the
+// experts' weighted products per token in LDS, in the order of the experts; the
 // waves' sums are joined in their order.
 template <int WAVES, int NL, int DEPTH, int TOKENS>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) {
@@ -122,14 +210,14 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
   constexpr int kRows = Stream::Slot::kRows;
   __shared__ typename Stream::Slot slots[WAVES];
   __shared__ float4_t sums[WAVES][TOKENS][4];  // 16 rows a token
-  __shared__ int32_t ids[kMx4MoePairs];
-  __shared__ uint16_t members[WAVES][TOKENS];
+  __shared__ Groups groups;
+  __shared__ uint16_t members[WAVES][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16;
-  for (int p = threadIdx.x; p < a.pairs; p += 64 * WAVES) ids[p] = a.ids[p];
   for (int i = lane; i < TOKENS * 4; i += 64) sums[wave][i / 4][i % 4] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  __syncthreads();
+  group_pairs<64 * WAVES>(groups, a);
   const uint32_t blocks = a.inter_blocks;
+  const int items = __builtin_amdgcn_readfirstlane(groups.count);
   Stream st;
   st.slot = slots + wave;
   st.first = 0;
@@ -139,49 +227,38 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
 #pragma unroll
   for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
   st.column = r & (kRows - 1);
-  int turn = 0;  // experts seen
-  for (int base = 0; base < a.pairs; base += 64) {
-    uint64_t todo = __ballot(base + lane < a.pairs && a.leads[min(base + lane, a.pairs - 1)] != 0);
-    for (; todo != 0ull; todo &= todo - 1, ++turn) {
-      if (turn % WAVES != wave) continue;
-      const int e = __builtin_amdgcn_readfirstlane(ids[base + __builtin_ctzll(todo)]);
-      int mine = -1;  // the pair of token `lane`
-      for (int s = 0; s < a.top_k; ++s) {
-        const int p = lane * a.top_k + s;
-        if (lane < a.T && ids[p] == e) mine = p;
-      }
-      const uint64_t m = __ballot(mine >= 0);
-      const int count = __popcll(m);
-      if (mine >= 0) members[wave][__popcll(m & ((1ull << lane) - 1))] = (uint16_t)mine;
-      wave_lds_fence();
-      const int64_t row0 = (int64_t)e * a.hidden_blocks * 32 + r0;
-      st.wr = make_rsrc(a.dn + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
-      const Mx4Scales ws(a.dns + row0 * blocks, 16 * blocks);
-      st.wsr = ws.rsrc;
-      st.wsoff = ws.word(mx4_s_row(lane) * blocks, lane);
-      st.ws_skew = ws.skew(r * blocks);
-      for (int m0 = 0; m0 < count; m0 += kRows) {
+  float weight_next = 0.0f;
+  auto set = [&](MoeItem<NL>& it) VQMI_INLINE {
+    if (it.index >= items) return set_none(it, a.h);
+    const int e = __builtin_amdgcn_readfirstlane(groups.ids[groups.leads[it.index]]);
+    if (it.m0 == 0) it.count = find_members(groups, a, e, members[wave], lane);
+    set_item<Stream>(it, e, a.dn, a.dns, (int64_t)e * a.hidden_blocks * 32 + r0, blocks, members[wave], 1, lane);
+    weight_next = a.weights[max(it.pair, 0)];
+  };
+  MoeItem<NL> cur, next;
+  cur.index = wave;
+  cur.m0 = cur.count = 0;
+  set(cur);
+  st.start(cur.src, 0, 1, lane);
+  while (cur.index < items) {
+    const float f = weight_next;
+    next.index = cur.index;
+    next.count = cur.count;
+    next.m0 = cur.m0 + kRows;
+    if (next.m0 >= cur.count) next.index += WAVES, next.m0 = 0;
+    set(next);
+    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    st.run(acc, cur.src, next.src, 0, 1, lane);
+    if (cur.pair >= 0) {
+      float4_t* s = &sums[wave][cur.pair / a.top_k][g];
+      const float4_t d = acc[0] + acc[1];
+      float4_t o = *s;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          const int row = m0 + mx4_x_row<kMx4XPlanes>(i, lane);
-          st.xoff[i] = row < count ? (uint32_t)members[wave][row] * blocks * 64u : kOutOfRange;
-        }
-        const bool live = r < kRows && m0 + r < count;
-        const int pair = live ? members[wave][m0 + r] : 0;
-        const float f = a.weights[pair];
-        float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        st.run(acc, 0, 1, lane);
-        if (live) {
-          float4_t* s = &sums[wave][pair / a.top_k][g];
-          const float4_t d = acc[0] + acc[1];
-          float4_t o = *s;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = fmaf(f, d[i], o[i]);
-          *s = o;
-        }
-        wave_lds_fence();
-      }
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(f, d[i], o[i]);
+      *s = o;
     }
+    wave_lds_fence();
+    cur = next;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * 4; i += 64 * WAVES) {
@@ -194,19 +271,20 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
   }
 }
 
-template <int XK, int NL>
+template <int XK>
 void run_up(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.inter_blocks * 4, (unsigned)a.pairs);
-  hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 4, NL, 3>), grid, dim3(256), 0, s, a);
+  const int tiles = a.inter_blocks * 4, most = min(a.pairs, a.experts) * tiles;  // items at most
+  if (a.T <= 2) {
+    hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 4, 1, 2>), dim3(min(most, 1 << 16)), dim3(256), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 1, 1, 2>), dim3(min((most + 3) / 4, 1024)), dim3(256), 0, s, a);
+  }
 }
-
-constexpr size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 }  // namespace
 
 size_t mx4_moe_workspace_bytes(int T, int top_k, int inter) {
-  const size_t pairs = (size_t)T * top_k;
-  return align16(pairs * sizeof(int32_t)) + kMx4Planes * pairs * inter * sizeof(uint16_t);
+  return kMx4Planes * (size_t)T * top_k * inter * sizeof(uint16_t);
 }
 
 hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4View& down, const void* logits,
@@ -226,13 +304,13 @@ hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4
   a.T = T;
   a.top_k = r.top_k;
   a.pairs = T * r.top_k;
-  a.leads = static_cast<int32_t*>(workspace);
-  a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + align16((size_t)a.pairs * sizeof(int32_t)));
+  a.experts = r.num_experts;
+  a.h = static_cast<uint16_t*>(workspace);
   a.hidden_blocks = gate_up.cols / kMx4Block;
   a.inter_blocks = down.cols / kMx4Block;
   a.y_kind = y_kind;
-  if (x_kind == kMx4XF16) T <= 4 ? run_up<kMx4XF16, 1>(a, s) : run_up<kMx4XF16, 2>(a, s);
-  else T <= 4 ? run_up<kMx4XBF16, 1>(a, s) : run_up<kMx4XBF16, 2>(a, s);
+  if (x_kind == kMx4XF16) run_up<kMx4XF16>(a, s);
+  else run_up<kMx4XBF16>(a, s);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)a.hidden_blocks * 2);
