@@ -331,6 +331,26 @@ def test_same_bits_again_other_stream_and_captured(x, T, R, C):
         assert torch.equal(y, binding.mx4_gemm(w, a, s))
 
 
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("kernel", range(26))
+def test_every_kernel_and_split(kernel, splits, monkeypatch):
+    """Every row of the table on tiles that end in the middle, whatever the
+    planner would choose."""
+    monkeypatch.setenv("VQMI_MX4_PLAN", f"{kernel},{splits}")
+    for x in ("mx4", "float16", "bfloat16"):
+        for T, R, C in ((1, 40, 2016), (37, 300, 1184), (270, 530, 1600)):
+            _product_check(_operands(T, R, C, ("every", T, R, C), x))
+        _product_check(_operands(70, 258, 1664, ("every", "swiglu"), x, 115, 127), "bfloat16", "swiglu")
+    (xq, xs), (wq, ws) = _operands(20, 200, 1440, ("every", "nan"))
+    xs[7, 3] = 255
+    ws[131, 44] = 255
+    y = _product_check(((xq, xs), (wq, ws))).cpu().numpy()
+    want = np.zeros_like(y, dtype=bool)
+    want[7] = True
+    want[:, 131] = True
+    assert np.array_equal(np.isnan(y), want)
+
+
 def test_quantized_chain_captured():
     """Quantize, multiply with the fused SwiGLU, quantize again, multiply: as an
     MLP runs, eager and replayed."""

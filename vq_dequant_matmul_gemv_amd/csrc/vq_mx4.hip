@@ -8,6 +8,9 @@
 #include "vq_mx4_device.h"
 #include "vq_store_device.h"
 
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
 #include <type_traits>
 
 namespace vqmi {
@@ -405,35 +408,277 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   });
 }
 
+// ---------------------------------------------------------------------------
+// product, many tokens, 16-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
+// block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token)
+// ---------------------------------------------------------------------------
+template <int XK, bool PRECISE, int WM, int WN, int MT, int NT>
+__global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args args) {
+  const Mx4Args a = split_args(args);
+  constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
+  constexpr int kWLoads = kTileRows / (16 * kWaves), kXLoads = kTileTokens / (4 * kWaves);  // a wave: 16 rows, 4 tokens
+  static_assert(kTileRows % (16 * kWaves) == 0 && kTileTokens % (4 * kWaves) == 0, "whole loads");
+  constexpr int kTileBytes = kTileRows * 64 + kTileTokens * 256;
+  constexpr int kPitch = 16 * MT + 4;  // of the outputs in LDS: fp32 a token
+  constexpr int kOutBytes = kWaves * 16 * kPitch * 4;
+  __shared__ __align__(1024) uint8_t lds[2 * kTileBytes > kOutBytes ? 2 * kTileBytes : kOutBytes];
+  __shared__ uint32_t lds_s[2][kTileRows];  // a row's scales of a step
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t blocks = a.blocks;
+  const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
+  int rt, tt;
+  xcd_tile(blockIdx.x, row_tiles, tok_tiles, &rt, &tt);
+  const int r0 = rt * kTileRows, t0 = tt * kTileTokens;
+  const int rows = min(kTileRows, a.rows - r0), toks = min(kTileTokens, a.T - t0);
+  const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
+  const rsrc_t xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * 64, (uint64_t)toks * blocks * 64);
+  const int wm = wave / WN * 16 * MT, wn = wave % WN * 16 * NT;
+  const uint32_t b0 = blockIdx.y * a.split_blocks, b1 = min(blocks, b0 + a.split_blocks);
+  const uint32_t steps = (b1 - b0 + 3) / 4;
+
+  // 16-byte pieces change places within a row (w: piece ^ row / 2 of 4, x: piece
+  // ^ token of 16), so reads of 16 rows touch all banks.
+  const uint32_t w_row = wave * 16 + (lane >> 2), w_piece = lane & 3, x_row = wave * 4 + (lane >> 4), x_piece = lane & 15;
+  u32x4 sw[kWLoads], sx[kXLoads];
+  uint32_t ss[2];
+  // scales of row threadIdx.x, as the two aligned words that a step's four lie in
+  const uint8_t* sc_base = a.ws + (int64_t)r0 * blocks;
+  const uint32_t sc_skew = (uint32_t)reinterpret_cast<uintptr_t>(sc_base) & 3u;
+  const rsrc_t sr = make_rsrc(sc_base - sc_skew, (uint64_t)((sc_skew + (uint64_t)rows * blocks + 3) & ~3ull));
+  const uint32_t sc_off = sc_skew + threadIdx.x * blocks + b0;
+  static_assert(kTileRows <= 64 * kWaves, "a thread loads one row's scales");
+  const bool sc_live = (int)threadIdx.x < rows;
+  auto load = [&](uint32_t s) VQMI_INLINE {  // past the end: zeros
+    const uint32_t bw = b0 + s * 4 + w_piece, bx = b0 + s * 4 + x_piece / 4;
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i)
+      sw[i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      sx[i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
+    const uint32_t off = sc_live ? (sc_off + s * 4) & ~3u : kOutOfRange;
+    ss[0] = buf_load_b32(sr, off);
+    ss[1] = buf_load_b32(sr, off + 4);
+  };
+  auto put = [&](uint32_t s) VQMI_INLINE {
+    uint8_t* to = lds + (s & 1) * kTileBytes;
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      const uint32_t row = w_row + i * 16 * kWaves;
+      *reinterpret_cast<u32x4*>(to + row * 64 + ((w_piece ^ (row >> 1 & 3)) * 16)) = sw[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i) {
+      const uint32_t row = x_row + i * 4 * kWaves;
+      *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[i];
+    }
+    if (threadIdx.x < kTileRows) {
+      // scales past the last column (another row's) are 1: NaN there would spoil the sum
+      const int left = (int)(b1 - b0) - (int)(4 * s);
+      const uint32_t mask = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1u;
+      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[1], ss[0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
+    }
+  };
+  const int r = lane & 15, g = lane >> 4;
+  float4_t acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  load(0);
+  put(0);
+  load(1);
+  lds_barrier();
+  for (uint32_t s = 0; s < steps; ++s) {
+    const uint8_t* wb = lds + (s & 1) * kTileBytes + (wm + r) * 64 + ((g ^ (r >> 1 & 3)) * 16);
+    const uint8_t* xb = lds + (s & 1) * kTileBytes + kTileRows * 64 + (wn + r) * 256;
+    u32x4 q[MT];
+    float sc[MT];
+    bool fit = true;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      q[m] = *reinterpret_cast<const u32x4*>(wb + m * 16 * 64);
+      const uint32_t byte = reinterpret_cast<const uint8_t*>(&lds_s[s & 1][wm + 16 * m + r])[g];
+      sc[m] = __uint_as_float(byte << 23);
+      fit = fit && byte - 104u <= 36u;
+    }
+    if constexpr (XK == kMx4XF16) fit = __ballot(!fit) == 0ull;
+    put(s + 1);
+    load(s + 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4 v[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const u32x4*>(xb + n * 16 * 256 + (((4 * g + i) ^ r) * 16));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const uint32_t c = i == 0 ? q[m].x : i == 1 ? q[m].y : i == 2 ? q[m].z : q[m].w;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = mx4_mfma16<XK>(c, sc[m], v[n], acc[m][n], fit);
+      }
+    }
+    lds_barrier();
+  }
+  // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
+  // token's rows leave in whole pieces.
+  float* out = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
+  static_for<NT>([&](auto n) VQMI_INLINE {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) *reinterpret_cast<float4_t*>(out + r * kPitch + 16 * m + 4 * g) = acc[m][n.value];
+    wave_lds_fence();
+    store_tokens<16 * MT, PRECISE>(a, out, kPitch, t0 + wn + 16 * n.value, r0 + wm, lane);
+    wave_lds_fence();
+  });
+}
+
+// ---------------------------------------------------------------------------
+// joining the splits: y = the sum of the planes, in their order
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void vq_mx4_join_kernel(Mx4Args a, int splits) { join_planes(a, splits); }
+
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <int XK, int WAVES, int NL, int DEPTH>
-void run_skinny(const Mx4Args& a, int splits, hipStream_t s) {
+void run_skinny(const Mx4Args& a, int, int splits, hipStream_t s) {
   constexpr int kTok = Mx4Slot<XK, 1, NL>::kRows;
   const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, kTok), splits);
   hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
 template <int WM, int WN, int MT, int NT, int AHEAD>
-void run_tile(const Mx4Args& a, int splits, hipStream_t s) {
+void run_tile(const Mx4Args& a, int, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
   const dim3 block(64 * WM * WN);
   if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
 }
 
-template <int XK>
-void run_kind(const Mx4Args& a, hipStream_t s) {
-  if constexpr (XK == kMx4XMx4) {
-    if (a.T > 128) return run_tile<4, 2, 4, 8, 1>(a, 1, s);
-    if (a.T <= 8) return run_skinny<XK, 4, 1, 3>(a, 1, s);
-    return run_skinny<XK, 4, 2, 3>(a, 1, s);
+template <int WM, int WN, int MT, int NT>
+void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN);
+  if (xk == kMx4XF16) {
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
   } else {
-    if (a.T <= 2) return run_skinny<XK, 4, 1, 3>(a, 1, s);
-    if (a.T <= 4) return run_skinny<XK, 4, 2, 3>(a, 1, s);
-    if (a.T <= 8) return run_skinny<XK, 4, 4, 2>(a, 1, s);
-    return run_skinny<XK, 4, 8, 2>(a, 1, s);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
   }
+}
+
+template <int WAVES, int NL, int DEPTH>
+void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
+  if (xk == kMx4XF16) run_skinny<kMx4XF16, WAVES, NL, DEPTH>(a, xk, splits, s);
+  else run_skinny<kMx4XBF16, WAVES, NL, DEPTH>(a, xk, splits, s);
+}
+
+// The kernels of the product and a time model of each (us):
+//   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
+//   and, split, 2 + join * (bytes of the planes, written and read, in MB)
+// with steps of 128 columns a wave runs through, rounds of 256 blocks, and
+// bytes the weight once, y, and `x_share` of the tokens' reads by every row
+// tile (MB; bw in TB/s).
+struct Mx4Kernel {
+  int rows, tokens;  // of a block
+  int k_waves;       // waves that split a block's columns
+  int unit_blocks;   // splits are multiples of these blocks of columns
+  bool mx4;          // 4-bit x (else 16-bit)
+  int min_T, max_T;  // tokens it is considered for
+  float base, latency, rate, bw, join, unit, x_share;
+  void (*run)(const Mx4Args&, int, int, hipStream_t);
+};
+constexpr int kAnyT = 1 << 30;
+const Mx4Kernel kMx4Kernels[] = {
+    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 3>},
+    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 2>},
+    {16, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 1, 2>},
+    {16, 8, 2, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 2, 1, 4>},
+    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 3>},
+    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 2>},
+    {16, 16, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 2>},
+    {128, 32, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 2, 1>},
+    {128, 64, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 4, 1>},
+    {128, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 4, 1>},
+    {128, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 6, 1>},
+    {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 2>},
+    {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 8, 1>},
+    {16, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 3>},
+    {16, 2, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 1, 2>},
+    {16, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 3>},
+    {16, 4, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 2>},
+    {16, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 4, 2>},
+    {16, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 8, 2>},
+    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2>},
+    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 2>},
+    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2>},
+    {128, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 4>},
+    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4>},
+};
+constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
+constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
+
+// Sizes a plan is for.
+struct Mx4Call {
+  int rows, blocks, T;
+  bool mx4;
+  bool operator==(const Mx4Call& o) const {
+    return rows == o.rows && blocks == o.blocks && T == o.T && mx4 == o.mx4;
+  }
+};
+
+// The call by kernel i with its columns in up to `splits` parts.  False where
+// the kernel does not serve the call, or the launch (fewer than 2^32 threads, a
+// block up to 512) or the planes grow too large.
+bool set_plan(const Mx4Call& c, int i, int splits, Mx4Plan* p) {
+  const Mx4Kernel& k = kMx4Kernels[i];
+  if (k.mx4 != c.mx4) return false;
+  if ((int64_t)ceil_div(c.rows, k.rows) * ceil_div(c.T, k.tokens) >= 1 << 22) return false;
+  p->kernel = i;
+  p->split_blocks = ceil_div(ceil_div(c.blocks, splits), k.unit_blocks) * k.unit_blocks;
+  p->splits = ceil_div(c.blocks, p->split_blocks);
+  p->workspace = p->splits > 1 ? (size_t)p->splits * c.T * c.rows * sizeof(float) : 0;
+  return p->workspace <= kMaxPlanBytes;
+}
+
+float plan_time(const Mx4Call& c, const Mx4Plan& p) {
+  const Mx4Kernel& k = kMx4Kernels[p.kernel];
+  const float split_steps = 0.25f * p.split_blocks, load_steps = split_steps / k.k_waves;
+  const int64_t units = (int64_t)ceil_div(c.rows, k.rows) * ceil_div(c.T, k.tokens) * p.splits;
+  const float out = (float)c.T * c.rows, w = 17.0f * c.rows * c.blocks, x = (c.mx4 ? 17.0f : 64.0f) * c.T * c.blocks;
+  const float bytes = (w + 4.0f * out + k.x_share * x * c.rows / k.rows) * 1e-6f;
+  const float a = k.latency * std::ceil(load_steps), b = (float)((units + 255) / 256) * (k.rate * load_steps + k.unit),
+              e = bytes / k.bw;
+  const float t = k.base + std::sqrt(std::sqrt(a * a * a * a + b * b * b * b + e * e * e * e));
+  return p.splits > 1 ? t + 2.0f + k.join * p.splits * out * 8e-6f : t;
+}
+
+Mx4Plan make_plan(const Mx4Call& c) {
+  Mx4Plan best;
+  float best_t = 0.0f;
+  for (int i = 0; i < kNumMx4Kernels; ++i) {
+    if (c.T < kMx4Kernels[i].min_T || c.T > kMx4Kernels[i].max_T) continue;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
+      Mx4Plan p;
+      if (!set_plan(c, i, s, &p) || p.splits != s) continue;
+      const float t = plan_time(c, p);
+      if (best.kernel < 0 || t < best_t) best = p, best_t = t;
+    }
+  }
+  return best;
+}
+
+Mx4Plan cached_plan(const Mx4Call& c) {
+  // the plans this thread made last (choosing takes a microsecond or two)
+  struct Slot {
+    Mx4Call call{};  // no rows: empty
+    Mx4Plan plan;
+  };
+  static thread_local Slot last[64];
+  Slot& slot = last[((unsigned)c.rows * 31u + (unsigned)c.blocks * 7u + (unsigned)c.T * 2u + (unsigned)c.mx4) % 64u];
+  if (!(slot.call == c)) slot.plan = make_plan(c), slot.call = c;
+  return slot.plan;
 }
 
 }  // namespace
@@ -459,11 +704,19 @@ hipError_t launch_mx4_dequant(const uint8_t* q, const uint8_t* scales, int64_t v
   return hipGetLastError();
 }
 
+// VQMI_MX4_PLAN = "kernel,splits" (a row of the table) forces the choice, for
+// tests; a kernel or split that set_plan refuses is passed over.
 Mx4Plans mx4_plans(int rows, int cols, int T) {
-  Mx4Plan p;
-  const int64_t tiles = (int64_t)ceil_div(rows, 16) * ceil_div(T, 16);
-  p.kernel = tiles < (1 << 24) ? 0 : -1;
-  return {p, p};
+  const char* e = getenv("VQMI_MX4_PLAN");
+  int k = 0, splits = 0;
+  const bool forced = e && sscanf(e, "%d,%d", &k, &splits) == 2 && k >= 0 && k < kNumMx4Kernels && splits >= 1 &&
+                      splits <= 64;
+  auto plan = [&](bool mx4) {
+    const Mx4Call c{rows, cols / kMx4Block, T, mx4};
+    Mx4Plan p;
+    return forced && set_plan(c, k, splits, &p) ? p : cached_plan(c);
+  };
+  return {plan(true), plan(false)};
 }
 
 hipError_t launch_mx4_gemm(const Mx4View& w, const IoSpec& io, const Mx4Plan& p, const void* x, int x_kind,
@@ -479,10 +732,12 @@ hipError_t launch_mx4_gemm(const Mx4View& w, const IoSpec& io, const Mx4Plan& p,
   a.T = T;
   a.y_kind = io.y_kind;
   a.swiglu = io.epi == kEpiSwiglu;
-  a.split_blocks = a.blocks;
-  if (x_kind == kMx4XMx4) run_kind<kMx4XMx4>(a, s);
-  else if (x_kind == kMx4XF16) run_kind<kMx4XF16>(a, s);
-  else run_kind<kMx4XBF16>(a, s);
+  a.part = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.split_blocks = p.split_blocks;
+  kMx4Kernels[p.kernel].run(a, x_kind, p.splits, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(vq_mx4_join_kernel, dim3((unsigned)ceil_div((int64_t)T * w.rows, 1024)), dim3(256), 0, s, a, p.splits);
   return hipGetLastError();
 }
 

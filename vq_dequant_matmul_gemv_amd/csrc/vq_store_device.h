@@ -75,6 +75,7 @@ __device__ __forceinline__ void store_tokens(const Args& a, const float* lds, in
   if (a.rows % 8 != 0) {  // one value a lane: a token's rows still leave side by side
     auto single = [&](auto swiglu) {
       constexpr int kPairs = swiglu.value ? 2 : 1, kOut = ROWS / kPairs;
+      static_assert(16 * kOut % (4 * 64) == 0, "whole rounds of the wave");
       const int rows = a.rows / kPairs, o0 = r0 / kPairs;
       for (int base = 0; base < 16 * kOut; base += 4 * 64) {
         float v[4];
@@ -130,6 +131,42 @@ __device__ __forceinline__ void store_rows4(const Args& a, int t, int row, const
     for (int i = 0; i < 4; ++i) {
       if (row + i < a.rows) store_out(a.y, (int64_t)t * a.rows + row + i, v[i], a.y_kind);
     }
+  }
+}
+
+// Joining the splits of a product's columns, four values a thread of 256: y =
+// the sum of the planes a.part [splits][T][rows], in their order.
+template <typename Args>
+__device__ __forceinline__ void join_planes(const Args& a, int splits) {
+  const int64_t n = (int64_t)a.T * a.rows, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  if (n % 4 == 0 && (!a.swiglu || a.rows % 2 == 0)) {
+    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float4_t p[8];  // eight planes in flight
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        p[s] = *reinterpret_cast<const float4_t*>(a.part + min(s0 + s, splits - 1) * n + i);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) v += s0 + s < splits ? p[s] : float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // pairs of rows never straddle a token: rows are even under SwiGLU
+    if (a.swiglu) {
+      store_out(a.y, i / 2, silu_mul<true>(v[0], v[1]), a.y_kind);
+      store_out(a.y, i / 2 + 1, silu_mul<true>(v[2], v[3]), a.y_kind);
+    } else {
+      const float o[4] = {v[0], v[1], v[2], v[3]};
+      store_run<4>(a.y, i, o, a.y_kind);
+    }
+    return;
+  }
+  for (int64_t k = i; k < min(n, i + 4); k += a.swiglu ? 2 : 1) {
+    float v = 0.0f, u = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+      v += a.part[s * n + k];
+      if (a.swiglu) u += a.part[s * n + k + 1];
+    }
+    store_out(a.y, a.swiglu ? k / 2 : k, a.swiglu ? silu_mul<true>(v, u) : v, a.y_kind);
   }
 }
 
