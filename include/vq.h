@@ -594,13 +594,13 @@ vq_status vq_mx4_gemm(const vq_mx4_tensor *w, const vq_io *io, const void *x, co
  *   x: device [T][hidden], y: device [T][hidden], 16-byte aligned;
  *   expert_ids: device [T][top_k] int32, route_weights: device [T][top_k]
  *   fp32, 4-byte aligned: outputs, as vq_moe_route leaves them;
- *   workspace: device, >= vq_mx4_moe_workspace_bytes(T, top_k, inter) bytes,
- *   16-byte aligned, as for vq_mx4_gemm.
- * 0 <= T <= 64 (0 enqueues nothing), T * top_k <= 1024, and T * top_k * inter
- * <= 2^26 (else VQ_ERR_SHAPE; larger batches belong to vq_moe_route and products
+ *   workspace: device, >= vq_mx4_moe_workspace_bytes(T, top_k, hidden, inter)
+ *   bytes, 16-byte aligned, as for vq_mx4_gemm.
+ * 0 <= T <= 64 (0 enqueues nothing), T * top_k <= 1024, and T * top_k * hidden
+ * and T * top_k * inter <= 2^26 (else VQ_ERR_SHAPE; larger batches belong to vq_moe_route and products
  * of their own).
  */
-size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t inter);
+size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t hidden, int32_t inter);
 vq_status vq_mx4_moe(const vq_router *r, const vq_mx4_tensor *gate_up, const vq_mx4_tensor *down, const vq_io *io,
                      const void *logits, const void *x, int32_t T, void *y, int32_t *expert_ids, float *route_weights,
                      void *workspace, size_t workspace_bytes, void *stream);

@@ -197,7 +197,7 @@ def test_same_bits_again_other_stream_and_captured(T):
         assert torch.equal(a, b)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
-    ws = torch.empty(binding.LIB.vq_mx4_moe_workspace_bytes(T, 4, 128), dtype=torch.uint8, device="cuda").fill_(0xff)
+    ws = torch.empty(binding.LIB.vq_mx4_moe_workspace_bytes(T, 4, 256, 128), dtype=torch.uint8, device="cuda").fill_(0xff)
     torch.cuda.synchronize()
     y = torch.empty_like(ref[0])
     ids, w = torch.empty_like(ref[1]), torch.empty_like(ref[2])

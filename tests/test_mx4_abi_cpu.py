@@ -210,9 +210,10 @@ def test_layer_refuses_experts_that_do_not_fit(b):
     assert _moe(b, router=many, gu=_tensor(b, 128, 96, 64), dn=_tensor(b, 96, 64, 64), T=64) == "VQ_ERR_SHAPE"
     # more activations than a launch holds
     assert _moe(b, gu=_tensor(b, 1 << 21, 96, 16), dn=_tensor(b, 96, 1 << 20, 16), T=64) == "VQ_ERR_SHAPE"
-    need = b.LIB.vq_mx4_moe_workspace_bytes(4, 2, 64)
+    need = b.LIB.vq_mx4_moe_workspace_bytes(4, 2, 96, 64)
     assert need >= 4 * 2 * 64 * 6 and _moe(b, wsb=need - 1) == "VQ_ERR_WORKSPACE"
-    assert b.LIB.vq_mx4_moe_workspace_bytes(65, 2, 64) == 0 and b.LIB.vq_mx4_moe_workspace_bytes(0, 2, 64) == 0
+    assert b.LIB.vq_mx4_moe_workspace_bytes(65, 2, 96, 64) == 0 and b.LIB.vq_mx4_moe_workspace_bytes(0, 2, 96, 64) == 0
+    assert b.LIB.vq_mx4_moe_workspace_bytes(4, 2, 90, 64) == 0
 
 
 # ---- binding --------------------------------------------------------------

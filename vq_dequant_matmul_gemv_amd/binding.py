@@ -159,7 +159,7 @@ def _load():
         "vq_mx4_dequant": (i32, [P, P, i32, i32, i32, P, P]),
         "vq_mx4_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
         "vq_mx4_gemm": (i32, [P, P, P, P, i32, P, P, ctypes.c_size_t, P]),
-        "vq_mx4_moe_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "vq_mx4_moe_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32]),
         "vq_mx4_moe": (i32, [P, P, P, P, P, P, i32, P, P, P, P, ctypes.c_size_t, P]),
         "vq_norm": (i32, [P, P, P, i32, P, P, P, P]),
         "vq_last_error": (ctypes.c_char_p, []),
@@ -935,7 +935,7 @@ def mx4_moe(router: Router, gate_up: MX4Tensor, down: MX4Tensor, logits, x, y=No
     if y is None:
         y = _rows(T, hidden, y_dtype, dev)
     if workspace is None:
-        need = LIB.vq_mx4_moe_workspace_bytes(T, router.top_k, inter)
+        need = LIB.vq_mx4_moe_workspace_bytes(T, router.top_k, hidden, inter)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(),

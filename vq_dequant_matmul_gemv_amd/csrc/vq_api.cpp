@@ -701,20 +701,23 @@ vq_status vq_mx4_gemm(const vq_mx4_tensor* w, const vq_io* io, const void* x, co
 }
 
 // Sizes of a layer call that its workspace depends on.
-static vq_status check_mx4_moe_sizes(const char* fn, int32_t T, int32_t top_k, int32_t inter) {
+static vq_status check_mx4_moe_sizes(const char* fn, int32_t T, int32_t top_k, int32_t hidden, int32_t inter) {
   if (T < 0 || T > vqmi::kMx4MoeTokens)
     return fail(VQ_ERR_SHAPE, "%s: T=%d outside [0, %d]", fn, T, vqmi::kMx4MoeTokens);
   if (top_k < 1 || top_k > 64 || T * top_k > vqmi::kMx4MoePairs)
     return fail(VQ_ERR_SHAPE, "%s: T=%d x top_k=%d outside [0, %d] (top_k in [1, 64])", fn, T, top_k,
                 vqmi::kMx4MoePairs);
-  if (!mx4_cols_ok(inter) || (int64_t)T * top_k * inter > (1 << 26))
-    return fail(VQ_ERR_SHAPE, "%s: inter=%d must be a multiple of 32, T * top_k * inter at most 2^26", fn, inter);
+  for (const int32_t n : {hidden, inter}) {
+    if (!mx4_cols_ok(n) || (int64_t)T * top_k * n > (1 << 26))
+      return fail(VQ_ERR_SHAPE, "%s: hidden=%d and inter=%d must be multiples of 32, T * top_k times each at most 2^26",
+                  fn, hidden, inter);
+  }
   return VQ_OK;
 }
 
-size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t inter) {
-  if (check_mx4_moe_sizes("vq_mx4_moe_workspace_bytes", T, top_k, inter) != VQ_OK) return 0;
-  return T == 0 ? 0 : vqmi::mx4_moe_workspace_bytes(T, top_k, inter);
+size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t hidden, int32_t inter) {
+  if (check_mx4_moe_sizes("vq_mx4_moe_workspace_bytes", T, top_k, hidden, inter) != VQ_OK) return 0;
+  return T == 0 ? 0 : vqmi::mx4_moe_workspace_bytes(T, top_k, hidden, inter);
 }
 
 vq_status vq_mx4_moe(const vq_router* r, const vq_mx4_tensor* gate_up, const vq_mx4_tensor* down, const vq_io* io,
@@ -734,7 +737,7 @@ vq_status vq_mx4_moe(const vq_router* r, const vq_mx4_tensor* gate_up, const vq_
   if (down->rows != gate_up->cols || gate_up->rows != 2 * (int64_t)down->cols)
     return fail(VQ_ERR_SHAPE, "%s: gate_up is %d x %d, so down must be %d x %d, not %d x %d", fn, gate_up->rows,
                 gate_up->cols, gate_up->cols, gate_up->rows / 2, down->rows, down->cols);
-  st = check_mx4_moe_sizes(fn, T, r->top_k, down->cols);
+  st = check_mx4_moe_sizes(fn, T, r->top_k, down->rows, down->cols);
   if (st != VQ_OK) return st;
   int x_kind = vqmi::kMx4XF16, y_kind = vqmi::kOutF32;
   if (io) {
@@ -752,7 +755,7 @@ vq_status vq_mx4_moe(const vq_router* r, const vq_mx4_tensor* gate_up, const vq_
   if (st != VQ_OK) return st;
   st = check_xy(x, y, "y");
   if (st != VQ_OK) return st;
-  st = check_workspace(fn, workspace, workspace_bytes, vqmi::mx4_moe_workspace_bytes(T, r->top_k, down->cols));
+  st = check_workspace(fn, workspace, workspace_bytes, vqmi::mx4_moe_workspace_bytes(T, r->top_k, down->rows, down->cols));
   if (st != VQ_OK) return st;
   const vqmi::Mx4View gu{gate_up->values, gate_up->scales, gate_up->rows, gate_up->cols};
   const vqmi::Mx4View dn{down->values, down->scales, down->rows, down->cols};

@@ -73,7 +73,7 @@ hipError_t launch_mx4_gemm(const Mx4View& w, const IoSpec& io, const Mx4Plan& p,
 constexpr int kMx4MoeTokens = 64;
 constexpr int kMx4MoePairs = 1024;  // T * top_k
 constexpr int kMx4MoeExperts = 1024;  // the router's limit
-size_t mx4_moe_workspace_bytes(int T, int top_k, int inter);
+size_t mx4_moe_workspace_bytes(int T, int top_k, int hidden, int inter);
 hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4View& down, const void* logits,
                           const void* x, int x_kind, int T, void* y, int y_kind, int32_t* ids, float* weights,
                           void* workspace, hipStream_t s);

@@ -167,6 +167,12 @@ struct Mx4Source {
   rsrc_t wr, wsr;               // values and scales of the rows
   uint32_t wsoff, xoff[NL];     // byte offsets of the lane's rows; kOutOfRange: no such row
   uint32_t ws_skew;             // of the row that the lane multiplies
+
+  __device__ __forceinline__ void take(const Mx4Source& o) {
+    wr = o.wr, wsr = o.wsr, wsoff = o.wsoff, ws_skew = o.ws_skew;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) xoff[i] = o.xoff[i];
+  }
 };
 
 template <int XK, int PL, int NL, int DEPTH>

@@ -22,7 +22,8 @@ struct MoeArgs {
   void* y;
   const int32_t* ids;
   const float* weights;
-  uint16_t* h;     // [kMx4Planes][pairs][inter]
+  uint16_t* h;      // [kMx4Planes][pairs][inter]
+  float* products;  // [pairs][hidden]
   int T, top_k, pairs, experts;
   int hidden_blocks, inter_blocks;  // blocks of 32 columns
   int y_kind;
@@ -42,139 +43,174 @@ __device__ __forceinline__ void split_planes(float v, uint32_t* p) {
 }
 
 // The pairs of a call grouped by expert, in LDS: every block works them out for
-// itself (about 1 us, less than another launch).
+// itself (1 to 2 us, less than another launch).
 struct Groups {
-  uint32_t first[kMx4MoeExperts];  // an expert's first pair
-  uint16_t ids[kMx4MoePairs];      // kNone: no expert
-  uint16_t leads[kMx4MoePairs];    // the experts' first pairs, in order
-  int count;                       // of experts that are hit
-  static constexpr uint16_t kNone = 0xffffu;
+  uint32_t mask[2][kMx4MoeExperts];      // the tokens that chose an expert
+  uint16_t at[kMx4MoeExperts];           // where an expert's pairs start in `pair`
+  uint16_t expert[kMx4MoePairs], start[kMx4MoePairs + 1];  // experts that are hit, in their order, and their pairs
+  uint16_t pair[kMx4MoePairs];           // by expert, then by token
+  uint8_t token[kMx4MoePairs];
+  int count;                             // of experts that are hit
 };
 
 template <int THREADS>
 __device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
-  const bool one = a.T == 1;  // a token's experts are distinct
-  for (int p = threadIdx.x; p < a.pairs; p += THREADS) s.ids[p] = (uint16_t)a.ids[p];
-  if (!one) {
-    for (int e = threadIdx.x; e < a.experts; e += THREADS) s.first[e] = ~0u;
+  constexpr int kPer = kMx4MoePairs / THREADS;
+  const int lane = threadIdx.x & 63;
+  if (a.T == 1) {  // a token's experts are distinct
+    if (threadIdx.x < 64) {
+      const int e = lane < a.pairs ? a.ids[lane] : -1;
+      const uint64_t m = __ballot(e >= 0);
+      const int i = __popcll(m & ((1ull << lane) - 1)), n = __popcll(m);
+      if (e >= 0) {
+        s.expert[i] = (uint16_t)e;
+        s.pair[i] = (uint16_t)lane;
+        s.token[i] = 0;
+      }
+      if (lane <= n) s.start[lane] = (uint16_t)lane;
+      if (lane == 0) s.start[n] = (uint16_t)n, s.count = n;
+    }
     __syncthreads();
-    for (int p = threadIdx.x; p < a.pairs; p += THREADS)
-      if (s.ids[p] != Groups::kNone) atomicMin(&s.first[s.ids[p]], (uint32_t)p);
+    return;
   }
+  int e[kPer], t[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = threadIdx.x + i * THREADS;
+    e[i] = p < a.pairs ? a.ids[p] : -1;
+    t[i] = p / a.top_k;
+  }
+  for (int x = threadIdx.x; x < a.experts; x += THREADS) s.mask[0][x] = s.mask[1][x] = 0u;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (e[i] >= 0) atomicOr(&s.mask[t[i] >> 5][e[i]], 1u << (t[i] & 31));
   __syncthreads();
   if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int n = 0;
-    for (int base = 0; base < a.pairs; base += 64) {
-      const int p = base + lane;
-      const uint16_t e = p < a.pairs ? s.ids[p] : Groups::kNone;
-      const bool lead = e != Groups::kNone && (one || s.first[e] == (uint32_t)p);
-      const uint64_t m = __ballot(lead);
-      if (lead) s.leads[n + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)p;
+    int n = 0, pairs = 0;
+    for (int base = 0; base < a.experts; base += 64) {
+      const int x = base + lane;
+      const int c = x < a.experts ? __popc(s.mask[0][x]) + __popc(s.mask[1][x]) : 0;
+      const uint64_t m = __ballot(c > 0);
+      int sum = c;  // of the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += v;
+      }
+      if (c > 0) {
+        const int i = n + __popcll(m & ((1ull << lane) - 1));
+        s.expert[i] = (uint16_t)x;
+        s.start[i] = s.at[x] = (uint16_t)(pairs + sum - c);
+      }
       n += __popcll(m);
+      pairs += __shfl(sum, 63, 64);
     }
-    if (lane == 0) s.count = n;
+    if (lane == 0) s.start[n] = (uint16_t)pairs, s.count = n;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (e[i] < 0) continue;
+    const uint32_t below = (1u << (t[i] & 31)) - 1u, lo = s.mask[0][e[i]], hi = s.mask[1][e[i]];
+    const int at = s.at[e[i]] + (t[i] < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+    s.pair[at] = (uint16_t)(threadIdx.x + i * THREADS);
+    s.token[at] = (uint8_t)t[i];
   }
   __syncthreads();
 }
 
-// The pairs of expert e: lane t looks for token t's.  Writes them in the order
-// of the tokens to `members` (the wave's own) and returns how many there are.
-__device__ __forceinline__ int find_members(const Groups& s, const MoeArgs& a, int e, uint16_t* members, int lane) {
-  int mine = -1;
-  for (int k = 0; k < a.top_k; ++k) {
-    const int p = lane * a.top_k + k;
-    if (lane < a.T && s.ids[p] == e) mine = p;
-  }
-  const uint64_t m = __ballot(mine >= 0);
-  wave_lds_fence();
-  if (mine >= 0) members[__popcll(m & ((1ull << lane) - 1))] = (uint16_t)mine;
-  wave_lds_fence();
-  return __popcll(m);
-}
-
-// A wave's (or block's) work: 16 rows of an expert and up to kRows of its
-// pairs.  `index` runs through experts (slowly) and tiles of rows (fast).
+// A wave's (or block's) work: 16 rows of an expert and up to kRows of its pairs.
 template <int NL>
 struct MoeItem {
   Mx4Source<NL> src;
-  int index, m0, count;  // count: the expert's pairs, m0: the first of them taken here
-  int r0, pair;          // first row; the lane's column's pair, or -1
+  int group, tile;  // which expert of those that are hit, which 16 rows
+  int p, end;       // its pairs from here on
+  int pair;         // of the column that the lane multiplies, or -1
+
+  // (member by member: as a whole the compiler copies it through memory, and
+  // waits for every load in flight)
+  __device__ __forceinline__ void take(const MoeItem& o) {
+    src.take(o.src);
+    group = o.group, tile = o.tile, p = o.p, end = o.end, pair = o.pair;
+  }
 };
 
-template <typename Stream, int NL>
-__device__ __forceinline__ void set_item(MoeItem<NL>& it, int e, const uint8_t* w, const uint8_t* ws, int64_t row0,
-                                         uint32_t blocks, const uint16_t* members, int top_k_or_one, int lane) {
-  it.src.wr = make_rsrc(w + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
-  const Mx4Scales sc(ws + row0 * blocks, 16 * blocks);
-  it.src.wsr = sc.rsrc;
-  it.src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
-  it.src.ws_skew = sc.skew((lane & 15) * blocks);
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const int row = it.m0 + mx4_x_row<kMx4XBF16>(i, lane);
-    it.src.xoff[i] = row < it.count ? (uint32_t)(members[min(row, 63)] / top_k_or_one) * blocks * 64u : kOutOfRange;
-  }
-  const int c = lane & 15;
-  it.pair = c < Stream::Slot::kRows && it.m0 + c < it.count ? members[min(it.m0 + c, 63)] : -1;
-}
-
-// No further work: loads of nothing.
-template <int NL>
-__device__ __forceinline__ void set_none(MoeItem<NL>& it, const void* any) {
-  it.src.wr = it.src.wsr = make_rsrc(any, 0);
-  it.src.wsoff = kOutOfRange;
-  it.src.ws_skew = 0;
-#pragma unroll
-  for (int i = 0; i < NL; ++i) it.src.xoff[i] = kOutOfRange;
-  it.pair = -1;
-}
-
-// Gate and up.  KW waves split the columns of an item (KW = 1: each wave has
+// Gate and up (UP: 16-bit activations, SwiGLU, h out) or down (h in, the pairs'
+// products out).  KW waves split the columns of an item (KW = 1: each wave has
 // items of its own); the loads of the next item are under way while one is
 // multiplied.
 template <int XK, int KW, int NL, int DEPTH>
-__global__ __launch_bounds__(256) void vq_mx4_moe_up_kernel(MoeArgs a) {
-  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
+__global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
+  constexpr bool kUp = XK != kMx4XPlanes;
+  typedef Mx4Stream<XK, kUp ? 1 : kMx4Planes, NL, DEPTH> Stream;
   constexpr int kRows = Stream::Slot::kRows, kWaves = 4;
   __shared__ typename Stream::Slot slots[kWaves];
   __shared__ float4_t part[KW > 1 ? kWaves : 1][64];
   __shared__ Groups groups;
-  __shared__ uint16_t members[kWaves][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   group_pairs<64 * kWaves>(groups, a);
-  const uint32_t blocks = a.hidden_blocks;
-  const int tiles = a.inter_blocks * 4, items = __builtin_amdgcn_readfirstlane(groups.count) * tiles;
-  const int stride = KW > 1 ? gridDim.x : gridDim.x * kWaves;
+  const int count = __builtin_amdgcn_readfirstlane(groups.count);
+  const uint32_t blocks = kUp ? a.hidden_blocks : a.inter_blocks;
+  const int tiles = kUp ? a.inter_blocks * 4 : a.hidden_blocks * 2;
+  const int units = KW > 1 ? gridDim.x : gridDim.x * kWaves;  // that share the items
+  const int step_group = units / tiles, step_tile = units % tiles;
+  const uint8_t *w = kUp ? a.gu : a.dn, *ws = kUp ? a.gus : a.dns;
   Stream st;
   st.slot = slots + wave;
   st.first = 0;
   st.end = blocks;
-  st.xr = make_rsrc(a.x, (uint64_t)a.T * blocks * 64);
-  st.plane = 0;
+  st.plane = kUp ? 0u : (uint32_t)a.pairs * blocks * 64u;
+  st.xr = kUp ? make_rsrc(a.x, (uint64_t)a.T * blocks * 64) : make_rsrc(a.h, (uint64_t)kMx4Planes * st.plane);
 #pragma unroll
   for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
   st.column = r & (kRows - 1);
-  auto set = [&](MoeItem<NL>& it) VQMI_INLINE {  // at it.index, its pairs from it.m0 on (0: to be found)
-    if (it.index >= items) return set_none(it, a.x);
-    const int e = __builtin_amdgcn_readfirstlane(groups.ids[groups.leads[it.index / tiles]]);
-    if (it.m0 == 0) it.count = find_members(groups, a, e, members[wave], lane);
-    it.r0 = it.index % tiles * 16;
-    set_item<Stream>(it, e, a.gu, a.gus, (int64_t)e * a.inter_blocks * 64 + it.r0, blocks, members[wave], a.top_k, lane);
+  auto set = [&](MoeItem<NL>& it, bool fresh) VQMI_INLINE {  // fresh: another expert's or other rows
+    if (it.group >= count) {                                 // no further work: loads of nothing
+      it.src.wr = it.src.wsr = make_rsrc(w, 0);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) it.src.xoff[i] = kOutOfRange;
+      return;
+    }
+    if (fresh) {
+      const int e = __builtin_amdgcn_readfirstlane(groups.expert[it.group]);
+      it.p = __builtin_amdgcn_readfirstlane(groups.start[it.group]);
+      it.end = __builtin_amdgcn_readfirstlane(groups.start[it.group + 1]);
+      const int64_t row0 = ((int64_t)e * tiles + it.tile) * 16;
+      it.src.wr = make_rsrc(w + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+      const Mx4Scales sc(ws + row0 * blocks, 16 * blocks);
+      it.src.wsr = sc.rsrc;
+      it.src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
+      it.src.ws_skew = sc.skew(r * blocks);
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int p = it.p + mx4_x_row<XK>(i, lane), q = min(p, it.end - 1);
+      const uint32_t row = kUp ? groups.token[q] : groups.pair[q];
+      it.src.xoff[i] = p < it.end ? row * blocks * 64u : kOutOfRange;
+    }
+    const int p = it.p + r;
+    it.pair = r < kRows && p < it.end ? groups.pair[min(p, it.end - 1)] : -1;
   };
   MoeItem<NL> cur, next;
-  cur.index = KW > 1 ? blockIdx.x : blockIdx.x * kWaves + wave;
-  cur.m0 = cur.count = 0;
-  set(cur);
+  const int unit = KW > 1 ? blockIdx.x : blockIdx.x * kWaves + wave;
+  cur.group = unit / tiles;
+  cur.tile = unit % tiles;
+  cur.pair = -1;
+  set(cur, true);
   const uint32_t from = KW > 1 ? wave : 0;
   st.start(cur.src, from, KW, lane);
-  while (cur.index < items) {
-    next.index = cur.index;
-    next.count = cur.count;
-    next.m0 = cur.m0 + kRows;
-    if (next.m0 >= cur.count) next.index += stride, next.m0 = 0;
-    set(next);
+  while (cur.group < count) {
+    next.take(cur);
+    next.p += kRows;
+    const bool fresh = next.p >= cur.end;
+    if (fresh) {
+      next.group += step_group;
+      next.tile += step_tile;
+      if (next.tile >= tiles) next.tile -= tiles, next.group += 1;
+    }
+    set(next, fresh);
     float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
     st.run(acc, cur.src, next.src, from, KW, lane);
     float4_t s = acc[0] + acc[1];
@@ -183,41 +219,64 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_up_kernel(MoeArgs a) {
       lds_barrier();
       s = part[0][lane];
 #pragma unroll
-      for (int w = 1; w < KW; ++w) s += part[w][lane];
+      for (int k = 1; k < KW; ++k) s += part[k][lane];
       lds_barrier();
     }
     if ((KW == 1 || wave == 0) && cur.pair >= 0) {
-      uint32_t lo[kMx4Planes], hi[kMx4Planes];
-      split_planes(silu_mul<true>(s[0], s[1]), lo);
-      split_planes(silu_mul<true>(s[2], s[3]), hi);
-      const int64_t inter = (int64_t)a.inter_blocks * 32;
-      uint16_t* out = a.h + cur.pair * inter + cur.r0 / 2 + 2 * g;
+      const int r0 = cur.tile * 16;
+      if constexpr (kUp) {
+        uint32_t lo[kMx4Planes], hi[kMx4Planes];
+        split_planes(silu_mul<true>(s[0], s[1]), lo);
+        split_planes(silu_mul<true>(s[2], s[3]), hi);
+        const int64_t inter = (int64_t)a.inter_blocks * 32;
+        uint16_t* out = a.h + cur.pair * inter + r0 / 2 + 2 * g;
 #pragma unroll
-      for (int p = 0; p < kMx4Planes; ++p)
-        *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
+        for (int p = 0; p < kMx4Planes; ++p)
+          *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
+      } else {
+        *reinterpret_cast<float4_t*>(a.products + ((int64_t)cur.pair * a.hidden_blocks * 32 + r0 + 4 * g)) = s;
+      }
     }
-    cur = next;
+    cur.take(next);
   }
 }
 
-// Down: a block takes 16 output rows for all tokens, its waves the experts in
-// turn, for the pairs of an expert, kRows at a time.  A wave adds up its
-// experts' weighted products per token in LDS, in the order of the experts; the
-// waves' sums are joined in their order.
-template <int WAVES, int NL, int DEPTH, int TOKENS>
+// The pairs' products, weighted, in the order of the slots: 4 columns a thread.
+__global__ __launch_bounds__(256) void vq_mx4_moe_sum_kernel(MoeArgs a) {
+  const int per = a.hidden_blocks * 8, i = blockIdx.x * 256 + threadIdx.x, t = i / per, c = i % per * 4;
+  if (t >= a.T) return;
+  float4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < a.top_k; s0 += 8) {
+    float4_t v[8];  // eight slots in flight
+    float f[8];
+    bool live[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int p = t * a.top_k + min(s0 + s, a.top_k - 1);
+      live[s] = s0 + s < a.top_k && a.ids[p] >= 0;
+      f[s] = a.weights[p];
+      v[s] = *reinterpret_cast<const float4_t*>(a.products + (int64_t)p * a.hidden_blocks * 32 + c);
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = live[s] ? fmaf(f[s], v[s][k], y[k]) : y[k];
+    }
+  }
+  const float v[4] = {y[0], y[1], y[2], y[3]};
+  store_run<4>(a.y, (int64_t)t * a.hidden_blocks * 32 + c, v, a.y_kind);
+}
+
+// Down for a token or two: a block takes 16 output rows, its waves the pairs in
+// turn; their weighted products are joined in the order of the waves.
+template <int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) {
-  typedef Mx4Stream<kMx4XPlanes, kMx4Planes, NL, DEPTH> Stream;
-  constexpr int kRows = Stream::Slot::kRows;
+  typedef Mx4Stream<kMx4XPlanes, kMx4Planes, 1, DEPTH> Stream;
   __shared__ typename Stream::Slot slots[WAVES];
-  __shared__ float4_t sums[WAVES][TOKENS][4];  // 16 rows a token
-  __shared__ Groups groups;
-  __shared__ uint16_t members[WAVES][64];
+  __shared__ float4_t part[WAVES][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16;
-  for (int i = lane; i < TOKENS * 4; i += 64) sums[wave][i / 4][i % 4] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  group_pairs<64 * WAVES>(groups, a);
+  const int r = lane & 15, g = lane >> 4, r0 = blockIdx.x * 16, t = blockIdx.y;
   const uint32_t blocks = a.inter_blocks;
-  const int items = __builtin_amdgcn_readfirstlane(groups.count);
   Stream st;
   st.slot = slots + wave;
   st.first = 0;
@@ -226,71 +285,83 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
   st.xr = make_rsrc(a.h, (uint64_t)kMx4Planes * st.plane);
 #pragma unroll
   for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
-  st.column = r & (kRows - 1);
-  float weight_next = 0.0f;
-  auto set = [&](MoeItem<NL>& it) VQMI_INLINE {
-    if (it.index >= items) return set_none(it, a.h);
-    const int e = __builtin_amdgcn_readfirstlane(groups.ids[groups.leads[it.index]]);
-    if (it.m0 == 0) it.count = find_members(groups, a, e, members[wave], lane);
-    set_item<Stream>(it, e, a.dn, a.dns, (int64_t)e * a.hidden_blocks * 32 + r0, blocks, members[wave], 1, lane);
-    weight_next = a.weights[max(it.pair, 0)];
-  };
-  MoeItem<NL> cur, next;
-  cur.index = wave;
-  cur.m0 = cur.count = 0;
-  set(cur);
-  st.start(cur.src, 0, 1, lane);
-  while (cur.index < items) {
-    const float f = weight_next;
-    next.index = cur.index;
-    next.count = cur.count;
-    next.m0 = cur.m0 + kRows;
-    if (next.m0 >= cur.count) next.index += WAVES, next.m0 = 0;
-    set(next);
-    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    st.run(acc, cur.src, next.src, 0, 1, lane);
-    if (cur.pair >= 0) {
-      float4_t* s = &sums[wave][cur.pair / a.top_k][g];
-      const float4_t d = acc[0] + acc[1];
-      float4_t o = *s;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(f, d[i], o[i]);
-      *s = o;
+  st.column = 0;
+  float f_next = 0.0f;
+  auto set = [&](Mx4Source<1>& src, int s) VQMI_INLINE {  // slot s of the token
+    const int p = t * a.top_k + s, e = s < a.top_k ? __builtin_amdgcn_readfirstlane(a.ids[p]) : -1;
+    f_next = 0.0f;
+    if (e < 0) {
+      src.wr = src.wsr = make_rsrc(a.dn, 0);
+      src.wsoff = src.xoff[0] = kOutOfRange;
+      src.ws_skew = 0;
+      return;
     }
-    wave_lds_fence();
-    cur = next;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * 4; i += 64 * WAVES) {
-    const int t = i / 4, q = i % 4;
-    float4_t s = sums[0][t][q];
+    const int64_t row0 = (int64_t)e * a.hidden_blocks * 32 + r0;
+    src.wr = make_rsrc(a.dn + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+    const Mx4Scales sc(a.dns + row0 * blocks, 16 * blocks);
+    src.wsr = sc.rsrc;
+    src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
+    src.ws_skew = sc.skew(r * blocks);
+    src.xoff[0] = mx4_x_row<kMx4XPlanes>(0, lane) == 0 ? (uint32_t)p * blocks * 64u : kOutOfRange;
+    f_next = a.weights[p];
+  };
+  Mx4Source<1> cur, next;
+  set(cur, wave);
+  st.start(cur, 0, 1, lane);
+  float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = wave; s < a.top_k; s += WAVES) {
+    const float f = f_next;
+    set(next, s + WAVES);
+    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    st.run(acc, cur, next, 0, 1, lane);
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) s += sums[w][t][q];
-    const float v[4] = {s[0], s[1], s[2], s[3]};
-    store_run<4>(a.y, (int64_t)t * a.hidden_blocks * 32 + r0 + 4 * q, v, a.y_kind);
+    for (int i = 0; i < 4; ++i) sum[i] = fmaf(f, acc[0][i] + acc[1][i], sum[i]);
+    cur.take(next);
   }
+  if (r == 0) part[wave][g] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 4) return;
+  float4_t y = part[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) y += part[w][threadIdx.x];
+  const float v[4] = {y[0], y[1], y[2], y[3]};
+  store_run<4>(a.y, (int64_t)t * a.hidden_blocks * 32 + r0 + 4 * threadIdx.x, v, a.y_kind);
+}
+
+constexpr int kFewTokens = 2;  // up to here each token's pairs are on their own
+
+template <int XK, int KW, int NL, int DEPTH>
+void run_products(const MoeArgs& a, int tiles, hipStream_t s) {
+  const int items = min(a.pairs, a.experts) * tiles;  // at most
+  const int grid = KW > 1 ? items : min((items + 3) / 4, 1024);
+  hipLaunchKernelGGL((vq_mx4_moe_kernel<XK, KW, NL, DEPTH>), dim3(grid), dim3(256), 0, s, a);
 }
 
 template <int XK>
-void run_up(const MoeArgs& a, hipStream_t s) {
-  const int tiles = a.inter_blocks * 4, most = min(a.pairs, a.experts) * tiles;  // items at most
-  if (a.T <= 2) {
-    hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 4, 1, 2>), dim3(min(most, 1 << 16)), dim3(256), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((vq_mx4_moe_up_kernel<XK, 1, 1, 2>), dim3(min((most + 3) / 4, 1024)), dim3(256), 0, s, a);
+hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
+  const int up = a.inter_blocks * 4, down = a.hidden_blocks * 2;
+  if (a.T <= kFewTokens) {
+    run_products<XK, 4, 1, 2>(a, up, s);
+    hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
+    return hipGetLastError();
   }
+  run_products<XK, 1, 1, 2>(a, up, s);
+  run_products<kMx4XPlanes, 1, 1, 2>(a, down, s);
+  hipLaunchKernelGGL(vq_mx4_moe_sum_kernel, dim3((a.T * a.hidden_blocks * 8 + 255) / 256), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t mx4_moe_workspace_bytes(int T, int top_k, int inter) {
-  return kMx4Planes * (size_t)T * top_k * inter * sizeof(uint16_t);
+size_t mx4_moe_workspace_bytes(int T, int top_k, int hidden, int inter) {
+  const size_t pairs = (size_t)T * top_k;
+  return kMx4Planes * pairs * inter * sizeof(uint16_t) + (T <= kFewTokens ? 0 : pairs * hidden * sizeof(float));
 }
 
 hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4View& down, const void* logits,
                           const void* x, int x_kind, int T, void* y, int y_kind, int32_t* ids, float* weights,
                           void* workspace, hipStream_t s) {
-  hipError_t e = launch_router(r, logits, T, ids, weights, s);
+  const hipError_t e = launch_router(r, logits, T, ids, weights, s);
   if (e != hipSuccess) return e;
   MoeArgs a{};
   a.gu = gate_up.values;
@@ -309,14 +380,8 @@ hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4
   a.hidden_blocks = gate_up.cols / kMx4Block;
   a.inter_blocks = down.cols / kMx4Block;
   a.y_kind = y_kind;
-  if (x_kind == kMx4XF16) run_up<kMx4XF16>(a, s);
-  else run_up<kMx4XBF16>(a, s);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)a.hidden_blocks * 2);
-  if (T <= 16) hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 1, 2, 16>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 1, 2, 64>), grid, dim3(512), 0, s, a);
-  return hipGetLastError();
+  a.products = reinterpret_cast<float*>(a.h + (size_t)kMx4Planes * a.pairs * down.cols);
+  return x_kind == kMx4XF16 ? run_layer<kMx4XF16>(a, s) : run_layer<kMx4XBF16>(a, s);
 }
 
 }  // namespace vqmi
