@@ -140,29 +140,30 @@ __device__ __forceinline__ Mx4Args split_args(Mx4Args a) {
   return a;
 }
 
-template <int XK, int WAVES, int NL, int DEPTH>
+template <int XK, int WAVES, int MT, int NL, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
-  typedef Mx4Stream<XK, 1, NL, DEPTH> Stream;
-  constexpr int kTok = Stream::Slot::kRows;
+  typedef Mx4Stream<XK, 1, MT, NL, DEPTH> Stream;
+  constexpr int kTok = Stream::Slot::kRows, kRows = 16 * MT;
   __shared__ typename Stream::Slot slots[WAVES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const unsigned row_tiles = (a.rows + 15) / 16;  // row tiles run fastest: they share the tokens
-  const int r0 = (blockIdx.x % row_tiles) * 16, t0 = (blockIdx.x / row_tiles) * kTok;
+  const unsigned row_tiles = (a.rows + kRows - 1) / kRows;  // row tiles run fastest: they share the tokens
+  const int r0 = (blockIdx.x % row_tiles) * kRows, t0 = (blockIdx.x / row_tiles) * kTok;
   const int r = lane & 15, g = lane >> 4;
   const uint32_t blocks = a.blocks;
-  const int rows = min(16, a.rows - r0), toks = min(kTok, a.T - t0);
+  const int rows = min(kRows, a.rows - r0), toks = min(kTok, a.T - t0);
   Stream st;
   st.slot = slots + wave;
   st.first = blockIdx.y * a.split_blocks;
   st.end = min(blocks, st.first + a.split_blocks);
   typename Stream::Source src;
-  src.wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
+  src.w = a.w + (int64_t)r0 * blocks * 16;
+  src.w_bytes = rows * blocks * 16;
   st.xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * Stream::kXBlock,
                     (uint64_t)toks * blocks * Stream::kXBlock);
   st.plane = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 2 * MT; ++i) {
     const int row = mx4_w_row(i, lane);
     st.woff[i] = row < rows ? row * blocks * 16 : kOutOfRange;
   }
@@ -173,34 +174,39 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
   }
   st.column = r & (kTok - 1);
   const Mx4Scales ws(a.ws + (int64_t)r0 * blocks, rows * blocks);
-  const int srow = mx4_s_row(lane);
-  src.wsr = ws.rsrc;
-  src.wsoff = srow < rows ? ws.word(srow * blocks + st.first, lane) : kOutOfRange;
-  src.ws_skew = ws.skew(r * blocks + st.first);
+  src.ws = ws.base;
+  src.ws_bytes = ws.bytes;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int row = mx4_s_row(i, lane);
+    src.wsoff[i] = row < rows ? ws.place(row * blocks + st.first, lane) : kOutOfRange;
+  }
   if constexpr (XK == kMx4XMx4) {
     const Mx4Scales xs(a.xs + (int64_t)t0 * blocks, toks * blocks);
-    st.xsr = xs.rsrc;
-    st.xsoff = srow < toks ? xs.word(srow * blocks + st.first, lane) : kOutOfRange;
-    st.xs_skew = xs.skew(st.column * blocks + st.first);
+    st.xsr = make_rsrc(xs.base, xs.bytes);
+    st.xsoff = mx4_s_row(0, lane) < toks ? xs.place(mx4_s_row(0, lane) * blocks + st.first, lane) : kOutOfRange;
   }
-  float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-  st.start(src, wave, WAVES, lane);
-  typename Stream::Source none = src;
-  none.wr = none.wsr = make_rsrc(a.w, 0);  // nothing follows
+  float4_t acc[MT][2];
 #pragma unroll
-  for (int i = 0; i < NL; ++i) none.xoff[i] = kOutOfRange;
+  for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  st.start(src, wave, WAVES, lane);
+  typename Stream::Source none;
+  none.take(src);
+  none.clear();
   st.run(acc, src, none, wave, WAVES, lane);
   __syncthreads();  // the slots are free: the waves' sums go there
   float4_t* part = reinterpret_cast<float4_t*>(slots);
-  part[wave * 64 + lane] = acc[0] + acc[1];
-  __syncthreads();
-  if (wave != 0) return;
-  float4_t sum = part[lane];
+  static_assert(sizeof(slots) >= WAVES * MT * 64 * sizeof(float4_t), "every wave's sums fit");
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) sum += part[w * 64 + lane];
+  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = acc[m][0] + acc[m][1];
+  __syncthreads();
+  if (wave >= MT) return;  // wave m joins row tile m
+  float4_t sum = part[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) sum += part[(w * MT + wave) * 64 + lane];
   const int t = t0 + r;
   const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-  if (r < toks) store_rows4(a, t, r0 + g * 4, v);
+  if (r < toks) store_rows4(a, t, r0 + wave * 16 + g * 4, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -539,11 +545,11 @@ __global__ __launch_bounds__(256) void vq_mx4_join_kernel(Mx4Args a, int splits)
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <int XK, int WAVES, int NL, int DEPTH>
+template <int XK, int WAVES, int MT, int NL, int DEPTH>
 void run_skinny(const Mx4Args& a, int, int splits, hipStream_t s) {
-  constexpr int kTok = Mx4Slot<XK, 1, NL>::kRows;
-  const dim3 grid((unsigned)ceil_div(a.rows, 16) * ceil_div(a.T, kTok), splits);
-  hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+  constexpr int kTok = Mx4Slot<XK, 1, MT, NL>::kRows;
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT) * ceil_div(a.T, kTok), splits);
+  hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, MT, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
 template <int WM, int WN, int MT, int NT, int AHEAD>
@@ -566,10 +572,10 @@ void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   }
 }
 
-template <int WAVES, int NL, int DEPTH>
+template <int WAVES, int MT, int NL, int DEPTH>
 void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
-  if (xk == kMx4XF16) run_skinny<kMx4XF16, WAVES, NL, DEPTH>(a, xk, splits, s);
-  else run_skinny<kMx4XBF16, WAVES, NL, DEPTH>(a, xk, splits, s);
+  if (xk == kMx4XF16) run_skinny<kMx4XF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
+  else run_skinny<kMx4XBF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
 }
 
 // The kernels of the product and a time model of each (us):
@@ -589,13 +595,14 @@ struct Mx4Kernel {
 };
 constexpr int kAnyT = 1 << 30;
 const Mx4Kernel kMx4Kernels[] = {
-    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 3>},
-    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 2>},
-    {16, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 1, 2>},
-    {16, 8, 2, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 2, 1, 4>},
-    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 3>},
-    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 2>},
-    {16, 16, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 2>},
+    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 1, 3>},
+    {16, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 1, 1, 2>},
+    {32, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 1, 2>},
+    {32, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 1, 2>},
+    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {32, 16, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 2, 2>},
     {128, 32, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 2, 1>},
     {128, 64, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 4, 1>},
     {128, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 4, 1>},
@@ -604,12 +611,17 @@ const Mx4Kernel kMx4Kernels[] = {
     {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 2>},
     {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 1>},
     {256, 256, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 8, 1>},
-    {16, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 3>},
-    {16, 2, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 1, 2>},
-    {16, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 3>},
-    {16, 4, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 2>},
-    {16, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 4, 2>},
-    {16, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 8, 2>},
+    {16, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 1, 2>},
+    {16, 2, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 1, 1, 2>},
+    {32, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 1, 2>},
+    {16, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 2, 2>},
+    {32, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 2, 2>},
+    {16, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 4, 2>},
+    {32, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 4, 2>},
+    {32, 8, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 4, 2>},
+    {32, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 8, 2>},
+    {16, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 8, 2>},
+    {32, 16, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 8, 1>},
     {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2>},
     {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 2>},
     {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2>},

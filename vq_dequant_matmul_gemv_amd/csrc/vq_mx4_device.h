@@ -121,80 +121,102 @@ __device__ __forceinline__ float4_t mx4_mfma16(uint32_t codes, float scale, u32x
 }
 
 // ---------------------------------------------------------------------------
-// a wave's stream over the columns: 16 rows of w, up to 16 rows of activations
+// a wave's stream over the columns: 16 * MT rows of w, up to 16 rows of
+// activations
 //
 // XK: what the activations are; PL: planes of them; NL: load instructions for a
 // step's rows of a plane (8 rows each of 4-bit values, 2 of 16-bit ones);
 // DEPTH: steps in flight.
 // ---------------------------------------------------------------------------
-template <int XK, int PL, int NL>
+template <int XK, int PL, int MT, int NL>
 struct Mx4Slot {
   static constexpr int kRows = NL * (XK == kMx4XMx4 ? 8 : 2);  // rows of activations
-  u32x4 w[16 * 8];
+  u32x4 w[MT * 16 * 8];
   u32x4 x[PL][NL * 64];
-  uint32_t ws[16 * 4], xs[XK == kMx4XMx4 ? 16 * 4 : 1];  // scales: the words they lie in
+  uint32_t ws[MT * 16 * 4], xs[XK == kMx4XMx4 ? 16 * 4 : 1];  // scales: four words a row, the first two used
 };
 
-// The row a lane loads for: of w's values by instruction i, of scales, and of
-// the activations by instruction i.
+// The row a lane loads for: of w's values by instruction i, of scales by
+// instruction i, and of the activations by instruction i.
 __device__ __forceinline__ int mx4_w_row(int i, int lane) { return 8 * i + (lane >> 3); }
-__device__ __forceinline__ int mx4_s_row(int lane) { return lane >> 2; }
+__device__ __forceinline__ int mx4_s_row(int i, int lane) { return 16 * i + (lane >> 2); }
 template <int XK>
 __device__ __forceinline__ int mx4_x_row(int i, int lane) {
   return XK == kMx4XMx4 ? 8 * i + (lane >> 3) : 2 * i + (lane >> 5);
 }
 
-// Rows of scales, which may start at any byte: a step's eight lie in three
-// aligned words at most, the first of them `skew` bytes before the row's.  No
-// word without a byte of the tensor's is read.
+// Scales of rows, which may start at any byte: a step's eight lie in three
+// aligned words at most, which three lanes of four read.  No word without a
+// byte of the tensor's is read.
 struct Mx4Scales {
-  rsrc_t rsrc;
-  uint32_t base_skew;
-  __device__ __forceinline__ Mx4Scales(const uint8_t* base, uint32_t bytes)
-      : rsrc(make_rsrc(base - (reinterpret_cast<uintptr_t>(base) & 3u),
-                       ((reinterpret_cast<uintptr_t>(base) & 3u) + (uint64_t)bytes + 3) & ~(uint64_t)3)),
-        base_skew((uint32_t)reinterpret_cast<uintptr_t>(base) & 3u) {}
-  // The lane's word of scales from byte `at` of the tensor on.
-  __device__ __forceinline__ uint32_t word(uint32_t at, int lane) const {
-    return (lane & 3) < 3 ? ((base_skew + at) & ~3u) + 4 * (lane & 3) : kOutOfRange;
+  const uint8_t* base;  // aligned
+  uint32_t skew, bytes;
+  __device__ __forceinline__ Mx4Scales(const uint8_t* p, uint32_t n)
+      : base(p - (reinterpret_cast<uintptr_t>(p) & 3u)), skew((uint32_t)reinterpret_cast<uintptr_t>(p) & 3u),
+        bytes((skew + n + 3u) & ~3u) {}
+  // Where the scales from byte `at` of the tensor on lie: their word's offset
+  // for this lane, with the bytes before them in the low two bits.
+  __device__ __forceinline__ uint32_t place(uint32_t at, int lane) const {
+    return (lane & 3) < 3 ? skew + at + 4 * (lane & 3) : kOutOfRange;
   }
-  __device__ __forceinline__ uint32_t skew(uint32_t at) const { return (base_skew + at) & 3u; }
 };
 
-// What a wave loads its steps from: 16 rows of w and rows of activations.
-template <int NL>
+// What a wave loads its steps from: rows of w and rows of activations.
+template <int MT, int NL>
 struct Mx4Source {
-  rsrc_t wr, wsr;               // values and scales of the rows
-  uint32_t wsoff, xoff[NL];     // byte offsets of the lane's rows; kOutOfRange: no such row
-  uint32_t ws_skew;             // of the row that the lane multiplies
+  const uint8_t *w, *ws;         // values and scales (aligned) of the rows
+  uint32_t w_bytes, ws_bytes;
+  uint32_t wsoff[MT], xoff[NL];  // of the lane's rows (Mx4Scales::place; bytes); kOutOfRange: no such row
 
+  // Nothing: loads of zeros.
+  __device__ __forceinline__ void clear() {
+    w_bytes = ws_bytes = 0u;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) xoff[i] = kOutOfRange;
+  }
+  // (member by member: as a whole the compiler copies it through memory, and
+  // waits for every load in flight)
   __device__ __forceinline__ void take(const Mx4Source& o) {
-    wr = o.wr, wsr = o.wsr, wsoff = o.wsoff, ws_skew = o.ws_skew;
+    w = o.w, ws = o.ws, w_bytes = o.w_bytes, ws_bytes = o.ws_bytes;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) wsoff[i] = o.wsoff[i];
 #pragma unroll
     for (int i = 0; i < NL; ++i) xoff[i] = o.xoff[i];
   }
+  // a, or b where `second` (the same in all lanes).  No branch: the loads in
+  // flight stay countable.
+  __device__ __forceinline__ void choose(bool second, const Mx4Source& a, const Mx4Source& b) {
+    w = second ? b.w : a.w, ws = second ? b.ws : a.ws;
+    w_bytes = second ? b.w_bytes : a.w_bytes, ws_bytes = second ? b.ws_bytes : a.ws_bytes;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) wsoff[i] = second ? b.wsoff[i] : a.wsoff[i];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) xoff[i] = second ? b.xoff[i] : a.xoff[i];
+  }
 };
 
-template <int XK, int PL, int NL, int DEPTH>
+template <int XK, int PL, int MT, int NL, int DEPTH>
 struct Mx4Stream {
-  typedef Mx4Slot<XK, PL, NL> Slot;
-  typedef Mx4Source<NL> Source;
+  typedef Mx4Slot<XK, PL, MT, NL> Slot;
+  typedef Mx4Source<MT, NL> Source;
   static constexpr uint32_t kXBlock = XK == kMx4XMx4 ? 16 : 64;  // bytes of a block of activations
   rsrc_t xr, xsr;
-  uint32_t woff[2], xsoff, xs_skew;
+  uint32_t woff[2 * MT], xsoff;
   uint32_t plane;       // bytes from one plane of activations to the next
   uint32_t first, end;  // blocks of columns: the first one, and behind the last
   int column;           // the row of activations that the lane multiplies
   Slot* slot;
-  u32x4 w[DEPTH][2], x[DEPTH][PL][NL];
-  uint32_t ws[DEPTH], xs[DEPTH];
+  u32x4 w[DEPTH][2 * MT], x[DEPTH][PL][NL];
+  uint32_t ws[DEPTH][MT], xs[DEPTH];
 
   __device__ __forceinline__ void load(int j, const Source& src, uint32_t k, int lane) {  // step k; past the end: zeros
     const uint32_t b = first + k * 8;
     const bool in_w = b + (lane & 7) < end;
+    const rsrc_t wr = make_rsrc(src.w, src.w_bytes), wsr = make_rsrc(src.ws, src.ws_bytes);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[j][i] = buf_load_b128(src.wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
-    ws[j] = buf_load_b32(src.wsr, src.wsoff + k * 8);
+    for (int i = 0; i < 2 * MT; ++i) w[j][i] = buf_load_b128(wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ws[j][i] = buf_load_b32(wsr, (src.wsoff[i] & ~3u) + k * 8);
     const uint32_t piece = XK == kMx4XMx4 ? lane & 7 : lane & 31;  // of 16 bytes
     const bool in_x = b + (XK == kMx4XMx4 ? piece : piece / 4) < end;
 #pragma unroll
@@ -203,16 +225,31 @@ struct Mx4Stream {
       for (int i = 0; i < NL; ++i)
         x[j][p][i] = buf_load_b128(xr, in_x ? src.xoff[i] + p * plane + b * kXBlock + piece * 16 : kOutOfRange);
     }
-    if constexpr (XK == kMx4XMx4) xs[j] = buf_load_b32(xsr, xsoff + k * 8);
+    if constexpr (XK == kMx4XMx4) xs[j] = buf_load_b32(xsr, (xsoff & ~3u) + k * 8);
   }
 
-  // The loaded step into LDS.  16-byte pieces change places within a row (4-bit:
-  // piece ^ row % 8 of 8, 16-bit: piece ^ row of 32), so reads of 16 rows touch
-  // all banks.
-  __device__ __forceinline__ void put(int j, int lane) {
+  // A row's eight scales of step k, four in each of the first two of its four
+  // lanes, from the words they lie in: the next lane's word follows.  Those past
+  // the last column (another row's) become 1, as NaN there would spoil the sum.
+  __device__ __forceinline__ uint32_t aligned(uint32_t word, uint32_t place, uint32_t k, int lane) const {
+    const uint32_t up = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, 0xf9, 0xf, 0xf, true);  // quad_perm 1 2 3 3
+    uint32_t v = __builtin_amdgcn_alignbyte(up, word, place);
+    if (first + k * 8 + 8 > end) {
+      const int left = min(max((int)(end - first - k * 8) - 4 * (lane & 3), 0), 4);
+      const uint32_t mask = (uint32_t)((1ull << (8 * left)) - 1ull);
+      v = (v & mask) | (~mask & 0x7f7f7f7fu);
+    }
+    return v;
+  }
+
+  // The loaded step k into LDS.  16-byte pieces change places within a row
+  // (4-bit: piece ^ row % 8 of 8, 16-bit: piece ^ row of 32), so reads of 16
+  // rows touch all banks.
+  __device__ __forceinline__ void put(int j, const Source& src, uint32_t k, int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) slot->w[mx4_w_row(i, lane) * 8 + ((lane & 7) ^ (lane >> 3))] = w[j][i];
-    slot->ws[lane] = ws[j];
+    for (int i = 0; i < 2 * MT; ++i) slot->w[mx4_w_row(i, lane) * 8 + ((lane & 7) ^ (lane >> 3))] = w[j][i];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) slot->ws[64 * i + lane] = aligned(ws[j][i], src.wsoff[i], k, lane);
 #pragma unroll
     for (int p = 0; p < PL; ++p) {
 #pragma unroll
@@ -222,43 +259,50 @@ struct Mx4Stream {
         else slot->x[p][row * 32 + ((lane & 31) ^ row)] = x[j][p][i];
       }
     }
-    if constexpr (XK == kMx4XMx4) slot->xs[lane] = xs[j];
+    if constexpr (XK == kMx4XMx4) slot->xs[lane] = aligned(xs[j], xsoff, k, lane);
   }
 
-  // The two scales of the lane's blocks of a step: those past the last column
-  // (another row's) are 1, as NaN there would spoil the sum.
-  __device__ __forceinline__ uint32_t scales(const uint32_t* words, int row, uint32_t skew, uint32_t k, int lane) const {
-    const uint32_t g2 = 2 * (lane >> 4), b = first + k * 8 + g2;
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(words + 4 * row) + skew + g2;
-    return (b < end ? p[0] : 127u) | (b + 1 < end ? p[1] : 127u) << 8;
-  }
-
-  // acc[0] + acc[1] += step k, which is in LDS.
-  __device__ __forceinline__ void dot(float4_t* acc, uint32_t ws_skew, uint32_t k, int lane) const {
+  // acc[m][0] + acc[m][1] += the step in LDS for rows 16 m to 16 m + 15.
+  __device__ __forceinline__ void dot(float4_t (*acc)[2], int lane) const {
     const int r = lane & 15, g = lane >> 4, n = column;
-    const uint32_t s_w = scales(slot->ws, r, ws_skew, k, lane);
-    u32x4 q[2];
+    u32x4 q[MT][2];
+    uint32_t s[MT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) q[h] = slot->w[r * 8 + ((2 * g + h) ^ (r & 7))];
+    for (int m = 0; m < MT; ++m) {
+      s[m] = reinterpret_cast<const uint16_t*>(slot->ws + 64 * m + 4 * r)[g];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) q[m][h] = slot->w[(16 * m + r) * 8 + ((2 * g + h) ^ (r & 7))];
+    }
     if constexpr (XK == kMx4XMx4) {
-      const uint32_t s_x = scales(slot->xs, n, xs_skew, k, lane);
+      const uint32_t s_x = reinterpret_cast<const uint16_t*>(slot->xs + 4 * n)[g];
       u32x4 v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) v[h] = slot->x[0][n * 8 + ((2 * g + h) ^ (n & 7))];
-      acc[0] = mx4_mfma<0>(q[0], v[0], acc[0], s_w, s_x);
-      acc[1] = mx4_mfma<1>(q[1], v[1], acc[1], s_w, s_x);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[m][0] = mx4_mfma<0>(q[m][0], v[0], acc[m][0], s[m], s_x);
+        acc[m][1] = mx4_mfma<1>(q[m][1], v[1], acc[m][1], s[m], s_x);
+      }
     } else {
-      const bool fit = XK == kMx4XF16 && __ballot(!mx4_scales_fit_half(s_w)) == 0ull;
-      const float s[2] = {mx4_scale<0>(s_w), mx4_scale<1>(s_w)};
+      bool fit = true;
+      if constexpr (XK == kMx4XF16) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) fit = fit && mx4_scales_fit_half(s[m]);
+        fit = __ballot(!fit) == 0ull;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t c[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          u32x4 v[PL];
 #pragma unroll
-          for (int p = PL - 1; p >= 0; --p) {
-            const u32x4 v = slot->x[p][n * 32 + ((8 * g + 4 * h + i) ^ n)];
-            acc[i & 1] = mx4_mfma16<XK>(c[i], s[h], v, acc[i & 1], fit);
+          for (int p = 0; p < PL; ++p) v[p] = slot->x[p][n * 32 + ((8 * g + 4 * h + i) ^ n)];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t c = i == 0 ? q[m][h].x : i == 1 ? q[m][h].y : i == 2 ? q[m][h].z : q[m][h].w;
+            const float f = h == 0 ? mx4_scale<0>(s[m]) : mx4_scale<1>(s[m]);
+#pragma unroll
+            for (int p = PL - 1; p >= 0; --p) acc[m][i & 1] = mx4_mfma16<XK>(c, f, v[p], acc[m][i & 1], fit);
           }
         }
       }
@@ -274,21 +318,22 @@ struct Mx4Stream {
 #pragma unroll
     for (int j = 0; j < DEPTH; ++j) load(j, src, from + j * stride, lane);
   }
-  // acc[0] + acc[1] += steps `from`, from + stride, ... of `cur`, whose first
-  // ones are on their way (start, or the call before); those of `next` are when
-  // it returns.
-  __device__ __forceinline__ void run(float4_t* acc, const Source& cur, const Source& next, uint32_t from,
+  // acc += steps `from`, from + stride, ... of `cur`, whose first ones are on
+  // their way (start, or the call before); those of `next` are when it returns.
+  __device__ __forceinline__ void run(float4_t (*acc)[2], const Source& cur, const Source& next, uint32_t from,
                                       uint32_t stride, int lane) {
     const uint32_t steps = (end - first + 7) / 8, n = turns(stride);
     for (uint32_t s = 0; s < n; s += DEPTH) {
+      const bool last = s + DEPTH >= n;
+      Source src;
+      src.choose(last, cur, next);
 #pragma unroll
       for (int j = 0; j < DEPTH; ++j) {
         const uint32_t k = from + (s + j) * stride;
-        put(j, lane);
-        if (s + DEPTH < n) load(j, cur, k + DEPTH * stride, lane);
-        else load(j, next, from + j * stride, lane);
+        put(j, cur, k, lane);
+        load(j, src, last ? from + j * stride : k + DEPTH * stride, lane);
         wave_lds_fence();
-        if (k < steps) dot(acc, cur.ws_skew, k, lane);
+        if (k < steps) dot(acc, lane);
         wave_lds_fence();
       }
     }

@@ -121,9 +121,9 @@ __device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
 }
 
 // A wave's (or block's) work: 16 rows of an expert and up to kRows of its pairs.
-template <int NL>
+template <int MT, int NL>
 struct MoeItem {
-  Mx4Source<NL> src;
+  Mx4Source<MT, NL> src;
   int group, tile;  // which expert of those that are hit, which 16 rows
   int p, end;       // its pairs from here on
   int pair;         // of the column that the lane multiplies, or -1
@@ -140,20 +140,20 @@ struct MoeItem {
 // products out).  KW waves split the columns of an item (KW = 1: each wave has
 // items of its own); the loads of the next item are under way while one is
 // multiplied.
-template <int XK, int KW, int NL, int DEPTH>
+template <int XK, int KW, int MT, int NL, int DEPTH>
 __global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
   constexpr bool kUp = XK != kMx4XPlanes;
-  typedef Mx4Stream<XK, kUp ? 1 : kMx4Planes, NL, DEPTH> Stream;
+  typedef Mx4Stream<XK, kUp ? 1 : kMx4Planes, MT, NL, DEPTH> Stream;
   constexpr int kRows = Stream::Slot::kRows, kWaves = 4;
   __shared__ typename Stream::Slot slots[kWaves];
-  __shared__ float4_t part[KW > 1 ? kWaves : 1][64];
+  __shared__ float4_t part[KW > 1 ? kWaves : 1][MT][64];
   __shared__ Groups groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
   group_pairs<64 * kWaves>(groups, a);
   const int count = __builtin_amdgcn_readfirstlane(groups.count);
   const uint32_t blocks = kUp ? a.hidden_blocks : a.inter_blocks;
-  const int tiles = kUp ? a.inter_blocks * 4 : a.hidden_blocks * 2;
+  const int tiles = (kUp ? a.inter_blocks * 4 : a.hidden_blocks * 2) / MT;
   const int units = KW > 1 ? gridDim.x : gridDim.x * kWaves;  // that share the items
   const int step_group = units / tiles, step_tile = units % tiles;
   const uint8_t *w = kUp ? a.gu : a.dn, *ws = kUp ? a.gus : a.dns;
@@ -164,25 +164,25 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
   st.plane = kUp ? 0u : (uint32_t)a.pairs * blocks * 64u;
   st.xr = kUp ? make_rsrc(a.x, (uint64_t)a.T * blocks * 64) : make_rsrc(a.h, (uint64_t)kMx4Planes * st.plane);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
+  for (int i = 0; i < 2 * MT; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
   st.column = r & (kRows - 1);
-  auto set = [&](MoeItem<NL>& it, bool fresh) VQMI_INLINE {  // fresh: another expert's or other rows
+  auto set = [&](MoeItem<MT, NL>& it, bool fresh) VQMI_INLINE {  // fresh: another expert's or other rows
     if (it.group >= count) {                                 // no further work: loads of nothing
-      it.src.wr = it.src.wsr = make_rsrc(w, 0);
-#pragma unroll
-      for (int i = 0; i < NL; ++i) it.src.xoff[i] = kOutOfRange;
+      it.src.clear();
       return;
     }
     if (fresh) {
       const int e = __builtin_amdgcn_readfirstlane(groups.expert[it.group]);
       it.p = __builtin_amdgcn_readfirstlane(groups.start[it.group]);
       it.end = __builtin_amdgcn_readfirstlane(groups.start[it.group + 1]);
-      const int64_t row0 = ((int64_t)e * tiles + it.tile) * 16;
-      it.src.wr = make_rsrc(w + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
-      const Mx4Scales sc(ws + row0 * blocks, 16 * blocks);
-      it.src.wsr = sc.rsrc;
-      it.src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
-      it.src.ws_skew = sc.skew(r * blocks);
+      const int64_t row0 = ((int64_t)e * tiles + it.tile) * (16 * MT);
+      it.src.w = w + row0 * blocks * 16;
+      it.src.w_bytes = 16 * MT * blocks * 16;
+      const Mx4Scales sc(ws + row0 * blocks, 16 * MT * blocks);
+      it.src.ws = sc.base;
+      it.src.ws_bytes = sc.bytes;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) it.src.wsoff[i] = sc.place(mx4_s_row(i, lane) * blocks, lane);
     }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -193,11 +193,14 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
     const int p = it.p + r;
     it.pair = r < kRows && p < it.end ? groups.pair[min(p, it.end - 1)] : -1;
   };
-  MoeItem<NL> cur, next;
+  MoeItem<MT, NL> cur, next;
   const int unit = KW > 1 ? blockIdx.x : blockIdx.x * kWaves + wave;
   cur.group = unit / tiles;
   cur.tile = unit % tiles;
   cur.pair = -1;
+  cur.src.w = cur.src.ws = w;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) cur.src.wsoff[i] = kOutOfRange;
   set(cur, true);
   const uint32_t from = KW > 1 ? wave : 0;
   st.start(cur.src, from, KW, lane);
@@ -211,30 +214,40 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
       if (next.tile >= tiles) next.tile -= tiles, next.group += 1;
     }
     set(next, fresh);
-    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    st.run(acc, cur.src, next.src, from, KW, lane);
-    float4_t s = acc[0] + acc[1];
-    if constexpr (KW > 1) {
-      part[wave][lane] = s;
-      lds_barrier();
-      s = part[0][lane];
+    float4_t acc[MT][2], s[MT];
 #pragma unroll
-      for (int k = 1; k < KW; ++k) s += part[k][lane];
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    st.run(acc, cur.src, next.src, from, KW, lane);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) s[m] = acc[m][0] + acc[m][1];
+    if constexpr (KW > 1) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) part[wave][m][lane] = s[m];
+      lds_barrier();
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        s[m] = part[0][m][lane];
+#pragma unroll
+        for (int k = 1; k < KW; ++k) s[m] += part[k][m][lane];
+      }
       lds_barrier();
     }
     if ((KW == 1 || wave == 0) && cur.pair >= 0) {
-      const int r0 = cur.tile * 16;
-      if constexpr (kUp) {
-        uint32_t lo[kMx4Planes], hi[kMx4Planes];
-        split_planes(silu_mul<true>(s[0], s[1]), lo);
-        split_planes(silu_mul<true>(s[2], s[3]), hi);
-        const int64_t inter = (int64_t)a.inter_blocks * 32;
-        uint16_t* out = a.h + cur.pair * inter + r0 / 2 + 2 * g;
 #pragma unroll
-        for (int p = 0; p < kMx4Planes; ++p)
-          *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
-      } else {
-        *reinterpret_cast<float4_t*>(a.products + ((int64_t)cur.pair * a.hidden_blocks * 32 + r0 + 4 * g)) = s;
+      for (int m = 0; m < MT; ++m) {
+        const int r0 = (cur.tile * MT + m) * 16;
+        if constexpr (kUp) {
+          uint32_t lo[kMx4Planes], hi[kMx4Planes];
+          split_planes(silu_mul<true>(s[m][0], s[m][1]), lo);
+          split_planes(silu_mul<true>(s[m][2], s[m][3]), hi);
+          const int64_t inter = (int64_t)a.inter_blocks * 32;
+          uint16_t* out = a.h + cur.pair * inter + r0 / 2 + 2 * g;
+#pragma unroll
+          for (int p = 0; p < kMx4Planes; ++p)
+            *reinterpret_cast<uint32_t*>(out + p * a.pairs * inter) = lo[p] | hi[p] << 16;
+        } else {
+          *reinterpret_cast<float4_t*>(a.products + ((int64_t)cur.pair * a.hidden_blocks * 32 + r0 + 4 * g)) = s[m];
+        }
       }
     }
     cur.take(next);
@@ -271,7 +284,7 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_sum_kernel(MoeArgs a) {
 // turn; their weighted products are joined in the order of the waves.
 template <int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) {
-  typedef Mx4Stream<kMx4XPlanes, kMx4Planes, 1, DEPTH> Stream;
+  typedef Mx4Stream<kMx4XPlanes, kMx4Planes, 1, 1, DEPTH> Stream;
   __shared__ typename Stream::Slot slots[WAVES];
   __shared__ float4_t part[WAVES][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -287,35 +300,36 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
   for (int i = 0; i < 2; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
   st.column = 0;
   float f_next = 0.0f;
-  auto set = [&](Mx4Source<1>& src, int s) VQMI_INLINE {  // slot s of the token
+  auto set = [&](Mx4Source<1, 1>& src, int s) VQMI_INLINE {  // slot s of the token
     const int p = t * a.top_k + s, e = s < a.top_k ? __builtin_amdgcn_readfirstlane(a.ids[p]) : -1;
     f_next = 0.0f;
     if (e < 0) {
-      src.wr = src.wsr = make_rsrc(a.dn, 0);
-      src.wsoff = src.xoff[0] = kOutOfRange;
-      src.ws_skew = 0;
+      src.w = src.ws = a.dn;
+      src.wsoff[0] = kOutOfRange;
+      src.clear();
       return;
     }
     const int64_t row0 = (int64_t)e * a.hidden_blocks * 32 + r0;
-    src.wr = make_rsrc(a.dn + row0 * blocks * 16, (uint64_t)16 * blocks * 16);
+    src.w = a.dn + row0 * blocks * 16;
+    src.w_bytes = 16 * blocks * 16;
     const Mx4Scales sc(a.dns + row0 * blocks, 16 * blocks);
-    src.wsr = sc.rsrc;
-    src.wsoff = sc.word(mx4_s_row(lane) * blocks, lane);
-    src.ws_skew = sc.skew(r * blocks);
+    src.ws = sc.base;
+    src.ws_bytes = sc.bytes;
+    src.wsoff[0] = sc.place(mx4_s_row(0, lane) * blocks, lane);
     src.xoff[0] = mx4_x_row<kMx4XPlanes>(0, lane) == 0 ? (uint32_t)p * blocks * 64u : kOutOfRange;
     f_next = a.weights[p];
   };
-  Mx4Source<1> cur, next;
+  Mx4Source<1, 1> cur, next;
   set(cur, wave);
   st.start(cur, 0, 1, lane);
   float4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = wave; s < a.top_k; s += WAVES) {
     const float f = f_next;
     set(next, s + WAVES);
-    float4_t acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    float4_t acc[1][2] = {{{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}}};
     st.run(acc, cur, next, 0, 1, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = fmaf(f, acc[0][i] + acc[1][i], sum[i]);
+    for (int i = 0; i < 4; ++i) sum[i] = fmaf(f, acc[0][0][i] + acc[0][1][i], sum[i]);
     cur.take(next);
   }
   if (r == 0) part[wave][g] = sum;
@@ -330,23 +344,23 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
 
 constexpr int kFewTokens = 2;  // up to here each token's pairs are on their own
 
-template <int XK, int KW, int NL, int DEPTH>
+template <int XK, int KW, int MT, int NL, int DEPTH>
 void run_products(const MoeArgs& a, int tiles, hipStream_t s) {
-  const int items = min(a.pairs, a.experts) * tiles;  // at most
+  const int items = min(a.pairs, a.experts) * (tiles / MT);  // at most
   const int grid = KW > 1 ? items : min((items + 3) / 4, 1024);
-  hipLaunchKernelGGL((vq_mx4_moe_kernel<XK, KW, NL, DEPTH>), dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((vq_mx4_moe_kernel<XK, KW, MT, NL, DEPTH>), dim3(grid), dim3(256), 0, s, a);
 }
 
 template <int XK>
 hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
   const int up = a.inter_blocks * 4, down = a.hidden_blocks * 2;
   if (a.T <= kFewTokens) {
-    run_products<XK, 4, 1, 2>(a, up, s);
+    run_products<XK, 4, 1, 1, 2>(a, up, s);
     hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
     return hipGetLastError();
   }
-  run_products<XK, 1, 1, 2>(a, up, s);
-  run_products<kMx4XPlanes, 1, 1, 2>(a, down, s);
+  run_products<XK, 1, 2, 2, 2>(a, up, s);
+  run_products<kMx4XPlanes, 1, 2, 2, 2>(a, down, s);
   hipLaunchKernelGGL(vq_mx4_moe_sum_kernel, dim3((a.T * a.hidden_blocks * 8 + 255) / 256), dim3(256), 0, s, a);
   return hipGetLastError();
 }
