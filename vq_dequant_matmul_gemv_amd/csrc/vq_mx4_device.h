@@ -316,7 +316,10 @@ struct Mx4Stream {
   }
   __device__ __forceinline__ void start(const Source& src, uint32_t from, uint32_t stride, int lane) {
 #pragma unroll
-    for (int j = 0; j < DEPTH; ++j) load(j, src, from + j * stride, lane);
+    for (int j = 0; j < DEPTH; ++j) {
+      load(j, src, from + j * stride, lane);
+      __builtin_amdgcn_sched_barrier(0);  // in the order that run() waits for them
+    }
   }
   // acc += steps `from`, from + stride, ... of `cur`, whose first ones are on
   // their way (start, or the call before); those of `next` are when it returns.
@@ -331,7 +334,9 @@ struct Mx4Stream {
       for (int j = 0; j < DEPTH; ++j) {
         const uint32_t k = from + (s + j) * stride;
         put(j, cur, k, lane);
+        __builtin_amdgcn_sched_barrier(0);
         load(j, src, last ? from + j * stride : k + DEPTH * stride, lane);
+        __builtin_amdgcn_sched_barrier(0);  // the loads stay in their order, so that the next ones' wait leaves these in flight
         wave_lds_fence();
         if (k < steps) dot(acc, lane);
         wave_lds_fence();
