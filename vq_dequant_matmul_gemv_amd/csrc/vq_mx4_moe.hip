@@ -45,16 +45,19 @@ __device__ __forceinline__ void split_planes(float v, uint32_t* p) {
 // The pairs of a call grouped by expert, in LDS: every block works them out for
 // itself (1 to 2 us, less than another launch).
 struct Groups {
-  uint32_t mask[2][kMx4MoeExperts];      // the tokens that chose an expert
-  uint16_t at[kMx4MoeExperts];           // where an expert's pairs start in `pair`
   uint16_t expert[kMx4MoePairs], start[kMx4MoePairs + 1];  // experts that are hit, in their order, and their pairs
   uint16_t pair[kMx4MoePairs];           // by expert, then by token
   uint8_t token[kMx4MoePairs];
   int count;                             // of experts that are hit
 };
 
+struct GroupScratch {                    // while they are worked out
+  uint32_t mask[2][kMx4MoeExperts];      // the tokens that chose an expert
+  uint16_t at[kMx4MoeExperts];           // where an expert's pairs start in `pair`
+};
+
 template <int THREADS>
-__device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
+__device__ __forceinline__ void group_pairs(Groups& s, GroupScratch& x, const MoeArgs& a) {
   constexpr int kPer = kMx4MoePairs / THREADS;
   const int lane = threadIdx.x & 63;
   if (a.T == 1) {  // a token's experts are distinct
@@ -80,17 +83,17 @@ __device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
     e[i] = p < a.pairs ? a.ids[p] : -1;
     t[i] = p / a.top_k;
   }
-  for (int x = threadIdx.x; x < a.experts; x += THREADS) s.mask[0][x] = s.mask[1][x] = 0u;
+  for (int k = threadIdx.x; k < a.experts; k += THREADS) x.mask[0][k] = x.mask[1][k] = 0u;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (e[i] >= 0) atomicOr(&s.mask[t[i] >> 5][e[i]], 1u << (t[i] & 31));
+    if (e[i] >= 0) atomicOr(&x.mask[t[i] >> 5][e[i]], 1u << (t[i] & 31));
   __syncthreads();
   if (threadIdx.x < 64) {
     int n = 0, pairs = 0;
     for (int base = 0; base < a.experts; base += 64) {
-      const int x = base + lane;
-      const int c = x < a.experts ? __popc(s.mask[0][x]) + __popc(s.mask[1][x]) : 0;
+      const int k = base + lane;
+      const int c = k < a.experts ? __popc(x.mask[0][k]) + __popc(x.mask[1][k]) : 0;
       const uint64_t m = __ballot(c > 0);
       int sum = c;  // of the lanes up to this one
 #pragma unroll
@@ -100,8 +103,8 @@ __device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
       }
       if (c > 0) {
         const int i = n + __popcll(m & ((1ull << lane) - 1));
-        s.expert[i] = (uint16_t)x;
-        s.start[i] = s.at[x] = (uint16_t)(pairs + sum - c);
+        s.expert[i] = (uint16_t)k;
+        s.start[i] = x.at[k] = (uint16_t)(pairs + sum - c);
       }
       n += __popcll(m);
       pairs += __shfl(sum, 63, 64);
@@ -112,8 +115,8 @@ __device__ __forceinline__ void group_pairs(Groups& s, const MoeArgs& a) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (e[i] < 0) continue;
-    const uint32_t below = (1u << (t[i] & 31)) - 1u, lo = s.mask[0][e[i]], hi = s.mask[1][e[i]];
-    const int at = s.at[e[i]] + (t[i] < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+    const uint32_t below = (1u << (t[i] & 31)) - 1u, lo = x.mask[0][e[i]], hi = x.mask[1][e[i]];
+    const int at = x.at[e[i]] + (t[i] < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
     s.pair[at] = (uint16_t)(threadIdx.x + i * THREADS);
     s.token[at] = (uint8_t)t[i];
   }
@@ -140,17 +143,20 @@ struct MoeItem {
 // products out).  KW waves split the columns of an item (KW = 1: each wave has
 // items of its own); the loads of the next item are under way while one is
 // multiplied.
-template <int XK, int KW, int MT, int NL, int DEPTH>
-__global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
+template <int XK, int KW, int MT, int NL, int DEPTH, int PER_CU>
+__global__ __launch_bounds__(256, PER_CU) void vq_mx4_moe_kernel(MoeArgs a) {
   constexpr bool kUp = XK != kMx4XPlanes;
   typedef Mx4Stream<XK, kUp ? 1 : kMx4Planes, MT, NL, DEPTH> Stream;
   constexpr int kRows = Stream::Slot::kRows, kWaves = 4;
-  __shared__ typename Stream::Slot slots[kWaves];
+  __shared__ union {
+    typename Stream::Slot slots[kWaves];
+    GroupScratch scratch;
+  } lds;
   __shared__ float4_t part[KW > 1 ? kWaves : 1][MT][64];
   __shared__ Groups groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  group_pairs<64 * kWaves>(groups, a);
+  group_pairs<64 * kWaves>(groups, lds.scratch, a);
   const int count = __builtin_amdgcn_readfirstlane(groups.count);
   const uint32_t blocks = kUp ? a.hidden_blocks : a.inter_blocks;
   const int tiles = (kUp ? a.inter_blocks * 4 : a.hidden_blocks * 2) / MT;
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(256) void vq_mx4_moe_kernel(MoeArgs a) {
   const int step_group = units / tiles, step_tile = units % tiles;
   const uint8_t *w = kUp ? a.gu : a.dn, *ws = kUp ? a.gus : a.dns;
   Stream st;
-  st.slot = slots + wave;
+  st.slot = lds.slots + wave;
   st.first = 0;
   st.end = blocks;
   st.plane = kUp ? 0u : (uint32_t)a.pairs * blocks * 64u;
@@ -344,23 +350,25 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
 
 constexpr int kFewTokens = 2;  // up to here each token's pairs are on their own
 
-template <int XK, int KW, int MT, int NL, int DEPTH>
+// PER_CU: blocks that a compute unit holds, so that all of a launch run at once.
+template <int XK, int KW, int MT, int NL, int DEPTH, int PER_CU>
 void run_products(const MoeArgs& a, int tiles, hipStream_t s) {
   const int items = min(a.pairs, a.experts) * (tiles / MT);  // at most
-  const int grid = KW > 1 ? items : min((items + 3) / 4, 1024);
-  hipLaunchKernelGGL((vq_mx4_moe_kernel<XK, KW, MT, NL, DEPTH>), dim3(grid), dim3(256), 0, s, a);
+  const int grid = min(KW > 1 ? items : (items + 3) / 4, 256 * PER_CU);
+  hipLaunchKernelGGL((vq_mx4_moe_kernel<XK, KW, MT, NL, DEPTH, PER_CU>), dim3(grid), dim3(256), 0, s, a);
 }
 
 template <int XK>
 hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
   const int up = a.inter_blocks * 4, down = a.hidden_blocks * 2;
   if (a.T <= kFewTokens) {
-    run_products<XK, 4, 1, 1, 2>(a, up, s);
+    run_products<XK, 4, 1, 1, 2, 4>(a, up, s);
     hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
     return hipGetLastError();
   }
-  run_products<XK, 1, 2, 2, 2>(a, up, s);
-  run_products<kMx4XPlanes, 1, 2, 2, 2>(a, down, s);
+  if (min(a.pairs, a.experts) * up <= 2048) run_products<XK, 4, 1, 2, 2, 4>(a, up, s);
+  else run_products<XK, 1, 2, 4, 2, 2>(a, up, s);
+  run_products<kMx4XPlanes, 1, 2, 2, 1, 3>(a, down, s);
   hipLaunchKernelGGL(vq_mx4_moe_sum_kernel, dim3((a.T * a.hidden_blocks * 8 + 255) / 256), dim3(256), 0, s, a);
   return hipGetLastError();
 }
