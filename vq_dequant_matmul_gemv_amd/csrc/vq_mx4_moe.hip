@@ -42,21 +42,34 @@ __device__ __forceinline__ void split_planes(float v, uint32_t* p) {
   p[2] = finite ? __float_as_uint(last) >> 16 : 0u;
 }
 
-// The pairs of a call grouped by expert, in LDS: every block works them out for
-// itself (1 to 2 us, less than another launch).
+// The pairs of a call in groups of one expert's, at most kRows each, in LDS:
+// every block works them out for itself (1 to 2 us, less than another launch).
 struct Groups {
-  uint16_t expert[kMx4MoePairs], start[kMx4MoePairs + 1];  // experts that are hit, in their order, and their pairs
-  uint16_t pair[kMx4MoePairs];           // by expert, then by token
+  uint16_t expert[kMx4MoePairs], start[kMx4MoePairs + 1];  // a group's expert, and where its pairs start
+  uint16_t pair[kMx4MoePairs];                             // by expert, then by token
   uint8_t token[kMx4MoePairs];
-  int count;                             // of experts that are hit
+  int count;                                               // of groups
+};
+struct GroupScratch {                // while they are worked out
+  uint32_t mask[2][kMx4MoeExperts];  // the tokens that chose an expert
+  uint16_t at[kMx4MoeExperts];       // where an expert's pairs start in `pair`
 };
 
-struct GroupScratch {                    // while they are worked out
-  uint32_t mask[2][kMx4MoeExperts];      // the tokens that chose an expert
-  uint16_t at[kMx4MoeExperts];           // where an expert's pairs start in `pair`
-};
+// The sum of v over the lanes up to this one: within rows of 16 by shifts, then
+// the rows before by their last lanes.
+__device__ __forceinline__ uint32_t lanes_sum_up_to(uint32_t v) {
+#define VQMI_ADD(ctrl, rows) v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false)
+  VQMI_ADD(0x111, 0xf);
+  VQMI_ADD(0x112, 0xf);
+  VQMI_ADD(0x114, 0xf);
+  VQMI_ADD(0x118, 0xf);
+  VQMI_ADD(0x142, 0xa);
+  VQMI_ADD(0x143, 0xc);
+#undef VQMI_ADD
+  return v;
+}
 
-template <int THREADS>
+template <int THREADS, int ROWS>
 __device__ __forceinline__ void group_pairs(Groups& s, GroupScratch& x, const MoeArgs& a) {
   constexpr int kPer = kMx4MoePairs / THREADS;
   const int lane = threadIdx.x & 63;
@@ -70,8 +83,8 @@ __device__ __forceinline__ void group_pairs(Groups& s, GroupScratch& x, const Mo
         s.pair[i] = (uint16_t)lane;
         s.token[i] = 0;
       }
-      if (lane <= n) s.start[lane] = (uint16_t)lane;
-      if (lane == 0) s.start[n] = (uint16_t)n, s.count = n;
+      s.start[lane] = (uint16_t)lane;
+      if (lane == 0) s.start[64] = 64, s.count = n;
     }
     __syncthreads();
     return;
@@ -90,26 +103,19 @@ __device__ __forceinline__ void group_pairs(Groups& s, GroupScratch& x, const Mo
     if (e[i] >= 0) atomicOr(&x.mask[t[i] >> 5][e[i]], 1u << (t[i] & 31));
   __syncthreads();
   if (threadIdx.x < 64) {
-    int n = 0, pairs = 0;
+    uint32_t before = 0;  // pairs, and groups in the upper half
     for (int base = 0; base < a.experts; base += 64) {
       const int k = base + lane;
-      const int c = k < a.experts ? __popc(x.mask[0][k]) + __popc(x.mask[1][k]) : 0;
-      const uint64_t m = __ballot(c > 0);
-      int sum = c;  // of the lanes up to this one
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(sum, o, 64);
-        if (lane >= o) sum += v;
+      const uint32_t c = k < a.experts ? __popc(x.mask[0][k]) + __popc(x.mask[1][k]) : 0;
+      const uint32_t both = c | (c + ROWS - 1) / ROWS << 16, sum = lanes_sum_up_to(both), at = before + sum - both;
+      if (c > 0) x.at[k] = (uint16_t)at;
+      for (uint32_t m = 0; m < c; m += ROWS) {
+        s.expert[(at >> 16) + m / ROWS] = (uint16_t)k;
+        s.start[(at >> 16) + m / ROWS] = (uint16_t)(at + m);
       }
-      if (c > 0) {
-        const int i = n + __popcll(m & ((1ull << lane) - 1));
-        s.expert[i] = (uint16_t)k;
-        s.start[i] = x.at[k] = (uint16_t)(pairs + sum - c);
-      }
-      n += __popcll(m);
-      pairs += __shfl(sum, 63, 64);
+      before += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
     }
-    if (lane == 0) s.start[n] = (uint16_t)pairs, s.count = n;
+    if (lane == 0) s.start[before >> 16] = (uint16_t)before, s.count = before >> 16;
   }
   __syncthreads();
 #pragma unroll
@@ -123,19 +129,18 @@ __device__ __forceinline__ void group_pairs(Groups& s, GroupScratch& x, const Mo
   __syncthreads();
 }
 
-// A wave's (or block's) work: 16 rows of an expert and up to kRows of its pairs.
+// A wave's (or block's) work: 16 * MT rows of a group's expert and its pairs.
 template <int MT, int NL>
 struct MoeItem {
   Mx4Source<MT, NL> src;
-  int group, tile;  // which expert of those that are hit, which 16 rows
-  int p, end;       // its pairs from here on
+  int group, tile;  // which group, which rows
   int pair;         // of the column that the lane multiplies, or -1
 
   // (member by member: as a whole the compiler copies it through memory, and
   // waits for every load in flight)
   __device__ __forceinline__ void take(const MoeItem& o) {
     src.take(o.src);
-    group = o.group, tile = o.tile, p = o.p, end = o.end, pair = o.pair;
+    group = o.group, tile = o.tile, pair = o.pair;
   }
 };
 
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(256, PER_CU) void vq_mx4_moe_kernel(MoeArgs a) {
   __shared__ Groups groups;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  group_pairs<64 * kWaves>(groups, lds.scratch, a);
+  group_pairs<64 * kWaves, kRows>(groups, lds.scratch, a);
   const int count = __builtin_amdgcn_readfirstlane(groups.count);
   const uint32_t blocks = kUp ? a.hidden_blocks : a.inter_blocks;
   const int tiles = (kUp ? a.inter_blocks * 4 : a.hidden_blocks * 2) / MT;
@@ -172,32 +177,26 @@ __global__ __launch_bounds__(256, PER_CU) void vq_mx4_moe_kernel(MoeArgs a) {
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) st.woff[i] = mx4_w_row(i, lane) * blocks * 16;
   st.column = r & (kRows - 1);
-  auto set = [&](MoeItem<MT, NL>& it, bool fresh) VQMI_INLINE {  // fresh: another expert's or other rows
-    if (it.group >= count) {                                 // no further work: loads of nothing
-      it.src.clear();
-      return;
-    }
-    if (fresh) {
-      const int e = __builtin_amdgcn_readfirstlane(groups.expert[it.group]);
-      it.p = __builtin_amdgcn_readfirstlane(groups.start[it.group]);
-      it.end = __builtin_amdgcn_readfirstlane(groups.start[it.group + 1]);
-      const int64_t row0 = ((int64_t)e * tiles + it.tile) * (16 * MT);
-      it.src.w = w + row0 * blocks * 16;
-      it.src.w_bytes = 16 * MT * blocks * 16;
-      const Mx4Scales sc(ws + row0 * blocks, 16 * MT * blocks);
-      it.src.ws = sc.base;
-      it.src.ws_bytes = sc.bytes;
+  auto set = [&](MoeItem<MT, NL>& it) VQMI_INLINE {
+    if (it.group >= count) return it.src.clear();  // no further work
+    const int e = __builtin_amdgcn_readfirstlane(groups.expert[it.group]);
+    const int first = groups.start[it.group], last = groups.start[it.group + 1] - 1;
+    const int64_t row0 = ((int64_t)e * tiles + it.tile) * (16 * MT);
+    it.src.w = w + row0 * blocks * 16;
+    it.src.w_bytes = 16 * MT * blocks * 16;
+    const Mx4Scales sc(ws + row0 * blocks, 16 * MT * blocks);
+    it.src.ws = sc.base;
+    it.src.ws_bytes = sc.bytes;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) it.src.wsoff[i] = sc.place(mx4_s_row(i, lane) * blocks, lane);
-    }
+    for (int i = 0; i < MT; ++i) it.src.wsoff[i] = sc.place(mx4_s_row(i, lane) * blocks, lane);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int p = it.p + mx4_x_row<XK>(i, lane), q = min(p, it.end - 1);
+      const int p = first + mx4_x_row<XK>(i, lane), q = min(p, last);
       const uint32_t row = kUp ? groups.token[q] : groups.pair[q];
-      it.src.xoff[i] = p < it.end ? row * blocks * 64u : kOutOfRange;
+      it.src.xoff[i] = p <= last ? row * blocks * 64u : kOutOfRange;
     }
-    const int p = it.p + r;
-    it.pair = r < kRows && p < it.end ? groups.pair[min(p, it.end - 1)] : -1;
+    const int pair = groups.pair[min(first + r, last)];
+    it.pair = first + r <= last ? pair : -1;
   };
   MoeItem<MT, NL> cur, next;
   const int unit = KW > 1 ? blockIdx.x : blockIdx.x * kWaves + wave;
@@ -207,19 +206,15 @@ __global__ __launch_bounds__(256, PER_CU) void vq_mx4_moe_kernel(MoeArgs a) {
   cur.src.w = cur.src.ws = w;
 #pragma unroll
   for (int i = 0; i < MT; ++i) cur.src.wsoff[i] = kOutOfRange;
-  set(cur, true);
+  set(cur);
   const uint32_t from = KW > 1 ? wave : 0;
   st.start(cur.src, from, KW, lane);
   while (cur.group < count) {
     next.take(cur);
-    next.p += kRows;
-    const bool fresh = next.p >= cur.end;
-    if (fresh) {
-      next.group += step_group;
-      next.tile += step_tile;
-      if (next.tile >= tiles) next.tile -= tiles, next.group += 1;
-    }
-    set(next, fresh);
+    next.group += step_group;
+    next.tile += step_tile;
+    if (next.tile >= tiles) next.tile -= tiles, next.group += 1;
+    set(next);
     float4_t acc[MT][2], s[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
