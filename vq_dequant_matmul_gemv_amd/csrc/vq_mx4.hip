@@ -418,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
 // product, many tokens, 16-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
 // block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token)
 // ---------------------------------------------------------------------------
-template <int XK, bool PRECISE, int WM, int WN, int MT, int NT>
+template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int DEPTH>
 __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
@@ -445,8 +445,8 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   // 16-byte pieces change places within a row (w: piece ^ row / 2 of 4, x: piece
   // ^ token of 16), so reads of 16 rows touch all banks.
   const uint32_t w_row = wave * 16 + (lane >> 2), w_piece = lane & 3, x_row = wave * 4 + (lane >> 4), x_piece = lane & 15;
-  u32x4 sw[kWLoads], sx[kXLoads];
-  uint32_t ss[2];
+  u32x4 sw[DEPTH][kWLoads], sx[DEPTH][kXLoads];  // steps on their way
+  uint32_t ss[DEPTH][2];
   // scales of row threadIdx.x, as the two aligned words that a step's four lie in
   const uint8_t* sc_base = a.ws + (int64_t)r0 * blocks;
   const uint32_t sc_skew = (uint32_t)reinterpret_cast<uintptr_t>(sc_base) & 3u;
@@ -454,35 +454,36 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   const uint32_t sc_off = sc_skew + threadIdx.x * blocks + b0;
   static_assert(kTileRows <= 64 * kWaves, "a thread loads one row's scales");
   const bool sc_live = (int)threadIdx.x < rows;
-  auto load = [&](uint32_t s) VQMI_INLINE {  // past the end: zeros
+  auto load = [&](int j, uint32_t s) VQMI_INLINE {  // past the end: zeros
     const uint32_t bw = b0 + s * 4 + w_piece, bx = b0 + s * 4 + x_piece / 4;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      sw[i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
+      sw[j][i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      sx[i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
+      sx[j][i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
     const uint32_t off = sc_live ? (sc_off + s * 4) & ~3u : kOutOfRange;
-    ss[0] = buf_load_b32(sr, off);
-    ss[1] = buf_load_b32(sr, off + 4);
+    ss[j][0] = buf_load_b32(sr, off);
+    ss[j][1] = buf_load_b32(sr, off + 4);
+    __builtin_amdgcn_sched_barrier(0);  // in the order that they are waited for
   };
-  auto put = [&](uint32_t s) VQMI_INLINE {
+  auto put = [&](int j, uint32_t s) VQMI_INLINE {
     uint8_t* to = lds + (s & 1) * kTileBytes;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i) {
       const uint32_t row = w_row + i * 16 * kWaves;
-      *reinterpret_cast<u32x4*>(to + row * 64 + ((w_piece ^ (row >> 1 & 3)) * 16)) = sw[i];
+      *reinterpret_cast<u32x4*>(to + row * 64 + ((w_piece ^ (row >> 1 & 3)) * 16)) = sw[j][i];
     }
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
       const uint32_t row = x_row + i * 4 * kWaves;
-      *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[i];
+      *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[j][i];
     }
     if (threadIdx.x < kTileRows) {
       // scales past the last column (another row's) are 1: NaN there would spoil the sum
       const int left = (int)(b1 - b0) - (int)(4 * s);
       const uint32_t mask = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1u;
-      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[1], ss[0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
+      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[j][1], ss[j][0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
     }
   };
   const int r = lane & 15, g = lane >> 4;
@@ -492,11 +493,12 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  load(0);
-  put(0);
-  load(1);
+  load(0, 0);
+  put(0, 0);
+#pragma unroll
+  for (int j = 1; j <= DEPTH; ++j) load(j % DEPTH, j);
   lds_barrier();
-  for (uint32_t s = 0; s < steps; ++s) {
+  auto step = [&](int j, uint32_t s) VQMI_INLINE {  // j: where step s + 1 is on its way
     const uint8_t* wb = lds + (s & 1) * kTileBytes + (wm + r) * 64 + ((g ^ (r >> 1 & 3)) * 16);
     const uint8_t* xb = lds + (s & 1) * kTileBytes + kTileRows * 64 + (wn + r) * 256;
     u32x4 q[MT];
@@ -510,8 +512,8 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
       fit = fit && byte - 104u <= 36u;
     }
     if constexpr (XK == kMx4XF16) fit = __ballot(!fit) == 0ull;
-    put(s + 1);
-    load(s + 2);
+    put(j, s + 1);
+    load(j, s + 1 + DEPTH);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 v[NT];
@@ -525,6 +527,11 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
       }
     }
     lds_barrier();
+  };
+  for (uint32_t s = 0; s < steps; s += DEPTH) {
+    static_for<DEPTH>([&](auto j) VQMI_INLINE {
+      if (s + j.value < steps) step((j.value + 1) % DEPTH, s + j.value);
+    });
   }
   // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
   // token's rows leave in whole pieces.
@@ -560,15 +567,15 @@ void run_tile(const Mx4Args& a, int, int splits, hipStream_t s) {
   else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT>
+template <int WM, int WN, int MT, int NT, int DEPTH>
 void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN);
   if (xk == kMx4XF16) {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
   } else {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
   }
 }
 
@@ -596,37 +603,29 @@ struct Mx4Kernel {
 constexpr int kAnyT = 1 << 30;
 const Mx4Kernel kMx4Kernels[] = {
     {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 1, 3>},
-    {16, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 1, 1, 2>},
-    {32, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 1, 2>},
-    {32, 8, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 1, 2>},
     {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
     {32, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {32, 16, 8, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 8, 2, 2, 2>},
     {128, 32, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 2, 1>},
     {128, 64, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 4, 1>},
     {128, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 4, 1>},
     {256, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 4, 1>},
-    {128, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 6, 1>},
-    {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 2>},
     {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 1>},
     {256, 256, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 8, 1>},
     {16, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 1, 2>},
-    {16, 2, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 1, 1, 2>},
-    {32, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 1, 2>},
     {16, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 2, 2>},
-    {32, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 2, 2>},
     {16, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 4, 2>},
-    {32, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 4, 2>},
-    {32, 8, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 4, 2>},
     {32, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 8, 2>},
-    {16, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 8, 2>},
     {32, 16, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 8, 1>},
-    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2>},
-    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 2>},
-    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2>},
-    {128, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 4>},
-    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4>},
+    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 1>},
+    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 2>},
+    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 3>},
+    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2, 1>},
+    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2, 2>},
+    {64, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 2, 2, 2>},
+    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 2, 2>},
+    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4, 1>},
+    {128, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 4, 2>},
+    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4, 2>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
