@@ -178,8 +178,8 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
   src.ws_bytes = ws.bytes;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int row = mx4_s_row(i, lane);
-    src.wsoff[i] = row < rows ? ws.place(row * blocks + st.first, lane) : kOutOfRange;
+    // rows past the end take the last one's: zeros would not fit fp16
+    src.wsoff[i] = ws.place(min(mx4_s_row(i, lane), rows - 1) * blocks + st.first, lane);
   }
   if constexpr (XK == kMx4XMx4) {
     const Mx4Scales xs(a.xs + (int64_t)t0 * blocks, toks * blocks);
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
 // product, many tokens, 4-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
 // block, steps of 256 columns (8 blocks, 128 bytes a row)
 // ---------------------------------------------------------------------------
-template <bool PRECISE, int WM, int WN, int MT, int NT, int AHEAD>
+template <bool PRECISE, int WM, int WN, int MT, int NT>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   static_assert(kTileRows % kLoadRows == 0 && kTileTokens % kLoadRows == 0, "whole loads");
   static_assert(kTileRows + kTileTokens <= 64 * kWaves && kTileRows % 64 == 0 && kTileTokens % 32 == 0,
                 "a thread loads one row's scales, a wave those of one operand");
-  static_assert(NT % (AHEAD + 1) == 0, "a ring of operands");
+  static_assert(NT % 2 == 0, "two token operands in turn");
   __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
   __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
   __shared__ __align__(1024) u32x4 lds_s[2][64 * kWaves];  // scales of two steps, a row a thread, twice
@@ -325,8 +325,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   }
   load_scales(1);
   lds_barrier();
-  constexpr int kRing = AHEAD + 1;  // token operands: the current one and the next AHEAD
-  Op av[MT], bv[kRing];
+  Op av[MT], bv[2];  // token operands: the current one and the next
   uint32_t sa[MT], sb[NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -334,11 +333,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
     read_hi(av[m], lds_w[0] + (wm + 16 * m) * 128);
     sa[m] = read_scale(0, wm + 16 * m);
   }
-#pragma unroll
-  for (int n = 0; n < AHEAD; ++n) {
-    read_lo(bv[n], lds_x[0] + (wn + n * 16) * 128);
-    read_hi(bv[n], lds_x[0] + (wn + n * 16) * 128);
-  }
+  read_lo(bv[0], lds_x[0] + wn * 128);
+  read_hi(bv[0], lds_x[0] + wn * 128);
 #pragma unroll
   for (int n = 0; n < NT; ++n) sb[n] = read_scale(0, kTileRows + wn + 16 * n);
 
@@ -355,19 +351,19 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
       // every wave has issued its last reads of this step before the barrier
       // waits for them, so behind it the next step's pieces in LDS are complete
       // and this one's buffers free
-      if constexpr (n == NT - AHEAD) lds_barrier();
-      const uint8_t* from = (n + AHEAD < NT ? xb : xnext) + (n + AHEAD) % NT * 16 * 128;
-      read_lo(bv[(n + AHEAD) % kRing], from);
-      read_hi(bv[(n + AHEAD) % kRing], from);
+      if constexpr (n == NT - 1) lds_barrier();
+      const uint8_t* from = (n + 1 < NT ? xb : xnext) + (n + 1) % NT * 16 * 128;
+      read_lo(bv[(n + 1) % 2], from);
+      read_hi(bv[(n + 1) % 2], from);
       static_for<2 * MT>([&](auto hm) VQMI_INLINE {
         constexpr int h = hm.value / MT, m = hm.value % MT;
-        const Op& b = bv[n % kRing];
+        const Op& b = bv[n % 2];
         if constexpr (h == 0) acc[m][n] = mx4_mfma<2 * P>(av[m].lo, b.lo, acc[m][n], sa[m], sb[n]);
         else acc[m][n] = mx4_mfma<2 * P + 1>(av[m].hi, b.hi, acc[m][n], sa[m], sb[n]);
         __builtin_amdgcn_sched_barrier(0);
         // the next step's pieces go to LDS, spread over the step, and the ones
         // after them are loaded in their place
-        constexpr int kSlots = (NT - AHEAD) * MT * 2, i = n * 2 * MT + hm.value;
+        constexpr int kSlots = (NT - 1) * MT * 2, i = n * 2 * MT + hm.value;
         static_for<kLoads>([&](auto k) VQMI_INLINE {
           if constexpr (k.value * kSlots / kLoads == i) {
             write_piece(s + 1, k.value);
@@ -418,7 +414,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
 // product, many tokens, 16-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
 // block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token)
 // ---------------------------------------------------------------------------
-template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int DEPTH>
+template <int XK, bool PRECISE, int WM, int WN, int MT, int NT>
 __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
@@ -445,45 +441,45 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   // 16-byte pieces change places within a row (w: piece ^ row / 2 of 4, x: piece
   // ^ token of 16), so reads of 16 rows touch all banks.
   const uint32_t w_row = wave * 16 + (lane >> 2), w_piece = lane & 3, x_row = wave * 4 + (lane >> 4), x_piece = lane & 15;
-  u32x4 sw[DEPTH][kWLoads], sx[DEPTH][kXLoads];  // steps on their way
-  uint32_t ss[DEPTH][2];
+  u32x4 sw[kWLoads], sx[kXLoads];  // the step on its way
+  uint32_t ss[2];
   // scales of row threadIdx.x, as the two aligned words that a step's four lie in
   const uint8_t* sc_base = a.ws + (int64_t)r0 * blocks;
   const uint32_t sc_skew = (uint32_t)reinterpret_cast<uintptr_t>(sc_base) & 3u;
   const rsrc_t sr = make_rsrc(sc_base - sc_skew, (uint64_t)((sc_skew + (uint64_t)rows * blocks + 3) & ~3ull));
-  const uint32_t sc_off = sc_skew + threadIdx.x * blocks + b0;
   static_assert(kTileRows <= 64 * kWaves, "a thread loads one row's scales");
-  const bool sc_live = (int)threadIdx.x < rows;
-  auto load = [&](int j, uint32_t s) VQMI_INLINE {  // past the end: zeros
+  // (rows past the end take the last one's: zeros would not fit fp16)
+  const uint32_t sc_off = sc_skew + min((int)threadIdx.x, rows - 1) * blocks + b0;
+  auto load = [&](uint32_t s) VQMI_INLINE {  // past the end: zeros
     const uint32_t bw = b0 + s * 4 + w_piece, bx = b0 + s * 4 + x_piece / 4;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      sw[j][i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
+      sw[i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      sx[j][i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
-    const uint32_t off = sc_live ? (sc_off + s * 4) & ~3u : kOutOfRange;
-    ss[j][0] = buf_load_b32(sr, off);
-    ss[j][1] = buf_load_b32(sr, off + 4);
+      sx[i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
+    const uint32_t off = (sc_off + s * 4) & ~3u;
+    ss[0] = buf_load_b32(sr, off);
+    ss[1] = buf_load_b32(sr, off + 4);
     __builtin_amdgcn_sched_barrier(0);  // in the order that they are waited for
   };
-  auto put = [&](int j, uint32_t s) VQMI_INLINE {
+  auto put = [&](uint32_t s) VQMI_INLINE {
     uint8_t* to = lds + (s & 1) * kTileBytes;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i) {
       const uint32_t row = w_row + i * 16 * kWaves;
-      *reinterpret_cast<u32x4*>(to + row * 64 + ((w_piece ^ (row >> 1 & 3)) * 16)) = sw[j][i];
+      *reinterpret_cast<u32x4*>(to + row * 64 + ((w_piece ^ (row >> 1 & 3)) * 16)) = sw[i];
     }
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
       const uint32_t row = x_row + i * 4 * kWaves;
-      *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[j][i];
+      *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[i];
     }
     if (threadIdx.x < kTileRows) {
       // scales past the last column (another row's) are 1: NaN there would spoil the sum
       const int left = (int)(b1 - b0) - (int)(4 * s);
       const uint32_t mask = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1u;
-      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[j][1], ss[j][0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
+      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[1], ss[0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
     }
   };
   const int r = lane & 15, g = lane >> 4;
@@ -493,12 +489,11 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  load(0, 0);
-  put(0, 0);
-#pragma unroll
-  for (int j = 1; j <= DEPTH; ++j) load(j % DEPTH, j);
+  load(0);
+  put(0);
+  load(1);
   lds_barrier();
-  auto step = [&](int j, uint32_t s) VQMI_INLINE {  // j: where step s + 1 is on its way
+  for (uint32_t s = 0; s < steps; ++s) {
     const uint8_t* wb = lds + (s & 1) * kTileBytes + (wm + r) * 64 + ((g ^ (r >> 1 & 3)) * 16);
     const uint8_t* xb = lds + (s & 1) * kTileBytes + kTileRows * 64 + (wn + r) * 256;
     u32x4 q[MT];
@@ -511,27 +506,26 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
       sc[m] = __uint_as_float(byte << 23);
       fit = fit && byte - 104u <= 36u;
     }
-    if constexpr (XK == kMx4XF16) fit = __ballot(!fit) == 0ull;
-    put(j, s + 1);
-    load(j, s + 1 + DEPTH);
+    fit = XK == kMx4XBF16 || __ballot(!fit) == 0ull;
+    put(s + 1);
+    load(s + 2);
+    auto products = [&](auto fit) VQMI_INLINE {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4 v[NT];
+      for (int i = 0; i < 4; ++i) {
+        u32x4 v[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const u32x4*>(xb + n * 16 * 256 + (((4 * g + i) ^ r) * 16));
+        for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const u32x4*>(xb + n * 16 * 256 + (((4 * g + i) ^ r) * 16));
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint32_t c = i == 0 ? q[m].x : i == 1 ? q[m].y : i == 2 ? q[m].z : q[m].w;
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t c = i == 0 ? q[m].x : i == 1 ? q[m].y : i == 2 ? q[m].z : q[m].w;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = mx4_mfma16<XK>(c, sc[m], v[n], acc[m][n], fit);
+          for (int n = 0; n < NT; ++n) acc[m][n] = mx4_mfma16<XK, decltype(fit)::value>(c, sc[m], v[n], acc[m][n]);
+        }
       }
-    }
+    };
+    if (fit) products(std::true_type{});
+    else if constexpr (XK == kMx4XF16) products(std::false_type{});
     lds_barrier();
-  };
-  for (uint32_t s = 0; s < steps; s += DEPTH) {
-    static_for<DEPTH>([&](auto j) VQMI_INLINE {
-      if (s + j.value < steps) step((j.value + 1) % DEPTH, s + j.value);
-    });
   }
   // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
   // token's rows leave in whole pieces.
@@ -559,23 +553,23 @@ void run_skinny(const Mx4Args& a, int, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, MT, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT, int AHEAD>
+template <int WM, int WN, int MT, int NT>
 void run_tile(const Mx4Args& a, int, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
   const dim3 block(64 * WM * WN);
-  if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT, AHEAD>), grid, block, 0, s, a);
+  if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT>), grid, block, 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT, int DEPTH>
+template <int WM, int WN, int MT, int NT>
 void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN);
   if (xk == kMx4XF16) {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
   } else {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT, DEPTH>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
   }
 }
 
@@ -596,36 +590,27 @@ struct Mx4Kernel {
   int k_waves;       // waves that split a block's columns
   int unit_blocks;   // splits are multiples of these blocks of columns
   bool mx4;          // 4-bit x (else 16-bit)
-  int min_T, max_T;  // tokens it is considered for
   float base, latency, rate, bw, join, unit, x_share;
   void (*run)(const Mx4Args&, int, int, hipStream_t);
 };
-constexpr int kAnyT = 1 << 30;
 const Mx4Kernel kMx4Kernels[] = {
-    {16, 8, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 2, 1>},
-    {128, 64, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 1, 2, 4, 1>},
-    {128, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile<4, 2, 4, 8, 1>},
-    {16, 2, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_skinny16<8, 2, 8, 1>},
-    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 1>},
-    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 2>},
-    {128, 32, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 1, 2, 2, 3>},
-    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2, 1>},
-    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 2, 2>},
-    {64, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 2, 2, 2>},
-    {128, 64, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<2, 2, 4, 2, 2>},
-    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4, 1>},
-    {128, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 2, 4, 2>},
-    {256, 128, 1, 4, false, 1, kAnyT, 4, 0.35f, 0.26f, 7, 0.2f, 0.7f, 1, run_tile16<4, 2, 4, 4, 2>},
+    {16, 8, 4, 8, true, 4.07f, 0.1f, 0.0937f, 7.1f, 0.321f, 0.479f, 0.829f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 3.95f, 0.0961f, 0.107f, 7.12f, 0.315f, 0.628f, 0.745f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 3.91f, 0.083f, 0.165f, 6.13f, 0.294f, 1.05f, 0.914f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 4.02f, 0.191f, 0.161f, 5.75f, 0.26f, 0.327f, 1.2f, run_tile<4, 1, 2, 2>},
+    {128, 64, 1, 16, true, 3.87f, 0.254f, 0.209f, 5.89f, 0.239f, 0.741f, 0.832f, run_tile<4, 1, 2, 4>},
+    {128, 128, 1, 16, true, 5.29f, 0.243f, 0.348f, 8, 0.216f, 0.196f, 0.715f, run_tile<4, 2, 2, 4>},
+    {256, 128, 1, 16, true, 4.19f, 0, 0.534f, 7.01f, 0.186f, 3.18f, 1.2f, run_tile<4, 2, 4, 4>},
+    {256, 192, 1, 16, true, 5.29f, 0.00156f, 0.635f, 6.82f, 0.165f, 3.48f, 1.2f, run_tile<4, 2, 4, 6>},
+    {256, 256, 1, 16, true, 4.94f, 0, 0.773f, 7.55f, 0.163f, 4.89f, 1.2f, run_tile<4, 2, 4, 8>},
+    {16, 2, 4, 8, false, 4.16f, 0.166f, 0.106f, 7.96f, 0.41f, 0.403f, 1.12f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 4.17f, 0.199f, 0.125f, 7.3f, 0.21f, 0.497f, 0.596f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 4.12f, 0.214f, 0.141f, 6.76f, 0.178f, 0.692f, 0.432f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 4.19f, 0.386f, 0.317f, 6.21f, 0.317f, 1.51f, 0.431f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 2.36f, 0.409f, 0.632f, 4.42f, 0.588f, 2.82f, 0.338f, run_skinny16<8, 2, 8, 1>},
+    {128, 32, 1, 4, false, 3.96f, 0.531f, 0.37f, 3.92f, 0.275f, 0.254f, 0, run_tile16<4, 1, 2, 2>},
+    {128, 64, 1, 4, false, 4.42f, 0.637f, 0.559f, 3.43f, 0.257f, 0, 0, run_tile16<4, 2, 2, 2>},
+    {256, 128, 1, 4, false, 5.42f, 0.396f, 1.58f, 4.09f, 0.205f, 1.58f, 0, run_tile16<4, 2, 4, 4>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
@@ -669,7 +654,6 @@ Mx4Plan make_plan(const Mx4Call& c) {
   Mx4Plan best;
   float best_t = 0.0f;
   for (int i = 0; i < kNumMx4Kernels; ++i) {
-    if (c.T < kMx4Kernels[i].min_T || c.T > kMx4Kernels[i].max_T) continue;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
       Mx4Plan p;
       if (!set_plan(c, i, s, &p) || p.splits != s) continue;

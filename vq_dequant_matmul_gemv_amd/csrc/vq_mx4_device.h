@@ -103,12 +103,14 @@ __device__ __forceinline__ void mx4_split_half(u32x4 x, bf16x8_t* hi, bf16x8_t* 
 }
 
 // Eight of a row's values times eight of a token's, over a step's four lane
-// groups: 16 rows x 16 tokens x 32 columns.  x: 16-bit values, or (bf16) the
-// planes whose sum they are.
-template <int XK>
-__device__ __forceinline__ float4_t mx4_mfma16(uint32_t codes, float scale, u32x4 x, float4_t acc, bool fit_half) {
+// groups: 16 rows x 16 tokens x 32 columns.  x: 16-bit values, or (bf16) one of
+// the planes whose sum they are.  FIT: with fp16 x, every lane's scale is one
+// that fits (chosen once a step: a branch at each product took two to six times
+// as long).
+template <int XK, bool FIT>
+__device__ __forceinline__ float4_t mx4_mfma16(uint32_t codes, float scale, u32x4 x, float4_t acc) {
   if constexpr (XK == kMx4XF16) {
-    if (fit_half)
+    if constexpr (FIT)
       return __builtin_amdgcn_mfma_f32_16x16x32_f16(mx4_half(codes, scale), __builtin_bit_cast(half8_t, x), acc, 0, 0, 0);
     const bf16x8_t a = mx4_bf16(codes, scale);
     bf16x8_t hi, lo;
@@ -284,28 +286,33 @@ struct Mx4Stream {
         acc[m][1] = mx4_mfma<1>(q[m][1], v[1], acc[m][1], s[m], s_x);
       }
     } else {
+      auto products = [&](auto fit) VQMI_INLINE {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u32x4 v[PL];
+#pragma unroll
+            for (int p = 0; p < PL; ++p) v[p] = slot->x[p][n * 32 + ((8 * g + 4 * h + i) ^ n)];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const uint32_t c = i == 0 ? q[m][h].x : i == 1 ? q[m][h].y : i == 2 ? q[m][h].z : q[m][h].w;
+              const float f = h == 0 ? mx4_scale<0>(s[m]) : mx4_scale<1>(s[m]);
+#pragma unroll
+              for (int p = PL - 1; p >= 0; --p)
+                acc[m][i & 1] = mx4_mfma16<XK, decltype(fit)::value>(c, f, v[p], acc[m][i & 1]);
+            }
+          }
+        }
+      };
       bool fit = true;
       if constexpr (XK == kMx4XF16) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) fit = fit && mx4_scales_fit_half(s[m]);
         fit = __ballot(!fit) == 0ull;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u32x4 v[PL];
-#pragma unroll
-          for (int p = 0; p < PL; ++p) v[p] = slot->x[p][n * 32 + ((8 * g + 4 * h + i) ^ n)];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t c = i == 0 ? q[m][h].x : i == 1 ? q[m][h].y : i == 2 ? q[m][h].z : q[m][h].w;
-            const float f = h == 0 ? mx4_scale<0>(s[m]) : mx4_scale<1>(s[m]);
-#pragma unroll
-            for (int p = PL - 1; p >= 0; --p) acc[m][i & 1] = mx4_mfma16<XK>(c, f, v[p], acc[m][i & 1], fit);
-          }
-        }
-      }
+      if (fit) products(std::true_type{});
+      else if constexpr (XK == kMx4XF16) products(std::false_type{});
     }
   }
 
