@@ -343,7 +343,20 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
   store_run<4>(a.y, (int64_t)t * a.hidden_blocks * 32 + r0 + 4 * threadIdx.x, v, a.y_kind);
 }
 
-constexpr int kFewTokens = 2;  // up to here each token's pairs are on their own
+// Down by each token's pairs on their own, without the launch that sums: saves
+// 4 to 5 us and reads an expert again for each further token that chose it.
+// The measured difference is m * (pairs / 20 + again / 3) us less those, for
+// matrices of m MB of which chance has `again` read again.  us, groups -> on
+// their own: 256 experts top 8 of 4096x1024 at 3 tokens 56.4 -> 52.7, 5 68.6 ->
+// 70.4, 16 123 -> 147; of 2048x512 at 3 27.1 -> 22.3, 8 38.2 -> 34.9, 12 41.1
+// -> 41.5; 60 top 4 of 1504x352 at 5 19.7 -> 15.7, 16 24.9 -> 25.3; 8 top 2 of
+// 4096x1792 at 3 27.0 -> 27.2, 4 27.7 -> 30.2.  (A single token has no room
+// for the products in its workspace.)
+bool down_by_token(const MoeArgs& a) {
+  const float m = 32.0f * 17.0f * a.hidden_blocks * a.inter_blocks * 1e-6f;
+  const float again = 0.5f * a.T * (a.T - 1) * a.top_k * a.top_k / a.experts;
+  return a.T == 1 || m * (a.pairs / 20.0f + again / 3.0f) < 3.5f;
+}
 
 // PER_CU: blocks that a compute unit holds, so that all of a launch run at once.
 template <int XK, int KW, int MT, int NL, int DEPTH, int PER_CU>
@@ -356,15 +369,25 @@ void run_products(const MoeArgs& a, int tiles, hipStream_t s) {
 template <int XK>
 hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
   const int up = a.inter_blocks * 4, down = a.hidden_blocks * 2;
-  if (a.T <= kFewTokens) {
-    run_products<XK, 4, 1, 1, 2, 4>(a, up, s);
-    hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
-    return hipGetLastError();
-  }
-  if (min(a.pairs, a.experts) * up <= 2048) run_products<XK, 4, 1, 2, 2, 4>(a, up, s);
+  // Gate and up by blocks that split the columns, with groups of 2 or 4 pairs,
+  // or by waves on their own with twice the rows and groups of 8.  The groups
+  // of 2 load least beside the weights (up to 5 tokens); waves on their own
+  // need many items to fill the card, and gain where most experts are chosen
+  // more than once.  us of the layer, groups of 2, 4 and 8: 256 experts top 8
+  // of 4096x1024 at 1 token 24.0, 24.8 and 30.0, at 4 54.7, 55.6 and 59.0, at 8
+  // 81.4, 79.5 and 81.8, at 16 128, 121 and 123, at 32 195, 182 and 175, at 64
+  // 316, 280 and 257; 60 top 4 of 1504x352 (2640 items) at 16 24.6, 23.5 and
+  // 24.7, at 64 38.3, 34.1 and 34.1; 8 top 2 of 4096x1792 (1792) at 16 45.2,
+  // 41.0 and 44.0, at 64 108, 83.8 and 85.7.
+  if (a.T <= 5) run_products<XK, 4, 1, 1, 2, 4>(a, up, s);
+  else if (a.pairs < a.experts || a.experts * up <= 4096) run_products<XK, 4, 1, 2, 2, 4>(a, up, s);
   else run_products<XK, 1, 2, 4, 2, 2>(a, up, s);
-  run_products<kMx4XPlanes, 1, 2, 2, 1, 3>(a, down, s);
-  hipLaunchKernelGGL(vq_mx4_moe_sum_kernel, dim3((a.T * a.hidden_blocks * 8 + 255) / 256), dim3(256), 0, s, a);
+  if (down_by_token(a)) {
+    hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
+  } else {
+    run_products<kMx4XPlanes, 1, 2, 2, 1, 3>(a, down, s);
+    hipLaunchKernelGGL(vq_mx4_moe_sum_kernel, dim3((a.T * a.hidden_blocks * 8 + 255) / 256), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -372,7 +395,7 @@ hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
 
 size_t mx4_moe_workspace_bytes(int T, int top_k, int hidden, int inter) {
   const size_t pairs = (size_t)T * top_k;
-  return kMx4Planes * pairs * inter * sizeof(uint16_t) + (T <= kFewTokens ? 0 : pairs * hidden * sizeof(float));
+  return kMx4Planes * pairs * inter * sizeof(uint16_t) + (T == 1 ? 0 : pairs * hidden * sizeof(float));
 }
 
 hipError_t launch_mx4_moe(const RouterSpec& r, const Mx4View& gate_up, const Mx4View& down, const void* logits,
