@@ -594,23 +594,23 @@ struct Mx4Kernel {
   void (*run)(const Mx4Args&, int, int, hipStream_t);
 };
 const Mx4Kernel kMx4Kernels[] = {
-    {16, 8, 4, 8, true, 4.07f, 0.1f, 0.0937f, 7.1f, 0.321f, 0.479f, 0.829f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 3.95f, 0.0961f, 0.107f, 7.12f, 0.315f, 0.628f, 0.745f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 3.91f, 0.083f, 0.165f, 6.13f, 0.294f, 1.05f, 0.914f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 4.02f, 0.191f, 0.161f, 5.75f, 0.26f, 0.327f, 1.2f, run_tile<4, 1, 2, 2>},
-    {128, 64, 1, 16, true, 3.87f, 0.254f, 0.209f, 5.89f, 0.239f, 0.741f, 0.832f, run_tile<4, 1, 2, 4>},
-    {128, 128, 1, 16, true, 5.29f, 0.243f, 0.348f, 8, 0.216f, 0.196f, 0.715f, run_tile<4, 2, 2, 4>},
-    {256, 128, 1, 16, true, 4.19f, 0, 0.534f, 7.01f, 0.186f, 3.18f, 1.2f, run_tile<4, 2, 4, 4>},
-    {256, 192, 1, 16, true, 5.29f, 0.00156f, 0.635f, 6.82f, 0.165f, 3.48f, 1.2f, run_tile<4, 2, 4, 6>},
-    {256, 256, 1, 16, true, 4.94f, 0, 0.773f, 7.55f, 0.163f, 4.89f, 1.2f, run_tile<4, 2, 4, 8>},
-    {16, 2, 4, 8, false, 4.16f, 0.166f, 0.106f, 7.96f, 0.41f, 0.403f, 1.12f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 4.17f, 0.199f, 0.125f, 7.3f, 0.21f, 0.497f, 0.596f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 4.12f, 0.214f, 0.141f, 6.76f, 0.178f, 0.692f, 0.432f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 4.19f, 0.386f, 0.317f, 6.21f, 0.317f, 1.51f, 0.431f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 2.36f, 0.409f, 0.632f, 4.42f, 0.588f, 2.82f, 0.338f, run_skinny16<8, 2, 8, 1>},
-    {128, 32, 1, 4, false, 3.96f, 0.531f, 0.37f, 3.92f, 0.275f, 0.254f, 0, run_tile16<4, 1, 2, 2>},
-    {128, 64, 1, 4, false, 4.42f, 0.637f, 0.559f, 3.43f, 0.257f, 0, 0, run_tile16<4, 2, 2, 2>},
-    {256, 128, 1, 4, false, 5.42f, 0.396f, 1.58f, 4.09f, 0.205f, 1.58f, 0, run_tile16<4, 2, 4, 4>},
+    {16, 8, 4, 8, true, 2.62f, 0.0952f, 0.121f, 5.22f, 1.15f, 0.454f, 0.55f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 2.5f, 0, 0.136f, 4.98f, 0.758f, 0.628f, 0.488f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 2.53f, 0, 0.191f, 4.63f, 0.533f, 1.04f, 0.701f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 2.59f, 0.266f, 0.18f, 4.31f, 0.292f, 0, 0.939f, run_tile<4, 1, 2, 2>},
+    {128, 64, 1, 16, true, 2.69f, 0.337f, 0.268f, 4.31f, 0.273f, 0.0511f, 0.158f, run_tile<4, 1, 2, 4>},
+    {128, 128, 1, 16, true, 3.97f, 0.366f, 0.367f, 7.61f, 0.236f, 0.053f, 0.662f, run_tile<4, 2, 2, 4>},
+    {256, 128, 1, 16, true, 3.97f, 0.297f, 0.597f, 6.91f, 0.204f, 2.2f, 0.875f, run_tile<4, 2, 4, 4>},
+    {256, 192, 1, 16, true, 4.97f, 0.244f, 0.686f, 7.04f, 0.181f, 2.65f, 1.2f, run_tile<4, 2, 4, 6>},
+    {256, 256, 1, 16, true, 4.47f, 0, 0.817f, 7.81f, 0.174f, 4.37f, 1.2f, run_tile<4, 2, 4, 8>},
+    {16, 2, 4, 8, false, 2.66f, 0.202f, 0.119f, 5.95f, 2, 0.409f, 0.962f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 2.74f, 0.209f, 0.143f, 5.35f, 1.58f, 0.464f, 0.459f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 2.75f, 0.217f, 0.168f, 4.61f, 0.912f, 0.634f, 0.277f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.04f, 0.331f, 0.362f, 4.07f, 0.484f, 1.39f, 0.238f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 1.42f, 0, 0.739f, 3.47f, 0.936f, 2.49f, 0.251f, run_skinny16<8, 2, 8, 1>},
+    {128, 32, 1, 4, false, 2.8f, 0.587f, 0.39f, 3.09f, 0.296f, 0, 0, run_tile16<4, 1, 2, 2>},
+    {128, 64, 1, 4, false, 3.09f, 0.714f, 0.607f, 2.98f, 0.269f, 0, 0, run_tile16<4, 2, 2, 2>},
+    {256, 128, 1, 4, false, 3.94f, 1.03f, 1.62f, 4.21f, 0.208f, 1.94f, 0, run_tile16<4, 2, 4, 4>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
