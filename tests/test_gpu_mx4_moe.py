@@ -132,6 +132,42 @@ def test_router_options(T):
     _check(layer, binding.Router(32, 4, groups=4, top_groups=2, scale=-0.5), l, x)
 
 
+@pytest.mark.parametrize("logits", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("E", [1, 16, 17, 33, 64, 65, 129, 256, 257])
+def test_few_tokens_with_every_router_shape(E, logits):
+    """Up to 5 tokens are routed by the layer's own blocks for these shapes; the
+    others by a launch before."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(E, 64, 32, ("shapes", E))
+    bias = torch.linspace(-0.1, 0.1, E, device="cuda")
+    for T in (1, 2, 3, 4, 5, 6):
+        l, x = _inputs(T, E, 64, ("shapes", T, E), logits=logits)
+        for k in {1, min(E, 8), min(E, 15), min(E, 31)}:
+            _check(layer, binding.Router(E, k), l, x)
+        _check(layer, binding.Router(E, min(E, 5), score="sigmoid", bias=bias), l, x)
+        if E % 8 == 0:
+            _check(layer, binding.Router(E, 2, score="sigmoid", bias=bias, groups=8, top_groups=2, group_score="top2"
+                                         if E > 8 else "max", renormalize=False), l, x)
+
+
+@pytest.mark.parametrize("T", [1, 3, 5])
+def test_scores_that_nearly_tie(T):
+    """Experts whose scores with the bias are closer than fp32 tells apart, and
+    equal ones: the choice falls in 64 bits, to the lowest expert."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    for E, groups in ((48, 1), (128, 4), (256, 8)):
+        layer = Layer(E, 64, 32, ("ties", E))
+        l, x = _inputs(T, E, 64, ("ties", T, E))
+        l = (l * 2).round() / 2 + torch.arange(E, device="cuda") % 3 * 1e-7
+        bias = torch.zeros(E, device="cuda")
+        bias[::7] = 1e-8
+        _check(layer, binding.Router(E, 6, score="sigmoid", bias=bias, groups=groups, top_groups=min(groups, 3),
+                                     group_score="top2"), l, x)
+        _check(layer, binding.Router(E, 6, bias=bias), l, x)
+
+
 @pytest.mark.parametrize("T", [1, 6, 35])
 def test_tokens_and_slots_without_an_expert(T):
     """Padded tokens (no expert in play) get zeros, fewer experts than slots
