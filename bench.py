@@ -41,6 +41,7 @@ sys.path.insert(0, ROOT)
 HBM_PEAK_GBPS = 8000.0          # MI355X HBM3E
 MFMA_F16_PEAK_TFLOPS = 2500.0   # MI355X dense fp16 MFMA
 MFMA_E4M3_PEAK_TFLOPS = 5000.0  # MI355X dense e4m3 MFMA
+MFMA_E2M1_PEAK_TFLOPS = 10000.0  # MI355X dense e2m1 MFMA
 
 WORKLOAD = "dense_mlp_5120x17408_d2k256"
 DECODE_T = 1
@@ -598,6 +599,61 @@ def configs_report(only=""):
         for (d, b) in ((2, 9), (4, 11), (4, 14), (8, 14)):
             spec = S(17408, 5120, d, b, 64)
             dense(nx, f"17408x5120 d{d}/K{1 << b}", spec, [1], [2048], (nx, d, b))
+    def mx4_rows(wl):
+        """The 4-bit operators: quantizing, reading back, products, the
+        mixture-of-experts layer (bytes of the experts that are chosen)."""
+        f16, bf16, f32 = torch.float16, torch.bfloat16, torch.float32
+
+        def codes(*shape):
+            return torch.randint(0, 256, shape, dtype=torch.uint8, device=dev)
+
+        def tensor(*shape):
+            return binding.MX4Tensor(codes(*shape[:-1], shape[-1] // 2),
+                                     torch.randint(118, 126, (*shape[:-1], shape[-1] // 32), dtype=torch.uint8, device=dev))
+
+        for T, cols, dt in ((4, 17408, bf16), (333, 2016, f32), (4096, 5120, f16)):
+            xs = [torch.randn(T, cols, device=dev).to(dt) for _ in range(6)]
+            q, sc = binding.mx4_quant(xs[0])
+            us = timed([(lambda x=xs[i % 6]: binding.mx4_quant(x, q, sc)) for i in range(12)])
+            nbytes = T * cols * (xs[0].element_size() + 17 / 32)
+            row(wl, f"{T}x{cols}, {str(dt)[6:]}", "vq_mx4_quant", T, us, nbytes, 2.0 * T * cols)
+            qs = [binding.mx4_quant(x) for x in xs]
+            us = timed([(lambda q=qs[i % 6]: binding.mx4_dequant(*q, y=xs[0])) for i in range(12)])
+            row(wl, f"{T}x{cols}, {str(dt)[6:]}", "vq_mx4_dequant", T, us, nbytes, 1.0 * T * cols)
+        for T, rows, cols, xdt, ydt, epi in (
+                (1, 17408, 5120, bf16, bf16, None), (1, 17408, 5120, None, bf16, None), (16, 5120, 17408, None, f32, None),
+                (61, 5121, 4096, f16, f16, None), (61, 5121, 4096, None, f32, None), (128, 5120, 5120, None, bf16, None),
+                (197, 1001, 2016, None, f32, None), (2048, 17408, 5120, None, bf16, "swiglu"),
+                (4096, 8192, 8192, None, bf16, None), (2048, 17408, 5120, bf16, bf16, None)):
+            n = int(max(1, min(48, 500e6 // (rows * cols // 2))))
+            ws = [tensor(rows, cols) for _ in range(n)]
+            x = (torch.randn(T, cols, device=dev).to(xdt),) if xdt else (codes(T, cols // 2), tensor(T, cols).scales)
+            y = torch.empty((T, rows // 2 if epi else rows), dtype=ydt, device=dev)
+            need = binding.LIB.vq_mx4_workspace_bytes(rows, cols, T)
+            wsp = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            us = timed([(lambda w=ws[i % n]: binding.mx4_gemm(w, *x, y=y, workspace=wsp, epilogue=epi))
+                        for i in range(max(16, n))])
+            row(wl, f"{rows}x{cols} {str(xdt)[6:] if xdt else '4-bit'} x, {str(ydt)[6:]} y{' swiglu' if epi else ''}",
+                "vq_mx4_gemm", T, us, (rows + (0 if xdt else T)) * cols * 17 / 32 + T * cols * (2 if xdt else 0)
+                + y.numel() * y.element_size(), 2.0 * T * rows * cols,
+                MFMA_F16_PEAK_TFLOPS if xdt else MFMA_E2M1_PEAK_TFLOPS)
+            del ws
+        grouped = dict(score="sigmoid", groups=8, top_groups=4, group_score="top2", scale=2.5)
+        for T, E, k, hidden, inter, kw in ((1, 256, 8, 4096, 1024, {}), (5, 60, 4, 1504, 352, {}),
+                                           (16, 256, 8, 4096, 1024, grouped), (64, 256, 8, 4096, 1024, grouped),
+                                           (64, 256, 8, 2048, 512, {})):
+            gate_up, down = tensor(E, 2 * inter, hidden), tensor(E, hidden, inter)
+            r = binding.Router(E, k, bias=0.05 * torch.randn(E, device=dev) if kw else None, **kw)
+            ins = [(torch.randn(T, E, device=dev), torch.randn(T, hidden, device=dev).to(bf16)) for _ in range(8)]
+            o = (torch.empty(T, hidden, dtype=bf16, device=dev), *binding.moe_route(r, ins[0][0]))
+            wsp = torch.empty(binding.LIB.vq_mx4_moe_workspace_bytes(T, k, hidden, inter), dtype=torch.uint8, device=dev)
+            us = timed([(lambda i=ins[j % 8]: binding.mx4_moe(r, gate_up, down, *i, *o, workspace=wsp)) for j in range(16)])
+            hit = sum(binding.moe_route(r, l)[0].unique().numel() for l, _ in ins) / 8
+            row(wl, f"{E} experts of {hidden}x{inter}, top-{k}", "vq_mx4_moe", T, us, hit * 3 * hidden * inter * 17 / 32,
+                6.0 * T * k * hidden * inter)
+            del gate_up, down
+        torch.cuda.empty_cache()
+
     def block_rows(wl):
         """The operators around the products, as a feed-forward block calls
         them (rotating inputs); bytes: every input read and output written
@@ -639,6 +695,7 @@ def configs_report(only=""):
                 T * cols + rows * cols + y.numel() * y.element_size(), 2.0 * T * rows * cols,
                 MFMA_E4M3_PEAK_TFLOPS if fast else MFMA_F16_PEAK_TFLOPS)
             del ws
+        mx4_rows(wl)
         for T, cols, bdt, hdt in ((1, 5120, f32, bf16), (333, 2000, f16, e4m3), (4096, 5120, bf16, bf16),
                                   (4096, 5119, bf16, bf16), (4096, 5120, f32, e4m3)):
             n = int(max(1, min(6, 800e6 // (T * cols * 8))))

@@ -43,8 +43,6 @@ COMMON = [
 # destinations must not be AGPRs.
 EXTRA = {
     "vq_fp8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-    "vq_mx4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-    "vq_mx4_moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 
