@@ -209,12 +209,40 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_skinny_kernel(Mx4Args args)
   if (r < toks) store_rows4(a, t, r0 + wave * 16 + g * 4, v);
 }
 
+// The sums of KW groups of kWaves waves, joined in their order by the first
+// group through each other's LDS (free now; at(group): where it is).  False for
+// the others, which are done.
+template <int KW, int WAVES, int MT, int NT, typename At>
+__device__ __forceinline__ bool join_groups(float4_t (&acc)[MT][NT], int group, int wave, int lane, At at) {
+  const int first = wave * MT * NT * 64 + lane;
+  if (group > 0) {
+    float4_t* part = reinterpret_cast<float4_t*>(at(group));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) part[first + (m * NT + n) * 64] = acc[m][n];
+    }
+  }
+  __syncthreads();
+  if (group > 0) return false;
+#pragma unroll
+  for (int o = 1; o < KW; ++o) {
+    const float4_t* part = reinterpret_cast<const float4_t*>(at(o));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] += part[first + (m * NT + n) * 64];
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // product, many tokens, 4-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
 // block, steps of 256 columns (8 blocks, 128 bytes a row)
 // ---------------------------------------------------------------------------
-template <bool PRECISE, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(Mx4Args args) {
+template <bool PRECISE, int WM, int WN, int MT, int NT, int KW>
+__global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_tile_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
   constexpr int kLoadRows = 8 * kWaves;  // rows the block loads at once
@@ -223,10 +251,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   static_assert(kTileRows + kTileTokens <= 64 * kWaves && kTileRows % 64 == 0 && kTileTokens % 32 == 0,
                 "a thread loads one row's scales, a wave those of one operand");
   static_assert(NT % 2 == 0, "two token operands in turn");
-  __shared__ __align__(1024) uint8_t lds_w[2][kTileRows * 128];
-  __shared__ __align__(1024) uint8_t lds_x[2][kTileTokens * 128];
-  __shared__ __align__(1024) u32x4 lds_s[2][64 * kWaves];  // scales of two steps, a row a thread, twice
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  __shared__ __align__(1024) uint8_t lds_w_all[KW][2][kTileRows * 128];
+  __shared__ __align__(1024) uint8_t lds_x_all[KW][2][kTileTokens * 128];
+  __shared__ __align__(1024) u32x4 lds_s_all[KW][2][64 * kWaves];  // scales of two steps, a row a thread, twice
+  const int group = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWaves;  // of the columns
+  const uint32_t thread = threadIdx.x - group * 64 * kWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(thread >> 6), lane = thread & 63;
+  uint8_t(*lds_w)[kTileRows * 128] = lds_w_all[group];
+  uint8_t(*lds_x)[kTileTokens * 128] = lds_x_all[group];
+  u32x4(*lds_s)[64 * kWaves] = lds_s_all[group];
   const uint32_t blocks = a.blocks, pitch = blocks * 16;
   const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
   int rt, tt;
@@ -243,8 +276,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   // banks.  Columns, rows and steps past the end arrive as zeros.
   const uint32_t ld_piece = lane & 7, ld_row = wave * 8 + (lane >> 3);
   const uint32_t ld_dst = ld_row * 128 + ((ld_piece ^ (lane >> 3)) * 16);
-  const uint32_t b0 = blockIdx.y * a.split_blocks, b1 = min(blocks, b0 + a.split_blocks);  // b0: a multiple of 16
-  const uint32_t pairs = (b1 - b0 + 15) / 16;  // steps are taken two by two
+  const uint32_t s0 = blockIdx.y * a.split_blocks, s1 = min(blocks, s0 + a.split_blocks);  // s0: a multiple of 16
+  const uint32_t pairs = ((s1 - s0 + 15) / 16 + KW - 1) / KW;  // steps of each group, taken two by two
+  const uint32_t b0 = s0 + group * pairs * 16, b1 = min(s1, b0 + pairs * 16);  // b1 <= b0: nothing left
   u32x4 stage[kLoads];
   auto stage_off = [&](uint32_t s) {
     const uint32_t b = b0 + s * 8 + ld_piece;
@@ -269,7 +303,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   const uint32_t sc_skew = (uint32_t)reinterpret_cast<uintptr_t>(sc_base) & 3u, sc_rows = sc_w ? rows : toks;
   const uint32_t sc_words = (sc_skew + sc_rows * blocks + 3) / 4;
   const rsrc_t sr = make_rsrc(sc_base - sc_skew, (uint64_t)sc_words * 4);
-  const uint32_t sc_row = sc_w ? threadIdx.x : threadIdx.x - kTileRows;
+  const uint32_t sc_row = sc_w ? thread : thread - kTileRows;
   const uint32_t sc_off = sc_skew + sc_row * blocks + b0;
   const bool sc_live = sc_row < sc_rows;
   int sc_left = (int)(b1 - b0);  // scales from the next ones to be written on
@@ -289,7 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
     }
     sc_left -= 16;
     // (no branch: the compiler would move matrix instructions past it)
-    lds_s[v & 1][threadIdx.x] = u32x4{(w[0] & 0xffffu) | w[2] << 16, w[0] >> 16 | (w[2] & 0xffff0000u),
+    lds_s[v & 1][thread] = u32x4{(w[0] & 0xffffu) | w[2] << 16, w[0] >> 16 | (w[2] & 0xffff0000u),
                                       (w[1] & 0xffffu) | w[3] << 16, w[1] >> 16 | (w[3] & 0xffff0000u)};
   };
   const int r = lane & 15, g = lane >> 4;
@@ -390,7 +424,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
       for (int n = 0; n < NT; ++n) sb[n] = sb_next[n];
     }
   };
-  const uint32_t steps = (b1 - b0 + 7) / 8;
+  const uint32_t steps = KW == 1 ? (b1 - b0 + 7) / 8 : 2 * pairs;  // (the barriers are every group's)
   for (uint32_t v = 0; v < pairs; ++v) {
     step(v, std::integral_constant<int, 0>{});
     if (2 * v + 1 < steps) step(v, std::integral_constant<int, 1>{});
@@ -398,8 +432,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
   // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
   // token's rows leave in whole pieces.
   lds_barrier();
+  if constexpr (KW > 1) {
+    if (!join_groups<KW, kWaves, MT, NT>(acc, group, wave, lane, [&](int o) VQMI_INLINE { return lds_w_all[o][0]; }))
+      return;
+  }
   constexpr int kPitch = 16 * MT + 4;  // fp32 a token
-  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds_w), "every wave's 16 tokens fit");
+  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds_w_all[0]), "every wave's 16 tokens fit");
+  static_assert(KW == 1 || kWaves * MT * NT * 1024 <= (int)sizeof(lds_w_all[0]), "a group's sums fit");
   float* out = reinterpret_cast<float*>(&lds_w[0][0]) + wave * 16 * kPitch;
   static_for<NT>([&](auto n) VQMI_INLINE {
 #pragma unroll
@@ -414,8 +453,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void vq_mx4_tile_kernel(
 // product, many tokens, 16-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
 // block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token)
 // ---------------------------------------------------------------------------
-template <int XK, bool PRECISE, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args args) {
+template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int KW>
+__global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Args args) {
   const Mx4Args a = split_args(args);
   constexpr int kWaves = WM * WN, kTileRows = 16 * MT * WM, kTileTokens = 16 * NT * WN;
   constexpr int kWLoads = kTileRows / (16 * kWaves), kXLoads = kTileTokens / (4 * kWaves);  // a wave: 16 rows, 4 tokens
@@ -423,9 +462,14 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   constexpr int kTileBytes = kTileRows * 64 + kTileTokens * 256;
   constexpr int kPitch = 16 * MT + 4;  // of the outputs in LDS: fp32 a token
   constexpr int kOutBytes = kWaves * 16 * kPitch * 4;
-  __shared__ __align__(1024) uint8_t lds[2 * kTileBytes > kOutBytes ? 2 * kTileBytes : kOutBytes];
-  __shared__ uint32_t lds_s[2][kTileRows];  // a row's scales of a step
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  static_assert(2 * kTileBytes >= kOutBytes && (KW == 1 || 2 * kTileBytes >= kWaves * MT * NT * 1024), "outputs fit");
+  __shared__ __align__(1024) uint8_t lds_all[KW][2 * kTileBytes];
+  __shared__ uint32_t lds_s_all[KW][2][kTileRows];  // a row's scales of a step
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWaves;  // of the columns
+  const int thread = threadIdx.x - group * 64 * kWaves, lane = thread & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
+  uint8_t* lds = lds_all[group];
+  uint32_t(*lds_s)[kTileRows] = lds_s_all[group];
   const uint32_t blocks = a.blocks;
   const int row_tiles = (a.rows + kTileRows - 1) / kTileRows, tok_tiles = (a.T + kTileTokens - 1) / kTileTokens;
   int rt, tt;
@@ -435,8 +479,9 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
   const rsrc_t xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * 64, (uint64_t)toks * blocks * 64);
   const int wm = wave / WN * 16 * MT, wn = wave % WN * 16 * NT;
-  const uint32_t b0 = blockIdx.y * a.split_blocks, b1 = min(blocks, b0 + a.split_blocks);
-  const uint32_t steps = (b1 - b0 + 3) / 4;
+  const uint32_t s0 = blockIdx.y * a.split_blocks, s1 = min(blocks, s0 + a.split_blocks);
+  const uint32_t steps = ((s1 - s0 + 3) / 4 + KW - 1) / KW;  // of each group
+  const uint32_t b0 = s0 + group * steps * 4, b1 = min(s1, b0 + steps * 4);  // b1 < b0: nothing left
 
   // 16-byte pieces change places within a row (w: piece ^ row / 2 of 4, x: piece
   // ^ token of 16), so reads of 16 rows touch all banks.
@@ -449,7 +494,7 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
   const rsrc_t sr = make_rsrc(sc_base - sc_skew, (uint64_t)((sc_skew + (uint64_t)rows * blocks + 3) & ~3ull));
   static_assert(kTileRows <= 64 * kWaves, "a thread loads one row's scales");
   // (rows past the end take the last one's: zeros would not fit fp16)
-  const uint32_t sc_off = sc_skew + min((int)threadIdx.x, rows - 1) * blocks + b0;
+  const uint32_t sc_off = sc_skew + min(thread, rows - 1) * blocks + b0;
   auto load = [&](uint32_t s) VQMI_INLINE {  // past the end: zeros
     const uint32_t bw = b0 + s * 4 + w_piece, bx = b0 + s * 4 + x_piece / 4;
 #pragma unroll
@@ -475,11 +520,11 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
       const uint32_t row = x_row + i * 4 * kWaves;
       *reinterpret_cast<u32x4*>(to + kTileRows * 64 + row * 256 + ((x_piece ^ (row & 15)) * 16)) = sx[i];
     }
-    if (threadIdx.x < kTileRows) {
+    if (thread < kTileRows) {
       // scales past the last column (another row's) are 1: NaN there would spoil the sum
       const int left = (int)(b1 - b0) - (int)(4 * s);
       const uint32_t mask = left >= 4 ? ~0u : (1u << (8 * max(left, 0))) - 1u;
-      lds_s[s & 1][threadIdx.x] = (__builtin_amdgcn_alignbyte(ss[1], ss[0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
+      lds_s[s & 1][thread] = (__builtin_amdgcn_alignbyte(ss[1], ss[0], sc_off) & mask) | (~mask & 0x7f7f7f7fu);
     }
   };
   const int r = lane & 15, g = lane >> 4;
@@ -527,6 +572,9 @@ __global__ __launch_bounds__(64 * WM * WN) void vq_mx4_tile16_kernel(Mx4Args arg
     else if constexpr (XK == kMx4XF16) products(std::false_type{});
     lds_barrier();
   }
+  if constexpr (KW > 1) {
+    if (!join_groups<KW, kWaves, MT, NT>(acc, group, wave, lane, [&](int o) VQMI_INLINE { return lds_all[o]; })) return;
+  }
   // The waves' outputs go through the same LDS, 16 tokens at a time, so that a
   // token's rows leave in whole pieces.
   float* out = reinterpret_cast<float*>(lds) + wave * 16 * kPitch;
@@ -553,23 +601,23 @@ void run_skinny(const Mx4Args& a, int, int splits, hipStream_t s) {
   hipLaunchKernelGGL((vq_mx4_skinny_kernel<XK, WAVES, MT, NL, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT>
+template <int WM, int WN, int MT, int NT, int KW>
 void run_tile(const Mx4Args& a, int, int splits, hipStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
-  const dim3 block(64 * WM * WN);
-  if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT>), grid, block, 0, s, a);
+  const dim3 block(64 * WM * WN * KW);
+  if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile_kernel<true, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((vq_mx4_tile_kernel<false, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
 }
 
-template <int WM, int WN, int MT, int NT>
+template <int WM, int WN, int MT, int NT, int KW>
 void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN);
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN * KW);
   if (xk == kMx4XF16) {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
   } else {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT>), grid, block, 0, s, a);
+    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
   }
 }
 
@@ -594,23 +642,28 @@ struct Mx4Kernel {
   void (*run)(const Mx4Args&, int, int, hipStream_t);
 };
 const Mx4Kernel kMx4Kernels[] = {
-    {16, 8, 4, 8, true, 2.62f, 0.0952f, 0.121f, 5.22f, 1.15f, 0.454f, 0.55f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 2.5f, 0, 0.136f, 4.98f, 0.758f, 0.628f, 0.488f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 2.53f, 0, 0.191f, 4.63f, 0.533f, 1.04f, 0.701f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 2.59f, 0.266f, 0.18f, 4.31f, 0.292f, 0, 0.939f, run_tile<4, 1, 2, 2>},
-    {128, 64, 1, 16, true, 2.69f, 0.337f, 0.268f, 4.31f, 0.273f, 0.0511f, 0.158f, run_tile<4, 1, 2, 4>},
-    {128, 128, 1, 16, true, 3.97f, 0.366f, 0.367f, 7.61f, 0.236f, 0.053f, 0.662f, run_tile<4, 2, 2, 4>},
-    {256, 128, 1, 16, true, 3.97f, 0.297f, 0.597f, 6.91f, 0.204f, 2.2f, 0.875f, run_tile<4, 2, 4, 4>},
-    {256, 192, 1, 16, true, 4.97f, 0.244f, 0.686f, 7.04f, 0.181f, 2.65f, 1.2f, run_tile<4, 2, 4, 6>},
-    {256, 256, 1, 16, true, 4.47f, 0, 0.817f, 7.81f, 0.174f, 4.37f, 1.2f, run_tile<4, 2, 4, 8>},
-    {16, 2, 4, 8, false, 2.66f, 0.202f, 0.119f, 5.95f, 2, 0.409f, 0.962f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 2.74f, 0.209f, 0.143f, 5.35f, 1.58f, 0.464f, 0.459f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 2.75f, 0.217f, 0.168f, 4.61f, 0.912f, 0.634f, 0.277f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.04f, 0.331f, 0.362f, 4.07f, 0.484f, 1.39f, 0.238f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1.42f, 0, 0.739f, 3.47f, 0.936f, 2.49f, 0.251f, run_skinny16<8, 2, 8, 1>},
-    {128, 32, 1, 4, false, 2.8f, 0.587f, 0.39f, 3.09f, 0.296f, 0, 0, run_tile16<4, 1, 2, 2>},
-    {128, 64, 1, 4, false, 3.09f, 0.714f, 0.607f, 2.98f, 0.269f, 0, 0, run_tile16<4, 2, 2, 2>},
-    {256, 128, 1, 4, false, 3.94f, 1.03f, 1.62f, 4.21f, 0.208f, 1.94f, 0, run_tile16<4, 2, 4, 4>},
+    {16, 8, 4, 8, true, 2.78f, 0, 0.139f, 6.13f, 1.21f, 0.367f, 0.697f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 2.64f, 0.133f, 0.132f, 5.13f, 0.733f, 0.572f, 0.54f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 3.02f, 0.00359f, 0.23f, 4.95f, 0.682f, 0.607f, 0.726f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 2.42f, 0.321f, 0.2f, 4.29f, 0.292f, 0.373f, 0.172f, run_tile<4, 1, 2, 2, 1>},
+    {128, 64, 2, 32, true, 1.71f, 0.443f, 0.54f, 4.29f, 0.277f, 2.68f, 0, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 1.14f, 0.74f, 0.473f, 4.71f, 0.05f, 3.43f, 0.554f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 4.86f, 0.301f, 0.291f, 7.12f, 0.267f, 0, 1.07f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 3.88f, 0.358f, 0.382f, 5.95f, 0.222f, 0.0485f, 0.252f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 3.98f, 0.323f, 0.598f, 7.05f, 0.201f, 1.88f, 0.923f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 3.48f, 0.266f, 0.701f, 7.57f, 0.178f, 3.63f, 1.2f, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 4.46f, 0, 0.813f, 7.88f, 0.168f, 4.25f, 1.2f, run_tile<4, 2, 4, 8, 1>},
+    {16, 2, 4, 8, false, 2.92f, 0.198f, 0.122f, 6.16f, 2, 0.356f, 0.94f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 2.89f, 0.185f, 0.188f, 8, 1.61f, 0.35f, 0.534f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 3, 0.173f, 0.214f, 4.71f, 0.755f, 0.485f, 0.27f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.34f, 0.392f, 0.348f, 4.43f, 0.581f, 1.26f, 0.304f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 1.77f, 0, 0.68f, 2.96f, 0.925f, 2.3f, 0.201f, run_skinny16<8, 2, 8, 1>},
+    {64, 32, 4, 16, false, 2.77f, 0.503f, 1.24f, 4.87f, 0.333f, 1.45f, 0.0873f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 3.37f, 0.663f, 0.465f, 3.11f, 0.423f, 0, 0.0471f, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 3.02f, 0.839f, 0.787f, 3.26f, 0.309f, 0.564f, 0, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 2.26f, 0.782f, 1.21f, 3.42f, 0.3f, 2.14f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.05f, 0.724f, 0.612f, 3.52f, 0.263f, 0.226f, 0, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 2.69f, 1.19f, 1.57f, 3.89f, 0.196f, 3.37f, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
