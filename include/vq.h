@@ -582,9 +582,9 @@ vq_status vq_mx4_gemm(const vq_mx4_tensor *w, const vq_io *io, const void *x, co
  *   y[t] = sum over the slots s with ids[t][s] >= 0 of weights[t][s] *
  *          W_down[e] h[t][s]
  * Products are exact, sums are in fp32, y is rounded to its type once.  A token
- * without an expert gets zeros.  Every expert's weights are read once per call
- * (per 16 of its tokens): the call is for decode batches.  The same call gives
- * the same bits every time; a token's last bits depend on the batch.
+ * without an expert gets zeros.  An expert's weights are read once for 2 to 8 of
+ * its tokens: the call is for decode batches.  The same call gives the same
+ * bits every time; a token's last bits depend on the batch.
  *   r: as for vq_moe_route, with num_experts those of both stacks;
  *   gate_up: [E][2 * inter][hidden], interleaved gate and up rows; down:
  *   [E][hidden][inter];
@@ -597,8 +597,8 @@ vq_status vq_mx4_gemm(const vq_mx4_tensor *w, const vq_io *io, const void *x, co
  *   workspace: device, >= vq_mx4_moe_workspace_bytes(T, top_k, hidden, inter)
  *   bytes, 16-byte aligned, as for vq_mx4_gemm.
  * 0 <= T <= 64 (0 enqueues nothing), T * top_k <= 1024, and T * top_k * hidden
- * and T * top_k * inter <= 2^26 (else VQ_ERR_SHAPE; larger batches belong to vq_moe_route and products
- * of their own).
+ * and T * top_k * inter <= 2^26 (else VQ_ERR_SHAPE; larger batches belong to
+ * vq_moe_route and products of their own).
  */
 size_t vq_mx4_moe_workspace_bytes(int32_t T, int32_t top_k, int32_t hidden, int32_t inter);
 vq_status vq_mx4_moe(const vq_router *r, const vq_mx4_tensor *gate_up, const vq_mx4_tensor *down, const vq_io *io,

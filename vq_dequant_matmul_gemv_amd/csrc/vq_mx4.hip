@@ -19,7 +19,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // quantizer and reader: rows are whole blocks, so a tensor is one run of
-// blocks of 32; 4 lanes a block, 8 values each
+// blocks of 32; 4 lanes a block, 8 values (16 bytes of 16-bit x) each, the
+// block's maximum by two lane exchanges.  Bound by memory: 4096 x 5120 fp16
+// values take 10.0 us each way, 5.3 TB/s, a large copy's rate; 4 x 17408 bf16
+// values 2.8, which is a launch.
 // ---------------------------------------------------------------------------
 
 // Eight values at x[i], and the largest magnitude as fp32 bits.
@@ -114,8 +117,14 @@ __global__ __launch_bounds__(256) void vq_mx4_dequant_kernel(const uint32_t* q, 
 }
 
 // ---------------------------------------------------------------------------
-// product, few tokens: a block takes 16 rows of w and up to 16 tokens, its waves
-// split the columns and join their sums in LDS
+// product, few tokens: a block takes 16 rows of w (or 32) and up to 16 tokens,
+// its waves split the columns and join their sums in LDS
+//
+// Bound by the weight's bytes: one token of 17408 x 5120 (47 MB) takes 12.7 us
+// with 4-bit x and 13.0 with bf16 x, 3.7 TB/s; less the launch's 2.3 us that is
+// 4.5 TB/s of a copy's 5.2.  Waves that stream rows' columns through LDS of
+// their own need no barrier until the end; fragments loaded straight from memory
+// took 18 us, and more than two steps in flight gained nothing.
 // ---------------------------------------------------------------------------
 struct Mx4Args {
   const uint8_t* w;
@@ -239,7 +248,17 @@ __device__ __forceinline__ bool join_groups(float4_t (&acc)[MT][NT], int group, 
 
 // ---------------------------------------------------------------------------
 // product, many tokens, 4-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
-// block, steps of 256 columns (8 blocks, 128 bytes a row)
+// block, steps of 256 columns (8 blocks, 128 bytes a row); with KW > 1 that many
+// groups of such waves split a block's columns, for products of too few tiles to
+// fill the card otherwise (128 tokens of 5120 x 5120: 17.3 us with splits that a
+// second launch joins, 13.5 with two groups)
+//
+// 2048 tokens of 17408 x 5120 with SwiGLU take 115 us, 3.2 PF/s; 4096 of 8192 x
+// 8192 138 us, 4.0 PF/s.  Bound by the matrix instructions at the card's power
+// limit: of 155 us that the latter took before the last steps, they alone ran
+// 104; without the writes to LDS it took 124, without the loads 138.  Loads straight into LDS,
+// three steps ahead, were slower: a block on its own took 141 us where this
+// takes 104.
 // ---------------------------------------------------------------------------
 template <bool PRECISE, int WM, int WN, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_tile_kernel(Mx4Args args) {
@@ -451,7 +470,14 @@ __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_ti
 
 // ---------------------------------------------------------------------------
 // product, many tokens, 16-bit x: WM x WN waves of 16*MT rows x 16*NT tokens a
-// block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token)
+// block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token), KW
+// groups of them as above
+//
+// 61 tokens of 5121 x 4096 take 15 us, bound by the latency of a step: LDS
+// reads, conversions and 16 matrix instructions one after the other in a wave,
+// of which four groups of waves overlap some (17.4 us in one, with splits).
+// 2048 tokens of 17408 x 5120 take 363 us, 1.0 PF/s, bound by the LDS traffic of
+// 16-bit x beside the matrix instructions.
 // ---------------------------------------------------------------------------
 template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Args args) {
@@ -627,7 +653,11 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   else run_skinny<kMx4XBF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
 }
 
-// The kernels of the product and a time model of each (us):
+// The kernels of the product and a time model of each (us), fitted to 21146
+// measured calls (1 to 4096 tokens, 32 to 17408 rows, 224 to 17408 columns, 1 to
+// 24 splits), the faster ones of a shape weighing more.  The model's choice takes
+// 0.6 % longer than the best one on average, 0.4 % above 20 us (the calls and the
+// fit: profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py):
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
 // with steps of 128 columns a wave runs through, rounds of 256 blocks, and
@@ -635,35 +665,37 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
 // tile (MB; bw in TB/s).
 struct Mx4Kernel {
   int rows, tokens;  // of a block
-  int k_waves;       // waves that split a block's columns
+  int k_waves;       // waves, or groups of them, that split a block's columns
   int unit_blocks;   // splits are multiples of these blocks of columns
   bool mx4;          // 4-bit x (else 16-bit)
   float base, latency, rate, bw, join, unit, x_share;
   void (*run)(const Mx4Args&, int, int, hipStream_t);
 };
 const Mx4Kernel kMx4Kernels[] = {
-    {16, 8, 4, 8, true, 2.78f, 0, 0.139f, 6.13f, 1.21f, 0.367f, 0.697f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 2.64f, 0.133f, 0.132f, 5.13f, 0.733f, 0.572f, 0.54f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 3.02f, 0.00359f, 0.23f, 4.95f, 0.682f, 0.607f, 0.726f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 2.42f, 0.321f, 0.2f, 4.29f, 0.292f, 0.373f, 0.172f, run_tile<4, 1, 2, 2, 1>},
-    {128, 64, 2, 32, true, 1.71f, 0.443f, 0.54f, 4.29f, 0.277f, 2.68f, 0, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 1.14f, 0.74f, 0.473f, 4.71f, 0.05f, 3.43f, 0.554f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 4.86f, 0.301f, 0.291f, 7.12f, 0.267f, 0, 1.07f, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 3.88f, 0.358f, 0.382f, 5.95f, 0.222f, 0.0485f, 0.252f, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 3.98f, 0.323f, 0.598f, 7.05f, 0.201f, 1.88f, 0.923f, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 3.48f, 0.266f, 0.701f, 7.57f, 0.178f, 3.63f, 1.2f, run_tile<4, 2, 4, 6, 1>},
+    // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
+    {16, 8, 4, 8, true, 2.83f, 0.00224f, 0.133f, 5.63f, 1.24f, 0.378f, 0.411f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 2.66f, 0.121f, 0.136f, 5.19f, 0.826f, 0.549f, 0.525f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 2.81f, 0.00476f, 0.294f, 5.12f, 0.823f, 0.558f, 0.0467f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 2.45f, 0.327f, 0.198f, 4.26f, 0.278f, 0.321f, 0.376f, run_tile<4, 1, 2, 2, 1>},
+    {128, 64, 2, 32, true, 1.79f, 0.3f, 0.547f, 4.47f, 0.235f, 2.76f, 0.325f, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 2.15f, 0.0116f, 0.48f, 6.33f, 0.05f, 3.19f, 1.11f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 4.52f, 0.342f, 0.296f, 7.55f, 0.341f, 0.117f, 0.982f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 3.94f, 0.353f, 0.379f, 6.34f, 0.225f, 0.0136f, 0.342f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 3.93f, 0.333f, 0.598f, 6.93f, 0.2f, 1.92f, 0.892f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 3.5f, 0.268f, 0.7f, 7.55f, 0.177f, 3.62f, 1.2f, run_tile<4, 2, 4, 6, 1>},
     {256, 256, 1, 16, true, 4.46f, 0, 0.813f, 7.88f, 0.168f, 4.25f, 1.2f, run_tile<4, 2, 4, 8, 1>},
-    {16, 2, 4, 8, false, 2.92f, 0.198f, 0.122f, 6.16f, 2, 0.356f, 0.94f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 2.89f, 0.185f, 0.188f, 8, 1.61f, 0.35f, 0.534f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 3, 0.173f, 0.214f, 4.71f, 0.755f, 0.485f, 0.27f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.34f, 0.392f, 0.348f, 4.43f, 0.581f, 1.26f, 0.304f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1.77f, 0, 0.68f, 2.96f, 0.925f, 2.3f, 0.201f, run_skinny16<8, 2, 8, 1>},
-    {64, 32, 4, 16, false, 2.77f, 0.503f, 1.24f, 4.87f, 0.333f, 1.45f, 0.0873f, run_tile16<2, 1, 2, 2, 4>},
-    {64, 32, 2, 8, false, 3.37f, 0.663f, 0.465f, 3.11f, 0.423f, 0, 0.0471f, run_tile16<2, 1, 2, 2, 2>},
-    {128, 32, 2, 8, false, 3.02f, 0.839f, 0.787f, 3.26f, 0.309f, 0.564f, 0, run_tile16<4, 1, 2, 2, 2>},
-    {128, 64, 2, 8, false, 2.26f, 0.782f, 1.21f, 3.42f, 0.3f, 2.14f, 0, run_tile16<4, 1, 2, 4, 2>},
-    {128, 64, 1, 4, false, 3.05f, 0.724f, 0.612f, 3.52f, 0.263f, 0.226f, 0, run_tile16<4, 2, 2, 2, 1>},
-    {256, 128, 1, 4, false, 2.69f, 1.19f, 1.57f, 3.89f, 0.196f, 3.37f, 0, run_tile16<4, 2, 4, 4, 1>},
+    // 16-bit x: the same
+    {16, 2, 4, 8, false, 2.89f, 0.196f, 0.135f, 5.8f, 2, 0.351f, 0.436f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 2.9f, 0.185f, 0.188f, 6.29f, 1.49f, 0.346f, 0.221f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 2.99f, 0.167f, 0.226f, 6.11f, 0.765f, 0.449f, 0.306f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.52f, 0.365f, 0.38f, 4.52f, 0.782f, 0.906f, 0.292f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 1.78f, 0, 0.672f, 3, 0.883f, 2.33f, 0.213f, run_skinny16<8, 2, 8, 1>},
+    {64, 32, 4, 16, false, 2.4f, 0, 1.18f, 3.86f, 0.406f, 1.59f, 0.0345f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 3.27f, 0.682f, 0.463f, 3.12f, 0.385f, 0.142f, 0.0558f, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 3, 0.833f, 0.787f, 3.35f, 0.304f, 0.584f, 0.0403f, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 2.22f, 0.76f, 1.21f, 3.54f, 0.304f, 2.16f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.07f, 0.724f, 0.611f, 3.47f, 0.265f, 0.186f, 0, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 2.87f, 1.17f, 1.58f, 3.82f, 0.198f, 3.11f, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split

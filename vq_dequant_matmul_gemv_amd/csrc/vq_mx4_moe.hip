@@ -1,13 +1,22 @@
 // vq_mx4_moe.hip -- a mixture-of-experts layer for a few tokens over 4-bit
-// experts: behind the routing, one kernel for the gate and up projections with
-// SwiGLU and one for the down projection with the weighted sum.
+// experts: one kernel for the gate and up projections with SwiGLU (and, up to 5
+// tokens, the routing) and one for the down projection with the weighted sum
+// (where many tokens share experts, the sum in a third).
 //
 //   h[t][s] = silu(W_gate[e] x_t) * (W_up[e] x_t),   e = ids[t][s]
 //   y[t]    = sum over the slots s of weight[t][s] * W_down[e] h[t][s]
 //
-// Bound by the bytes of the experts that the tokens hit, so each expert's
-// weights are read once: the tokens that chose it are the columns of its
-// matrix products.
+// Bound by the bytes of the experts that the tokens hit, so an expert's weights
+// are read once for a group of the pairs (token and slot) that chose it, which
+// are the columns of its matrix products.  256 experts, top 8, of 4096 x 1024:
+// 64 tokens that hit 182 of them (1.2 GB) take 290 us, 16 that hit 90 138 us,
+// 4.2 to 4.4 TB/s of a copy's 5.2; one token (53 MB) 21.5 us: 12 of gate and up
+// with the routing, 8 of down, each launch's latency and ramp beside 7 and 3.5
+// us of bytes.
+//
+// h is kept in fp32 as three bf16 planes, so that the down products take it
+// whole: rounding it to 16 bits would add an error that the caller's sums of
+// 16-bit products do not have.
 #include "vq_block_kernels.h"
 #include "vq_mx4_device.h"
 #include "vq_router_device.h"
