@@ -381,3 +381,160 @@ def test_quantized_chain_captured():
         h, y = mlp()
         torch.cuda.synchronize()
         assert torch.equal(h, hc) and torch.equal(y, yc)
+
+
+# ---- streams, workspaces, refusals ---------------------------------------
+
+def _random_tensor(R, C, g, lo=120, hi=126):
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    return binding.MX4Tensor(torch.randint(0, 256, (R, C // 2), dtype=torch.uint8, device="cuda", generator=g),
+                             torch.randint(lo, hi + 1, (R, C // 32), dtype=torch.uint8, device="cuda", generator=g))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap in time, each with a workspace of its own."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = _random_tensor(640, 17408, g)
+    xs = [torch.randn(T, 17408, device="cuda", generator=g).bfloat16() for T in (16, 33)]
+    ref = [(binding.mx4_gemm(w, x), binding.mx4_gemm(w, *binding.mx4_quant(x))) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(6):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append((binding.mx4_gemm(w, xs[k]), binding.mx4_gemm(w, *binding.mx4_quant(xs[k]))))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for a, b in got[k]:
+            assert torch.equal(a, ref[k][0]) and torch.equal(b, ref[k][1])
+
+
+def test_graphs_in_turn_on_one_workspace():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = [_random_tensor(640, 17408, g) for _ in range(2)]
+    x = torch.randn(48, 17408, device="cuda", generator=g).half()
+    need = binding.LIB.vq_mx4_workspace_bytes(640, 17408, 48)
+    assert need > 0
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    ys, graphs = [], []
+    for t in w:
+        binding.mx4_gemm(t, x, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ys.append(binding.mx4_gemm(t, x, workspace=ws))
+        graphs.append(graph)
+    for k in range(4):
+        x.copy_(torch.randn(48, 17408, device="cuda", generator=g).half())
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for t, y in zip(w, ys):
+            assert torch.equal(y, binding.mx4_gemm(t, x))
+        ws.fill_(0xff)
+
+
+def test_refusals_on_the_gpu():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = _random_tensor(64, 256, g)
+    x = torch.randn(6, 256, device="cuda").bfloat16()
+    q, s = binding.mx4_quant(x)
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.mx4_quant(torch.randn(6, 512, device="cuda")[:, :256])
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.mx4_gemm(w, x.repeat(1, 2)[:, :256])
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.mx4_gemm(w, q, s.repeat(1, 2)[:, :8])
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.mx4_dequant(q.t().contiguous().t(), s)
+    with pytest.raises(ValueError, match="y must"):
+        binding.mx4_gemm(w, x, y=torch.empty(6, 63, device="cuda"))
+    with pytest.raises(ValueError, match="y must be torch.float32"):
+        binding.mx4_gemm(w, x, y=torch.empty(6, 64, dtype=torch.bfloat16, device="cuda"), y_dtype=torch.float32)
+    with pytest.raises(ValueError, match="dtype"):
+        binding.mx4_gemm(w, x, y=torch.empty(6, 64, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError, match="one tensor"):
+        binding.mx4_gemm(binding.MX4Tensor(w.values.view(2, 32, 128), w.scales.view(2, 32, 8)), x)
+    with pytest.raises(ValueError, match="cuda"):
+        binding.mx4_gemm(w, x.cpu())
+    off = torch.empty(6 * 256 + 4, device="cuda").bfloat16()[4:].view(6, 256)     # 8 bytes off
+    with pytest.raises(binding.VQError, match="align"):
+        binding.mx4_gemm(w, off)
+    with pytest.raises(binding.VQError, match="align"):
+        binding.mx4_quant(off)
+    with pytest.raises(binding.VQError, match="workspace has"):
+        need = binding.LIB.vq_mx4_workspace_bytes(64, 17408, 40)
+        assert need > 0
+        big = _random_tensor(64, 17408, g)
+        binding.mx4_gemm(big, torch.zeros(40, 17408, device="cuda").half(),
+                         workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    y = binding.mx4_gemm(w, x[:0])
+    assert y.shape == (0, 64) and binding.mx4_quant(x[:0])[0].shape == (0, 128)
+
+
+# ---- offsets past 32 bits -------------------------------------------------
+# Scales of 1 and codes of at most 6 (16-bit x: whole numbers up to 4): sums of
+# 8192 products are whole quarters below 2^20, exact in fp32 in any order, so the
+# end of a large call equals a small one bit for bit.
+
+def test_quantizer_past_4_gib():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    T, C = (1 << 16) + 7, 33280                       # 2.18e9 values: 4.4 GB in fp16, 1.1 of codes
+    x = torch.empty(T, C, dtype=torch.float16, device="cuda")
+    x.view(torch.int16).fill_(0x3c00)
+    x[-5:] = torch.randn(5, C, device="cuda").half()
+    announce("mx4_quant past 4 GiB", T, C)
+    q, s = binding.mx4_quant(x)
+    sq, ss = binding.mx4_quant(x[-5:])
+    assert torch.equal(q.view(torch.uint8)[-5:], sq.view(torch.uint8))
+    assert torch.equal(s.view(torch.uint8)[-5:], ss.view(torch.uint8))
+    assert torch.all(q.view(torch.uint8)[:-5] == 0x66).item()   # 1 = 4 * 2^-2
+    binding.mx4_dequant(q, s, y=x)
+    assert torch.equal(x[-5:], binding.mx4_dequant(sq, ss, dtype=torch.float16)) and torch.all(x[:-5] == 1).item()
+
+
+@pytest.mark.parametrize("x", ["mx4", "bfloat16"])
+def test_weight_past_4_gib(x):
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = torch.Generator(device="cuda").manual_seed(8)
+    R, C = (1 << 20) + 33, 8192
+    w = _random_tensor(R, C, g, 127, 127)
+    end = binding.MX4Tensor(w.values[-70:], w.scales[-70:])
+    for T in (1, 40, 300):
+        a = torch.randint(-4, 5, (T, C), device="cuda", generator=g).to(torch.bfloat16)
+        a = (a,) if x != "mx4" else (torch.randint(0, 256, (T, C // 2), dtype=torch.uint8, device="cuda", generator=g),
+                                     torch.full((T, C // 32), 127, dtype=torch.uint8, device="cuda"))
+        announce("mx4_gemm weight past 4 GiB", x, T)
+        y = binding.mx4_gemm(w, *a)
+        assert torch.equal(y[:, -70:], binding.mx4_gemm(end, *a))
+        assert y[:, :-70].abs().amax().item() > 0
+
+
+@pytest.mark.parametrize("x,T,R,C", [("mx4", (1 << 20) + 9, 48, 8192), ("float16", (1 << 18) + 9, 48, 8192),
+                                     ("mx4", (1 << 18) + 9, 5001, 256), ("bfloat16", (1 << 18) + 9, 5000, 256)])
+def test_tokens_past_4_gib(x, T, R, C):
+    """Activations, and outputs, of more than 4 GiB."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w = _random_tensor(R, C, g, 127, 127)
+    if x == "mx4":
+        a = (torch.randint(0, 256, (T, C // 2), dtype=torch.uint8, device="cuda", generator=g),
+             torch.full((T, C // 32), 127, dtype=torch.uint8, device="cuda"))
+    else:
+        a = (torch.randint(-4, 5, (T, C), device="cuda", generator=g, dtype=torch.int8).to(_dt(x)),)
+    announce("mx4_gemm tokens past 4 GiB", x, T, R, C)
+    y = binding.mx4_gemm(w, *a)
+    assert torch.equal(y[-130:], binding.mx4_gemm(w, *(t[-130:] for t in a)))

@@ -310,3 +310,88 @@ def test_layer_between_norms():
         torch.cuda.synchronize()
         for a, b in zip(out, block()):
             assert torch.equal(a, b)
+
+
+class _Last:
+    """The values of a stack's experts, one at a time."""
+    def __init__(self, t):
+        self.t, self.shape = t, (t.values.shape[0], t.values.shape[1], 2 * t.values.shape[2])
+
+    def __getitem__(self, e):
+        return O.mx4_values(self.t.values[int(e)].cpu().numpy(), self.t.scales[int(e)].cpu().numpy())
+
+
+def test_experts_past_4_gib():
+    """Stacks of 4.3 and 8.6 GB: the last experts are read at their own places."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    E, H, I = 1024, 2048, 4096
+    g = torch.Generator(device="cuda").manual_seed(11)
+    layer = Layer.__new__(Layer)
+    layer.E, layer.H, layer.I = E, H, I
+    layer.tensors = [binding.MX4Tensor(torch.randint(0, 256, (E, r, c // 2), dtype=torch.uint8, device="cuda", generator=g),
+                                       torch.randint(116, 125, (E, r, c // 32), dtype=torch.uint8, device="cuda",
+                                                     generator=g)) for r, c in ((2 * I, H), (H, I))]
+    layer.values = lambda: [_Last(t) for t in layer.tensors]
+    for T in (1, 4, 7):
+        l = torch.zeros(T, E, device="cuda")
+        l[:, -1] = 3.0
+        l[:, -2] = 2.0
+        x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+        _check(layer, binding.Router(E, 2), l, x)
+
+
+def test_refusals_on_the_gpu():
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layer = Layer(8, 96, 64, ("refuse",))
+    gu, dn = layer.tensors
+    r = binding.Router(8, 2)
+    l, x = _inputs(3, 8, 96, ("refuse",))
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.mx4_moe(r, gu, dn, l, x.repeat(1, 2)[:, :96])
+    with pytest.raises(ValueError, match="x must be"):
+        binding.mx4_moe(r, gu, dn, l, x[:2])
+    with pytest.raises(ValueError, match="x must be"):
+        binding.mx4_moe(r, gu, dn, l, x.float())
+    with pytest.raises(ValueError, match="must be"):
+        binding.mx4_moe(r, dn, gu, l, x)
+    with pytest.raises(ValueError, match="ids must"):
+        binding.mx4_moe(r, gu, dn, l, x, ids=torch.empty(3, 3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="y must"):
+        binding.mx4_moe(r, gu, dn, l, x, y=torch.empty(3, 97, device="cuda"))
+    with pytest.raises(binding.VQError, match="outside"):
+        binding.mx4_moe(r, gu, dn, l.repeat(22, 1), x.repeat(22, 1))
+    with pytest.raises(binding.VQError, match="workspace has"):
+        binding.mx4_moe(r, gu, dn, l, x, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    y, ids, weights = binding.mx4_moe(r, gu, dn, l[:0], x[:0])
+    assert y.shape == (0, 96) and ids.shape == weights.shape == (0, 2)
+
+
+@pytest.mark.parametrize("T", [2, 12])
+def test_graphs_in_turn_on_one_workspace(T):
+    """Two layers captured with the same workspace, replayed one after the other."""
+    import torch
+    from vq_dequant_matmul_gemv_amd import binding
+    layers = [Layer(16, 160, 96, ("shared", k)) for k in range(2)]
+    r = binding.Router(16, 4)
+    l, x = _inputs(T, 16, 160, ("shared", T))
+    ws = torch.full((binding.LIB.vq_mx4_moe_workspace_bytes(T, 4, 160, 96),), 0xff, dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for layer in layers:
+        binding.mx4_moe(r, *layer.tensors, l, x, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(binding.mx4_moe(r, *layer.tensors, l, x, workspace=ws))
+        graphs.append(graph)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    for _ in range(4):
+        l.copy_(torch.randn(l.shape, device="cuda", generator=g))
+        x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for layer, out in zip(layers, outs):
+            assert all(torch.equal(a, b) for a, b in zip(out, binding.mx4_moe(r, *layer.tensors, l, x)))
+        ws.fill_(0xff)

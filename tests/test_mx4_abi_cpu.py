@@ -238,5 +238,10 @@ def test_wrappers_refuse_before_the_library(b):
         b.mx4_gemm(b.MX4Tensor(u8(64, 64), u8(64, 2)), u8(3, 64), u8(3, 4))
     with pytest.raises(ValueError, match="must be .*uint8"):
         b.mx4_gemm(b.MX4Tensor(torch.zeros(64, 64), u8(64, 4)), u8(3, 64), u8(3, 4))
+    many = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device="meta")  # noqa: E731
+    with pytest.raises(ValueError, match="at most 2"):
+        b.mx4_quant(many(1 << 32, 32, dtype=torch.float16))
+    with pytest.raises(ValueError, match="at most 2"):
+        b.mx4_dequant(many(1 << 32, 16, dtype=torch.uint8), many(1 << 32, 1, dtype=torch.uint8))
     assert b.mx4_quant.__doc__ and b.mx4_moe.__doc__
     assert ctypes.sizeof(b.CMX4Tensor) == len(b._pack_mx4(1, 2, 3, 4, 5, 0, 7, 8))

@@ -743,6 +743,13 @@ def _mx4_bytes(t, what, scales=False):
         raise ValueError(f"{what} must be {own} or uint8, got {t.dtype}")
 
 
+def _mx4_tokens(T):
+    """The token count of a 4-bit call: the library's argument has 32 bits."""
+    if T >> 31:
+        raise ValueError(f"{T} rows: at most 2^31 - 1")
+    return T
+
+
 @dataclass
 class MX4Tensor:
     """Device-resident 4-bit weight or stack of experts (see `vq_mx4_tensor` in
@@ -793,7 +800,7 @@ def mx4_quant(x, q=None, scales=None, stream=None):
     code = _dtype_code(x.dtype)
     if x.dim() != 2 or x.shape[1] % 32 != 0:
         raise ValueError("x must be [T][cols] with cols a multiple of 32")
-    T, cols = x.shape
+    T, cols = _mx4_tokens(x.shape[0]), x.shape[1]
     gpu = _gpu(x)
     dev = x.device
     if q is not None:
@@ -824,7 +831,7 @@ def mx4_dequant(q, scales, dtype=None, y=None, stream=None):
     _mx4_bytes(scales, "scales", scales=True)
     if q.dim() != 2 or q.shape[1] % 16 != 0:
         raise ValueError("q must be [T][cols/2] with cols a multiple of 32")
-    T, cols = q.shape[0], 2 * q.shape[1]
+    T, cols = _mx4_tokens(q.shape[0]), 2 * q.shape[1]
     if scales.shape != (T, cols // 32):
         raise ValueError(f"scales must be {(T, cols // 32)}")
     dtype = y.dtype if (y is not None and dtype is None) else (dtype or torch.bfloat16)
@@ -865,7 +872,7 @@ def mx4_gemm(w: MX4Tensor, x, x_scales=None, y=None, workspace=None, stream=None
         _mx4_bytes(x_scales, "x_scales", scales=True)
     if x.dim() != 2 or x.shape[1] != (cols if half else cols // 2):
         raise ValueError(f"x must be [T][{cols}] in 16 bits, or [T][{cols // 2}] bytes of 4-bit values")
-    T = x.shape[0]
+    T = _mx4_tokens(x.shape[0])
     if not half and x_scales.shape != (T, cols // 32):
         raise ValueError(f"x_scales must be {(T, cols // 32)}")
     if epilogue not in EPILOGUES or epilogue == "combine":
