@@ -332,7 +332,7 @@ def test_same_bits_again_other_stream_and_captured(x, T, R, C):
 
 
 @pytest.mark.parametrize("splits", [1, 3])
-@pytest.mark.parametrize("kernel", range(22))
+@pytest.mark.parametrize("kernel", range(24))
 def test_every_kernel_and_split(kernel, splits, monkeypatch):
     """Every row of the table on tiles that end in the middle, whatever the
     planner would choose."""

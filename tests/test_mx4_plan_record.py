@@ -12,7 +12,7 @@ def test_the_tables_choices_are_near_the_best_measured_ones():
     fit = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fit)
     table, measured = fit.kernels(), fit.calls()
-    assert len(table) == 22 and all(len(k.constants) == 7 for k in table)
+    assert len(table) == 24 and all(len(k.constants) == 7 for k in table)
     assert sum(len(v) for v in measured.values()) > 7000
     for x in ("mx4", "x16"):
         part = fit.losses(table, {k: v for k, v in measured.items() if k[0] == x})

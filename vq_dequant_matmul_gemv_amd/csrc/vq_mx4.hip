@@ -653,10 +653,10 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   else run_skinny<kMx4XBF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 21146
+// The kernels of the product and a time model of each (us), fitted to 22944
 // measured calls (1 to 4096 tokens, 32 to 17408 rows, 224 to 17408 columns, 1 to
 // 24 splits), the faster ones of a shape weighing more.  The model's choice takes
-// 0.6 % longer than the best one on average, 0.4 % above 20 us (the calls and the
+// 0.6 % longer than the best one on average, also above 20 us (the calls and the
 // fit: profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py):
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
@@ -673,29 +673,31 @@ struct Mx4Kernel {
 };
 const Mx4Kernel kMx4Kernels[] = {
     // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
-    {16, 8, 4, 8, true, 2.83f, 0.00224f, 0.133f, 5.63f, 1.24f, 0.378f, 0.411f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 2.66f, 0.121f, 0.136f, 5.19f, 0.826f, 0.549f, 0.525f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 2.81f, 0.00476f, 0.294f, 5.12f, 0.823f, 0.558f, 0.0467f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 2.45f, 0.327f, 0.198f, 4.26f, 0.278f, 0.321f, 0.376f, run_tile<4, 1, 2, 2, 1>},
-    {128, 64, 2, 32, true, 1.79f, 0.3f, 0.547f, 4.47f, 0.235f, 2.76f, 0.325f, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 2.15f, 0.0116f, 0.48f, 6.33f, 0.05f, 3.19f, 1.11f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 4.52f, 0.342f, 0.296f, 7.55f, 0.341f, 0.117f, 0.982f, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 3.94f, 0.353f, 0.379f, 6.34f, 0.225f, 0.0136f, 0.342f, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 3.93f, 0.333f, 0.598f, 6.93f, 0.2f, 1.92f, 0.892f, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 3.5f, 0.268f, 0.7f, 7.55f, 0.177f, 3.62f, 1.2f, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 4.46f, 0, 0.813f, 7.88f, 0.168f, 4.25f, 1.2f, run_tile<4, 2, 4, 8, 1>},
+    {16, 8, 4, 8, true, 2.71f, 0.0972f, 0.123f, 5.37f, 1.21f, 0.435f, 0.617f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 2.59f, 0, 0.146f, 5.2f, 0.839f, 0.593f, 0.432f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 2.9f, 0.0029f, 0.221f, 5.06f, 0.631f, 0.761f, 0.952f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 2.57f, 0.296f, 0.19f, 4.24f, 0.29f, 0.249f, 0.69f, run_tile<4, 1, 2, 2, 1>},
+    {128, 32, 2, 32, true, 2.03f, 0, 0.427f, 3.97f, 0.278f, 1.45f, 1.2f, run_tile<4, 1, 2, 2, 2>},
+    {128, 64, 2, 32, true, 1.48f, 0.292f, 0.538f, 4.1f, 0.221f, 2.88f, 0.515f, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 1.69f, 0.00471f, 0.497f, 4.84f, 0.0718f, 3.17f, 0.435f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 3.3f, 0.417f, 0.28f, 5.49f, 0.278f, 0.779f, 0.635f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 3.89f, 0.362f, 0.378f, 6.15f, 0.227f, 0, 0.392f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 3.84f, 0.34f, 0.598f, 6.6f, 0.201f, 2.01f, 0.816f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 3.53f, 0.267f, 0.702f, 7.71f, 0.181f, 3.59f, 1.2f, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 4.46f, 0, 0.812f, 7.77f, 0.17f, 4.28f, 1.2f, run_tile<4, 2, 4, 8, 1>},
     // 16-bit x: the same
-    {16, 2, 4, 8, false, 2.89f, 0.196f, 0.135f, 5.8f, 2, 0.351f, 0.436f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 2.9f, 0.185f, 0.188f, 6.29f, 1.49f, 0.346f, 0.221f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 2.99f, 0.167f, 0.226f, 6.11f, 0.765f, 0.449f, 0.306f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.52f, 0.365f, 0.38f, 4.52f, 0.782f, 0.906f, 0.292f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1.78f, 0, 0.672f, 3, 0.883f, 2.33f, 0.213f, run_skinny16<8, 2, 8, 1>},
-    {64, 32, 4, 16, false, 2.4f, 0, 1.18f, 3.86f, 0.406f, 1.59f, 0.0345f, run_tile16<2, 1, 2, 2, 4>},
-    {64, 32, 2, 8, false, 3.27f, 0.682f, 0.463f, 3.12f, 0.385f, 0.142f, 0.0558f, run_tile16<2, 1, 2, 2, 2>},
-    {128, 32, 2, 8, false, 3, 0.833f, 0.787f, 3.35f, 0.304f, 0.584f, 0.0403f, run_tile16<4, 1, 2, 2, 2>},
-    {128, 64, 2, 8, false, 2.22f, 0.76f, 1.21f, 3.54f, 0.304f, 2.16f, 0, run_tile16<4, 1, 2, 4, 2>},
-    {128, 64, 1, 4, false, 3.07f, 0.724f, 0.611f, 3.47f, 0.265f, 0.186f, 0, run_tile16<4, 2, 2, 2, 1>},
-    {256, 128, 1, 4, false, 2.87f, 1.17f, 1.58f, 3.82f, 0.198f, 3.11f, 0, run_tile16<4, 2, 4, 4, 1>},
+    {16, 2, 4, 8, false, 2.77f, 0.2f, 0.118f, 5.99f, 2, 0.405f, 0.997f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 2.82f, 0.194f, 0.171f, 5.16f, 1.57f, 0.416f, 0.158f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 2.86f, 0.251f, 0.146f, 4.23f, 0.932f, 0.661f, 0.297f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.17f, 0.343f, 0.374f, 4.09f, 0.516f, 1.45f, 0.223f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 1.48f, 0, 0.73f, 3.47f, 0.989f, 2.5f, 0.256f, run_skinny16<8, 2, 8, 1>},
+    {64, 16, 4, 16, false, 2.87f, 0.408f, 0.782f, 3.77f, 0.449f, 0.317f, 0.242f, run_tile16<2, 1, 2, 1, 4>},
+    {64, 32, 4, 16, false, 1.76f, 0.694f, 1.11f, 3.76f, 0.46f, 1.98f, 0.0669f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 3.1f, 0.681f, 0.466f, 3.08f, 0.328f, 0.362f, 0.0662f, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 2.95f, 0.817f, 0.787f, 3.16f, 0.295f, 0.63f, 0, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 1.87f, 0.838f, 1.22f, 3.59f, 0.282f, 2.48f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.13f, 0.737f, 0.604f, 3.43f, 0.273f, 0.129f, 0, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 2.86f, 1.18f, 1.58f, 3.9f, 0.197f, 3.24f, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
