@@ -4,8 +4,8 @@
     python3 profiles/mx4_plan_fit.py --fit      # the constants fitted anew, and what their choices lose
 
 Reads the measured calls (mx4_product_calls.txt beside this file) and the table `kMx4Kernels` in csrc/vq_mx4.hip.
-A call's time is that of the calls captured into one graph, the median of three replays, with bf16 y, over weights
-that rotate through 400 MB (64 weights at most).
+A call's time is that of the calls captured into one graph, the median of three replays, with bf16 y: the geometric
+mean of one over weights that rotate through 400 MB (64 weights at most) and of one over two weights in turn.
 """
 
 import collections
@@ -91,7 +91,7 @@ def report(table, measured):
               f"above 20 us: {len(big)}, mean {big.mean():.4f}")
 
 
-def fit(table, measured, rounds=60):
+def fit(table, measured, rounds=40):
     """The table with constants fitted to the calls, the faster ones of a shape weighing more; after each round the
     calls of wrong choices gain weight, and the round with the least loss stays."""
     from scipy.optimize import least_squares

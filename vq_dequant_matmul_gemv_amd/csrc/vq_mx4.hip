@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t top) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(256) void vq_mx4_quant_kernel(const void* x, uint32_t* q, uint8_t* scales, int64_t pieces) {
+__global__ __launch_bounds__(256) void vq_mx4_quant_kernel(const void* x, uint32_t* q, uint8_t* scales,
+                                                           int64_t pieces) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;  // piece of 8 values
   const bool in = p < pieces;                                 // (a multiple of 4)
   u32x4 raw[2];
@@ -253,8 +254,8 @@ __device__ __forceinline__ bool join_groups(float4_t (&acc)[MT][NT], int group, 
 // fill the card otherwise (128 tokens of 5120 x 5120: 17.3 us with splits that a
 // second launch joins, 13.5 with two groups)
 //
-// 2048 tokens of 17408 x 5120 with SwiGLU take 115 us, 3.2 PF/s; 4096 of 8192 x
-// 8192 138 us, 4.0 PF/s.  Bound by the matrix instructions at the card's power
+// 2048 tokens of 17408 x 5120 with SwiGLU take 114 to 123 us, 3.0 to 3.2 PF/s;
+// 4096 of 8192 x 8192 139 to 150 us, 3.7 to 3.9 PF/s.  Bound by the matrix instructions at the card's power
 // limit: of 155 us that the latter took before the last steps, they alone ran
 // 104; without the writes to LDS it took 124, without the loads 138.  Loads straight into LDS,
 // three steps ahead, were slower: a block on its own took 141 us where this
@@ -326,7 +327,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_ti
   const uint32_t sc_off = sc_skew + sc_row * blocks + b0;
   const bool sc_live = sc_row < sc_rows;
   int sc_left = (int)(b1 - b0);  // scales from the next ones to be written on
-  asm("" : "+v"(sc_left));       // in vector registers: scalar compares keep the compiler from interleaving what follows
+  // (in vector registers: scalar compares keep the compiler from interleaving what follows)
+  asm("" : "+v"(sc_left));
   uint32_t stage_s[5];
   auto load_scales = [&](uint32_t v) VQMI_INLINE {
     const uint32_t off = sc_live ? (sc_off + v * 16) & ~3u : kOutOfRange;
@@ -476,7 +478,7 @@ __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_ti
 // 61 tokens of 5121 x 4096 take 15 us, bound by the latency of a step: LDS
 // reads, conversions and 16 matrix instructions one after the other in a wave,
 // of which four groups of waves overlap some (17.4 us in one, with splits).
-// 2048 tokens of 17408 x 5120 take 363 us, 1.0 PF/s, bound by the LDS traffic of
+// 2048 tokens of 17408 x 5120 take 362 to 378 us, 1.0 PF/s, bound by the LDS traffic of
 // 16-bit x beside the matrix instructions.
 // ---------------------------------------------------------------------------
 template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int KW>
@@ -503,7 +505,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Arg
   const int r0 = rt * kTileRows, t0 = tt * kTileTokens;
   const int rows = min(kTileRows, a.rows - r0), toks = min(kTileTokens, a.T - t0);
   const rsrc_t wr = make_rsrc(a.w + (int64_t)r0 * blocks * 16, (uint64_t)rows * blocks * 16);
-  const rsrc_t xr = make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * 64, (uint64_t)toks * blocks * 64);
+  const rsrc_t xr =
+      make_rsrc(static_cast<const uint8_t*>(a.x) + (int64_t)t0 * blocks * 64, (uint64_t)toks * blocks * 64);
   const int wm = wave / WN * 16 * MT, wn = wave % WN * 16 * NT;
   const uint32_t s0 = blockIdx.y * a.split_blocks, s1 = min(blocks, s0 + a.split_blocks);
   const uint32_t steps = ((s1 - s0 + 3) / 4 + KW - 1) / KW;  // of each group
@@ -511,7 +514,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Arg
 
   // 16-byte pieces change places within a row (w: piece ^ row / 2 of 4, x: piece
   // ^ token of 16), so reads of 16 rows touch all banks.
-  const uint32_t w_row = wave * 16 + (lane >> 2), w_piece = lane & 3, x_row = wave * 4 + (lane >> 4), x_piece = lane & 15;
+  const uint32_t w_row = wave * 16 + (lane >> 2), w_piece = lane & 3;
+  const uint32_t x_row = wave * 4 + (lane >> 4), x_piece = lane & 15;
   u32x4 sw[kWLoads], sx[kXLoads];  // the step on its way
   uint32_t ss[2];
   // scales of row threadIdx.x, as the two aligned words that a step's four lie in
@@ -528,7 +532,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Arg
       sw[i] = buf_load_b128(wr, bw < b1 ? ((w_row + i * 16 * kWaves) * blocks + bw) * 16 : kOutOfRange);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      sx[i] = buf_load_b128(xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
+      sx[i] = buf_load_b128(
+          xr, bx < b1 ? ((x_row + i * 4 * kWaves) * blocks + b0 + s * 4) * 64 + x_piece * 16 : kOutOfRange);
     const uint32_t off = (sc_off + s * 4) & ~3u;
     ss[0] = buf_load_b32(sr, off);
     ss[1] = buf_load_b32(sr, off + 4);
@@ -585,7 +590,8 @@ __global__ __launch_bounds__(64 * WM * WN * KW) void vq_mx4_tile16_kernel(Mx4Arg
       for (int i = 0; i < 4; ++i) {
         u32x4 v[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const u32x4*>(xb + n * 16 * 256 + (((4 * g + i) ^ r) * 16));
+        for (int n = 0; n < NT; ++n)
+          v[n] = *reinterpret_cast<const u32x4*>(xb + n * 16 * 256 + (((4 * g + i) ^ r) * 16));
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint32_t c = i == 0 ? q[m].x : i == 1 ? q[m].y : i == 2 ? q[m].z : q[m].w;
@@ -637,14 +643,16 @@ void run_tile(const Mx4Args& a, int, int splits, hipStream_t s) {
 
 template <int WM, int WN, int MT, int NT, int KW>
 void run_tile16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits), block(64 * WM * WN * KW);
-  if (xk == kMx4XF16) {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, true, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XF16, false, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
-  } else {
-    if (a.y_kind == kOutF32) hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, true, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((vq_mx4_tile16_kernel<kMx4XBF16, false, WM, WN, MT, NT, KW>), grid, block, 0, s, a);
-  }
+  const dim3 grid((unsigned)ceil_div(a.rows, 16 * MT * WM) * ceil_div(a.T, 16 * NT * WN), splits);
+  const dim3 block(64 * WM * WN * KW);
+  auto run = [&](auto kind, auto precise) {
+    hipLaunchKernelGGL((vq_mx4_tile16_kernel<decltype(kind)::value, decltype(precise)::value, WM, WN, MT, NT, KW>), grid,
+                       block, 0, s, a);
+  };
+  const std::integral_constant<int, kMx4XF16> f16{};
+  const std::integral_constant<int, kMx4XBF16> bf16{};
+  if (a.y_kind == kOutF32) xk == kMx4XF16 ? run(f16, std::true_type{}) : run(bf16, std::true_type{});
+  else xk == kMx4XF16 ? run(f16, std::false_type{}) : run(bf16, std::false_type{});
 }
 
 template <int WAVES, int MT, int NL, int DEPTH>
@@ -653,11 +661,13 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   else run_skinny<kMx4XBF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 22944
+// The kernels of the product and a time model of each (us), fitted to 22908
 // measured calls (1 to 4096 tokens, 32 to 17408 rows, 224 to 17408 columns, 1 to
-// 24 splits), the faster ones of a shape weighing more.  The model's choice takes
-// 0.6 % longer than the best one on average, also above 20 us (the calls and the
-// fit: profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py):
+// 24 splits; the geometric means of a call's times with its weight in memory and
+// in the card's cache), the faster ones of a shape weighing more.  The model's
+// choice takes 1.3 % longer than the best one on average with 4-bit x, 0.8 % with
+// 16-bit x, 0.2 % above 20 us (the calls and the fit:
+// profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py):
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, 2 + join * (bytes of the planes, written and read, in MB)
 // with steps of 128 columns a wave runs through, rounds of 256 blocks, and
@@ -673,31 +683,31 @@ struct Mx4Kernel {
 };
 const Mx4Kernel kMx4Kernels[] = {
     // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
-    {16, 8, 4, 8, true, 2.71f, 0.0972f, 0.123f, 5.37f, 1.21f, 0.435f, 0.617f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 2.59f, 0, 0.146f, 5.2f, 0.839f, 0.593f, 0.432f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 2.9f, 0.0029f, 0.221f, 5.06f, 0.631f, 0.761f, 0.952f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 2.57f, 0.296f, 0.19f, 4.24f, 0.29f, 0.249f, 0.69f, run_tile<4, 1, 2, 2, 1>},
-    {128, 32, 2, 32, true, 2.03f, 0, 0.427f, 3.97f, 0.278f, 1.45f, 1.2f, run_tile<4, 1, 2, 2, 2>},
-    {128, 64, 2, 32, true, 1.48f, 0.292f, 0.538f, 4.1f, 0.221f, 2.88f, 0.515f, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 1.69f, 0.00471f, 0.497f, 4.84f, 0.0718f, 3.17f, 0.435f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 3.3f, 0.417f, 0.28f, 5.49f, 0.278f, 0.779f, 0.635f, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 3.89f, 0.362f, 0.378f, 6.15f, 0.227f, 0, 0.392f, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 3.84f, 0.34f, 0.598f, 6.6f, 0.201f, 2.01f, 0.816f, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 3.53f, 0.267f, 0.702f, 7.71f, 0.181f, 3.59f, 1.2f, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 4.46f, 0, 0.812f, 7.77f, 0.17f, 4.28f, 1.2f, run_tile<4, 2, 4, 8, 1>},
+    {16, 8, 4, 8, true, 3.68f, 0.126f, 0.0852f, 6.71f, 0.54f, 0.417f, 0.886f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 3.45f, 0.132f, 0.0926f, 6.02f, 0.423f, 0.636f, 0.719f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 3.57f, 0.15f, 0.177f, 5.6f, 0.514f, 0.813f, 0.791f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 3.24f, 0.249f, 0.186f, 5.14f, 0.274f, 0.401f, 0, run_tile<4, 1, 2, 2, 1>},
+    {128, 32, 2, 32, true, 2.2f, 0.00304f, 0.4f, 4.98f, 0.246f, 2.01f, 1.03f, run_tile<4, 1, 2, 2, 2>},
+    {128, 64, 2, 32, true, 2.32f, 0.00284f, 0.449f, 5.03f, 0.215f, 2.91f, 0.696f, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 2.16f, 0.0117f, 0.374f, 5.14f, 0.168f, 3.25f, 0.686f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 3.79f, 0.368f, 0.247f, 7.9f, 0.259f, 1.05f, 0.781f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 4.58f, 0.303f, 0.347f, 6.88f, 0.197f, 0.25f, 0.562f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 3.6f, 0, 0.534f, 7.08f, 0.187f, 3.08f, 1.2f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 3.71f, 0, 0.657f, 6.89f, 0.166f, 4.12f, 1.2f, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 4.23f, 0, 0.788f, 7.34f, 0.161f, 4.98f, 1.2f, run_tile<4, 2, 4, 8, 1>},
     // 16-bit x: the same
-    {16, 2, 4, 8, false, 2.77f, 0.2f, 0.118f, 5.99f, 2, 0.405f, 0.997f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 2.82f, 0.194f, 0.171f, 5.16f, 1.57f, 0.416f, 0.158f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 2.86f, 0.251f, 0.146f, 4.23f, 0.932f, 0.661f, 0.297f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.17f, 0.343f, 0.374f, 4.09f, 0.516f, 1.45f, 0.223f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1.48f, 0, 0.73f, 3.47f, 0.989f, 2.5f, 0.256f, run_skinny16<8, 2, 8, 1>},
-    {64, 16, 4, 16, false, 2.87f, 0.408f, 0.782f, 3.77f, 0.449f, 0.317f, 0.242f, run_tile16<2, 1, 2, 1, 4>},
-    {64, 32, 4, 16, false, 1.76f, 0.694f, 1.11f, 3.76f, 0.46f, 1.98f, 0.0669f, run_tile16<2, 1, 2, 2, 4>},
-    {64, 32, 2, 8, false, 3.1f, 0.681f, 0.466f, 3.08f, 0.328f, 0.362f, 0.0662f, run_tile16<2, 1, 2, 2, 2>},
-    {128, 32, 2, 8, false, 2.95f, 0.817f, 0.787f, 3.16f, 0.295f, 0.63f, 0, run_tile16<4, 1, 2, 2, 2>},
-    {128, 64, 2, 8, false, 1.87f, 0.838f, 1.22f, 3.59f, 0.282f, 2.48f, 0, run_tile16<4, 1, 2, 4, 2>},
-    {128, 64, 1, 4, false, 3.13f, 0.737f, 0.604f, 3.43f, 0.273f, 0.129f, 0, run_tile16<4, 2, 2, 2, 1>},
-    {256, 128, 1, 4, false, 2.86f, 1.18f, 1.58f, 3.9f, 0.197f, 3.24f, 0, run_tile16<4, 2, 4, 4, 1>},
+    {16, 2, 4, 8, false, 3.68f, 0.205f, 0.106f, 7.28f, 1.16f, 0.331f, 1.2f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 3.56f, 0.206f, 0.128f, 6.06f, 0.381f, 0.496f, 0.425f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 3.57f, 0.251f, 0.167f, 6.2f, 0.286f, 0.633f, 0.336f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.68f, 0.378f, 0.349f, 5, 0.331f, 1.54f, 0.273f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 1.93f, 0.009f, 0.668f, 4.01f, 0.684f, 2.67f, 0.261f, run_skinny16<8, 2, 8, 1>},
+    {64, 16, 4, 16, false, 3.47f, 0.471f, 0.669f, 4.18f, 0.41f, 0.497f, 0.163f, run_tile16<2, 1, 2, 1, 4>},
+    {64, 32, 4, 16, false, 2.39f, 0.385f, 1.03f, 4.1f, 0.414f, 2.05f, 0.119f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 3.64f, 0.647f, 0.457f, 3.79f, 0.299f, 0.502f, 0, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 3.43f, 0.75f, 0.736f, 3.79f, 0.26f, 0.889f, 0, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 2.46f, 0.827f, 1.16f, 4.18f, 0.268f, 2.51f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.79f, 0.663f, 0.564f, 3.5f, 0.244f, 0.204f, 0, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 4.14f, 1, 1.56f, 3.75f, 0.2f, 2.31f, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
@@ -819,7 +829,8 @@ hipError_t launch_mx4_gemm(const Mx4View& w, const IoSpec& io, const Mx4Plan& p,
   kMx4Kernels[p.kernel].run(a, x_kind, p.splits, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(vq_mx4_join_kernel, dim3((unsigned)ceil_div((int64_t)T * w.rows, 1024)), dim3(256), 0, s, a, p.splits);
+  const dim3 grid((unsigned)ceil_div((int64_t)T * w.rows, 1024));
+  hipLaunchKernelGGL(vq_mx4_join_kernel, grid, dim3(256), 0, s, a, p.splits);
   return hipGetLastError();
 }
 

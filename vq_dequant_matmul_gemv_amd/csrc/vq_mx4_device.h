@@ -112,14 +112,16 @@ template <int XK, bool FIT>
 __device__ __forceinline__ float4_t mx4_mfma16(uint32_t codes, float scale, u32x4 x, float4_t acc) {
   if constexpr (XK == kMx4XF16) {
     if constexpr (FIT)
-      return __builtin_amdgcn_mfma_f32_16x16x32_f16(mx4_half(codes, scale), __builtin_bit_cast(half8_t, x), acc, 0, 0, 0);
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(mx4_half(codes, scale), __builtin_bit_cast(half8_t, x), acc, 0, 0,
+                                                    0);
     const bf16x8_t a = mx4_bf16(codes, scale);
     bf16x8_t hi, lo;
     mx4_split_half(x, &hi, &lo);
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, acc, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, acc, 0, 0, 0);
   } else {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx4_bf16(codes, scale), __builtin_bit_cast(bf16x8_t, x), acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx4_bf16(codes, scale), __builtin_bit_cast(bf16x8_t, x), acc, 0, 0,
+                                                   0);
   }
 }
 
@@ -217,7 +219,8 @@ struct Mx4Stream {
     const bool in_w = b + (lane & 7) < end;
     const rsrc_t wr = make_rsrc(src.w, src.w_bytes), wsr = make_rsrc(src.ws, src.ws_bytes);
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) w[j][i] = buf_load_b128(wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
+    for (int i = 0; i < 2 * MT; ++i)
+      w[j][i] = buf_load_b128(wr, in_w ? woff[i] + b * 16 + (lane & 7) * 16 : kOutOfRange);
 #pragma unroll
     for (int i = 0; i < MT; ++i) ws[j][i] = buf_load_b32(wsr, (src.wsoff[i] & ~3u) + k * 8);
     const uint32_t piece = XK == kMx4XMx4 ? lane & 7 : lane & 31;  // of 16 bytes
@@ -344,7 +347,7 @@ struct Mx4Stream {
         put(j, cur, k, lane);
         __builtin_amdgcn_sched_barrier(0);
         load(j, src, last ? from + j * stride : k + DEPTH * stride, lane);
-        __builtin_amdgcn_sched_barrier(0);  // the loads stay in their order, so that the next ones' wait leaves these in flight
+        __builtin_amdgcn_sched_barrier(0);  // the loads in their order: the next ones' wait leaves these in flight
         wave_lds_fence();
         if (k < steps) dot(acc, lane);
         wave_lds_fence();

@@ -9,8 +9,8 @@
 // Bound by the bytes of the experts that the tokens hit, so an expert's weights
 // are read once for a group of the pairs (token and slot) that chose it, which
 // are the columns of its matrix products.  256 experts, top 8, of 4096 x 1024:
-// 64 tokens that hit 182 of them (1.2 GB) take 290 us, 16 that hit 90 138 us,
-// 4.2 to 4.4 TB/s of a copy's 5.2; one token (53 MB) 21.5 us: 12 of gate and up
+// 64 tokens that hit 182 of them (1.2 GB) take 277 to 295 us, 16 that hit 90 136
+// to 141, 4.1 to 4.4 TB/s of a copy's 5.2; one token (53 MB) 21.5 us: 12 of gate and up
 // with the routing, 8 of down, each launch's latency and ramp beside 7 and 3.5
 // us of bytes.
 //
