@@ -508,8 +508,7 @@ vq_status vq_fp8_gemm_fast(const vq_fp8_tensor *w, const vq_io *io, const uint8_
  * a positive multiple of 32, at most 2^20; num_experts >= 1 (else
  * VQ_ERR_SHAPE).  value_bytes == E * rows * cols / 2 and scale_bytes == E *
  * rows * cols / 32, so a short or sliced buffer is refused.  values 16-byte
- * aligned; scales anywhere (4-byte aligned scales with cols a multiple of 128
- * are read in whole words, which is faster).
+ * aligned; scales anywhere.
  * Activations: x [T][cols/2] with x_scales [T][cols/32], as vq_mx4_quant leaves
  * them.
  */
