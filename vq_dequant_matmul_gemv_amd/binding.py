@@ -515,6 +515,14 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
+def _size(n, what="rows"):
+    """A size of a call: the library's arguments have 32 bits, and ctypes cuts
+    what does not fit."""
+    if n >> 31:
+        raise ValueError(f"{n} {what}: at most 2^31 - 1")
+    return n
+
+
 def _rows(T, cols, dtype, device):
     """An uninitialised [T][cols] (empty_strided takes a quarter less time than
     empty, which parses its sizes)."""
@@ -565,7 +573,7 @@ def _check_route(r, logits, ids, weights):
     shape = logits.shape
     if len(shape) != 2 or shape[1] != r.num_experts:
         raise ValueError(f"logits must be [T][{r.num_experts}]")
-    T, k = shape[0], r.top_k
+    T, k = _size(shape[0]), r.top_k
     gpu = _gpu(logits)
     bias = 0
     if r.bias is not None:
@@ -662,7 +670,7 @@ def fp8_quant(x, q=None, scales=None, stream=None):
     torch = _torch()
     if x.dtype not in (torch.float16, torch.bfloat16) or x.dim() != 2:
         raise ValueError("x must be fp16 or bf16 [T][cols]")
-    T, cols = x.shape
+    T, cols = _size(x.shape[0]), _size(x.shape[1], "columns")
     gpu = _gpu(x)
     dev = x.device
     sshape = (T, _blocks(cols))
@@ -697,7 +705,7 @@ def fp8_gemm(w: FP8Tensor, x, x_scales, y=None, workspace=None, stream=None, y_d
     v, ws = w.values, w.scales
     if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.dim() != 2 or x.shape[1] != cols:
         raise ValueError(f"x must be float8_e4m3fn (or uint8 codes) [T][{cols}]")
-    T = x.shape[0]
+    T = _size(x.shape[0])
     if x_scales.dtype != torch.float32 or x_scales.shape != (T, _blocks(cols)):
         raise ValueError(f"x_scales must be fp32 {(T, _blocks(cols))}")
     if epilogue not in EPILOGUES or epilogue == "combine":
@@ -743,13 +751,6 @@ def _mx4_bytes(t, what, scales=False):
         raise ValueError(f"{what} must be {own} or uint8, got {t.dtype}")
 
 
-def _mx4_tokens(T):
-    """The token count of a 4-bit call: the library's argument has 32 bits."""
-    if T >> 31:
-        raise ValueError(f"{T} rows: at most 2^31 - 1")
-    return T
-
-
 @dataclass
 class MX4Tensor:
     """Device-resident 4-bit weight or stack of experts (see `vq_mx4_tensor` in
@@ -783,6 +784,8 @@ class MX4Tensor:
         if cols % 32 != 0 or s.shape != (*shape[:-1], cols // 32):
             raise ValueError(f"{name}.scales must hold one byte for each 32 columns, {(*shape[:-1], cols / 32)}, got "
                              f"{tuple(s.shape)}")
+        if (experts | rows | cols) >> 31:
+            raise ValueError(f"{name} is {experts} x {rows} x {cols}: at most 2^31 - 1 each")
         gpu = _gpu(v)
         _placed(s, gpu)
         return experts, rows, cols, gpu
@@ -800,7 +803,7 @@ def mx4_quant(x, q=None, scales=None, stream=None):
     code = _dtype_code(x.dtype)
     if x.dim() != 2 or x.shape[1] % 32 != 0:
         raise ValueError("x must be [T][cols] with cols a multiple of 32")
-    T, cols = _mx4_tokens(x.shape[0]), x.shape[1]
+    T, cols = _size(x.shape[0]), _size(x.shape[1], "columns")
     gpu = _gpu(x)
     dev = x.device
     if q is not None:
@@ -831,7 +834,7 @@ def mx4_dequant(q, scales, dtype=None, y=None, stream=None):
     _mx4_bytes(scales, "scales", scales=True)
     if q.dim() != 2 or q.shape[1] % 16 != 0:
         raise ValueError("q must be [T][cols/2] with cols a multiple of 32")
-    T, cols = _mx4_tokens(q.shape[0]), 2 * q.shape[1]
+    T, cols = _size(q.shape[0]), _size(2 * q.shape[1], "columns")
     if scales.shape != (T, cols // 32):
         raise ValueError(f"scales must be {(T, cols // 32)}")
     dtype = y.dtype if (y is not None and dtype is None) else (dtype or torch.bfloat16)
@@ -872,7 +875,7 @@ def mx4_gemm(w: MX4Tensor, x, x_scales=None, y=None, workspace=None, stream=None
         _mx4_bytes(x_scales, "x_scales", scales=True)
     if x.dim() != 2 or x.shape[1] != (cols if half else cols // 2):
         raise ValueError(f"x must be [T][{cols}] in 16 bits, or [T][{cols // 2}] bytes of 4-bit values")
-    T = _mx4_tokens(x.shape[0])
+    T = _size(x.shape[0])
     if not half and x_scales.shape != (T, cols // 32):
         raise ValueError(f"x_scales must be {(T, cols // 32)}")
     if epilogue not in EPILOGUES or epilogue == "combine":
