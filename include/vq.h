@@ -501,7 +501,11 @@ vq_status vq_fp8_gemm_fast(const vq_fp8_tensor *w, const vq_io *io, const uint8_
  * 2, 3, 4, 6 and their negatives: codes 0 to 7, plus 8 for the sign; no
  * infinities, no NaN) with an e8m0 scale for each 32 columns (byte b stands for
  * 2^(b - 127), 255 for NaN).  A value stands for code * scale, a block whose
- * scale is 255 for NaN throughout.
+ * scale is 255 for NaN throughout.  Values of 2^128 and above, which fp32 does
+ * not hold (4 and 6 under byte 253, 2 and above under 254; vq_mx4_quant leaves
+ * at most 252), are infinite to vq_mx4_dequant, and in a weight make products
+ * with 16-bit activations, vq_mx4_moe's included, infinite or NaN; products
+ * with 4-bit activations take them as they are.
  *
  * One tensor or a stack of experts: values [E][rows][cols/2], two codes a byte,
  * the even column in the low half; scales [E][rows][cols/32].  rows >= 1; cols
@@ -536,8 +540,8 @@ typedef struct vq_mx4_tensor {
  *   cols as for vq_mx4_tensor; T >= 0 (0 enqueues nothing), T * cols <= 2^34.
  *
  * vq_mx4_dequant: y[t][c] = code * scale, rounded to y_dtype (F32, F16 or BF16)
- * once: exact in fp32 and bf16, and in fp16 where that can hold it (larger ones
- * become infinite, smaller ones round).  y: device [T][cols], 16-byte aligned.
+ * once: exact in fp32 and bf16 below 2^128, and in fp16 where that can hold it
+ * (larger ones become infinite, smaller ones round).  y: device [T][cols], 16-byte aligned.
  */
 vq_status vq_mx4_quant(const void *x, int32_t x_dtype, int32_t T, int32_t cols, uint8_t *q, uint8_t *scales,
                        void *stream);

@@ -21,11 +21,12 @@
 //   scales, an instruction is off by at most 4 units of 2^-24 of the largest
 //   block sum or accumulator (its products are not cut the way the e4m3
 //   instructions cut theirs).
-//   4-bit x 16-bit: the 4-bit values times their scale are bf16 values, and
-//   fp16 values where the scale is between 2^-23 and 2^13, so one conversion
-//   per pair feeds the 16 x 16 x 32 instructions, whose products are exact.
-//   With fp16 activations, steps that hold another scale take x apart into two
-//   bf16 values instead (11 bits are 8 and 3), and twice the instructions.
+//   4-bit x 16-bit: the 4-bit values times their scale are bf16 values below
+//   2^128 (infinite above), and fp16 values where the scale is between 2^-23
+//   and 2^13, so one conversion per pair feeds the 16 x 16 x 32 instructions,
+//   whose products are exact.  With fp16 activations, steps that hold another
+//   scale take x apart into two bf16 values instead (11 bits are 8 and 3), and
+//   twice the instructions.
 #pragma once
 
 #include "vq_block_device.h"
