@@ -101,25 +101,39 @@ class _Layer:
         return self.gu, self.dn
 
 
+def _eights(pairs, experts, inter):
+    """Items of the gate and up products in groups of 8."""
+    return (pairs + 7 * min(pairs, experts)) // 8 * (inter // 16)
+
+
 @pytest.mark.parametrize("x", ["float16", "bfloat16"])
 @pytest.mark.parametrize("T", [6, 40, 64])
 def test_layer_groups_of_eight_and_grouped_down(T, x):
     """Gate and up by waves of their own with groups of 8 pairs (more than 5
-    tokens, pairs >= experts, experts * inter > 32768): 5 steps of 256 columns;
-    down by groups of 4: 4 steps, the next item's behind them."""
+    tokens, pairs >= experts, 1200 items and more): 5 steps of 256 columns; down
+    by groups of 4: 4 steps, the next item's behind them."""
     from vq_dequant_matmul_gemv_amd import binding
     E, k, H, I = 33, 6, 1056, 1024
-    assert T * k >= E and E * I > 32768
+    assert T * k >= E and _eights(T * k, E, I) >= 1200
     _check(_Layer(E, H, I), binding.Router(E, k), *_inputs(T, E, H, ("eight", T), x), "bfloat16" if T == 40 else "float32")
 
 
-@pytest.mark.parametrize("E,k,T", [(16, 4, 20), (64, 2, 20), (16, 4, 64), (5, 1, 6)])
+@pytest.mark.parametrize("E,k,T", [(16, 4, 20), (64, 2, 20), (6, 2, 64), (5, 1, 6)])
 def test_layer_groups_of_four(E, k, T):
     """More than 5 tokens with pairs < experts, or few items: gate and up by
     blocks whose four waves share 10 steps; down by groups of 4, 3 steps."""
     from vq_dequant_matmul_gemv_amd import binding
     H, I = 2336, 544
-    assert T > 5 and (T * k < E or E * I <= 32768)
+    assert T > 5 and (T * k < E or _eights(T * k, E, I) < 1200)
+    _check(_Layer(E, H, I), binding.Router(E, k), *_inputs(T, E, H, ("four", E, T)))
+
+
+@pytest.mark.parametrize("E,k,T", [(16, 4, 64), (8, 4, 64), (40, 4, 10)])
+def test_layer_groups_of_eight_over_many_steps(E, k, T):
+    """The same with 10 steps of a wave's own, down with 3."""
+    from vq_dequant_matmul_gemv_amd import binding
+    H, I = 2336, 544
+    assert T * k >= E and _eights(T * k, E, I) >= 1200
     _check(_Layer(E, H, I), binding.Router(E, k), *_inputs(T, E, H, ("four", E, T)))
 
 

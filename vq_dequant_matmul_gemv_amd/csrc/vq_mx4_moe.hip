@@ -408,11 +408,14 @@ __global__ __launch_bounds__(64 * WAVES) void vq_mx4_moe_down_kernel(MoeArgs a) 
 // 4 to 5 us and reads an expert again for each further token that chose it.
 // The measured difference is m * (pairs / 20 + again / 3) us less those, for
 // matrices of m MB of which chance has `again` read again.  us, groups -> on
-// their own: 256 experts top 8 of 4096x1024 at 3 tokens 56.4 -> 52.7, 5 68.6 ->
-// 70.4, 16 123 -> 147; of 2048x512 at 3 27.1 -> 22.3, 8 38.2 -> 34.9, 12 41.1
-// -> 41.5; 60 top 4 of 1504x352 at 5 19.7 -> 15.7, 16 24.9 -> 25.3; 8 top 2 of
-// 4096x1792 at 3 27.0 -> 27.2, 4 27.7 -> 30.2.  (A single token has no room
-// for the products in its workspace.)
+// their own: 256 experts top 8 of 4096x1024 at 3 tokens 46.0 -> 41.1, 5 58.3 ->
+// 57.5, 16 118 -> 140; of 2048x512 at 3 25.8 -> 20.5, 8 37.2 -> 33.6, 12 42.7
+// -> 41.2, 16 44.7 -> 48.1; 60 top 4 of 1504x352 at 5 18.4 -> 14.4, 16 24.2 ->
+// 24.6; 8 top 2 of 4096x1792 at 3 25.5 -> 25.8, 4 27.4 -> 30.0; 2 top 1 of
+// 1024x512 at 16 16.3 -> 15.0, 32 17.2 -> 22.4.  Over 13 layers of 2 to 256
+// experts at 2 to 64 tokens the choice takes 0.7 % longer than the better one on
+// average, 15 % at worst (64 top 6 of 2048x1408 at 4: 35.8 -> 31.0, not taken).
+// (A single token has no room for the products in its workspace.)
 bool down_by_token(const MoeArgs& a) {
   const float m = 32.0f * 17.0f * a.hidden_blocks * a.inter_blocks * 1e-6f;
   const float again = 0.5f * a.T * (a.T - 1) * a.top_k * a.top_k / a.experts;
@@ -439,16 +442,23 @@ hipError_t run_layer(const MoeArgs& a, hipStream_t s) {
   // Gate and up by blocks that split the columns, with groups of 2 or 4 pairs,
   // or by waves on their own with twice the rows and groups of 8.  The groups
   // of 2 load least beside the weights (up to 5 tokens); waves on their own
-  // need many items to fill the card, and gain where most experts are chosen
-  // more than once.  us of the layer, groups of 2, 4 and 8: 256 experts top 8
-  // of 4096x1024 at 1 token 24.0, 24.8 and 30.0, at 4 54.7, 55.6 and 59.0, at 8
-  // 81.4, 79.5 and 81.8, at 16 128, 121 and 123, at 32 195, 182 and 175, at 64
-  // 316, 280 and 257; 60 top 4 of 1504x352 (2640 items) at 16 24.6, 23.5 and
-  // 24.7, at 64 38.3, 34.1 and 34.1; 8 top 2 of 4096x1792 (1792) at 16 45.2,
-  // 41.0 and 44.0, at 64 108, 83.8 and 85.7.
+  // need 1200 items or so to fill the card (2048 of them run at once), and gain
+  // where most experts are chosen more than once.  us of the layer, groups of
+  // 4 and 8 (and their items): 8 top 2 of 4096x1792 at 8 tokens 31.7 and 34.6
+  // (1008), at 16 40.8 and 39.7 (1232), at 32 53.4 and 54.5 (1680), at 64 79.0
+  // and 70.3 (2240); 32 top 4 of 1024x512 at 8 15.7 and 16.1 (1024), at 64 31.9
+  // and 26.7 (1920); 4 top 2 of 2048x1024 at 16 21.7 and 23.8 (448), at 64 34.6
+  // and 31.8 (1216); 60 top 4 of 1504x352 at 16 24.1 and 25.2 (1331), at 32 28.3
+  // and 27.5 (1452); 256 top 8 of 4096x1024 at 16 117.9 and 119.9 (pairs <
+  // experts), at 32 173 and 166 (16384), at 64 269 and 244.  Over 13 layers of 2
+  // to 256 experts at 6 to 64 tokens the choice takes 0.4 % longer than the
+  // better one on average, 9 % at worst (8 top 2 of 1024x512 at 64: 736 items,
+  // 22.8 and 20.9).  Groups of 2 and 4 with 256 top 8 of 4096x1024: at 2 tokens
+  // 31.8 and 32.6, at 5 58.8 and 59.4, at 8 79.7 and 79.4, at 16 122 and 118.
+  const int eights = mx4_moe_max_groups(a.pairs, a.experts, 8) * (up / 2);
   if (a.route_kind >= 0) run_products<XK, 4, 1, 1, 2, 4, true>(a, up, s);
   else if (a.T <= kRouteTokens) run_products<XK, 4, 1, 1, 2, 4>(a, up, s);
-  else if (a.pairs < a.experts || a.experts * up <= 4096) run_products<XK, 4, 1, 2, 2, 4>(a, up, s);
+  else if (a.pairs < a.experts || eights < 1200) run_products<XK, 4, 1, 2, 2, 4>(a, up, s);
   else run_products<XK, 1, 2, 4, 2, 2>(a, up, s);
   if (down_by_token(a)) {
     hipLaunchKernelGGL((vq_mx4_moe_down_kernel<8, 2>), dim3(down, a.T), dim3(512), 0, s, a);
