@@ -661,18 +661,18 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
   else run_skinny<kMx4XBF16, WAVES, MT, NL, DEPTH>(a, xk, splits, s);
 }
 
-// The kernels of the product and a time model of each (us), fitted to 22908
-// measured calls (1 to 4096 tokens, 32 to 17408 rows, 224 to 17408 columns, 1 to
-// 24 splits; the geometric means of a call's times with its weight in memory and
-// in the card's cache), the faster ones of a shape weighing more.  The model's
-// choice takes 1.3 % longer than the best one on average with 4-bit x, 0.8 % with
-// 16-bit x, 0.2 % above 20 us (the calls and the fit:
-// profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py):
+// The kernels of the product and a time model of each (us), fitted to measured
+// calls of 1535 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
+// 1 to 24 splits) whose weights come from memory, as those of a pass through a
+// model's layers do.  make_plan's choice takes 0.6 % longer than the shape's best
+// call on average with 4-bit x and 0.5 % with 16-bit x (27 % at worst), on 300
+// further shapes 0.9 and 1.0 % (38 %); the calls, the fit and the same choice
+// replayed: profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py.
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
-//   and, split, 2 + join * (bytes of the planes, written and read, in MB)
+//   and, split, kMx4Split + join * (bytes of the planes, written and read, in MB)
 // with steps of 128 columns a wave runs through, rounds of 256 blocks, and
-// bytes the weight once, y, and `x_share` of the tokens' reads by every row
-// tile (MB; bw in TB/s).
+// bytes the weight once, y, and the tokens once and `x_share` of that for every
+// further row tile (MB; bw in TB/s).
 struct Mx4Kernel {
   int rows, tokens;  // of a block
   int k_waves;       // waves, or groups of them, that split a block's columns
@@ -683,33 +683,35 @@ struct Mx4Kernel {
 };
 const Mx4Kernel kMx4Kernels[] = {
     // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
-    {16, 8, 4, 8, true, 3.68f, 0.126f, 0.0852f, 6.71f, 0.54f, 0.417f, 0.886f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 3.45f, 0.132f, 0.0926f, 6.02f, 0.423f, 0.636f, 0.719f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 3.57f, 0.15f, 0.177f, 5.6f, 0.514f, 0.813f, 0.791f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 3.24f, 0.249f, 0.186f, 5.14f, 0.274f, 0.401f, 0, run_tile<4, 1, 2, 2, 1>},
-    {128, 32, 2, 32, true, 2.2f, 0.00304f, 0.4f, 4.98f, 0.246f, 2.01f, 1.03f, run_tile<4, 1, 2, 2, 2>},
-    {128, 64, 2, 32, true, 2.32f, 0.00284f, 0.449f, 5.03f, 0.215f, 2.91f, 0.696f, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 2.16f, 0.0117f, 0.374f, 5.14f, 0.168f, 3.25f, 0.686f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 3.79f, 0.368f, 0.247f, 7.9f, 0.259f, 1.05f, 0.781f, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 4.58f, 0.303f, 0.347f, 6.88f, 0.197f, 0.25f, 0.562f, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 3.6f, 0, 0.534f, 7.08f, 0.187f, 3.08f, 1.2f, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 3.71f, 0, 0.657f, 6.89f, 0.166f, 4.12f, 1.2f, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 4.23f, 0, 0.788f, 7.34f, 0.161f, 4.98f, 1.2f, run_tile<4, 2, 4, 8, 1>},
+    {16, 8, 4, 8, true, 0.0558f, 0.207f, 0.00666f, 11.3f, 0.109f, 1.21f, 9.59f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 0.698f, 0.21f, 0.102f, 2.86f, 0.156f, 0.914f, 0.496f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 1.86f, 0.252f, 0.231f, 3.81f, 0.551f, 0.747f, 0.508f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 0.454f, 0.512f, 0.0592f, 2.79f, 0.306f, 1.98f, 1.04f, run_tile<4, 1, 2, 2, 1>},
+    {128, 32, 2, 32, true, 0.797f, 0.00304f, 0.552f, 4.22f, 0.355f, 2.58f, 0.0392f, run_tile<4, 1, 2, 2, 2>},
+    {128, 64, 2, 32, true, 0.326f, 0.00284f, 0.614f, 4.11f, 0.207f, 5.8f, 0.139f, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 0.0612f, 0.011f, 0.511f, 3.48f, 0.00766f, 5.2f, 0.156f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 0.943f, 0.5f, 0.327f, 4.76f, 0.00206f, 4.82f, 0.034f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 6.25f, 0.0497f, 0.397f, 12, 0.138f, 0.00495f, 0.0716f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 0.386f, 0, 0.623f, 12, 0.148f, 8.92f, 0.197f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 2.81f, 0, 0.624f, 4.16f, 0.0872f, 11.9f, 0.18f, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 1.03f, 0, 0.876f, 12, 0.152f, 9.55f, 0.106f, run_tile<4, 2, 4, 8, 1>},
     // 16-bit x: the same
-    {16, 2, 4, 8, false, 3.68f, 0.205f, 0.106f, 7.28f, 1.16f, 0.331f, 1.2f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 3.56f, 0.206f, 0.128f, 6.06f, 0.381f, 0.496f, 0.425f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 3.57f, 0.251f, 0.167f, 6.2f, 0.286f, 0.633f, 0.336f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.68f, 0.378f, 0.349f, 5, 0.331f, 1.54f, 0.273f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 1.93f, 0.009f, 0.668f, 4.01f, 0.684f, 2.67f, 0.261f, run_skinny16<8, 2, 8, 1>},
-    {64, 16, 4, 16, false, 3.47f, 0.471f, 0.669f, 4.18f, 0.41f, 0.497f, 0.163f, run_tile16<2, 1, 2, 1, 4>},
-    {64, 32, 4, 16, false, 2.39f, 0.385f, 1.03f, 4.1f, 0.414f, 2.05f, 0.119f, run_tile16<2, 1, 2, 2, 4>},
-    {64, 32, 2, 8, false, 3.64f, 0.647f, 0.457f, 3.79f, 0.299f, 0.502f, 0, run_tile16<2, 1, 2, 2, 2>},
-    {128, 32, 2, 8, false, 3.43f, 0.75f, 0.736f, 3.79f, 0.26f, 0.889f, 0, run_tile16<4, 1, 2, 2, 2>},
-    {128, 64, 2, 8, false, 2.46f, 0.827f, 1.16f, 4.18f, 0.268f, 2.51f, 0, run_tile16<4, 1, 2, 4, 2>},
-    {128, 64, 1, 4, false, 3.79f, 0.663f, 0.564f, 3.5f, 0.244f, 0.204f, 0, run_tile16<4, 2, 2, 2, 1>},
-    {256, 128, 1, 4, false, 4.14f, 1, 1.56f, 3.75f, 0.2f, 2.31f, 0, run_tile16<4, 2, 4, 4, 1>},
+    {16, 2, 4, 8, false, 0.0504f, 0.236f, 0.00547f, 10.2f, 12, 1.35f, 6.73f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 0.632f, 0.257f, 0.164f, 12, 0.299f, 1.05f, 0.0405f, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 0.595f, 0.297f, 0.182f, 5.44f, 0.0073f, 1.33f, 0.609f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.14f, 0.448f, 0.399f, 3.14f, 0.0356f, 1.53f, 0.00237f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 0.00841f, 0.00881f, 1.05f, 3, 1.63f, 2.87f, 0.00793f, run_skinny16<8, 2, 8, 1>},
+    {64, 16, 4, 16, false, 0.0858f, 0.0883f, 1.09f, 12, 0.00789f, 2.09f, 0.0281f, run_tile16<2, 1, 2, 1, 4>},
+    {64, 32, 4, 16, false, 0.0932f, 0.0967f, 1.24f, 7.5f, 0.0701f, 3.54f, 0.027f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 2.14f, 0.88f, 0.456f, 2.52f, 0.094f, 1.48f, 0.0101f, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 0.436f, 0.904f, 0.802f, 12, 0.332f, 3.64f, 0, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 0.177f, 0.128f, 1.24f, 12, 0.00226f, 7.13f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.53f, 0.817f, 0.507f, 3.85f, 0.261f, 0.0311f, 0.242f, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 2.27f, 0.301f, 1.24f, 12, 0.0821f, 11.9f, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
+constexpr float kMx4Split = 4.04f;  // us of the launch that joins a split's planes
+constexpr int kMx4Splits[] = {1, 2, 3, 4, 6, 8, 12};  // (16 and 24 were the best of no shape)
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
 
 // Sizes a plan is for.
@@ -737,21 +739,22 @@ bool set_plan(const Mx4Call& c, int i, int splits, Mx4Plan* p) {
 
 float plan_time(const Mx4Call& c, const Mx4Plan& p) {
   const Mx4Kernel& k = kMx4Kernels[p.kernel];
+  const int row_tiles = ceil_div(c.rows, k.rows);
   const float split_steps = 0.25f * p.split_blocks, load_steps = split_steps / k.k_waves;
-  const int64_t units = (int64_t)ceil_div(c.rows, k.rows) * ceil_div(c.T, k.tokens) * p.splits;
+  const int64_t units = (int64_t)row_tiles * ceil_div(c.T, k.tokens) * p.splits;
   const float out = (float)c.T * c.rows, w = 17.0f * c.rows * c.blocks, x = (c.mx4 ? 17.0f : 64.0f) * c.T * c.blocks;
-  const float bytes = (w + 4.0f * out + k.x_share * x * c.rows / k.rows) * 1e-6f;
+  const float bytes = (w + 4.0f * out + (1.0f + k.x_share * (row_tiles - 1)) * x) * 1e-6f;
   const float a = k.latency * std::ceil(load_steps), b = (float)((units + 255) / 256) * (k.rate * load_steps + k.unit),
               e = bytes / k.bw;
   const float t = k.base + std::sqrt(std::sqrt(a * a * a * a + b * b * b * b + e * e * e * e));
-  return p.splits > 1 ? t + 2.0f + k.join * p.splits * out * 8e-6f : t;
+  return p.splits > 1 ? t + kMx4Split + k.join * p.splits * out * 8e-6f : t;
 }
 
 Mx4Plan make_plan(const Mx4Call& c) {
   Mx4Plan best;
   float best_t = 0.0f;
   for (int i = 0; i < kNumMx4Kernels; ++i) {
-    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
+    for (const int s : kMx4Splits) {
       Mx4Plan p;
       if (!set_plan(c, i, s, &p) || p.splits != s) continue;
       const float t = plan_time(c, p);
