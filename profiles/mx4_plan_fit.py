@@ -6,9 +6,8 @@
 Reads the measured calls (mx4_product_calls.txt beside this file) and the table `kMx4Kernels` with `kMx4Split` and
 `kMx4Splits` in csrc/vq_mx4.hip, and goes through the same candidates as `make_plan` there: a choice that nobody measured
 is an error.  A shape has the times of its calls captured into one graph with bf16 y, each the median of three replays:
-"cold" over weights at distinct places, read once a replay after 640 MB were written over the card's cache, and "warm"
-over two weights in turn.  The model is fitted to the cold ones, which a pass through a model's layers meets, over the
-shapes that are not marked as held out.
+"cold" over weights at distinct places, read once a replay after 640 MB of other data were read, and "warm" over two
+weights in turn.  A pass through a model's layers meets the cold ones.  Shapes marked as held out are not fitted.
 """
 
 import collections
@@ -140,10 +139,12 @@ def report(table, split=None):
                       f"worst {r.max():.2f}" + (f"; above 20 us: {len(big)}, mean {big.mean():.4f}" if len(big) else ""))
 
 
-def fit(table, steps=6000, fidelity=.03):
+def fit(table, steps=5000, fidelity=.03, warm=.5, heavy=4.):
     """The table and the split's cost with the least loss of the choices: gradients of the loss that each shape expects
     when calls are taken with the softmax of their predicted times, which sharpens from 12 to 1.5 %, and `fidelity` of the
-    predictions' own errors.  Calls that are not on record (twice the best and more) count as 4 times."""
+    predictions' own errors.  A call's loss is that of its cold time, what is above 5 % of it four times, and `warm` of
+    that of its warm one, which decides between calls that take nearly the same time with cold weights.  Weights of 2^24
+    values and more count `heavy` times; calls that are not on record (twice the best and more) as 4 times the best."""
     import torch
     times, held = record()
     keys = [key for key in times if key not in held]
@@ -156,6 +157,10 @@ def fit(table, steps=6000, fidelity=.03):
     us = torch.tensor([times[keys[i]].get((k, s), (4 * best[i], 0))[0] for i, k, s in flat], dtype=torch.float64)
     cost = torch.log(us / torch.tensor(best, dtype=torch.float64)[shape])
     seen = cost < .69
+    warmest = [min(t[1] for t in times[key].values()) for key in keys]
+    second = torch.tensor([np.log(times[keys[i]].get((k, s), (0, 4 * warmest[i]))[1] / warmest[i]) for i, k, s in flat])
+    weight = torch.tensor([heavy if key[2] * key[3] >= 1 << 24 else 1. for key in keys], dtype=torch.float64)
+    value = (cost + 3 * torch.relu(cost - .05) + warm * second) * (weight / weight.mean())[shape]
     T, rows, blocks, splits, part, units, row_tiles, k_waves, x_bytes = f.T
     wave_steps, rounds, is_split = .25 * part / k_waves, torch.ceil(units / 256), (splits > 1).double()
     raw = torch.tensor(np.log(np.maximum([k.constants for k in table], 2e-3))).requires_grad_(True)
@@ -179,7 +184,7 @@ def fit(table, steps=6000, fidelity=.03):
         z = -guess / (.12 * (1 - late) + .015 * late)
         e = torch.exp(z - over(z.detach(), "amax", -1e9)[shape])
         share = e / over(e, "sum", 0.)[shape]
-        expected = over(share * (cost + 2 * torch.relu(cost - .05)), "sum", 0.).mean()
+        expected = over(share * value, "sum", 0.).mean()
         loss = expected + fidelity * (guess - torch.log(us))[seen].abs().mean()
         optimizer.zero_grad()
         loss.backward()
@@ -189,8 +194,7 @@ def fit(table, steps=6000, fidelity=.03):
             if step % 20 == 0 or step == steps - 1:
                 guess = torch.log(predict())
                 chosen = guess <= over(guess, "amin", 1e9)[shape]
-                hard = over(torch.where(chosen, cost, torch.zeros_like(cost)), "amax", 0.)
-                hard = (hard + torch.relu(hard - .05)).mean().item()
+                hard = over(torch.where(chosen, value, torch.zeros_like(value)), "amax", 0.).mean().item()
                 unused = len(table) - len(set(kernel[chosen].tolist()))
                 if hard + .001 * unused < kept[0]:
                     kept = hard + .001 * unused, torch.exp(raw).numpy().copy(), torch.exp(split).item()

@@ -662,17 +662,20 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
 }
 
 // The kernels of the product and a time model of each (us), fitted to measured
-// calls of 1535 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
-// 1 to 24 splits) whose weights come from memory, as those of a pass through a
-// model's layers do.  make_plan's choice takes 0.6 % longer than the shape's best
-// call on average with 4-bit x and 0.5 % with 16-bit x (27 % at worst), on 300
-// further shapes 0.9 and 1.0 % (38 %); the calls, the fit and the same choice
-// replayed: profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py.
+// calls of 1534 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
+// 1 to 24 splits), each with its weight in memory, as in a pass through a model's
+// layers, and in the card's cache.  With weights from memory make_plan's choice
+// takes 0.7 % longer than the shape's best call on average with 4-bit x and 0.5 %
+// with 16-bit x (26 % at worst), on 300 further shapes 0.8 and 1.0 % (38 %); with
+// cached ones 1.0 and 0.9 %.  The calls, the fit and the same choice replayed:
+// profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py.
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, kMx4Split + join * (bytes of the planes, written and read, in MB)
 // with steps of 128 columns a wave runs through, rounds of 256 blocks, and
 // bytes the weight once, y, and the tokens once and `x_share` of that for every
-// further row tile (MB; bw in TB/s).
+// further row tile (MB; bw in TB/s).  The constants are fitted to the order of the
+// calls first: predicted times are off by about a fifth.  Past the fitted sizes (up
+// to 100000 tokens, 65536 rows and columns, 33 shapes) the choice is within 15 %.
 struct Mx4Kernel {
   int rows, tokens;  // of a block
   int k_waves;       // waves, or groups of them, that split a block's columns
@@ -683,35 +686,35 @@ struct Mx4Kernel {
 };
 const Mx4Kernel kMx4Kernels[] = {
     // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
-    {16, 8, 4, 8, true, 0.0558f, 0.207f, 0.00666f, 11.3f, 0.109f, 1.21f, 9.59f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 0.698f, 0.21f, 0.102f, 2.86f, 0.156f, 0.914f, 0.496f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 1.86f, 0.252f, 0.231f, 3.81f, 0.551f, 0.747f, 0.508f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 0.454f, 0.512f, 0.0592f, 2.79f, 0.306f, 1.98f, 1.04f, run_tile<4, 1, 2, 2, 1>},
-    {128, 32, 2, 32, true, 0.797f, 0.00304f, 0.552f, 4.22f, 0.355f, 2.58f, 0.0392f, run_tile<4, 1, 2, 2, 2>},
-    {128, 64, 2, 32, true, 0.326f, 0.00284f, 0.614f, 4.11f, 0.207f, 5.8f, 0.139f, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 0.0612f, 0.011f, 0.511f, 3.48f, 0.00766f, 5.2f, 0.156f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 0.943f, 0.5f, 0.327f, 4.76f, 0.00206f, 4.82f, 0.034f, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 6.25f, 0.0497f, 0.397f, 12, 0.138f, 0.00495f, 0.0716f, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 0.386f, 0, 0.623f, 12, 0.148f, 8.92f, 0.197f, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 2.81f, 0, 0.624f, 4.16f, 0.0872f, 11.9f, 0.18f, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 1.03f, 0, 0.876f, 12, 0.152f, 9.55f, 0.106f, run_tile<4, 2, 4, 8, 1>},
+    {16, 8, 4, 8, true, 0, 0.188f, 0.111f, 12, 1.59f, 0.868f, 4.21f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 1.06f, 0.183f, 0.00223f, 4.15f, 0.216f, 0.583f, 0.809f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 0.0531f, 0.00865f, 0.235f, 7.04f, 0.332f, 2.23f, 1.48f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 0.00214f, 0.456f, 0.0858f, 7.2f, 0.449f, 1.94f, 4.36f, run_tile<4, 1, 2, 2, 1>},
+    {128, 32, 2, 32, true, 0, 0.00304f, 0.563f, 12, 0.203f, 3.09f, 0, run_tile<4, 1, 2, 2, 2>},
+    {128, 64, 2, 32, true, 0, 0.00284f, 0.543f, 12, 0.302f, 5.95f, 0, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 0, 0.00794f, 0.646f, 12, 0.00293f, 3.93f, 0.0452f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 0, 0.492f, 0.169f, 12, 0, 9.32f, 0, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 5.93f, 0.00509f, 0.362f, 11.9f, 0.173f, 0, 0, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 0, 0, 0.559f, 12, 0.178f, 8.82f, 0, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 4.51f, 0, 0.509f, 2.86f, 0.0651f, 11.7f, 0, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 8.21f, 0.002f, 0.711f, 8.82f, 0.109f, 10, 0, run_tile<4, 2, 4, 8, 1>},
     // 16-bit x: the same
-    {16, 2, 4, 8, false, 0.0504f, 0.236f, 0.00547f, 10.2f, 12, 1.35f, 6.73f, run_skinny16<4, 1, 1, 2>},
-    {16, 4, 4, 8, false, 0.632f, 0.257f, 0.164f, 12, 0.299f, 1.05f, 0.0405f, run_skinny16<4, 1, 2, 2>},
-    {16, 8, 4, 8, false, 0.595f, 0.297f, 0.182f, 5.44f, 0.0073f, 1.33f, 0.609f, run_skinny16<4, 1, 4, 2>},
-    {32, 16, 4, 8, false, 3.14f, 0.448f, 0.399f, 3.14f, 0.0356f, 1.53f, 0.00237f, run_skinny16<4, 2, 8, 2>},
-    {32, 16, 8, 8, false, 0.00841f, 0.00881f, 1.05f, 3, 1.63f, 2.87f, 0.00793f, run_skinny16<8, 2, 8, 1>},
-    {64, 16, 4, 16, false, 0.0858f, 0.0883f, 1.09f, 12, 0.00789f, 2.09f, 0.0281f, run_tile16<2, 1, 2, 1, 4>},
-    {64, 32, 4, 16, false, 0.0932f, 0.0967f, 1.24f, 7.5f, 0.0701f, 3.54f, 0.027f, run_tile16<2, 1, 2, 2, 4>},
-    {64, 32, 2, 8, false, 2.14f, 0.88f, 0.456f, 2.52f, 0.094f, 1.48f, 0.0101f, run_tile16<2, 1, 2, 2, 2>},
-    {128, 32, 2, 8, false, 0.436f, 0.904f, 0.802f, 12, 0.332f, 3.64f, 0, run_tile16<4, 1, 2, 2, 2>},
-    {128, 64, 2, 8, false, 0.177f, 0.128f, 1.24f, 12, 0.00226f, 7.13f, 0, run_tile16<4, 1, 2, 4, 2>},
-    {128, 64, 1, 4, false, 3.53f, 0.817f, 0.507f, 3.85f, 0.261f, 0.0311f, 0.242f, run_tile16<4, 2, 2, 2, 1>},
-    {256, 128, 1, 4, false, 2.27f, 0.301f, 1.24f, 12, 0.0821f, 11.9f, 0, run_tile16<4, 2, 4, 4, 1>},
+    {16, 2, 4, 8, false, 0, 0.229f, 0.0164f, 12, 12, 1.28f, 8.17f, run_skinny16<4, 1, 1, 2>},
+    {16, 4, 4, 8, false, 0.919f, 0.237f, 0.17f, 10.2f, 0.403f, 0.799f, 0, run_skinny16<4, 1, 2, 2>},
+    {16, 8, 4, 8, false, 0.868f, 0.266f, 0.218f, 4.19f, 0.0251f, 0.997f, 0.176f, run_skinny16<4, 1, 4, 2>},
+    {32, 16, 4, 8, false, 3.77f, 0.274f, 0.474f, 7.36f, 0.244f, 0.915f, 0.0191f, run_skinny16<4, 2, 8, 2>},
+    {32, 16, 8, 8, false, 0, 0.00811f, 1.08f, 11.3f, 3.41f, 2.61f, 0, run_skinny16<8, 2, 8, 1>},
+    {64, 16, 4, 16, false, 0, 0.0117f, 1.04f, 12, 0.00273f, 1.96f, 0, run_tile16<2, 1, 2, 1, 4>},
+    {64, 32, 4, 16, false, 0, 0.0161f, 1.1f, 6.46f, 0.15f, 3.68f, 0.992f, run_tile16<2, 1, 2, 2, 4>},
+    {64, 32, 2, 8, false, 1.84f, 0.943f, 0.427f, 3.64f, 0.133f, 1.66f, 0.125f, run_tile16<2, 1, 2, 2, 2>},
+    {128, 32, 2, 8, false, 0, 0.978f, 0.667f, 12, 0.376f, 4.07f, 0, run_tile16<4, 1, 2, 2, 2>},
+    {128, 64, 2, 8, false, 0, 0.015f, 1.1f, 12, 0, 8.47f, 0, run_tile16<4, 1, 2, 4, 2>},
+    {128, 64, 1, 4, false, 3.57f, 0.765f, 0.571f, 6.44f, 0.253f, 0.0119f, 0.0237f, run_tile16<4, 2, 2, 2, 1>},
+    {256, 128, 1, 4, false, 2.36f, 0.0247f, 1.36f, 12, 0.0988f, 12, 0, run_tile16<4, 2, 4, 4, 1>},
 };
 constexpr int kNumMx4Kernels = sizeof(kMx4Kernels) / sizeof(kMx4Kernels[0]);
-constexpr float kMx4Split = 4.04f;  // us of the launch that joins a split's planes
-constexpr int kMx4Splits[] = {1, 2, 3, 4, 6, 8, 12};  // (16 and 24 were the best of no shape)
+constexpr float kMx4Split = 3.83f;  // us of the launch that joins a split's planes
+constexpr int kMx4Splits[] = {1, 2, 3, 4, 6, 8, 12};  // (16 and 24 were the best of no fitted shape)
 constexpr size_t kMaxPlanBytes = (size_t)512 << 20;  // planes of a split
 
 // Sizes a plan is for.
