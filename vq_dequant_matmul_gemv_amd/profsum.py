@@ -32,7 +32,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 ENCODER_SOURCES = ("vq_encode.hip",)
 BLOCK_SOURCES = ("vq_block_device.h", "vq_block_kernels.h", "vq_fp8.hip", "vq_fp8_device.h", "vq_mx4.hip", "vq_mx4_device.h",
-                 "vq_mx4_moe.hip", "vq_norm.hip", "vq_router.hip", "vq_router_device.h", "vq_store_device.h")
+                 "vq_mx4_groups.h", "vq_mx4_moe.hip", "vq_norm.hip", "vq_router.hip", "vq_router_device.h", "vq_store_device.h")
 
 
 def source_digest(part: str = "matmul") -> str:
