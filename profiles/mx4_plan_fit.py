@@ -7,7 +7,7 @@ Reads the measured calls (mx4_product_calls.txt beside this file) and the table 
 `kMx4Splits` in csrc/vq_mx4.hip, and goes through the same candidates as `make_plan` there: a choice that nobody measured
 is an error.  A shape has the times of its calls captured into one graph with bf16 y, each the median of three replays:
 "cold" over weights at distinct places, read once a replay after 640 MB of other data were read, and "warm" over two
-weights in turn.  A pass through a model's layers meets the cold ones.  Shapes marked as held out are not fitted.
+weights in turn.  A pass through a model's layers meets the cold ones.  Shapes marked as held out or later are not fitted.
 """
 
 import collections
@@ -45,10 +45,13 @@ def split_counts():
     return [int(s) for s in re.search(r"constexpr int kMx4Splits\[\] = \{([\d, ]+)\};", open(SOURCE).read()).group(1).split(",")]
 
 
-def record():
-    """{(x, T, rows, cols): {(kernel, splits): (cold us, warm us)}} and the shapes that are held out; x: "mx4" or "x16"."""
+def record(later=False):
+    """{(x, T, rows, cols): {(kernel, splits): (cold us, warm us)}} and the shapes that are not fitted; x: "mx4" or "x16".
+    later: with those that were measured after the fit."""
     out, held, hold = {}, set(), False
     for line in open(CALLS):
+        if line.startswith("# later") and not later:
+            break
         if line.startswith("#"):
             hold = hold or line.startswith("# held out")
             continue
@@ -124,7 +127,7 @@ def losses(table, measured, split=None):
 
 
 def report(table, split=None):
-    times, held = record()
+    times, held = record(later=True)
     for x in ("mx4", "x16"):
         for name, pick in (("fitted", lambda key: key not in held), ("held out", lambda key: key in held)):
             for k, state in enumerate(("cold", "warm")):

@@ -256,10 +256,12 @@ __device__ __forceinline__ bool join_groups(float4_t (&acc)[MT][NT], int group, 
 //
 // 2048 tokens of 17408 x 5120 with SwiGLU take 114 to 123 us, 3.0 to 3.2 PF/s;
 // 4096 of 8192 x 8192 139 to 150 us, 3.7 to 3.9 PF/s.  Bound by the matrix instructions at the card's power
-// limit: of 155 us that the latter took before the last steps, they alone ran
-// 104; without the writes to LDS it took 124, without the loads 138.  Loads straight into LDS,
-// three steps ahead, were slower: a block on its own took 141 us where this
-// takes 104.
+// limit, then by the loads and their way through LDS: of 139 us that the latter
+// takes in a warm loop they alone run 96; without the loads and their writes to LDS
+// it takes 115, without the loads 122, without scales 129, without fragment reads
+// 130 (parts left out of a copy of this kernel; the 2048 tokens without SwiGLU
+// 129, 93 alone, 110, 119, 120 and 121).  Loads straight into LDS, three steps
+// ahead, were slower: a block on its own took 141 us where this takes 104.
 // ---------------------------------------------------------------------------
 template <bool PRECISE, int WM, int WN, int MT, int NT, int KW>
 __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_tile_kernel(Mx4Args args) {
@@ -475,10 +477,13 @@ __global__ __launch_bounds__(64 * WM * WN * KW, WM * WN * KW / 4) void vq_mx4_ti
 // block, steps of 128 columns (4 blocks: 64 bytes a row of w, 256 a token), KW
 // groups of them as above
 //
-// 61 tokens of 5121 x 4096 take 15 us, bound by the latency of a step: LDS
-// reads, conversions and 16 matrix instructions one after the other in a wave,
-// of which four groups of waves overlap some (17.4 us in one, with splits).
-// 2048 tokens of 17408 x 5120 take 362 to 378 us, 1.0 PF/s, bound by the LDS traffic of
+// 61 tokens of 5121 x 4096 take 15.1 us, bound by the latency of a step, of which
+// four groups of waves overlap some (17.4 us in one, with splits): the loads' way
+// through LDS first, without which a copy took 10.4 (12.3 without the loads alone),
+// then conversions (14.3 without) and the reads of x (14.0), 9.5 without all four.
+// (4-bit x in the kernel above, two groups of 64 x 64: 15.1, without the same 11.5,
+// the loads 12.5, scales 13.4, fragment reads 15.1, all 10.7.)
+// 2048 tokens of 17408 x 5120 take 360 to 378 us, 1.0 PF/s, bound by the LDS traffic of
 // 16-bit x beside the matrix instructions.
 // ---------------------------------------------------------------------------
 template <int XK, bool PRECISE, int WM, int WN, int MT, int NT, int KW>
@@ -662,12 +667,13 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
 }
 
 // The kernels of the product and a time model of each (us), fitted to measured
-// calls of 1534 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
+// calls of 2155 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
 // 1 to 24 splits), each with its weight in memory, as in a pass through a model's
 // layers, and in the card's cache.  With weights from memory make_plan's choice
-// takes 0.7 % longer than the shape's best call on average with 4-bit x and 0.5 %
-// with 16-bit x (26 % at worst), on 300 further shapes 0.8 and 1.0 % (38 %); with
-// cached ones 1.0 and 0.9 %.  The calls, the fit and the same choice replayed:
+// takes 0.8 % longer than the shape's best call on average with 4-bit x and 0.5 %
+// with 16-bit x (27 % at worst), on shapes kept apart 0.7 % (159, 38 %) and 1.7 %
+// (420, 40 %); with cached weights 1.0 to 2.0 %.  The calls, the fit and the same
+// choice replayed:
 // profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py.
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
 //   and, split, kMx4Split + join * (bytes of the planes, written and read, in MB)
@@ -675,7 +681,7 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
 // bytes the weight once, y, and the tokens once and `x_share` of that for every
 // further row tile (MB; bw in TB/s).  The constants are fitted to the order of the
 // calls first: predicted times are off by about a fifth.  Past the fitted sizes (up
-// to 100000 tokens, 65536 rows and columns, 33 shapes) the choice is within 15 %.
+// to 100000 tokens, 65536 rows and columns, 33 shapes) the choice is within 10 %.
 struct Mx4Kernel {
   int rows, tokens;  // of a block
   int k_waves;       // waves, or groups of them, that split a block's columns
@@ -686,18 +692,18 @@ struct Mx4Kernel {
 };
 const Mx4Kernel kMx4Kernels[] = {
     // 4-bit x: streams for few tokens, then tiles, with groups of waves where there are few
-    {16, 8, 4, 8, true, 0, 0.188f, 0.111f, 12, 1.59f, 0.868f, 4.21f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
-    {16, 16, 4, 8, true, 1.06f, 0.183f, 0.00223f, 4.15f, 0.216f, 0.583f, 0.809f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
-    {32, 16, 4, 8, true, 0.0531f, 0.00865f, 0.235f, 7.04f, 0.332f, 2.23f, 1.48f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
-    {128, 32, 1, 16, true, 0.00214f, 0.456f, 0.0858f, 7.2f, 0.449f, 1.94f, 4.36f, run_tile<4, 1, 2, 2, 1>},
-    {128, 32, 2, 32, true, 0, 0.00304f, 0.563f, 12, 0.203f, 3.09f, 0, run_tile<4, 1, 2, 2, 2>},
-    {128, 64, 2, 32, true, 0, 0.00284f, 0.543f, 12, 0.302f, 5.95f, 0, run_tile<4, 1, 2, 4, 2>},
-    {64, 32, 4, 64, true, 0, 0.00794f, 0.646f, 12, 0.00293f, 3.93f, 0.0452f, run_tile<2, 1, 2, 2, 4>},
-    {64, 64, 2, 32, true, 0, 0.492f, 0.169f, 12, 0, 9.32f, 0, run_tile<2, 1, 2, 4, 2>},
-    {128, 128, 1, 16, true, 5.93f, 0.00509f, 0.362f, 11.9f, 0.173f, 0, 0, run_tile<4, 2, 2, 4, 1>},
-    {256, 128, 1, 16, true, 0, 0, 0.559f, 12, 0.178f, 8.82f, 0, run_tile<4, 2, 4, 4, 1>},
-    {256, 192, 1, 16, true, 4.51f, 0, 0.509f, 2.86f, 0.0651f, 11.7f, 0, run_tile<4, 2, 4, 6, 1>},
-    {256, 256, 1, 16, true, 8.21f, 0.002f, 0.711f, 8.82f, 0.109f, 10, 0, run_tile<4, 2, 4, 8, 1>},
+    {16, 8, 4, 8, true, 0.0721f, 0.209f, 0.102f, 12, 0.635f, 0.844f, 3.26f, run_skinny<kMx4XMx4, 4, 1, 1, 2>},
+    {16, 16, 4, 8, true, 0.464f, 0.174f, 0.176f, 10.9f, 0.255f, 0.697f, 2.22f, run_skinny<kMx4XMx4, 4, 1, 2, 2>},
+    {32, 16, 4, 8, true, 1.17f, 0.0388f, 0.222f, 10.8f, 0.423f, 1.06f, 3.75f, run_skinny<kMx4XMx4, 4, 2, 2, 2>},
+    {128, 32, 1, 16, true, 0.0073f, 0.549f, 0.147f, 6.49f, 0.371f, 1.48f, 2.24f, run_tile<4, 1, 2, 2, 1>},
+    {128, 32, 2, 32, true, 1.39f, 0.00304f, 0.628f, 12, 0.0332f, 3.08f, 0.166f, run_tile<4, 1, 2, 2, 2>},
+    {128, 64, 2, 32, true, 0.129f, 0.00284f, 0.553f, 11.5f, 0.244f, 6.82f, 0.252f, run_tile<4, 1, 2, 4, 2>},
+    {64, 32, 4, 64, true, 0.029f, 0.00854f, 0.609f, 12, 0.00328f, 4.83f, 0.118f, run_tile<2, 1, 2, 2, 4>},
+    {64, 64, 2, 32, true, 0.364f, 0.491f, 0.192f, 12, 0.00643f, 8.91f, 0.073f, run_tile<2, 1, 2, 4, 2>},
+    {128, 128, 1, 16, true, 6.01f, 0.0773f, 0.394f, 12, 0.183f, 0.017f, 0.0517f, run_tile<4, 2, 2, 4, 1>},
+    {256, 128, 1, 16, true, 0.709f, 0, 0.531f, 12, 0.106f, 12, 0.292f, run_tile<4, 2, 4, 4, 1>},
+    {256, 192, 1, 16, true, 8.08f, 0.002f, 0.55f, 12, 0.112f, 11.8f, 0.234f, run_tile<4, 2, 4, 6, 1>},
+    {256, 256, 1, 16, true, 9.15f, 0.002f, 0.772f, 12, 0.131f, 9.17f, 0.216f, run_tile<4, 2, 4, 8, 1>},
     // 16-bit x: the same
     {16, 2, 4, 8, false, 0, 0.229f, 0.0164f, 12, 12, 1.28f, 8.17f, run_skinny16<4, 1, 1, 2>},
     {16, 4, 4, 8, false, 0.919f, 0.237f, 0.17f, 10.2f, 0.403f, 0.799f, 0, run_skinny16<4, 1, 2, 2>},
