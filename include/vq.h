@@ -585,9 +585,12 @@ vq_status vq_mx4_gemm(const vq_mx4_tensor *w, const vq_io *io, const void *x, co
  *   y[t] = sum over the slots s with ids[t][s] >= 0 of weights[t][s] *
  *          W_down[e] h[t][s]
  * Products are exact, sums are in fp32, y is rounded to its type once.  A token
- * without an expert gets zeros.  An expert's weights are read once for 2 to 8 of
- * its tokens: the call is for decode batches.  The same call gives the same
- * bits every time; a token's last bits depend on the batch.
+ * without an expert gets zeros.  The call is for decode batches: gate and up
+ * rows of an expert are read once for 2 to 8 of its tokens, down rows for 4, or
+ * (a token or a few that share little) once for every token and slot.  A
+ * token's slots are added in their order, on the latter path those 8 apart
+ * first, then these sums in order.  The same call gives the same bits every
+ * time; a token's last bits depend on the batch.
  *   r: as for vq_moe_route, with num_experts those of both stacks;
  *   gate_up: [E][2 * inter][hidden], interleaved gate and up rows; down:
  *   [E][hidden][inter];

@@ -86,7 +86,11 @@ __device__ __forceinline__ uint32_t lanes_sum_up_to(uint32_t v) {
 // its own would, for the shapes (lanes of a token, experts of a lane) that
 // routers of up to 256 experts commonly have.  Saves that launch, less what the
 // blocks take: 24.0 -> 22.5 us with 256 experts top 8 of 4096x1024 and one
-// token, 11.5 -> 10.1 with 60 top 4 of 1504x352.
+// token, 11.5 -> 10.1 with 60 top 4 of 1504x352.  Up to 5 tokens: those of the
+// kernel with groups of 2 pairs.  The kernel with groups of 4 would gain as much
+// with a copy of its own (256 top 8 of 4096x1024 at 6 tokens 67.2 -> 65.1, 8 78.9
+// -> 77.5; 60 top 4 of 1504x352 at 6 18.0 -> 16.7, 16 24.0 -> 22.7; 8 top 2 of
+// 1024x512 at 8 13.3 -> 11.9), which is not built.
 constexpr int kRouteTokens = 5, kRoutePairs = kRouteTokens * 32;
 struct RouteScratch {
   double wave[4][kRouteLds<32, 8>];
