@@ -667,12 +667,12 @@ void run_skinny16(const Mx4Args& a, int xk, int splits, hipStream_t s) {
 }
 
 // The kernels of the product and a time model of each (us), fitted to measured
-// calls of 2155 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
+// calls of 2152 shapes (1 to 4096 tokens, 16 to 17408 rows, 32 to 17408 columns,
 // 1 to 24 splits), each with its weight in memory, as in a pass through a model's
 // layers, and in the card's cache.  With weights from memory make_plan's choice
 // takes 0.8 % longer than the shape's best call on average with 4-bit x and 0.5 %
 // with 16-bit x (27 % at worst), on shapes kept apart 0.7 % (159, 38 %) and 1.7 %
-// (420, 40 %); with cached weights 1.0 to 2.0 %.  The calls, the fit and the same
+// (419, 40 %); with cached weights 1.0 to 2.0 %.  The calls, the fit and the same
 // choice replayed:
 // profiles/mx4_product_calls.txt, profiles/mx4_plan_fit.py.
 //   base + 4-norm(latency * steps, rounds * (rate * steps + unit), bytes / bw)
